@@ -289,6 +289,135 @@ MM_MOE_API mm_moe_status mm_moe_fp8_block_quantize(const uint16_t* in, uint8_t* 
                                                    uint8_t* scales, int64_t rows, int64_t cols,
                                                    int layout, void* stream);
 
+/* Element types of the operators around the layer (layer norm, balance loss,
+ * gradient clipping). */
+typedef enum { MM_MOE_DT_BF16 = 0, MM_MOE_DT_F16 = 1, MM_MOE_DT_F32 = 2 } mm_moe_dtype;
+
+/* Layer normalisation in front of the layer (the source pages start at the layer and
+ * have no counterpart to this and the next two operators; a training step around the
+ * layer needs them):
+ *   mean = 1/H sum x,  rstd = (1/H sum (x - mean)^2 + eps)^(-1/2),
+ *   y = weight (x - mean) rstd + bias
+ * T tokens of H channels, 1 <= T < 2^31, 1 <= H <= 2^20, eps >= 0.  dtype: of x, y and
+ * their gradients; param_dtype: of weight, bias and their gradients, dtype itself or
+ * fp32.  Everything is computed in fp32 and rounded once where it is stored. */
+typedef struct {
+  int64_t T, H;
+  int32_t dtype, param_dtype; /* mm_moe_dtype */
+  float eps;
+} mm_moe_norm_shape;
+
+/* Bytes of the backward's working memory. */
+MM_MOE_API mm_moe_status mm_moe_norm_workspace_size(const mm_moe_norm_shape* shape,
+                                                    size_t* bytes);
+
+/*   x, y        [T, H], rows ldx / ldy elements apart (>= H); y may equal x when the
+ *               strides are equal
+ *   weight      [H];  bias [H] or NULL
+ *   mean, rstd  [T] fp32 out, for the backward
+ * Pointers aligned to their element; rows on 16-byte boundaries run faster.  Errors as
+ * for the layer. */
+MM_MOE_API mm_moe_status mm_moe_norm_forward(const mm_moe_norm_shape* shape, const void* x,
+                                             int64_t ldx, const void* weight, const void* bias,
+                                             void* y, int64_t ldy, float* mean, float* rstd,
+                                             void* stream);
+
+/* With xh = (x - mean) rstd and g = weight dy:
+ *   dx = rstd (g - 1/H sum g - xh 1/H sum g xh)  [+ dx_add]
+ *   dweight = sum_t dy xh,  dbias = sum_t dy
+ *   dx_add   [T, H] or NULL: a gradient that joins dx (the residual path's), added in fp32
+ *   dx       [T, H] out; may equal dx_add when the strides are equal, must not overlap
+ *            dy or x
+ *   dweight  [H] out;  dbias [H] out or NULL (overwritten, not accumulated)
+ *   workspace  of mm_moe_norm_workspace_size, 16-byte aligned
+ * All sums have a fixed order: bitwise deterministic. */
+MM_MOE_API mm_moe_status mm_moe_norm_backward(
+    const mm_moe_norm_shape* shape, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+    const void* weight, const float* mean, const float* rstd, const void* dx_add, int64_t ldadd,
+    void* dx, int64_t lddx, void* dweight, void* dbias, void* workspace, void* stream);
+
+/* The router's auxiliary losses and per-expert counts, over T tokens split into G
+ * sequences.  A token counts when its mask is set and its logits are not all -inf.
+ * With p = softmax(logits), n_s the counting tokens of sequence s, S the sequences with
+ * n_s > 0, N = sum n_s:
+ *   counts[s, e] = (token, slot) pairs of s routed to e (an index outside [0, E) is
+ *                  dropped)
+ *   seq_loss[s]  = sum_e (E / (k n_s) counts[s, e]) (1 / n_s sum_t p[t, e])  (0 for n_s = 0)
+ *   losses[0]    = 1 / S sum_s seq_loss[s]          the balance loss (1 for an even load)
+ *   losses[1]    = 1 / N sum_t lse_t^2              the z loss
+ * 1 <= T < 2^31 - 65536, 1 <= E <= 1024, 1 <= k <= E, 1 <= G <= 2^24.  dtype: of the
+ * logits and their gradient (the router's are fp32). */
+typedef struct {
+  int64_t T, E, k, G;
+  int32_t dtype; /* mm_moe_dtype */
+} mm_moe_balance_shape;
+
+MM_MOE_API mm_moe_status mm_moe_balance_workspace_size(const mm_moe_balance_shape* shape,
+                                                       size_t* bytes);
+
+/*   logits       [T, E], contiguous;  topk_idx [T, k] int32 (the router's outputs)
+ *   seq_offsets  [G + 1] int32 on the device, ascending: sequence s is tokens
+ *                [seq_offsets[s], seq_offsets[s + 1]) (empty ones allowed; a token in no
+ *                sequence does not count); NULL with G = 1: one sequence of all tokens
+ *   mask         [T] uint8 (0: the token does not count), or NULL
+ *   losses [2], seq_loss [G] fp32;  counts [G, E], tokens [G] (n_s) int32
+ *   lse          [T] fp32: log sum exp of a token's logits, 0 where it does not count
+ *   workspace    16-byte aligned; the backward reads it, so it must not change between
+ *                the two
+ * No atomics on floating-point values: bitwise deterministic.  Errors as for the layer. */
+MM_MOE_API mm_moe_status mm_moe_balance_forward(
+    const mm_moe_balance_shape* shape, const void* logits, const int32_t* topk_idx,
+    const int32_t* seq_offsets, const uint8_t* mask, float* losses, float* seq_loss,
+    int32_t* counts, int32_t* tokens, float* lse, void* workspace, void* stream);
+
+/* The gradient of dlosses[0] balance + dlosses[1] z with the counts held constant (the
+ * forward's arguments, its counts, tokens and workspace):
+ *   dlosses  [2] fp32 on the device
+ *   dlogits  [T, E] out (overwritten; zero where a token does not count); must not
+ *            overlap logits.  mm_moe_router_backward_aux takes it (fp32). */
+MM_MOE_API mm_moe_status mm_moe_balance_backward(
+    const mm_moe_balance_shape* shape, const void* logits, const int32_t* seq_offsets,
+    const uint8_t* mask, const int32_t* counts, const int32_t* tokens, const float* dlosses,
+    void* dlogits, const void* workspace, void* stream);
+
+/* mm_moe_router_backward with a further gradient of the logits, dlogits_aux [T, E] fp32
+ * (the auxiliary losses'), added before the logit gradient is rounded to bf16 for the two
+ * products.  dlogits_aux NULL: mm_moe_router_backward itself. */
+MM_MOE_API mm_moe_status mm_moe_router_backward_aux(
+    const mm_moe_shape* shape, const uint16_t* x, const uint16_t* W_router,
+    const int32_t* topk_idx, const float* topk_w, const float* dtopk_w, const float* dlogits_aux,
+    uint16_t* dlogits, uint16_t* dx, uint16_t* dW_router, void* stream);
+
+/* The global L2 norm of many gradient tensors, and clipping by it:
+ *   norm = (sum over all tensors and elements of g^2)^(1/2)
+ *   coef = min(1, max_norm / (norm + eps)),  out = coef grad
+ * as IEEE arithmetic gives them: an infinite norm has coef 0 (finite gradients become 0,
+ * infinite ones NaN), a NaN norm makes every gradient NaN.  Squares that leave fp32's
+ * range although their values do not are summed in fp64. */
+#define MM_MOE_MAX_GRADS 65536
+typedef struct {
+  const void* grad;  /* device, contiguous, aligned to its element */
+  void* out;         /* clip: may equal grad (in place) or must not overlap any grad */
+  int64_t numel;     /* >= 0 (0: the pointers are not looked at) */
+  int32_t dtype;     /* mm_moe_dtype of grad */
+  int32_t out_dtype; /* of out: dtype, or MM_MOE_DT_F32 (out of place) */
+} mm_moe_grad;
+
+/* Working memory for calls with up to n_tensors tensors (0 .. MM_MOE_MAX_GRADS). */
+MM_MOE_API mm_moe_status mm_moe_grad_workspace_size(int64_t n_tensors, size_t* bytes);
+
+/*   grads  host array of n_tensors entries, read during the call (at most 2^43 elements
+ *          together); the norm alone ignores out and out_dtype
+ *   norm   [1] fp32 device out;  workspace 16-byte aligned
+ *   max_norm >= 0 (may be infinite), eps >= 0
+ * In place and with coef 1 the gradients are not written.  Deterministic: the same
+ * tensors give the same bits.  Errors as for the layer. */
+MM_MOE_API mm_moe_status mm_moe_grad_norm(const mm_moe_grad* grads, int64_t n_tensors,
+                                          float* norm, void* workspace, void* stream);
+MM_MOE_API mm_moe_status mm_moe_grad_clip(const mm_moe_grad* grads, int64_t n_tensors,
+                                          float max_norm, float eps, float* norm,
+                                          void* workspace, void* stream);
+
 /* Synchronises `stream`, then returns the device status word of `scratch`
  * (MM_MOE_OK, MM_MOE_EBADIDX or MM_MOE_ETIMEOUT), or MM_MOE_ECUDA when the
  * synchronisation itself fails.  The only blocking call of the library. */

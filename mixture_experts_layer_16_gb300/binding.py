@@ -6,6 +6,7 @@ library is missing or fails to load, every call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -26,7 +27,10 @@ EXPORTS = ("mm_moe_workspace_size", "mm_moe_forward", "mm_moe_backward", "mm_moe
            "mm_moe_profile_stop", "mm_moe_kernel_name", "mm_moe_kernel_count",
            "mm_moe_route_noalloc", "mm_moe_mx_qdq", "mm_moe_router_forward",
            "mm_moe_router_backward", "mm_moe_fp8_block_qdq", "mm_moe_mx_quantize",
-           "mm_moe_fp8_block_quantize")
+           "mm_moe_fp8_block_quantize", "mm_moe_router_backward_aux",
+           "mm_moe_norm_workspace_size", "mm_moe_norm_forward", "mm_moe_norm_backward",
+           "mm_moe_balance_workspace_size", "mm_moe_balance_forward", "mm_moe_balance_backward",
+           "mm_moe_grad_workspace_size", "mm_moe_grad_norm", "mm_moe_grad_clip")
 
 
 class MoEError(RuntimeError):
@@ -39,6 +43,27 @@ class Shape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("I", ctypes.c_int64),
                 ("E", ctypes.c_int64), ("k", ctypes.c_int64), ("prec", ctypes.c_int32),
                 ("flags", ctypes.c_int32)]
+
+
+# element types of the operators around the layer (mm_moe_dtype)
+MM_MOE_DT_BF16, MM_MOE_DT_F16, MM_MOE_DT_F32 = 0, 1, 2
+DTYPE = {"bf16": MM_MOE_DT_BF16, "fp16": MM_MOE_DT_F16, "fp32": MM_MOE_DT_F32}
+MM_MOE_MAX_GRADS = 65536
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class BalanceShape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("G", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class Grad(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
 MM_MOE_RECOMPUTE = 1  # activation checkpointing (include/mm_moe.h)
@@ -87,6 +112,19 @@ def lib() -> ctypes.CDLL:
                                                 ctypes.c_int, _vp]
         L.mm_moe_router_forward.argtypes = [sp] + [_vp] * 6
         L.mm_moe_router_backward.argtypes = [sp] + [_vp] * 9
+        L.mm_moe_router_backward_aux.argtypes = [sp] + [_vp] * 10
+        i64, szp = ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)
+        nsp, bsp = ctypes.POINTER(NormShape), ctypes.POINTER(BalanceShape)
+        L.mm_moe_norm_workspace_size.argtypes = [nsp, szp]
+        L.mm_moe_norm_forward.argtypes = [nsp, _vp, i64, _vp, _vp, _vp, i64, _vp, _vp, _vp]
+        L.mm_moe_norm_backward.argtypes = [nsp, _vp, i64, _vp, i64, _vp, _vp, _vp, _vp, i64, _vp,
+                                           i64, _vp, _vp, _vp, _vp]
+        L.mm_moe_balance_workspace_size.argtypes = [bsp, szp]
+        L.mm_moe_balance_forward.argtypes = [bsp] + [_vp] * 11
+        L.mm_moe_balance_backward.argtypes = [bsp] + [_vp] * 9
+        L.mm_moe_grad_workspace_size.argtypes = [i64, szp]
+        L.mm_moe_grad_norm.argtypes = [_vp, i64, _vp, _vp, _vp]
+        L.mm_moe_grad_clip.argtypes = [_vp, i64, ctypes.c_float, ctypes.c_float, _vp, _vp, _vp]
         for fn in EXPORTS:
             getattr(L, fn).restype = ctypes.c_int
         L.mm_moe_kernel_name.restype = ctypes.c_char_p
@@ -242,6 +280,85 @@ def mm_moe_router_backward(shape: Shape, x, W_router, topk_idx, topk_w, dtopk_w,
     if check:
         _check("mm_moe_router_backward", st)
     return st
+
+
+def mm_moe_router_backward_aux(shape: Shape, x, W_router, topk_idx, topk_w, dtopk_w, dlogits_aux,
+                               dlogits, dx, dW_router, stream=None) -> None:
+    _check("mm_moe_router_backward_aux", lib().mm_moe_router_backward_aux(
+        ctypes.byref(shape), _ptr(x), _ptr(W_router), _ptr(topk_idx), _ptr(topk_w),
+        _ptr(dtopk_w), _ptr(dlogits_aux), _ptr(dlogits), _ptr(dx), _ptr(dW_router),
+        _stream(stream)))
+
+
+def _size(fn: str, arg) -> int:
+    n = ctypes.c_size_t(0)
+    _check(fn, getattr(lib(), fn)(arg, ctypes.byref(n)))
+    return n.value
+
+
+def mm_moe_norm_workspace_size(shape: NormShape) -> int:
+    return _size("mm_moe_norm_workspace_size", ctypes.byref(shape))
+
+
+def mm_moe_norm_forward(shape: NormShape, x, weight, bias, y, mean, rstd, stream=None) -> None:
+    """x and y [T, H] with rows stride(0) elements apart."""
+    _check("mm_moe_norm_forward", lib().mm_moe_norm_forward(
+        ctypes.byref(shape), _ptr(x), x.stride(0), _ptr(weight), _ptr(bias), _ptr(y),
+        y.stride(0), _ptr(mean), _ptr(rstd), _stream(stream)))
+
+
+def mm_moe_norm_backward(shape: NormShape, dy, x, weight, mean, rstd, dx_add, dx, dweight, dbias,
+                         workspace, stream=None) -> None:
+    _check("mm_moe_norm_backward", lib().mm_moe_norm_backward(
+        ctypes.byref(shape), _ptr(dy), dy.stride(0), _ptr(x), x.stride(0), _ptr(weight),
+        _ptr(mean), _ptr(rstd), _ptr(dx_add), 0 if dx_add is None else dx_add.stride(0),
+        _ptr(dx), dx.stride(0), _ptr(dweight), _ptr(dbias), _ptr(workspace), _stream(stream)))
+
+
+def mm_moe_balance_workspace_size(shape: BalanceShape) -> int:
+    return _size("mm_moe_balance_workspace_size", ctypes.byref(shape))
+
+
+def mm_moe_balance_forward(shape: BalanceShape, logits, topk_idx, seq_offsets, mask, losses,
+                           seq_loss, counts, tokens, lse, workspace, stream=None) -> None:
+    _check("mm_moe_balance_forward", lib().mm_moe_balance_forward(
+        ctypes.byref(shape), _ptr(logits), _ptr(topk_idx), _ptr(seq_offsets), _ptr(mask),
+        _ptr(losses), _ptr(seq_loss), _ptr(counts), _ptr(tokens), _ptr(lse), _ptr(workspace),
+        _stream(stream)))
+
+
+def mm_moe_balance_backward(shape: BalanceShape, logits, seq_offsets, mask, counts, tokens,
+                            dlosses, dlogits, workspace, stream=None) -> None:
+    _check("mm_moe_balance_backward", lib().mm_moe_balance_backward(
+        ctypes.byref(shape), _ptr(logits), _ptr(seq_offsets), _ptr(mask), _ptr(counts),
+        _ptr(tokens), _ptr(dlosses), _ptr(dlogits), _ptr(workspace), _stream(stream)))
+
+
+def mm_moe_grad_workspace_size(n_tensors: int) -> int:
+    return _size("mm_moe_grad_workspace_size", int(n_tensors))
+
+
+def _grad_array(entries):
+    """[(grad pointer, out pointer, numel, dtype, out dtype)] as a packed mm_moe_grad array."""
+    flat = array.array("Q")
+    for g, o, n, d, od in entries:
+        flat.extend((g, o, n, d | od << 32))
+    return flat
+
+
+def mm_moe_grad_norm(entries, norm, workspace, stream=None) -> None:
+    """entries as for mm_moe_grad_clip (the out fields are ignored)."""
+    flat = _grad_array(entries)
+    _check("mm_moe_grad_norm", lib().mm_moe_grad_norm(
+        flat.buffer_info()[0], len(entries), _ptr(norm), _ptr(workspace), _stream(stream)))
+
+
+def mm_moe_grad_clip(entries, max_norm: float, eps: float, norm, workspace, stream=None) -> None:
+    """entries: (grad data_ptr, out data_ptr, numel, dtype, out dtype) of every tensor."""
+    flat = _grad_array(entries)
+    _check("mm_moe_grad_clip", lib().mm_moe_grad_clip(
+        flat.buffer_info()[0], len(entries), float(max_norm), float(eps), _ptr(norm),
+        _ptr(workspace), _stream(stream)))
 
 
 def mm_moe_read_status(scratch, stream=None) -> int:

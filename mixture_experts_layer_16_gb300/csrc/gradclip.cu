@@ -1,0 +1,356 @@
+// gradclip.cu -- the global L2 norm of many gradient tensors, and clipping by it.
+//
+//   norm = (sum over tensors and elements of g^2)^(1/2)
+//   coef = min(1, max_norm / (norm + eps)),   out = coef g
+//
+// The tensors' addresses travel in the kernels' parameters, so a call needs no copy to
+// the device and holds nothing from one call to the next.  The tensors are cut into
+// chunks of CHUNK elements; the CTAs of a launch take every gridDim.x-th chunk.  Squares
+// are summed in fp32 inside a thread's share of a chunk and in fp64 from there on; a
+// share whose fp32 sum leaves [1e-30, 1e36] (squares that overflow or vanish although
+// their values do not) is summed again in fp64.  Every sum has a fixed order.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "dtype.cuh"
+#include "internal.h"
+
+namespace mmmoe {
+
+constexpr int GC_THREADS = 256;
+constexpr int GC_CHUNK = 16384;  // elements: 8 16-byte vectors per thread in 16 bits, 16 in fp32
+constexpr int GC_MAX = 384;      // tensors per launch
+constexpr int GC_CTAS = 8;       // CTAs per SM
+
+// The tensors of one launch.  Elements [0, head) of a tensor precede its first 16-byte
+// boundary; chunk c covers head + [c, c + 1) CHUNK, the first chunk the head too.
+struct GradList {
+  const void* in[GC_MAX];
+  void* out[GC_MAX];
+  int64_t n[GC_MAX];
+  int first[GC_MAX + 1];  // first chunk of each tensor in the launch's numbering
+  uint8_t dt[GC_MAX];     // in | out << 4
+  int count;
+};
+
+__device__ __forceinline__ int find_tensor(const GradList& g, int chunk) {
+  int lo = 0, hi = g.count - 1;  // the last tensor whose first chunk is <= chunk
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (g.first[mid] <= chunk)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+template <typename T>
+__device__ __forceinline__ int64_t head_of(const T* p, int64_t n) {
+  const int64_t h = (16 - (reinterpret_cast<uintptr_t>(p) & 15)) % 16 / sizeof(T);
+  return h < n ? h : n;
+}
+
+
+template <typename T>
+__device__ __forceinline__ double sq_chunk(const T* p, int64_t n, int64_t chunk) {
+  constexpr int N = VN<T>;
+  constexpr int PER = GC_CHUNK / N / GC_THREADS;
+  const int64_t head = head_of(p, n);
+  const int64_t a = head + chunk * GC_CHUNK;
+  const int64_t len = n > a ? (n - a < GC_CHUNK ? n - a : GC_CHUNK) : 0;
+  const uint4* v = reinterpret_cast<const uint4*>(p + a);
+  const int nv = static_cast<int>(len / N);
+  double acc = 0.0;
+  uint4 q[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int j = threadIdx.x + i * GC_THREADS;
+    q[i] = j < nv ? __ldg(v + j) : make_uint4(0, 0, 0, 0);
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    float f[N];
+    unpack(q[i], f, p);
+#pragma unroll
+    for (int j = 0; j < N; ++j) s = fmaf(f[j], f[j], s);
+  }
+  bool again = !(s <= 1e36f);
+  if (s < 1e-30f) {
+    uint32_t bits = 0;  // (all zero: an expert without tokens, nothing to add again)
+#pragma unroll
+    for (int i = 0; i < PER; ++i) bits |= (q[i].x | q[i].y | q[i].z | q[i].w) & 0x7fff7fffu;
+    again = bits != 0;
+  }
+  if (again) {
+#pragma unroll 1
+    for (int i = 0; i < PER; ++i) {
+      const int j = threadIdx.x + i * GC_THREADS;
+      if (j >= nv) break;
+      float f[N];
+      unpack(__ldg(v + j), f, p);
+#pragma unroll
+      for (int t = 0; t < N; ++t) acc += static_cast<double>(f[t]) * static_cast<double>(f[t]);
+    }
+  } else {
+    acc = s;
+  }
+  // the elements before the first and after the last whole vector
+  const int tail = static_cast<int>(len - static_cast<int64_t>(nv) * N);
+  if (static_cast<int>(threadIdx.x) < tail) {
+    const double f = to_f32(p[a + static_cast<int64_t>(nv) * N + threadIdx.x]);
+    acc += f * f;
+  }
+  if (chunk == 0 && static_cast<int>(threadIdx.x) < head) {
+    const double f = to_f32(p[threadIdx.x]);
+    acc += f * f;
+  }
+  return acc;
+}
+
+// part[blockIdx.x] = the CTA's share of the sum of squares.
+__global__ void __launch_bounds__(GC_THREADS) grad_sq_kernel(const __grid_constant__ GradList g,
+                                                             double* __restrict__ part) {
+  __shared__ double s[GC_THREADS / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int total = g.first[g.count];
+  double acc = 0.0;
+  int t = blockIdx.x < total ? find_tensor(g, blockIdx.x) : 0;
+  for (int c = blockIdx.x; c < total; c += gridDim.x) {
+    while (t + 1 < g.count && g.first[t + 1] <= c) ++t;
+    const int64_t k = c - g.first[t];
+    const int d = g.dt[t] & 15;
+    if (d == MM_MOE_DT_BF16)
+      acc += sq_chunk(static_cast<const __nv_bfloat16*>(g.in[t]), g.n[t], k);
+    else if (d == MM_MOE_DT_F16)
+      acc += sq_chunk(static_cast<const __half*>(g.in[t]), g.n[t], k);
+    else
+      acc += sq_chunk(static_cast<const float*>(g.in[t]), g.n[t], k);
+  }
+  acc = block_sum(acc, s);
+  if (threadIdx.x == 0) part[blockIdx.x] = acc;
+}
+
+// Sum of n partials, the same in every CTA: the norm.
+__device__ __forceinline__ double norm_of(const double* part, int n, double* s) {
+  double a = 0.0;
+  for (int i = threadIdx.x; i < n; i += GC_THREADS) a += part[i];
+  return sqrt(block_sum(a, s));
+}
+
+__global__ void __launch_bounds__(GC_THREADS) grad_norm_kernel(const double* __restrict__ part,
+                                                               int n, float* __restrict__ norm) {
+  __shared__ double s[GC_THREADS / 32];
+  pdl_wait();
+  pdl_trigger();
+  const double v = norm_of(part, n, s);
+  if (threadIdx.x == 0) *norm = static_cast<float>(v);
+}
+
+template <typename TI, typename TO>
+__device__ __forceinline__ void scale_chunk(const TI* p, TO* o, int64_t n, int64_t chunk,
+                                            float coef) {
+  constexpr int N = VN<TI>;
+  constexpr int PER = GC_CHUNK / N / GC_THREADS;
+  const int64_t head = head_of(p, n);
+  const int64_t a = head + chunk * GC_CHUNK;
+  const int64_t len = n > a ? (n - a < GC_CHUNK ? n - a : GC_CHUNK) : 0;
+  int done = 0;
+  if (reinterpret_cast<uintptr_t>(o + a) % 16 == 0) {
+    const uint4* v = reinterpret_cast<const uint4*>(p + a);
+    const int nv = static_cast<int>(len / N);
+    uint4 q[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int j = threadIdx.x + i * GC_THREADS;
+      if (j < nv) q[i] = v[j];
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int j = threadIdx.x + i * GC_THREADS;
+      if (j >= nv) break;
+      float f[N];
+      unpack(q[i], f, p);
+#pragma unroll
+      for (int t = 0; t < N; ++t) f[t] *= coef;
+      if constexpr (sizeof(TO) == sizeof(TI)) {
+        reinterpret_cast<uint4*>(o + a)[j] = pack(f, o);
+      } else {  // 16 bits in, fp32 out
+        uint4* w = reinterpret_cast<uint4*>(o + a) + 2 * j;
+        w[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                          __float_as_uint(f[3]));
+        w[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
+                          __float_as_uint(f[7]));
+      }
+    }
+    done = nv * N;
+  }
+  for (int j = done + threadIdx.x; j < len; j += GC_THREADS)
+    o[a + j] = from_f32<TO>(to_f32(p[a + j]) * coef);
+  if (chunk == 0 && static_cast<int>(threadIdx.x) < head)
+    o[threadIdx.x] = from_f32<TO>(to_f32(p[threadIdx.x]) * coef);
+}
+
+// Every CTA joins the partial sums by itself (a few KB from L2), so no launch and no
+// counter stands between the two passes; the first one also stores the norm.
+__global__ void __launch_bounds__(GC_THREADS) grad_scale_kernel(const __grid_constant__ GradList g,
+                                                                const double* __restrict__ part,
+                                                                int n_part, float max_norm,
+                                                                float eps,
+                                                                float* __restrict__ norm) {
+  __shared__ double s[GC_THREADS / 32];
+  pdl_wait();
+  pdl_trigger();
+  const float nrm = static_cast<float>(norm_of(part, n_part, s));
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = nrm;
+  const float ratio = max_norm / (nrm + eps);
+  const float coef = ratio > 1.f ? 1.f : ratio;  // a NaN stays one
+  const int total = g.first[g.count];
+  int t = blockIdx.x < total ? find_tensor(g, blockIdx.x) : 0;
+  for (int c = blockIdx.x; c < total; c += gridDim.x) {
+    while (t + 1 < g.count && g.first[t + 1] <= c) ++t;
+    const void* in = g.in[t];
+    void* out = g.out[t];
+    if (in == out && coef == 1.f) continue;  // nothing changes
+    const int64_t k = c - g.first[t], n = g.n[t];
+    switch (g.dt[t]) {
+      case MM_MOE_DT_BF16 | MM_MOE_DT_BF16 << 4:
+        scale_chunk(static_cast<const __nv_bfloat16*>(in), static_cast<__nv_bfloat16*>(out), n, k,
+                    coef);
+        break;
+      case MM_MOE_DT_F16 | MM_MOE_DT_F16 << 4:
+        scale_chunk(static_cast<const __half*>(in), static_cast<__half*>(out), n, k, coef);
+        break;
+      case MM_MOE_DT_BF16 | MM_MOE_DT_F32 << 4:
+        scale_chunk(static_cast<const __nv_bfloat16*>(in), static_cast<float*>(out), n, k, coef);
+        break;
+      case MM_MOE_DT_F16 | MM_MOE_DT_F32 << 4:
+        scale_chunk(static_cast<const __half*>(in), static_cast<float*>(out), n, k, coef);
+        break;
+      default:
+        scale_chunk(static_cast<const float*>(in), static_cast<float*>(out), n, k, coef);
+    }
+  }
+}
+
+static bool al(const void* p, uintptr_t a) {
+  return p != nullptr && reinterpret_cast<uintptr_t>(p) % a == 0;
+}
+
+// Elements of all tensors together: their chunks count in 32 bits.
+constexpr int64_t MAX_TOTAL = int64_t{1} << 43;
+
+static bool grads_ok(const mm_moe_grad* g, int64_t n, bool clip) {
+  if (n < 0 || n > MM_MOE_MAX_GRADS || (n > 0 && g == nullptr)) return false;
+  int64_t total = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    if (!dtype_ok(g[i].dtype) || g[i].numel < 0 || g[i].numel > MAX_TOTAL) return false;
+    if ((total += g[i].numel) > MAX_TOTAL) return false;
+    if (g[i].numel > 0 && !al(g[i].grad, dtype_bytes(g[i].dtype))) return false;
+    if (!clip) continue;
+    if (g[i].out_dtype != g[i].dtype && g[i].out_dtype != MM_MOE_DT_F32) return false;
+    if (g[i].numel > 0 && !al(g[i].out, dtype_bytes(g[i].out_dtype))) return false;
+    if (g[i].numel > 0 && g[i].out == g[i].grad && g[i].out_dtype != g[i].dtype) return false;
+  }
+  return true;
+}
+
+// Up to GC_MAX tensors from i on into a list; returns the first one left out.
+static int64_t fill_list(GradList* l, const mm_moe_grad* g, int64_t i, int64_t n) {
+  l->count = 0;
+  int64_t chunks = 0;
+  for (; i < n && l->count < GC_MAX; ++i) {
+    if (g[i].numel == 0) continue;
+    const int64_t c = (g[i].numel + GC_CHUNK - 1) / GC_CHUNK;
+    l->in[l->count] = g[i].grad;
+    l->out[l->count] = g[i].out;
+    l->n[l->count] = g[i].numel;
+    l->dt[l->count] = static_cast<uint8_t>(g[i].dtype | g[i].out_dtype << 4);
+    l->first[l->count++] = static_cast<int>(chunks);
+    chunks += c;
+  }
+  l->first[l->count] = static_cast<int>(chunks);
+  return i;
+}
+
+static int64_t max_lists(int64_t n) { return n / GC_MAX + 1; }
+
+// Sum-of-squares launches over all tensors; *n_part partials are written.
+static cudaError_t launch_sq(const Ctx& c, const mm_moe_grad* g, int64_t n, double* part,
+                             int* n_part) {
+  GradList l;
+  int at = 0;
+  for (int64_t i = 0; i < n;) {
+    i = fill_list(&l, g, i, n);
+    if (l.count == 0) break;
+    const int grid = std::min(c.num_sms * GC_CTAS, l.first[l.count]);
+    prof_begin(c, K_GRAD_SQ);
+    const cudaError_t e =
+        launch_k(c.stream, grad_sq_kernel, dim3(grid), dim3(GC_THREADS), 0, l, part + at);
+    prof_end(c, K_GRAD_SQ);
+    if (e != cudaSuccess) return e;
+    at += grid;
+  }
+  *n_part = at;
+  return cudaSuccess;
+}
+
+}  // namespace mmmoe
+
+using namespace mmmoe;
+
+extern "C" MM_MOE_API mm_moe_status mm_moe_grad_workspace_size(int64_t n_tensors, size_t* bytes) {
+  if (n_tensors < 0 || n_tensors > MM_MOE_MAX_GRADS || bytes == nullptr) return MM_MOE_EINVAL;
+  *bytes = static_cast<size_t>(max_lists(n_tensors)) * 152 * GC_CTAS * sizeof(double);
+  return MM_MOE_OK;
+}
+
+extern "C" MM_MOE_API mm_moe_status mm_moe_grad_norm(const mm_moe_grad* grads, int64_t n_tensors,
+                                                     float* norm, void* workspace, void* stream) {
+  if (!grads_ok(grads, n_tensors, false) || !al(norm, 4) || !al(workspace, 16))
+    return MM_MOE_EINVAL;
+  const int sms = std::min(152, sm_count_103());
+  if (sms == 0) return MM_MOE_ENOTSUP;
+  int launches = 0;
+  const Ctx c{static_cast<cudaStream_t>(stream), sms, &launches};
+  double* part = static_cast<double*>(workspace);
+  int n_part = 0;
+  if (launch_sq(c, grads, n_tensors, part, &n_part) != cudaSuccess) return MM_MOE_ECUDA;
+  prof_begin(c, K_GRAD_NORM);
+  const cudaError_t e = launch_k(c.stream, grad_norm_kernel, dim3(1), dim3(GC_THREADS), 0,
+                                 static_cast<const double*>(part), n_part, norm);
+  prof_end(c, K_GRAD_NORM);
+  return e == cudaSuccess ? MM_MOE_OK : MM_MOE_ECUDA;
+}
+
+extern "C" MM_MOE_API mm_moe_status mm_moe_grad_clip(const mm_moe_grad* grads, int64_t n_tensors,
+                                                     float max_norm, float eps, float* norm,
+                                                     void* workspace, void* stream) {
+  if (!grads_ok(grads, n_tensors, true) || !(max_norm >= 0.f) || !(eps >= 0.f) || !al(norm, 4) ||
+      !al(workspace, 16))
+    return MM_MOE_EINVAL;
+  const int sms = std::min(152, sm_count_103());
+  if (sms == 0) return MM_MOE_ENOTSUP;
+  int launches = 0;
+  const Ctx c{static_cast<cudaStream_t>(stream), sms, &launches};
+  double* part = static_cast<double*>(workspace);
+  int n_part = 0;
+  if (launch_sq(c, grads, n_tensors, part, &n_part) != cudaSuccess) return MM_MOE_ECUDA;
+  GradList l;
+  int64_t i = 0;
+  do {  // at least one launch: it stores the norm
+    i = fill_list(&l, grads, i, n_tensors);
+    const int grid = std::max(1, std::min(c.num_sms * GC_CTAS, l.first[l.count]));
+    prof_begin(c, K_GRAD_SCALE);
+    const cudaError_t e =
+        launch_k(c.stream, grad_scale_kernel, dim3(grid), dim3(GC_THREADS), 0, l,
+                 static_cast<const double*>(part), n_part, max_norm, eps, norm);
+    prof_end(c, K_GRAD_SCALE);
+    if (e != cudaSuccess) return MM_MOE_ECUDA;
+  } while (i < n_tensors);
+  return MM_MOE_OK;
+}

@@ -15,7 +15,9 @@ static const char* const kKernelNames[K_COUNT] = {
     "gemm_dgrad_gateup", "unpermute_reduce", "gemm_wgrad_down", "gemm_wgrad_gateup", "gemm_wgrad",
     "mx_qdq_rows", "mx_qdq_cols", "fp8block_rows", "fp8block_cols", "fp8block_tiles", "fbq_rows",
     "fbq_cols", "fbq_tiles", "mxq_rows", "mxq_cols",
-    "gemm_dense_nt", "gemm_dense_nn", "gemm_dense_tn", "router_topk", "router_dlogits"};
+    "gemm_dense_nt", "gemm_dense_nn", "gemm_dense_tn", "router_topk", "router_dlogits",
+    "norm_fwd", "norm_bwd", "norm_bwd_finish", "balance_fwd", "balance_finish", "balance_bwd",
+    "grad_sq", "grad_norm", "grad_scale"};
 
 namespace {
 struct Rec {

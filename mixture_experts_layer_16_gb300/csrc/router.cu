@@ -91,11 +91,13 @@ __global__ void __launch_bounds__(256) router_topk_kernel(const float* __restric
 }
 
 // One warp per token: dlogits[t, e_j] = w_j (g_j - sum_i w_i g_i), zero elsewhere,
-// written as a dense bf16 row for the two backward GEMMs.
+// written as a dense bf16 row for the two backward GEMMs.  A non-null aux [T, E] (the
+// auxiliary losses' logit gradient) is added in fp32 before the rounding.
 template <int PL>
 __global__ void __launch_bounds__(256) router_dlogits_kernel(const int32_t* __restrict__ topk_idx,
                                                              const float* __restrict__ topk_w,
                                                              const float* __restrict__ dtopk_w,
+                                                             const float* __restrict__ aux,
                                                              int64_t T, int E, int k,
                                                              __nv_bfloat16* __restrict__ dlogits) {
   pdl_wait();
@@ -112,13 +114,16 @@ __global__ void __launch_bounds__(256) router_dlogits_kernel(const int32_t* __re
   const float d_mine = w * (g - s);
   float out[PL];
 #pragma unroll
-  for (int i = 0; i < PL; ++i) out[i] = 0.f;
+  for (int i = 0; i < PL; ++i) {
+    const int e = lane + 32 * i;
+    out[i] = aux != nullptr && e < E ? __ldg(aux + t * E + e) : 0.f;
+  }
   for (int j = 0; j < k; ++j) {
     const int e = __shfl_sync(0xffffffffu, e_mine, j);
     const float d = __shfl_sync(0xffffffffu, d_mine, j);
 #pragma unroll
     for (int i = 0; i < PL; ++i)
-      if (e == lane + 32 * i) out[i] = d;
+      if (e == lane + 32 * i) out[i] = aux != nullptr ? out[i] + d : d;
   }
   __nv_bfloat16* row = dlogits + t * E;
 #pragma unroll
@@ -156,11 +161,11 @@ static void launch_topk(const Ctx& c, const float* logits, int64_t T, int E, int
 
 template <int PL>
 static void launch_dlogits(const Ctx& c, const int32_t* idx, const float* w, const float* g,
-                           int64_t T, int E, int k, __nv_bfloat16* dl) {
+                           const float* aux, int64_t T, int E, int k, __nv_bfloat16* dl) {
   const int64_t blocks = (T * 32 + 255) / 256;
   prof_begin(c, K_ROUTER_DLOGITS);
   launch_k(c.stream, router_dlogits_kernel<PL>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-           idx, w, g, T, E, k, dl);
+           idx, w, g, aux, T, E, k, dl);
   prof_end(c, K_ROUTER_DLOGITS);
 }
 
@@ -203,9 +208,17 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_router_backward(
     const mm_moe_shape* shape, const uint16_t* x, const uint16_t* W_router,
     const int32_t* topk_idx, const float* topk_w, const float* dtopk_w, uint16_t* dlogits,
     uint16_t* dx, uint16_t* dW_router, void* stream) {
+  return mm_moe_router_backward_aux(shape, x, W_router, topk_idx, topk_w, dtopk_w, nullptr,
+                                    dlogits, dx, dW_router, stream);
+}
+
+extern "C" MM_MOE_API mm_moe_status mm_moe_router_backward_aux(
+    const mm_moe_shape* shape, const uint16_t* x, const uint16_t* W_router,
+    const int32_t* topk_idx, const float* topk_w, const float* dtopk_w, const float* dlogits_aux,
+    uint16_t* dlogits, uint16_t* dx, uint16_t* dW_router, void* stream) {
   if (!router_shape_ok(shape)) return MM_MOE_EINVAL;
   if (!al(x, 16) || !al(W_router, 16) || !al(topk_idx, 4) || !al(topk_w, 4) ||
-      !al(dtopk_w, 4) || !al(dlogits, 16) || !al(dx, 16) || !al(dW_router, 16))
+      !al(dtopk_w, 4) || (dlogits_aux != nullptr && !al(dlogits_aux, 4)) || !al(dlogits, 16) || !al(dx, 16) || !al(dW_router, 16))
     return MM_MOE_EINVAL;
   int sms = 0;
   if (!device_ok(&sms)) return MM_MOE_ENOTSUP;
@@ -216,11 +229,11 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_router_backward(
   const Ctx c{st, sms, &launches};
   __nv_bfloat16* dl = reinterpret_cast<__nv_bfloat16*>(dlogits);
   if (E <= 128)
-    launch_dlogits<4>(c, topk_idx, topk_w, dtopk_w, T, E, k, dl);
+    launch_dlogits<4>(c, topk_idx, topk_w, dtopk_w, dlogits_aux, T, E, k, dl);
   else if (E <= 256)
-    launch_dlogits<8>(c, topk_idx, topk_w, dtopk_w, T, E, k, dl);
+    launch_dlogits<8>(c, topk_idx, topk_w, dtopk_w, dlogits_aux, T, E, k, dl);
   else
-    launch_dlogits<32>(c, topk_idx, topk_w, dtopk_w, T, E, k, dl);
+    launch_dlogits<32>(c, topk_idx, topk_w, dtopk_w, dlogits_aux, T, E, k, dl);
   if (cudaGetLastError() != cudaSuccess) return MM_MOE_ECUDA;
   // dW_router [E, H] = dlogits [T, E]^T . x [T, H]
   if (launch_dense(c, GEMM_DENSE_TN, dlogits, x, dW_router, E, H, T) != cudaSuccess)

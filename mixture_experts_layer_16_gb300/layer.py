@@ -125,8 +125,10 @@ class MoERouter:
         B.mm_moe_router_forward(self.shape, x, W_router, self.logits, idx, w, stream)
         return idx, w
 
-    def backward(self, x, W_router, topk_idx, topk_w, dtopk_w, dx, dW_router=None, stream=None):
-        """Adds the router's input gradient to dx (in place) and returns dW_router."""
+    def backward(self, x, W_router, topk_idx, topk_w, dtopk_w, dx, dW_router=None, stream=None,
+                 dlogits_aux=None):
+        """Adds the router's input gradient to dx (in place) and returns dW_router.
+        dlogits_aux [T, E] fp32: a further gradient of the logits (MoEBalanceLoss's)."""
         d, bf = self.device, torch.bfloat16
         _need(x, "x", (self.T, self.H), bf, d)
         _need(W_router, "W_router", (self.E, self.H), bf, d)
@@ -137,6 +139,11 @@ class MoERouter:
         if dW_router is None:
             dW_router = torch.empty((self.E, self.H), dtype=bf, device=d)
         _need(dW_router, "dW_router", (self.E, self.H), bf, d)
-        B.mm_moe_router_backward(self.shape, x, W_router, topk_idx, topk_w, dtopk_w,
-                                 self.dlogits, dx, dW_router, stream)
+        if dlogits_aux is None:
+            B.mm_moe_router_backward(self.shape, x, W_router, topk_idx, topk_w, dtopk_w,
+                                     self.dlogits, dx, dW_router, stream)
+        else:
+            _need(dlogits_aux, "dlogits_aux", (self.T, self.E), torch.float32, d)
+            B.mm_moe_router_backward_aux(self.shape, x, W_router, topk_idx, topk_w, dtopk_w,
+                                         dlogits_aux, self.dlogits, dx, dW_router, stream)
         return dW_router

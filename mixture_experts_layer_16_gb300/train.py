@@ -1,0 +1,224 @@
+"""The operators a training step needs around MoELayer: MoELayerNorm in front of it,
+MoEBalanceLoss on the router's logits, MoEGradClip over the step's gradients.
+
+Like MoELayer these are handles that own their small device buffers (torch allocations),
+check tensor dtypes, shapes and devices, and forward every call to the C ABI.  No
+arithmetic happens here.
+"""
+from __future__ import annotations
+
+from typing import Optional, Sequence, Tuple
+
+import torch
+
+from . import binding as B
+from .layer import _need
+
+TORCH_DTYPE = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+_CODE = {TORCH_DTYPE[n]: c for n, c in B.DTYPE.items()}
+
+
+def _device(device) -> torch.device:
+    device = torch.device("cuda" if device is None else device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
+def _dtype(name: str) -> torch.dtype:
+    if name not in TORCH_DTYPE:
+        raise ValueError(f"dtype must be one of {tuple(TORCH_DTYPE)}, got {name!r}")
+    return TORCH_DTYPE[name]
+
+
+def _need_rows(t, name: str, shape, dtype, device) -> None:
+    """As _need, but the rows may lie apart (a slice of wider rows)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    T, H = shape
+    if (H > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) < H):
+        raise ValueError(f"{name}: each row must be contiguous, rows at least {H} apart")
+
+
+class MoELayerNorm:
+    """Layer normalisation of T tokens of H channels: y = weight (x - mean) rstd + bias.
+
+    dtype: of x, y and their gradients; param_dtype: of weight, bias and theirs (dtype
+    itself, the default, or "fp32").  The forward keeps the mean and the reciprocal
+    standard deviation of every token (self.mean, self.rstd, fp32) for its backward."""
+
+    def __init__(self, T: int, H: int, dtype: str = "bf16", param_dtype: Optional[str] = None,
+                 eps: float = 1e-5, bias: bool = True, device: Optional[torch.device] = None):
+        param_dtype = dtype if param_dtype is None else param_dtype
+        self.T, self.H, self.eps, self.bias = T, H, eps, bias
+        self.dtype, self.param_dtype = _dtype(dtype), _dtype(param_dtype)
+        self.device = _device(device)
+        self.shape = B.NormShape(int(T), int(H), B.DTYPE[dtype], B.DTYPE[param_dtype], eps)
+        n = B.mm_moe_norm_workspace_size(self.shape)
+        self.mean = torch.empty(T, dtype=torch.float32, device=self.device)
+        self.rstd = torch.empty(T, dtype=torch.float32, device=self.device)
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def _check_params(self, weight, bias, prefix=""):
+        _need(weight, prefix + "weight", (self.H,), self.param_dtype, self.device)
+        if self.bias:
+            _need(bias, prefix + "bias", (self.H,), self.param_dtype, self.device)
+        elif bias is not None:
+            raise ValueError(f"{prefix}bias: this layer norm has none")
+
+    def forward(self, x, weight, bias=None, y: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+        shp = (self.T, self.H)
+        _need_rows(x, "x", shp, self.dtype, self.device)
+        self._check_params(weight, bias)
+        if y is None:
+            y = torch.empty(shp, dtype=self.dtype, device=self.device)
+        else:
+            _need_rows(y, "y", shp, self.dtype, self.device)
+        B.mm_moe_norm_forward(self.shape, x, weight, bias, y, self.mean, self.rstd, stream)
+        return y
+
+    def backward(self, dy, x, weight, dx_add=None, out=None, stream=None
+                 ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+        """Gradients (dx, dweight, dbias) of the last forward, whose x and weight are given
+        again (dbias None without a bias).  dx_add: a gradient that joins dx (the residual
+        path's); dx may be written over it (out)."""
+        shp = (self.T, self.H)
+        _need_rows(dy, "dy", shp, self.dtype, self.device)
+        _need_rows(x, "x", shp, self.dtype, self.device)
+        _need(weight, "weight", (self.H,), self.param_dtype, self.device)
+        if dx_add is not None:
+            _need_rows(dx_add, "dx_add", shp, self.dtype, self.device)
+        if out is None:
+            w = dict(dtype=self.param_dtype, device=self.device)
+            out = (torch.empty(shp, dtype=self.dtype, device=self.device),
+                   torch.empty(self.H, **w), torch.empty(self.H, **w) if self.bias else None)
+        else:
+            _need_rows(out[0], "dx", shp, self.dtype, self.device)
+            self._check_params(out[1], out[2], "d")
+        dx, dweight, dbias = out
+        B.mm_moe_norm_backward(self.shape, dy, x, weight, self.mean, self.rstd, dx_add, dx,
+                               dweight, dbias, self.workspace, stream)
+        return dx, dweight, dbias
+
+
+class MoEBalanceLoss:
+    """The router's balance and z losses over T tokens in `sequences` sequences, with the
+    per-expert counts, and their logit gradient.
+
+    The forward takes the router's logits and topk_idx and returns (losses [2] fp32: the
+    balance and the z loss; counts [sequences, E] int32).  seq_offsets [sequences + 1]
+    int32 (ascending, on the device) splits the tokens; a token whose mask is 0 does not
+    count.  self.seq_loss, self.tokens, self.lse hold each sequence's balance loss, its
+    counting tokens and each token's log-sum-exp."""
+
+    def __init__(self, T: int, E: int, k: int, sequences: int = 1, dtype: str = "fp32",
+                 device: Optional[torch.device] = None):
+        self.T, self.E, self.k, self.G = T, E, k, sequences
+        self.dtype = _dtype(dtype)
+        self.device = _device(device)
+        self.shape = B.BalanceShape(int(T), int(E), int(k), int(sequences), B.DTYPE[dtype])
+        n = B.mm_moe_balance_workspace_size(self.shape)
+        f, i, d = torch.float32, torch.int32, self.device
+        self.losses = torch.empty(2, dtype=f, device=d)
+        self.seq_loss = torch.empty(sequences, dtype=f, device=d)
+        self.counts = torch.empty((sequences, E), dtype=i, device=d)
+        self.tokens = torch.empty(sequences, dtype=i, device=d)
+        self.lse = torch.empty(T, dtype=f, device=d)
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=d)
+
+    def _check(self, logits, seq_offsets, mask):
+        _need(logits, "logits", (self.T, self.E), self.dtype, self.device)
+        if seq_offsets is not None:
+            _need(seq_offsets, "seq_offsets", (self.G + 1,), torch.int32, self.device)
+        elif self.G != 1:
+            raise ValueError("seq_offsets: needed for more than one sequence")
+        if mask is not None:
+            if isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
+                mask = mask.view(torch.uint8)
+            _need(mask, "mask", (self.T,), torch.uint8, self.device)
+        return mask
+
+    def forward(self, logits, topk_idx, seq_offsets=None, mask=None, stream=None
+                ) -> Tuple[torch.Tensor, torch.Tensor]:
+        mask = self._check(logits, seq_offsets, mask)
+        _need(topk_idx, "topk_idx", (self.T, self.k), torch.int32, self.device)
+        B.mm_moe_balance_forward(self.shape, logits, topk_idx, seq_offsets, mask, self.losses,
+                                 self.seq_loss, self.counts, self.tokens, self.lse,
+                                 self.workspace, stream)
+        return self.losses, self.counts
+
+    def backward(self, logits, dlosses, seq_offsets=None, mask=None,
+                 dlogits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The logit gradient of dlosses[0] balance + dlosses[1] z (dlosses [2] fp32 on the
+        device) of the last forward, whose logits, seq_offsets and mask are given again.
+        MoERouter.backward takes it as dlogits_aux."""
+        mask = self._check(logits, seq_offsets, mask)
+        _need(dlosses, "dlosses", (2,), torch.float32, self.device)
+        if dlogits is None:
+            dlogits = torch.empty((self.T, self.E), dtype=self.dtype, device=self.device)
+        else:
+            _need(dlogits, "dlogits", (self.T, self.E), self.dtype, self.device)
+        B.mm_moe_balance_backward(self.shape, logits, seq_offsets, mask, self.counts, self.tokens,
+                                  dlosses, dlogits, self.workspace, stream)
+        return dlogits
+
+
+class MoEGradClip:
+    """The global L2 norm of up to max_tensors gradients, and clipping by it: every
+    gradient times min(1, max_norm / (norm + eps))."""
+
+    def __init__(self, max_tensors: int = 1024, eps: float = 1e-6,
+                 device: Optional[torch.device] = None):
+        self.max_tensors, self.eps = max_tensors, eps
+        self.device = _device(device)
+        n = B.mm_moe_grad_workspace_size(max_tensors)
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def _entries(self, grads: Sequence[torch.Tensor], out):
+        if len(grads) > self.max_tensors:
+            raise ValueError(f"grads: {len(grads)} tensors, made for at most {self.max_tensors}")
+        if out is not None and len(out) != len(grads):
+            raise ValueError(f"out: expected {len(grads)} tensors, got {len(out)}")
+        dev, code = self.device, _CODE
+        entries = []
+        for i, g in enumerate(grads):
+            d = code.get(g.dtype)
+            if d is None or g.device != dev or not g.is_contiguous():
+                raise ValueError(f"grads[{i}]: expected a contiguous bf16, fp16 or fp32 tensor "
+                                 f"on {dev}")
+            p = g.data_ptr()
+            entries.append((p, p, g.numel(), d, d))
+        if out is not None:
+            f32 = B.MM_MOE_DT_F32
+            for i, (o, g) in enumerate(zip(out, grads)):
+                od, (p, _, n, d, _) = code.get(o.dtype), entries[i]
+                if (od != d and od != f32) or o.device != dev or not o.is_contiguous() \
+                        or o.shape != g.shape:
+                    raise ValueError(f"out[{i}]: expected a contiguous tensor like grads[{i}], of "
+                                     "its dtype or fp32")
+                entries[i] = (p, o.data_ptr(), n, d, od)
+        return entries
+
+    def norm(self, grads: Sequence[torch.Tensor], stream=None) -> torch.Tensor:
+        """The norm as a 0-d fp32 tensor on the device (no synchronisation)."""
+        norm = torch.empty((), dtype=torch.float32, device=self.device)
+        B.mm_moe_grad_norm(self._entries(grads, None), norm, self.workspace, stream)
+        return norm
+
+    def clip(self, grads: Sequence[torch.Tensor], max_norm: float, out=None,
+             stream=None) -> torch.Tensor:
+        """Clips in place, or into `out` (tensors of the gradients' dtypes or fp32);
+        returns the norm before clipping as a 0-d fp32 tensor on the device."""
+        if not max_norm >= 0.0:
+            raise ValueError(f"max_norm must be >= 0, got {max_norm}")
+        norm = torch.empty((), dtype=torch.float32, device=self.device)
+        B.mm_moe_grad_clip(self._entries(grads, out), max_norm, self.eps, norm, self.workspace,
+                           stream)
+        return norm

@@ -1,0 +1,252 @@
+"""MoELayerNorm on the GPU against the fp64 oracle.
+
+Bounds (u: half an ulp of the stored type, e = 2^-24 of fp32).  A sum over H channels is a
+chain of at most H / 256 + 32 fp32 additions (a thread's share, then a tree), so its
+relative error is at most gam = (H / 256 + 32) e of the sum of magnitudes: the mean is off by at
+most gam A, A = mean |x|, which moves xh by at most gam rstd A; the centred squares, rstd
+and the products add a few more roundings.  With a factor 8 for those:
+  y   : u |y| + 8 gam (|w| (|xh| + rstd A) + |b|)
+  dx  : u |dx| + 16 gam rstd (|g| + <|g|> + (|xh| + rstd A) (<|g xh|> + rstd A <|g|>)) + e |add|
+  dw  : u |dw| + (8 gam + gamT) sum_t |dy| (|xh| + rstd A),  db likewise with sum_t |dy|
+where gamT = (T / 64 + 128) e covers the sums over the tokens.  fp16 adds half its smallest
+subnormal step.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle.train as ot
+from mixture_experts_layer_16_gb300 import MoELayerNorm
+from tests import gpu_util as G
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+U = {n: torch.finfo(t).eps / 2 for n, t in DT.items()}
+SUB = {"bf16": 0.0, "fp16": 2.0 ** -25, "fp32": 0.0}
+E32 = 2.0 ** -24
+EPS = 1e-5
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    G.ensure_built()
+
+
+def data(T, H, dtype, param, seed=0, offset=1.0, pad=0):
+    """x, dy, add [T, H] (rows H + pad apart), weight, bias."""
+    r = np.random.default_rng(seed + 7 * T + H)
+
+    def dev(a, dt):
+        return torch.from_numpy(a.astype(np.float32)).to("cuda", DT[dt])
+
+    def rows(a):
+        if pad == 0:
+            return dev(a, dtype)
+        wide = torch.full((T, H + pad), 777.0, dtype=DT[dtype], device="cuda")
+        wide[:, :H] = dev(a, dtype)
+        return wide[:, :H]
+
+    sc = np.exp(r.normal(0, 0.7, H))
+    return dict(x=rows(r.standard_normal((T, H)) * sc + offset * r.standard_normal(H)),
+                dy=rows(r.standard_normal((T, H))), add=rows(r.standard_normal((T, H))),
+                w=dev(1 + 0.3 * r.standard_normal(H), param), b=dev(r.standard_normal(H), param))
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def check(name, got, want, bound):
+    bad = np.abs(got - want) > bound
+    assert not bad.any(), (name, int(bad.sum()), np.argwhere(bad)[:3],
+                           float((np.abs(got - want) / bound).max()))
+
+
+def check_all(d, dtype, param, norm, y, grads, bias=True, add=True):
+    x, dy, w, b = (f64(d[n]) for n in ("x", "dy", "w", "b"))
+    T, H = x.shape
+    gam, gamT = (H / 256 + 32) * E32, (T / 64 + 128) * E32
+    f = ot.norm_forward(x, w, b if bias else None, EPS)
+    g64 = ot.norm_backward(dy, x, w, EPS, f64(d["add"]) if add else None)
+    A = np.abs(x).mean(1)[:, None]
+    r = f["rstd"][:, None]
+    axh = np.abs(f["xh"]) + r * A
+    check("mean", f64(norm.mean), f["mean"], gam * A[:, 0] + 1e-38)
+    # var's error: 2 gam of itself, plus the mean's error squared
+    dvar = 4 * gam / f["rstd"] ** 2 + (gam * A[:, 0]) ** 2
+    check("rstd", f64(norm.rstd), f["rstd"],
+          f["rstd"] * (4 * E32 + 1 - 1 / np.sqrt(1 + f["rstd"] ** 2 * dvar)) * 2)
+    check("y", f64(y), f["y"], U[dtype] * np.abs(f["y"]) + SUB[dtype] +
+          8 * gam * (np.abs(w) * axh + (np.abs(b) if bias else 0)) + 1e-38)
+    if grads is None:
+        return
+    dx, dw, db = grads
+    g = np.abs(dy * w)
+    gm, gx = g.mean(1)[:, None], (g * np.abs(f["xh"])).mean(1)[:, None]
+    bound = U[dtype] * np.abs(g64["dx"]) + SUB[dtype] + \
+        16 * gam * r * (g + gm + axh * (gx + r * A * gm)) + 1e-38
+    if add:
+        bound = bound + E32 * np.abs(f64(d["add"]))
+    check("dx", f64(dx), g64["dx"], bound)
+    ady = np.abs(dy)
+    check("dweight", f64(dw), g64["dweight"], U[param] * np.abs(g64["dweight"]) + SUB[param] +
+          (8 * gam + gamT) * (ady * axh).sum(0) + 1e-38)
+    if bias:
+        check("dbias", f64(db), g64["dbias"], U[param] * np.abs(g64["dbias"]) + SUB[param] +
+              (8 * gam + gamT) * ady.sum(0) + 1e-38)
+    else:
+        assert db is None
+
+
+def go(T, H, dtype="bf16", param="bf16", bias=True, add=True, **kw):
+    d = data(T, H, dtype, param, **kw)
+    n = MoELayerNorm(T, H, dtype, param, eps=EPS, bias=bias)
+    y = n.forward(d["x"], d["w"], d["b"] if bias else None)
+    grads = n.backward(d["dy"], d["x"], d["w"], dx_add=d["add"] if add else None)
+    torch.cuda.synchronize()
+    check_all(d, dtype, param, n, y, grads, bias, add)
+    return d, n, y, grads
+
+
+@pytest.mark.parametrize("T,H", [
+    (1, 1), (1, 2), (2, 7), (1, 2048), (3, 8), (5, 64), (64, 128), (33, 129), (7, 1000), (129, 1111),
+    (700, 256), (1201, 264), (300, 2048), (157, 4096), (40, 4104), (12, 8192), (9, 8191),
+    (3, 16384), (5, 20001), (2, 70000)])
+@pytest.mark.parametrize("dtype,param", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp32")])
+def test_norm(T, H, dtype, param):
+    go(T, H, dtype, param, bias=(T + H) % 2 == 0, add=T % 2 == 1)
+
+
+@pytest.mark.parametrize("dtype,param", [("bf16", "fp32"), ("fp16", "fp16")])
+@pytest.mark.parametrize("T,H,pad", [(65, 256, 8), (65, 256, 3), (33, 1000, 24), (9, 333, 1),
+                                     (1, 512, 5), (20, 4096, 64)])
+def test_norm_rows_apart(dtype, param, T, H, pad):
+    go(T, H, dtype, param, pad=pad)
+
+
+@pytest.mark.parametrize("T", [4096, 5003])
+def test_norm_many_rows(T):
+    go(T, 512)
+    go(T, 100, "fp32", "fp32", bias=False)
+
+
+def test_norm_unaligned_pointers():
+    # a row that starts on its element only (2 bytes past a 16-byte boundary)
+    T, H = 19, 256
+    d = data(T, H, "bf16", "bf16")
+    sh = {k: torch.empty(T * H + 1, dtype=torch.bfloat16, device="cuda")[1:].view(T, H).copy_(d[k])
+          for k in ("x", "dy", "add")}
+    n = MoELayerNorm(T, H, eps=EPS)
+    y = n.forward(sh["x"], d["w"], d["b"])
+    grads = n.backward(sh["dy"], sh["x"], d["w"], dx_add=sh["add"])
+    check_all(d, "bf16", "bf16", n, y, grads)
+    # parameters off their 16-byte boundary, rows on theirs
+    ow, ob = (torch.empty(H + 1, dtype=torch.bfloat16, device="cuda")[1:].copy_(d[k]) for k in "wb")
+    out = (torch.empty_like(d["x"]), torch.empty(H + 1, dtype=torch.bfloat16, device="cuda")[1:],
+           torch.empty(H + 1, dtype=torch.bfloat16, device="cuda")[1:])
+    y2 = n.forward(d["x"], ow, ob)
+    check_all(d, "bf16", "bf16", n, y2, n.backward(d["dy"], d["x"], ow, dx_add=d["add"], out=out))
+
+
+@pytest.mark.parametrize("offset", [0.0, 300.0])
+def test_norm_large_mean_and_constant_rows(offset):
+    """A mean far above the spread, and rows of one value (variance 0: rstd = eps^-1/2)."""
+    T, H = 20, 1024
+    d = data(T, H, "fp32", "fp32", offset=offset)
+    d["x"][3] = 5.0
+    d["x"][4] = 0.0
+    n = MoELayerNorm(T, H, "fp32", eps=EPS)
+    y = n.forward(d["x"], d["w"], d["b"])
+    check_all(d, "fp32", "fp32", n, y, n.backward(d["dy"], d["x"], d["w"], dx_add=d["add"]))
+    assert torch.equal(y[4], d["b"])
+
+
+def test_norm_in_place_and_out():
+    T, H = 50, 768
+    d, n, y, grads = go(T, H)
+    x2 = d["x"].clone()
+    n.forward(x2, d["w"], d["b"], y=x2)
+    assert torch.equal(x2, y)
+    n.forward(d["x"], d["w"], d["b"])
+    add2 = d["add"].clone()
+    out = (add2, torch.empty_like(d["w"]), torch.empty_like(d["b"]))
+    n.backward(d["dy"], d["x"], d["w"], dx_add=add2, out=out)
+    for a, b in zip(out, grads):
+        assert torch.equal(a, b)
+
+
+def test_norm_nan_and_inf_stay_in_their_row():
+    T, H = 40, 640
+    d = data(T, H, "bf16", "bf16")
+    clean = MoELayerNorm(T, H, eps=EPS)
+    y0 = clean.forward(d["x"], d["w"], d["b"])
+    x = d["x"].clone()
+    x[7, 3], x[21, 600] = float("nan"), float("inf")
+    n = MoELayerNorm(T, H, eps=EPS)
+    y = n.forward(x, d["w"], d["b"])
+    keep = [t for t in range(T) if t not in (7, 21)]
+    assert torch.equal(y[keep], y0[keep]) and y[7].isnan().all() and y[21].isnan().any()
+    dx, dw, db = n.backward(d["dy"], x, d["w"])
+    clean.forward(d["x"], d["w"], d["b"])
+    dx0, _, db0 = clean.backward(d["dy"], d["x"], d["w"])
+    assert torch.equal(dx[keep], dx0[keep]) and torch.equal(db, db0) and dw.isnan().all()
+
+
+def test_norm_gradient_against_differences():
+    """<gradient, v> against the central difference of the oracle's loss, in fp32."""
+    T, H = 31, 200
+    d = data(T, H, "fp32", "fp32")
+    n = MoELayerNorm(T, H, "fp32", eps=EPS)
+    n.forward(d["x"], d["w"], d["b"])
+    grads = n.backward(d["dy"], d["x"], d["w"])
+    x, w, b, dy = (f64(d[k]) for k in ("x", "w", "b", "dy"))
+    r = np.random.default_rng(1)
+    h = 1e-5
+    for i, (val, g) in enumerate(zip((x, w, b), grads)):
+        v = r.standard_normal(val.shape)
+
+        def L(z):
+            a = [x, w, b]
+            a[i] = z
+            return float((ot.norm_forward(*a, EPS)["y"] * dy).sum())
+        num = (L(val + h * v) - L(val - h * v)) / (2 * h)
+        # fp32 gradients: 1e-5 of the terms' magnitudes; the difference itself is good to h^2
+        assert abs(num - (f64(g) * v).sum()) <= 1e-5 * np.abs(f64(g) * v).sum() + 1e-6
+
+
+def test_norm_repeats_bit_for_bit_and_on_another_stream():
+    d, n, y, grads = go(3000, 384)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y2, out = torch.empty_like(y), tuple(torch.empty_like(g) for g in grads)
+    n.forward(d["x"], d["w"], d["b"], y=y2, stream=s)
+    n.backward(d["dy"], d["x"], d["w"], dx_add=d["add"], out=out, stream=s)
+    s.synchronize()
+    assert torch.equal(y, y2) and all(torch.equal(a, b) for a, b in zip(out, grads))
+
+
+def test_norm_in_a_cuda_graph():
+    d, n, y, grads = go(257, 512)
+    y2, out = torch.empty_like(y), tuple(torch.empty_like(g) for g in grads)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        n.forward(d["x"], d["w"], d["b"], y=y2)
+        n.backward(d["dy"], d["x"], d["w"], dx_add=d["add"], out=out)
+    for _ in range(2):
+        for t in (y2, *out):
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and all(torch.equal(a, b) for a, b in zip(out, grads))
+
+
+def test_norm_rows_past_32_bits():
+    """Rows so far apart that their offsets pass 2^31 elements (one buffer of 5 GB)."""
+    T, H, ld = 5, 256, (1 << 29) + 8
+    d = data(T, H, "bf16", "bf16")
+    big = torch.empty((T - 1) * ld + H, dtype=torch.bfloat16, device="cuda")
+    x = big.as_strided((T, H), (ld, 1))
+    x.copy_(d["x"])
+    n = MoELayerNorm(T, H, eps=EPS)
+    y = n.forward(x, d["w"], d["b"])
+    check_all(d, "bf16", "bf16", n, y, n.backward(d["dy"], x, d["w"], dx_add=d["add"]))
