@@ -27,334 +27,526 @@ struct Rows {
   __device__ __forceinline__ T* row(int64_t t) const { return p + t * ld; }
 };
 
-// A unit is V bytes of a row: 16 where the rows and the parameters allow it, else 4, else
-// one 16-bit element.
-template <int V>
-struct Raw;
-template <>
-struct Raw<16> { using type = uint4; };
-template <>
-struct Raw<4> { using type = uint32_t; };
-template <>
-struct Raw<2> { using type = uint16_t; };
-
-template <typename T, int V>
-__device__ __forceinline__ void unit_unpack(const typename Raw<V>::type& q,
-                                            float (&f)[V / sizeof(T)]) {
-  if constexpr (V == 16) {
-    unpack(q, f, static_cast<const T*>(nullptr));
-  } else {
-    const T* h = reinterpret_cast<const T*>(&q);
-#pragma unroll
-    for (int i = 0; i < V / static_cast<int>(sizeof(T)); ++i) f[i] = to_f32(h[i]);
-  }
+// ------------------------------------------------------------------ two fp32 in a pair
+// Packed fp32 arithmetic: one instruction for two values (add, mul, fma .f32x2).
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 f2_make(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
 }
-template <typename T, int V>
-__device__ __forceinline__ typename Raw<V>::type unit_pack(const float (&f)[V / sizeof(T)]) {
-  if constexpr (V == 16) {
-    return pack(f, static_cast<const T*>(nullptr));
-  } else {
-    typename Raw<V>::type q;
-    T* h = reinterpret_cast<T*>(&q);
-#pragma unroll
-    for (int i = 0; i < V / static_cast<int>(sizeof(T)); ++i) h[i] = from_f32<T>(f[i]);
-    return q;
-  }
+__device__ __forceinline__ void f2_split(f2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float f2_sum(f2 v) {
+  float a, b;
+  f2_split(v, a, b);
+  return a + b;
 }
 
-// U consecutive parameters from column c on.
-template <typename P, int U>
-__device__ __forceinline__ void load_params(const P* __restrict__ p, int c, float (&f)[U]) {
-  if constexpr (U * sizeof(P) >= 16) {
-    constexpr int N = VN<P>;
+// The elements of 16 bytes as fp32 pairs, and back.
+template <typename T>
+__device__ __forceinline__ void unpack2(const uint4& q, f2 (&v)[VN<T> / 2]) {
+  float f[VN<T>];
+  unpack(q, f, static_cast<const T*>(nullptr));
 #pragma unroll
-    for (int i = 0; i < U / N; ++i) {
-      float t[N];
-      unpack(__ldg(reinterpret_cast<const uint4*>(p + c) + i), t, p);
+  for (int i = 0; i < VN<T> / 2; ++i) v[i] = f2_make(f[2 * i], f[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack2(const f2 (&v)[VN<T> / 2]) {
+  float f[VN<T>];
 #pragma unroll
-      for (int j = 0; j < N; ++j) f[i * N + j] = t[j];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < U; ++i) f[i] = to_f32(p[c + i]);
-  }
+  for (int i = 0; i < VN<T> / 2; ++i) f2_split(v[i], f[2 * i], f[2 * i + 1]);
+  return pack(f, static_cast<const T*>(nullptr));
 }
 
+// ---------------------------------------------------------------- rows over a group
+// Both passes split a CTA into groups of GT threads (a power of two up to 32, or whole
+// warps); a group takes every gridDim * groups-th row.  A row is cut into units of 16
+// bytes at the 16-byte boundaries of memory, so its first unit may begin up to 15 bytes in
+// front of the row (of the row before it: read, and masked) and its last one may end past it
+// (copied with a shorter source size).  The cut repeats every 8 rows at most, and a grid
+// of more than one round has a multiple of 8 CTAs, so a group sees the same cut in all
+// its rows and each of its threads the same columns: unit j + i GT, i < NU.
+//
+// Units come through a ring in shared memory, S - 1 rows ahead, by cp.async: a thread
+// copies its own units and reads nothing but what it copied, so no barrier guards the ring.
+constexpr int NORM_THREADS = 512;
+
+// Rows in the ring: what keeps 128 KB (forward) or 96 to 192 KB (backward) of it.
+template <int NU>
+constexpr int norm_fwd_stages = NU <= 4 ? 4 : 2;
+template <int NU>
+constexpr int norm_bwd_stages = NU <= 2 ? 4 : 2;
+// Parameters stay in registers up to 16 columns a thread, else in shared memory.
+template <typename T, int NU>
+constexpr bool norm_params_shared = NU * VN<T> > 16;
+
+__device__ __forceinline__ void async_copy(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async_copy(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ ulonglong2 lds16_f2(uint32_t a) {
+  ulonglong2 v;
+  asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts16_zero(uint32_t a) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+}
 __device__ __forceinline__ void group_bar(int g, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(threads) : "memory");
 }
 
-// Sum over a group of GT threads (whole warps): the warps' sums meet in s[warps], each
-// thread adds them in order.  One barrier; `s` must not be in use from the previous sum.
+// A thread's place: its group and its columns.  EVEN: every row is whole units (it starts
+// on a 16-byte boundary and ends on one), so nothing is masked or cut short.
+template <typename T, int NU, bool EVEN>
+struct Place {
+  static constexpr int U = VN<T>;
+  int GT, g, j, groups, H;
+  int shift;  // elements the row's first unit begins in front of the row
+  int units;
+  __device__ __forceinline__ void init(int GT_, int H_) {
+    GT = GT_;
+    H = H_;
+    g = threadIdx.x / GT;
+    j = threadIdx.x - g * GT;
+    groups = blockDim.x / GT;
+  }
+  template <typename V>
+  __device__ __forceinline__ void cut(const Rows<V>& r, int64_t t) {
+    shift = EVEN ? 0
+                 : static_cast<int>((reinterpret_cast<uintptr_t>(r.p + t * r.ld) & 15) / sizeof(T));
+    units = EVEN ? H / U : (H + shift + U - 1) / U;
+  }
+  // first column of unit i (may be negative, or past the row)
+  __device__ __forceinline__ int col(int i) const { return (j + i * GT) * U - shift; }
+  __device__ __forceinline__ bool has(int i) const { return j + i * GT < units; }
+  // the whole unit lies in the row
+  __device__ __forceinline__ bool whole(int i) const {
+    return EVEN ? has(i) : col(i) >= 0 && col(i) + U <= H;
+  }
+  __device__ __forceinline__ bool in(int c) const { return c >= 0 && c < H; }
+  // The thread's first unit of a row (unit i lies i GT units further on).
+  template <typename V>
+  __device__ __forceinline__ V* at(const Rows<V>& r, int64_t t) const {
+    return r.p + t * r.ld + col(0);
+  }
+  // unit i of the row whose first unit of this thread is at p; what lies past the row
+  // arrives as zero
+  __device__ __forceinline__ void copy(uint32_t slot, const T* p, int i) const {
+    if constexpr (EVEN)
+      async_copy(slot, p + i * GT * U);
+    else
+      async_copy(slot, p + i * GT * U, min(U, H - col(i)) * static_cast<int>(sizeof(T)));
+  }
+  // zero in front of the row
+  __device__ __forceinline__ void mask(uint4& q, int i) const {
+    if (EVEN || i != 0) return;
+    if (j == 0 && shift != 0) {
+      T* h = reinterpret_cast<T*>(&q);
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (k < shift) h[k] = from_f32<T>(0.f);
+    }
+  }
+  __device__ __forceinline__ void store(T* p, int i, const uint4& q) const {
+    T* o = p + i * GT * U;
+    if (whole(i)) {
+      *reinterpret_cast<uint4*>(o) = q;
+    } else if constexpr (!EVEN) {
+      const T* h = reinterpret_cast<const T*>(&q);
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (in(col(i) + k)) o[k] = h[k];
+    }
+  }
+  // parameters of the thread's columns as pairs, zero outside the row
+  template <typename P>
+  __device__ __forceinline__ void params(const P* p, f2 (&v)[NU * U / 2]) const {
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+#pragma unroll
+      for (int k = 0; k < U; k += 2) {
+        const int c = col(i) + k;
+        const float a = p != nullptr && in(c) ? to_f32(p[c]) : 0.f;
+        const float b = p != nullptr && in(c + 1) ? to_f32(p[c + 1]) : 0.f;
+        v[(i * U + k) / 2] = f2_make(a, b);
+      }
+  }
+  // f(column, value) for the thread's pairs of values, inside the row
+  template <typename F>
+  __device__ __forceinline__ void each(const f2 (&v)[NU * U / 2], F f) const {
+#pragma unroll
+    for (int k = 0; k < NU * U / 2; ++k) {
+      const int c = col(2 * k / U) + 2 * k % U;
+      float lo, hi;
+      f2_split(v[k], lo, hi);
+      if (in(c)) f(c, lo);
+      if (in(c + 1)) f(c + 1, hi);
+    }
+  }
+};
+
+// Sums over a group, the same in each of its threads: within a warp by shuffles, across
+// a group's warps through s (one entry per warp of the CTA, not in use from an earlier sum),
+// added in order after one barrier.
+__device__ __forceinline__ float lanes_sum(float v, int GT) {
+  if (GT >= 32) return warp_sum(v);
+  for (int o = GT >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
 __device__ __forceinline__ float group_sum(float v, float* s, int g, int GT) {
-  v = warp_sum(v);
-  if (GT == 32) return v;
-  const int w = (threadIdx.x >> 5) - g * (GT >> 5);
-  if ((threadIdx.x & 31) == 0) s[w] = v;
+  v = lanes_sum(v, GT);
+  if (GT <= 32) return v;
+  const int gw = GT >> 5;
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
   group_bar(g, GT);
+  s += g * gw;
   float t = s[0];
-  for (int i = 1; i < (GT >> 5); ++i) t += s[i];
+  for (int i = 1; i < gw; ++i) t += s[i];
   return t;
 }
 
 // ------------------------------------------------------------------------- forward
-// A row sits in the registers of GT threads (NU units each) from its one read to its
-// output; the CTA holds blockDim / GT rows.
-template <typename T, typename P, int V, int NU>
-__global__ void __launch_bounds__(512) norm_fwd_kernel(Rows<const T> x, Rows<T> y, int T_, int H,
-                                                       int GT, const P* __restrict__ w,
-                                                       const P* __restrict__ b, float eps,
-                                                       float* __restrict__ mean,
-                                                       float* __restrict__ rstd) {
-  constexpr int U = V / static_cast<int>(sizeof(T));
-  using R = typename Raw<V>::type;
-  __shared__ float s[2][16];
+// A thread with up to 16 columns holds its parameters in registers; with more columns a
+// row needs fewer threads, so fewer sums across warps (none up to 2048 columns of 16 bits:
+// 16384 x 2048 bf16 takes 31.8 us with 128 threads a row, 16 columns each), and the
+// parameters come from shared memory.
+template <typename T, typename P, int NU, bool EVEN>
+__global__ void __launch_bounds__(NORM_THREADS, 1) norm_fwd_kernel(
+    Rows<const T> x, Rows<T> y, int T_, int H, int GT, const P* __restrict__ w,
+    const P* __restrict__ b, float eps, float* __restrict__ mean, float* __restrict__ rstd) {
+  constexpr int U = VN<T>, C2 = NU * U / 2, S = norm_fwd_stages<NU>;
+  constexpr bool PS = norm_params_shared<T, NU>;
+  static_assert(EVEN || !PS, "a shifted row's columns do not line up with the parameters");
+  extern __shared__ __align__(16) unsigned char ring_bytes[];
+  __shared__ float s_sum[2][NORM_THREADS / 32];
+  const int nt = blockDim.x;
+  const uint32_t ring =
+      static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)) + threadIdx.x * 16;
+  const uint32_t unit_bytes = nt * 16, stage_bytes = NU * unit_bytes;
   pdl_wait();
   pdl_trigger();
-  const int g = threadIdx.x / GT, j = threadIdx.x - g * GT;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / GT) + g;
-  if (t >= T_) return;  // a group leaves as a whole, and its barrier is its own
-  const int units = H / U;
+  Place<T, NU, EVEN> p;
+  p.init(GT, H);
   const float inv = 1.f / static_cast<float>(H);
-  float* const s0 = s[0] + g * (GT >> 5);
-  float* const s1 = s[1] + g * (GT >> 5);
-  const R* xr = reinterpret_cast<const R*>(x.row(t));
-  R q[NU];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * p.groups;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * p.groups + p.g;
+  // the first row of the warp: its groups loop together
+  int64_t tw = GT < 32 ? t - (p.g & (32 / GT - 1)) : t;
+  p.cut(x, t);
+  const int64_t step_x = step * x.ld, step_y = step * y.ld;
+  const T* px = p.at(x, t);  // the row to copy next
+  T* py = p.at(y, t);
+  int64_t ta = t;
+  const auto issue = [&](uint32_t stage) {
+    if (ta < T_) {
 #pragma unroll
-  for (int i = 0; i < NU; ++i) {
-    const int u = j + i * GT;
-    if (u < units) q[i] = xr[u];
+      for (int i = 0; i < NU; ++i)
+        if (p.has(i)) p.copy(stage + i * unit_bytes, px, i);
+    }
+    async_commit();
+    ta += step;
+    px += step_x;
+  };
+#pragma unroll
+  for (int i = 0; i < S * NU; ++i)
+    if (!p.has(i % NU)) sts16_zero(ring + i * unit_bytes);
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(ring + i * stage_bytes);
+  f2 wv[PS ? 1 : C2], bv[PS ? 1 : C2];
+  // shared: weight then bias in fp32, the two halves of the units apart (16-byte reads of
+  // consecutive units then meet no bank twice)
+  const uint32_t sw = ring - threadIdx.x * 16 + S * stage_bytes;
+  if constexpr (PS) {
+    float* s = reinterpret_cast<float*>(ring_bytes + S * stage_bytes);
+    for (int c = threadIdx.x; c < H; c += nt) {
+      const int at = ((c % U / 4) * p.units + c / U) * 4 + c % 4;
+      s[at] = to_f32(w[c]);
+      s[H + at] = b != nullptr ? to_f32(b[c]) : 0.f;
+    }
+    __syncthreads();
+  } else {
+    p.params(w, wv);
+    p.params(b, bv);
   }
-  float a = 0.f;
+  bool full = true;
 #pragma unroll
-  for (int i = 0; i < NU; ++i) {
-    if (j + i * GT >= units) break;
-    float f[U];
-    unit_unpack<T, V>(q[i], f);
+  for (int i = 0; i < NU; ++i) full = full && p.whole(i);
+  uint32_t st = ring, st_in = ring + (S - 1) * stage_bytes;
+  const uint32_t ring_end = ring + S * stage_bytes;
+  for (; tw < T_; t += step, tw += step, py += step_y) {
+    issue(st_in);
+    async_wait<S - 1>();
+    f2 v[C2];
+    f2 a2 = 0;
 #pragma unroll
-    for (int k = 0; k < U; ++k) a += f[k];
+    for (int i = 0; i < NU; ++i) {
+      uint4 q = lds16(st + i * unit_bytes);
+      p.mask(q, i);
+      f2 u[U / 2];
+      unpack2<T>(q, u);
+#pragma unroll
+      for (int k = 0; k < U / 2; ++k) {
+        v[i * U / 2 + k] = u[k];
+        a2 = f2_add(a2, u[k]);
+      }
+    }
+    st_in = st;
+    st += stage_bytes;
+    if (st == ring_end) st = ring;
+    const float mu = group_sum(f2_sum(a2), s_sum[0], p.g, GT) * inv;
+    const f2 nmu = f2_make(-mu, -mu);
+#pragma unroll
+    for (int k = 0; k < C2; ++k) v[k] = f2_add(v[k], nmu);
+    if (!full) {  // what is not in the row has no deviation either
+#pragma unroll
+      for (int k = 0; k < C2; ++k) {
+        const int c = p.col(2 * k / U) + 2 * k % U;
+        float lo, hi;
+        f2_split(v[k], lo, hi);
+        v[k] = f2_make(p.in(c) ? lo : 0.f, p.in(c + 1) ? hi : 0.f);
+      }
+    }
+    a2 = 0;
+#pragma unroll
+    for (int k = 0; k < C2; ++k) a2 = f2_fma(v[k], v[k], a2);
+    const float r = rsqrtf(group_sum(f2_sum(a2), s_sum[1], p.g, GT) * inv + eps);
+    const f2 r2 = f2_make(r, r);
+    if (t < T_) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        if (!p.has(i)) break;
+        f2 u[U / 2];
+        if constexpr (PS) {
+          const uint32_t at = sw + (p.j + i * GT) * 16;
+#pragma unroll
+          for (int h = 0; h < U / 4; ++h) {
+            const ulonglong2 w4 = lds16_f2(at + h * p.units * 16),
+                             b4 = lds16_f2(at + H * 4 + h * p.units * 16);
+            const int e = i * U / 2 + 2 * h;
+            u[2 * h] = f2_fma(f2_mul(v[e], r2), w4.x, b4.x);
+            u[2 * h + 1] = f2_fma(f2_mul(v[e + 1], r2), w4.y, b4.y);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < U / 2; ++k) {
+            const int e = i * U / 2 + k;
+            u[k] = f2_fma(f2_mul(v[e], r2), wv[e], bv[e]);
+          }
+        }
+        p.store(py, i, pack2<T>(u));
+      }
+      if (p.j == 0) {
+        mean[t] = mu;
+        rstd[t] = r;
+      }
+    }
   }
-  const float mu = group_sum(a, s0, g, GT) * inv;
-  a = 0.f;
-#pragma unroll
-  for (int i = 0; i < NU; ++i) {
-    if (j + i * GT >= units) break;
-    float f[U];
-    unit_unpack<T, V>(q[i], f);
-#pragma unroll
-    for (int k = 0; k < U; ++k) a = fmaf(f[k] - mu, f[k] - mu, a);
-  }
-  const float r = rsqrtf(group_sum(a, s1, g, GT) * inv + eps);
-  R* yr = reinterpret_cast<R*>(y.row(t));
-#pragma unroll
-  for (int i = 0; i < NU; ++i) {
-    const int u = j + i * GT;
-    if (u >= units) break;
-    float f[U], wf[U], bf[U] = {};
-    unit_unpack<T, V>(q[i], f);
-    load_params<P, U>(w, u * U, wf);
-    if (b != nullptr) load_params<P, U>(b, u * U, bf);
-#pragma unroll
-    for (int k = 0; k < U; ++k) f[k] = fmaf((f[k] - mu) * r, wf[k], bf[k]);
-    yr[u] = unit_pack<T, V>(f);
-  }
-  if (j == 0) {
-    mean[t] = mu;
-    rstd[t] = r;
-  }
+  async_wait<0>();
 }
 
 // ------------------------------------------------------------------------ backward
-template <int V>
-__device__ __forceinline__ void async_copy(void* dst, const void* src) {
-  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-  if constexpr (V == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
-}
-
-constexpr int NORM_BWD_THREADS = 512;
-
-// Rows in flight per group: three rows ahead for 32 bytes of a row per thread, one for 64
-// (fp32, 16 columns a thread), so that the ring stays within 192 KB.
-template <typename T, int V, int NU>
-constexpr int norm_stages = V * NU <= 32 ? 4 : 2;
-
-// dx and the CTA's column sums in one read of x, dy (and dx_add).  A group of GT threads
-// takes a row at a time, its threads the same columns in every row, so the column sums
-// stay in their registers.  A thread copies its own units of the next rows into shared
-// memory with cp.async and reads nothing but what it copied itself: no barrier guards
-// the ring, and the one barrier of a row is that of its two sums.
-template <typename T, int V, int NU>
-__global__ void __launch_bounds__(NORM_BWD_THREADS, 1) norm_bwd_kernel(
+// dx and the CTA's column sums in one read of x, dy (and dx_add): the column sums stay
+// in the registers of the threads that own the columns, and a row needs one barrier, that
+// of its two sums.
+template <typename T, int NU, bool EVEN>
+__global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
     Rows<const T> dy, Rows<const T> x, Rows<const T> add, Rows<T> dx, const void* __restrict__ w,
     bool w32, const float* __restrict__ mean, const float* __restrict__ rstd, int T_, int H, int GT,
     float* __restrict__ part) {
-  constexpr int U = V / static_cast<int>(sizeof(T));
-  constexpr int C = NU * U;  // columns per thread
-  constexpr int S = norm_stages<T, V, NU>;
-  using R = typename Raw<V>::type;
-  extern __shared__ __align__(16) unsigned char ring[];
-  __shared__ float2 s_sum[2][NORM_BWD_THREADS / 32];
+  constexpr int U = VN<T>, C2 = NU * U / 2, S = norm_bwd_stages<NU>;
+  extern __shared__ __align__(16) unsigned char ring_bytes[];
+  __shared__ f2 s_sum[2][NORM_THREADS / 32];
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const bool with_add = add.p != nullptr;
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)) + tid * 16;
+  const uint32_t unit_bytes = nt * 16, array_bytes = NU * unit_bytes,
+                 stage_bytes = (with_add ? 3 : 2) * array_bytes;
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, nt = blockDim.x;
-  const int g = tid / GT, j = tid - g * GT, groups = nt / GT, gw = GT >> 5;
-  const int units = H / U;
-  const bool with_add = add.p != nullptr;
-  const int arrays = with_add ? 3 : 2;
+  Place<T, NU, EVEN> p;
+  p.init(GT, H);
   const float inv = 1.f / static_cast<float>(H);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  int64_t t = static_cast<int64_t>(blockIdx.x) * groups + g;
-
-  float wf[C], dw[C], db[C];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * p.groups;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * p.groups + p.g;
+  int64_t tw = GT < 32 ? t - (p.g & (32 / GT - 1)) : t;
+  p.cut(x, t);
+  const int64_t step_x = step * x.ld, step_g = step * dy.ld, step_a = step * add.ld,
+                step_d = step * dx.ld;
+  const T *px = p.at(x, t), *pg = p.at(dy, t), *pa = with_add ? p.at(add, t) : nullptr;
+  T* pd = p.at(dx, t);
+  int64_t ta = t;
+  const auto issue = [&](uint32_t stage) {
+    if (ta < T_) {
 #pragma unroll
-  for (int i = 0; i < NU; ++i)
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int c = (j + i * GT) * U + k;
-      wf[i * U + k] = j + i * GT >= units ? 0.f
-                      : w32               ? static_cast<const float*>(w)[c]
-                                          : to_f32(static_cast<const T*>(w)[c]);
-      dw[i * U + k] = db[i * U + k] = 0.f;
-    }
-
-  const auto slot = [&](int st, int arr, int i) {
-    return reinterpret_cast<R*>(ring) + (static_cast<size_t>((st * arrays + arr) * NU + i) * nt + tid);
-  };
-  const auto issue = [&](int64_t row, int st) {
-    if constexpr (V >= 4) {
-      if (row < T_) {
-        const R* xr = reinterpret_cast<const R*>(x.row(row));
-        const R* gr = reinterpret_cast<const R*>(dy.row(row));
-        const R* ar = with_add ? reinterpret_cast<const R*>(add.row(row)) : nullptr;
-#pragma unroll
-        for (int i = 0; i < NU; ++i) {
-          const int u = j + i * GT;
-          if (u < units) {
-            async_copy<V>(slot(st, 0, i), xr + u);
-            async_copy<V>(slot(st, 1, i), gr + u);
-            if (with_add) async_copy<V>(slot(st, 2, i), ar + u);
-          }
+      for (int i = 0; i < NU; ++i)
+        if (p.has(i)) {
+          p.copy(stage + i * unit_bytes, px, i);
+          p.copy(stage + array_bytes + i * unit_bytes, pg, i);
+          if (with_add) p.copy(stage + 2 * array_bytes + i * unit_bytes, pa, i);
         }
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     }
+    async_commit();
+    ta += step;
+    px += step_x;
+    pg += step_g;
+    if (with_add) pa += step_a;
   };
-  for (int p = 0; p < S - 1; ++p) issue(t + p * step, p);
+  for (int i = 0; i < S * (with_add ? 3 : 2) * NU; ++i)
+    if (!p.has(i % NU)) sts16_zero(ring + i * unit_bytes);
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(ring + i * stage_bytes);
+  f2 wv[C2], dw[C2], db[C2];
+  if (w32)
+    p.params(static_cast<const float*>(w), wv);
+  else
+    p.params(static_cast<const T*>(w), wv);
+#pragma unroll
+  for (int k = 0; k < C2; ++k) dw[k] = db[k] = 0;
   float mu_n = 0.f, r_n = 0.f;
   if (t < T_) {
     mu_n = __ldg(mean + t);
     r_n = __ldg(rstd + t);
   }
-  int st = 0, buf = 0;
-  for (; t < T_; t += step) {
-    issue(t + (S - 1) * step, st == 0 ? S - 1 : st - 1);
-    const float mu = mu_n, r = r_n;
+  int buf = 0;
+  const int gw = GT >> 5;
+  uint32_t st = ring, st_in = ring + (S - 1) * stage_bytes;
+  const uint32_t ring_end = ring + S * stage_bytes;
+  for (; tw < T_; t += step, tw += step, pd += step_d) {
+    issue(st_in);
+    const bool on = t < T_;
+    const float r = r_n;
+    const f2 r2 = f2_make(r, r), m2 = f2_make(-mu_n, -mu_n);
     if (t + step < T_) {
       mu_n = __ldg(mean + t + step);
       r_n = __ldg(rstd + t + step);
     }
-    if constexpr (V >= 4) asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
-    float xh[C], gv[C];
-    float a = 0.f, c = 0.f;
+    async_wait<S - 1>();
+    f2 xh[C2], gv[C2];
+    f2 a2 = 0, c2 = 0;
+    if (on) {
 #pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      const int u = j + i * GT;
-      float fx[U] = {}, fg[U] = {};
-      if (u < units) {
-        if constexpr (V >= 4) {
-          unit_unpack<T, V>(*slot(st, 0, i), fx);
-          unit_unpack<T, V>(*slot(st, 1, i), fg);
-        } else {
-          unit_unpack<T, V>(reinterpret_cast<const R*>(x.row(t))[u], fx);
-          unit_unpack<T, V>(reinterpret_cast<const R*>(dy.row(t))[u], fg);
-        }
+      for (int i = 0; i < NU; ++i) {
+        uint4 qx = lds16(st + i * unit_bytes), qg = lds16(st + array_bytes + i * unit_bytes);
+        p.mask(qx, i);
+        p.mask(qg, i);  // (a zero dy takes the column out of every sum)
+        f2 fx[U / 2], fg[U / 2];
+        unpack2<T>(qx, fx);
+        unpack2<T>(qg, fg);
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          const int e = i * U + k;
-          xh[e] = (fx[k] - mu) * r;
-          dw[e] = fmaf(fg[k], xh[e], dw[e]);
-          db[e] += fg[k];
-          gv[e] = fg[k] * wf[e];
-          a += gv[e];
-          c = fmaf(gv[e], xh[e], c);
+        for (int k = 0; k < U / 2; ++k) {
+          const int e = i * U / 2 + k;
+          xh[e] = f2_mul(f2_add(fx[k], m2), r2);
+          dw[e] = f2_fma(fg[k], xh[e], dw[e]);
+          db[e] = f2_add(db[e], fg[k]);
+          gv[e] = f2_mul(fg[k], wv[e]);
+          a2 = f2_add(a2, gv[e]);
+          c2 = f2_fma(gv[e], xh[e], c2);
         }
       }
     }
-    a = warp_sum(a);
-    c = warp_sum(c);
+    float a = lanes_sum(f2_sum(a2), GT), c = lanes_sum(f2_sum(c2), GT);
     if (GT > 32) {
-      float2* s = s_sum[buf] + g * gw;
-      if ((tid & 31) == 0) s[(tid >> 5) - g * gw] = make_float2(a, c);
-      group_bar(g, GT);
-      a = c = 0.f;
-      for (int i = 0; i < gw; ++i) {
-        const float2 v = s[i];
-        a += v.x;
-        c += v.y;
-      }
+      f2* const m = s_sum[buf] + p.g * gw;
+      if ((tid & 31) == 0) m[(tid >> 5) - p.g * gw] = f2_make(a, c);
+      group_bar(p.g, GT);
+      f2 t2 = m[0];
+      for (int i = 1; i < gw; ++i) t2 = f2_add(t2, m[i]);
+      f2_split(t2, a, c);
       buf ^= 1;
     }
-    a *= inv;
-    c *= inv;
-    R* o = reinterpret_cast<R*>(dx.row(t));
+    if (on) {
+      const f2 na = f2_make(-a * inv, -a * inv), nc = f2_make(-c * inv, -c * inv);
 #pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      const int u = j + i * GT;
-      if (u >= units) break;
-      float f[U] = {};
-      if (with_add) {
-        if constexpr (V >= 4)
-          unit_unpack<T, V>(*slot(st, 2, i), f);
-        else
-          unit_unpack<T, V>(reinterpret_cast<const R*>(add.row(t))[u], f);
-      }
+      for (int i = 0; i < NU; ++i) {
+        if (!p.has(i)) break;
+        f2 u[U / 2];
+        if (with_add) {
+          unpack2<T>(lds16(st + 2 * array_bytes + i * unit_bytes), u);
+        } else {
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int e = i * U + k;
-        f[k] = fmaf(gv[e] - a - xh[e] * c, r, f[k]);
+          for (int k = 0; k < U / 2; ++k) u[k] = 0;
+        }
+#pragma unroll
+        for (int k = 0; k < U / 2; ++k) {
+          const int e = i * U / 2 + k;
+          u[k] = f2_fma(f2_fma(xh[e], nc, f2_add(gv[e], na)), r2, u[k]);
+        }
+        p.store(pd, i, pack2<T>(u));
       }
-      o[u] = unit_pack<T, V>(f);
     }
-    st = st + 1 == S ? 0 : st + 1;
+    st_in = st;
+    st += stage_bytes;
+    if (st == ring_end) st = ring;
   }
-  if constexpr (V >= 4) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  async_wait<0>();
 
   // the groups' column sums, added in order
   float* const p0 = part + static_cast<int64_t>(blockIdx.x) * 2 * H;
-  if (groups == 1) {
-#pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      const int u = j + i * GT;
-      if (u >= units) break;
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        p0[u * U + k] = dw[i * U + k];
-        p0[H + u * U + k] = db[i * U + k];
-      }
-    }
+  if (p.groups == 1) {
+    p.each(dw, [&](int c, float v) { p0[c] = v; });
+    p.each(db, [&](int c, float v) { p0[H + c] = v; });
     return;
   }
-  float* sj = reinterpret_cast<float*>(ring);
+  // Groups may cut their rows differently, so the sums meet by column.
+  float* const sj = reinterpret_cast<float*>(ring_bytes);  // [groups][2][H]
   __syncthreads();
+  if constexpr (EVEN) {
+    float* const q = sj + 2 * p.g * H;
 #pragma unroll
-  for (int e = 0; e < C; ++e) {
-    sj[e * nt + tid] = dw[e];
-    sj[(C + e) * nt + tid] = db[e];
+    for (int i = 0; i < NU; ++i) {
+      if (!p.has(i)) break;
+      ulonglong2* const o = reinterpret_cast<ulonglong2*>(q + p.col(i));
+      ulonglong2* const ob = reinterpret_cast<ulonglong2*>(q + H + p.col(i));
+#pragma unroll
+      for (int k = 0; k < U / 4; ++k) {
+        o[k] = make_ulonglong2(dw[i * U / 2 + 2 * k], dw[i * U / 2 + 2 * k + 1]);
+        ob[k] = make_ulonglong2(db[i * U / 2 + 2 * k], db[i * U / 2 + 2 * k + 1]);
+      }
+    }
+  } else {
+    p.each(dw, [&](int c, float v) { sj[2 * p.g * H + c] = v; });
+    p.each(db, [&](int c, float v) { sj[(2 * p.g + 1) * H + c] = v; });
   }
   __syncthreads();
-  for (int e = g; e < C; e += groups) {
-    const int u = j + e / U * GT;
-    if (u >= units) break;
-    float a = 0.f, c = 0.f;
-    for (int q = 0; q < groups; ++q) {
-      a += sj[e * nt + q * GT + j];
-      c += sj[(C + e) * nt + q * GT + j];
-    }
-    p0[u * U + e % U] = a;
-    p0[H + u * U + e % U] = c;
+  for (int i = tid; i < 2 * H; i += nt) {
+    float v = sj[i];
+#pragma unroll 4
+    for (int k = 1; k < p.groups; ++k) v += sj[2 * k * H + i];
+    p0[i] = v;
   }
 }
 
@@ -452,34 +644,38 @@ __global__ void __launch_bounds__(256) norm_cols_loop_kernel(Rows<const T> dy, R
   part[(static_cast<int64_t>(blockIdx.y) * 2 + 1) * H + i] = c;
 }
 
-// dweight / dbias from n partial rows, added in order.
+// dweight (blockIdx.y 0) / dbias (1) from n partial rows: 16 warps take every 16th row of
+// 32 columns, ten loads in flight each, and are added in order.
 template <typename P>
-__global__ void __launch_bounds__(256) norm_cols_finish_kernel(const float* __restrict__ part,
+__global__ void __launch_bounds__(512) norm_cols_finish_kernel(const float* __restrict__ part,
                                                                int n, int H, P* __restrict__ dw,
                                                                P* __restrict__ db) {
+  constexpr int W = 16, B = 10;
   pdl_wait();
   pdl_trigger();
-  __shared__ float s[2][8][33];
+  __shared__ float s[W][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane;
-  float a = 0.f, c = 0.f;
+  float a = 0.f;
   if (i < H) {
-    for (int j = w; j < n; j += 8) {
-      a += part[(static_cast<int64_t>(j) * 2) * H + i];
-      c += part[(static_cast<int64_t>(j) * 2 + 1) * H + i];
+    const float* p = part + static_cast<int64_t>(blockIdx.y) * H + i;
+    for (int j = w; j < n; j += W * B) {
+      float v[B];
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+        v[b] = j + b * W < n ? __ldcg(p + static_cast<int64_t>(j + b * W) * 2 * H) : 0.f;
+#pragma unroll
+      for (int b = 0; b < B; ++b) a += v[b];
     }
   }
-  s[0][w][lane] = a;
-  s[1][w][lane] = c;
+  s[w][lane] = a;
   __syncthreads();
-  if (w < 2 && i < H) {
+  if (w == 0 && i < H) {
     float t = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) t += s[w][j][lane];
-    if (w == 0)
-      dw[i] = from_f32<P>(t);
-    else if (db != nullptr)
-      db[i] = from_f32<P>(t);
+    for (int j = 0; j < W; ++j) t += s[j][lane];
+    P* out = blockIdx.y == 0 ? dw : db;
+    out[i] = from_f32<P>(t);
   }
 }
 
@@ -502,66 +698,106 @@ static bool vec_ok(const void* p, size_t a) {
   return p != nullptr && reinterpret_cast<uintptr_t>(p) % a == 0;
 }
 
-// Whether rows (null: absent) split into units of V bytes.
+// The cut of an operand's rows (see Place): the same for rows that start on a 16-byte
+// boundary and lie equally far apart modulo 16 bytes.
+template <typename A, typename B>
+static bool same_cut(const Rows<A>& a, const Rows<B>& b, int64_t rows) {
+  if (a.p == nullptr) return true;
+  return reinterpret_cast<uintptr_t>(a.p) % 16 == 0 && reinterpret_cast<uintptr_t>(b.p) % 16 == 0 &&
+         (rows == 1 || (a.ld - b.ld) * sizeof(A) % 16 == 0);
+}
+
+// Threads of a group that holds a row of H elements of T in NU units a thread, whatever
+// its cut (`even`: every row starts on a 16-byte boundary); 0 when no CTA does.
+template <typename T, int NU>
+static int group_threads(int H, bool even) {
+  const int units = (H + (even ? 1 : 2) * (VN<T> - 1)) / VN<T>;
+  const int n = (units + NU - 1) / NU;
+  if (n > NORM_THREADS) return 0;
+  if (n > 32) return (n + 31) / 32 * 32;
+  int g = 1;
+  while (g < n) g *= 2;
+  return g;
+}
+
+struct NormGrid {
+  int GT, groups, ctas;
+};
+
+// Rows spread over every SM first, then over the groups of a CTA (all of a warp's groups).
+// A grid of several rounds has a multiple of 8 CTAs (see Place).
+static NormGrid norm_grid(int GT, int T, int sms, int most_groups = NORM_THREADS) {
+  sms = std::max(8, sms / 8 * 8);
+  const int per_warp = GT < 32 ? 32 / GT : 1;
+  const int most = std::min(most_groups, NORM_THREADS / GT);
+  int groups = std::min(most, (T + sms - 1) / sms);
+  groups = (groups + per_warp - 1) / per_warp * per_warp;
+  return NormGrid{GT, groups, std::min(sms, (T + groups - 1) / groups)};
+}
+
+template <typename K>
+static cudaError_t allow_smem(K* kern, size_t bytes) {
+  if (bytes <= 40 * 1024) return cudaSuccess;  // (48 KB with the static part)
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(bytes));
+}
+
 template <typename T>
-static bool units_ok(const Rows<T>& r, int64_t rows, int H, size_t V) {
-  return r.p == nullptr || (reinterpret_cast<uintptr_t>(r.p) % V == 0 && H * sizeof(T) % V == 0 &&
-                            (rows == 1 || r.ld * sizeof(T) % V == 0));
+static bool even_rows(const Rows<T>& r, int64_t rows) {
+  return rows == 1 || r.ld * sizeof(T) % 16 == 0;
 }
 
-static int round32(int n) { return (n + 31) / 32 * 32; }
-
-template <typename T, typename P, int V, int NU>
-static cudaError_t fwd_launch(const Ctx& c, int GT, Rows<const T> x, Rows<T> y, int T_, int H,
-                              const P* w, const P* b, float eps, float* mean, float* rstd) {
-  const int groups = GT >= 256 ? 1 : 256 / GT;
-  return launch_k(c.stream, norm_fwd_kernel<T, P, V, NU>, dim3((T_ + groups - 1) / groups),
-                  dim3(groups * GT), 0, x, y, T_, H, GT, w, b, eps, mean, rstd);
-}
-
-template <typename T, typename P, int V>
-static cudaError_t fwd_units(const Ctx& c, Rows<const T> x, Rows<T> y, int T_, int H, const P* w,
-                             const P* b, float eps, float* mean, float* rstd) {
-  const int units = H / (V / static_cast<int>(sizeof(T)));
-  constexpr int NMAX = V == 16 ? 8 : 16;
-  // few rows: a row over more threads ends sooner; many: fewer threads sum it more cheaply
-  const int want = T_ <= c.num_sms * 4 ? NMAX / 8 : NMAX;
-  const int GT = std::min(512, round32((units + want - 1) / want));
-  const int nu = (units + GT - 1) / GT;
-#define MM_FWD(N) \
-  if (nu <= N) return fwd_launch<T, P, V, N>(c, GT, x, y, T_, H, w, b, eps, mean, rstd)
-  if constexpr (V == 16) {
-    MM_FWD(1);
-    MM_FWD(2);
-    MM_FWD(4);
-    MM_FWD(8);
-  } else {
-    MM_FWD(2);
-    MM_FWD(16);
-  }
-#undef MM_FWD
-  return launch_k(c.stream, norm_fwd_loop_kernel<T, P>, dim3(std::min(T_, c.num_sms * 8)),
-                  dim3(256), 0, x, y, T_, H, w, b, eps, mean, rstd);
+template <typename T, typename P, int NU>
+static cudaError_t fwd_launch(const Ctx& c, Rows<const T> x, Rows<T> y, int T_, int H, const P* w,
+                              const P* b, float eps, float* mean, float* rstd) {
+  const int GT = group_threads<T, NU>(H, even_rows(x, T_));
+  constexpr int RING = norm_fwd_stages<NU> * NU * 16;  // bytes per thread
+  // the ring and shared parameters have to fit beside each other (H above 8192: one group)
+  const int fit = norm_params_shared<T, NU> ? (224 * 1024 - 8 * H) / (RING * GT) : NORM_THREADS;
+  const NormGrid n = norm_grid(GT, T_, c.num_sms, fit);
+  const int nt = n.GT * n.groups;
+  size_t smem = static_cast<size_t>(RING) * nt;
+  auto* kern = norm_fwd_kernel<T, P, NU, true>;
+  if constexpr (norm_params_shared<T, NU>)
+    smem += sizeof(float) * 2 * H;
+  else if (!(even_rows(x, T_) && H % VN<T> == 0))
+    kern = norm_fwd_kernel<T, P, NU, false>;
+  const cudaError_t e = allow_smem(kern, smem);
+  if (e != cudaSuccess) return e;
+  return launch_k(c.stream, kern, dim3(n.ctas), dim3(nt), smem, x, y, T_, H, n.GT, w, b, eps, mean,
+                  rstd);
 }
 
 template <typename T, typename P>
-static mm_moe_status norm_forward(const Ctx& c, const mm_moe_norm_shape* s, const void* x,
-                                  int64_t ldx, const void* w_, const void* b_, void* y,
+static mm_moe_status norm_forward(const Ctx& c, const mm_moe_norm_shape* s, const void* x_,
+                                  int64_t ldx, const void* w_, const void* b_, void* y_,
                                   int64_t ldy, float* mean, float* rstd) {
   const int T_ = static_cast<int>(s->T), H = static_cast<int>(s->H);
-  const Rows<const T> xr{static_cast<const T*>(x), ldx};
-  const Rows<T> yr{static_cast<T*>(y), ldy};
+  const Rows<const T> x{static_cast<const T*>(x_), ldx};
+  const Rows<T> y{static_cast<T*>(y_), ldy};
   const P* w = static_cast<const P*>(w_);
   const P* b = static_cast<const P*>(b_);
-  const auto ok = [&](size_t V) { return units_ok(xr, T_, H, V) && units_ok(yr, T_, H, V); };
+  constexpr int MOST = 16 / VN<T>;  // units of 16 columns
+  const bool even = even_rows(x, T_);
+  const auto go = [&](auto nu) {
+    return fwd_launch<T, P, decltype(nu)::value>(c, x, y, T_, H, w, b, s->eps, mean, rstd);
+  };
+  const auto pick = [&]() -> cudaError_t {
+    using std::integral_constant;
+    if (same_cut(x, y, T_)) {
+      if (T_ <= c.num_sms && group_threads<T, 1>(H, even) != 0)
+        return go(integral_constant<int, 1>{});  // one row a CTA: spread it wide
+      if constexpr (sizeof(T) == 2) {
+        if (even && H % VN<T> == 0 && H > 512 && H <= 16384)
+          return H <= 1024 ? go(integral_constant<int, 4>{}) : go(integral_constant<int, 8>{});
+      }
+      if (group_threads<T, MOST>(H, even) != 0) return go(integral_constant<int, MOST>{});
+    }
+    return launch_k(c.stream, norm_fwd_loop_kernel<T, P>, dim3(std::min(T_, c.num_sms * 8)),
+                    dim3(256), 0, x, y, T_, H, w, b, s->eps, mean, rstd);
+  };
   prof_begin(c, K_NORM_FWD);
-  cudaError_t e;
-  if (ok(16) && vec_ok(w, 16) && (b == nullptr || vec_ok(b, 16)))
-    e = fwd_units<T, P, 16>(c, xr, yr, T_, H, w, b, s->eps, mean, rstd);
-  else if (sizeof(T) == 4 || ok(4))
-    e = fwd_units<T, P, 4>(c, xr, yr, T_, H, w, b, s->eps, mean, rstd);
-  else
-    e = fwd_units<T, P, sizeof(T)>(c, xr, yr, T_, H, w, b, s->eps, mean, rstd);
+  const cudaError_t e = pick();
   prof_end(c, K_NORM_FWD);
   return e == cudaSuccess ? MM_MOE_OK : MM_MOE_ECUDA;
 }
@@ -578,39 +814,21 @@ struct BwdArgs {
   float* part;
 };
 
-template <typename T, int V, int NU>
-static cudaError_t bwd_launch(const Ctx& c, const BwdArgs<T>& a, int units, int* n_part) {
-  constexpr int C = NU * V / static_cast<int>(sizeof(T));
-  const int GT = round32((units + NU - 1) / NU);
-  const int groups =
-      std::min(NORM_BWD_THREADS / GT, (a.T_ + c.num_sms - 1) / c.num_sms);
-  const int nt = GT * groups;
-  size_t smem = groups > 1 ? static_cast<size_t>(2) * C * nt * sizeof(float) : 0;
-  if (V >= 4)
-    smem = std::max(smem, static_cast<size_t>(norm_stages<T, V, NU>) *
-                              (a.add.p != nullptr ? 3 : 2) * NU * V * nt);
-  auto* kern = norm_bwd_kernel<T, V, NU>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+template <typename T, int NU>
+static cudaError_t bwd_launch(const Ctx& c, const BwdArgs<T>& a, int* n_part) {
+  const NormGrid n = norm_grid(group_threads<T, NU>(a.H, even_rows(a.x, a.T_)), a.T_, c.num_sms);
+  const int nt = n.GT * n.groups;
+  size_t smem =
+      static_cast<size_t>(norm_bwd_stages<NU>) * (a.add.p != nullptr ? 3 : 2) * NU * 16 * nt;
+  if (n.groups > 1) smem = std::max(smem, sizeof(float) * 2 * n.groups * a.H);
+  auto* kern = even_rows(a.x, a.T_) && a.H % VN<T> == 0 ? norm_bwd_kernel<T, NU, true>
+                                                        : norm_bwd_kernel<T, NU, false>;
+  const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
-  *n_part = std::min(c.num_sms, (a.T_ + groups - 1) / groups);
-  return launch_k(c.stream, kern, dim3(*n_part), dim3(nt), smem, a.dy, a.x, a.add, a.dx, a.w,
-                  a.w32, a.mean, a.rstd, a.T_, a.H, GT, a.part);
+  *n_part = n.ctas;
+  return launch_k(c.stream, kern, dim3(n.ctas), dim3(nt), smem, a.dy, a.x, a.add,
+                  a.dx, a.w, a.w32, a.mean, a.rstd, a.T_, a.H, n.GT, a.part);
 }
-
-// 16 columns a thread where a warp would otherwise not hold the row, else as few as fill it
-template <typename T, int V>
-static cudaError_t bwd_units(const Ctx& c, const BwdArgs<T>& a, int* n_part) {
-  constexpr int U = V / static_cast<int>(sizeof(T));
-  const int units = a.H / U;
-  if (units <= 32) return bwd_launch<T, V, 1>(c, a, units, n_part);
-  if constexpr (V == 16 && sizeof(T) == 4) {
-    if (a.H <= 4096) return bwd_launch<T, V, 2>(c, a, units, n_part);
-  }
-  return bwd_launch<T, V, 16 / U>(c, a, units, n_part);
-}
-
-constexpr int NORM_BWD_MAX_H = NORM_BWD_THREADS * 16;
 
 template <typename T, typename P>
 static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, const void* dy,
@@ -630,20 +848,19 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
                      T_,
                      H,
                      part};
-  const auto ok = [&](size_t V) {
-    return units_ok(a.dy, T_, H, V) && units_ok(a.x, T_, H, V) && units_ok(a.add, T_, H, V) &&
-           units_ok(a.dx, T_, H, V);
-  };
+  constexpr int MOST = 16 / VN<T>;
+  const bool even = even_rows(a.x, T_);
   cudaError_t e;
   int n = 0;
-  if (H <= NORM_BWD_MAX_H) {
+  if (same_cut(a.dy, a.x, T_) && same_cut(a.add, a.x, T_) && same_cut(a.dx, a.x, T_) &&
+      group_threads<T, MOST>(H, even) != 0) {
     prof_begin(c, K_NORM_BWD);
-    if (ok(16))
-      e = bwd_units<T, 16>(c, a, &n);
-    else if (sizeof(T) == 4 || ok(4))
-      e = bwd_units<T, 4>(c, a, &n);
+    if (T_ <= c.num_sms && group_threads<T, 1>(H, even) != 0)
+      e = bwd_launch<T, 1>(c, a, &n);
+    else if (MOST == 4 && group_threads<T, 2>(H, even) != 0)
+      e = bwd_launch<T, 2>(c, a, &n);
     else
-      e = bwd_units<T, sizeof(T)>(c, a, &n);
+      e = bwd_launch<T, MOST>(c, a, &n);
     prof_end(c, K_NORM_BWD);
     if (e != cudaSuccess) return MM_MOE_ECUDA;
   } else {
@@ -662,8 +879,9 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
     if (e != cudaSuccess) return MM_MOE_ECUDA;
   }
   prof_begin(c, K_NORM_BWD_FINISH);
-  e = launch_k(c.stream, norm_cols_finish_kernel<P>, dim3((H + 31) / 32), dim3(256), 0,
-               static_cast<const float*>(part), n, H, static_cast<P*>(dw), static_cast<P*>(db));
+  e = launch_k(c.stream, norm_cols_finish_kernel<P>, dim3((H + 31) / 32, db != nullptr ? 2 : 1),
+               dim3(512), 0, static_cast<const float*>(part), n, H, static_cast<P*>(dw),
+               static_cast<P*>(db));
   prof_end(c, K_NORM_BWD_FINISH);
   return e == cudaSuccess ? MM_MOE_OK : MM_MOE_ECUDA;
 }
