@@ -338,27 +338,26 @@ def mm_moe_grad_workspace_size(n_tensors: int) -> int:
     return _size("mm_moe_grad_workspace_size", int(n_tensors))
 
 
-def _grad_array(entries):
+def grad_array(entries):
     """[(grad pointer, out pointer, numel, dtype, out dtype)] as a packed mm_moe_grad array."""
-    flat = array.array("Q")
+    words = []
     for g, o, n, d, od in entries:
-        flat.extend((g, o, n, d | od << 32))
-    return flat
+        words += (g, o, n, d | od << 32)
+    return array.array("Q", words)
 
 
-def mm_moe_grad_norm(entries, norm, workspace, stream=None) -> None:
-    """entries as for mm_moe_grad_clip (the out fields are ignored)."""
-    flat = _grad_array(entries)
-    _check("mm_moe_grad_norm", lib().mm_moe_grad_norm(
-        flat.buffer_info()[0], len(entries), _ptr(norm), _ptr(workspace), _stream(stream)))
+def mm_moe_grad_norm(grads, norm, workspace, stream=None) -> None:
+    """grads: a packed mm_moe_grad array (grad_array); the out fields are ignored."""
+    p, n = grads.buffer_info()
+    _check("mm_moe_grad_norm", lib().mm_moe_grad_norm(p, n // 4, _ptr(norm), _ptr(workspace),
+                                                      _stream(stream)))
 
 
-def mm_moe_grad_clip(entries, max_norm: float, eps: float, norm, workspace, stream=None) -> None:
-    """entries: (grad data_ptr, out data_ptr, numel, dtype, out dtype) of every tensor."""
-    flat = _grad_array(entries)
-    _check("mm_moe_grad_clip", lib().mm_moe_grad_clip(
-        flat.buffer_info()[0], len(entries), float(max_norm), float(eps), _ptr(norm),
-        _ptr(workspace), _stream(stream)))
+def mm_moe_grad_clip(grads, max_norm: float, eps: float, norm, workspace, stream=None) -> None:
+    """grads: a packed mm_moe_grad array (grad_array)."""
+    p, n = grads.buffer_info()
+    _check("mm_moe_grad_clip", lib().mm_moe_grad_clip(p, n // 4, max_norm, eps, _ptr(norm),
+                                                      _ptr(workspace), _stream(stream)))
 
 
 def mm_moe_read_status(scratch, stream=None) -> int:

@@ -4,7 +4,9 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/mm_moe.h"
@@ -88,15 +90,20 @@ auto with_dtype(int32_t d, F f) {
   return f(static_cast<__nv_bfloat16*>(nullptr));
 }
 
-// The running device's SM count, or 0 off sm_103.
+// The current device's SM count, or 0 off sm_103 (asked once per device).
 inline int sm_count_103() {
+  static std::atomic<int> known[64];  // count + 1; 0: not asked yet
   int dev = 0, major = 0, minor = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  if (dev < 64 && known[dev].load(std::memory_order_relaxed) != 0)
+    return known[dev].load(std::memory_order_relaxed) - 1;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 0;
-  return major == 10 && minor == 3 ? sms : 0;
+  const int n = major == 10 && minor == 3 ? sms : 0;
+  if (dev < 64) known[dev].store(n + 1, std::memory_order_relaxed);
+  return n;
 }
 
 template <typename V>

@@ -7,6 +7,7 @@ arithmetic happens here.
 """
 from __future__ import annotations
 
+from array import array
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -31,18 +32,25 @@ def _dtype(name: str) -> torch.dtype:
     return TORCH_DTYPE[name]
 
 
+def _stream(stream, device: torch.device) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return int(getattr(stream, "cuda_stream", stream))
+
+
 def _need_rows(t, name: str, shape, dtype, device) -> None:
     """As _need, but the rows may lie apart (a slice of wider rows)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 2 or tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
     T, H = shape
-    if (H > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) < H):
+    ld, one = t.stride()
+    if (H > 1 and one != 1) or (T > 1 and ld < H):
         raise ValueError(f"{name}: each row must be contiguous, rows at least {H} apart")
 
 
@@ -64,24 +72,25 @@ class MoELayerNorm:
         self.mean = torch.empty(T, dtype=torch.float32, device=self.device)
         self.rstd = torch.empty(T, dtype=torch.float32, device=self.device)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+        self._rows, self._cols = torch.Size((T, H)), torch.Size((H,))
 
     def _check_params(self, weight, bias, prefix=""):
-        _need(weight, prefix + "weight", (self.H,), self.param_dtype, self.device)
+        _need(weight, prefix + "weight", self._cols, self.param_dtype, self.device)
         if self.bias:
-            _need(bias, prefix + "bias", (self.H,), self.param_dtype, self.device)
+            _need(bias, prefix + "bias", self._cols, self.param_dtype, self.device)
         elif bias is not None:
             raise ValueError(f"{prefix}bias: this layer norm has none")
 
     def forward(self, x, weight, bias=None, y: Optional[torch.Tensor] = None,
                 stream=None) -> torch.Tensor:
-        shp = (self.T, self.H)
-        _need_rows(x, "x", shp, self.dtype, self.device)
+        _need_rows(x, "x", self._rows, self.dtype, self.device)
         self._check_params(weight, bias)
         if y is None:
-            y = torch.empty(shp, dtype=self.dtype, device=self.device)
+            y = torch.empty(self._rows, dtype=self.dtype, device=self.device)
         else:
-            _need_rows(y, "y", shp, self.dtype, self.device)
-        B.mm_moe_norm_forward(self.shape, x, weight, bias, y, self.mean, self.rstd, stream)
+            _need_rows(y, "y", self._rows, self.dtype, self.device)
+        B.mm_moe_norm_forward(self.shape, x, weight, bias, y, self.mean, self.rstd,
+                              _stream(stream, self.device))
         return y
 
     def backward(self, dy, x, weight, dx_add=None, out=None, stream=None
@@ -89,22 +98,21 @@ class MoELayerNorm:
         """Gradients (dx, dweight, dbias) of the last forward, whose x and weight are given
         again (dbias None without a bias).  dx_add: a gradient that joins dx (the residual
         path's); dx may be written over it (out)."""
-        shp = (self.T, self.H)
-        _need_rows(dy, "dy", shp, self.dtype, self.device)
-        _need_rows(x, "x", shp, self.dtype, self.device)
-        _need(weight, "weight", (self.H,), self.param_dtype, self.device)
+        _need_rows(dy, "dy", self._rows, self.dtype, self.device)
+        _need_rows(x, "x", self._rows, self.dtype, self.device)
+        _need(weight, "weight", self._cols, self.param_dtype, self.device)
         if dx_add is not None:
-            _need_rows(dx_add, "dx_add", shp, self.dtype, self.device)
+            _need_rows(dx_add, "dx_add", self._rows, self.dtype, self.device)
         if out is None:
             w = dict(dtype=self.param_dtype, device=self.device)
-            out = (torch.empty(shp, dtype=self.dtype, device=self.device),
-                   torch.empty(self.H, **w), torch.empty(self.H, **w) if self.bias else None)
+            out = (torch.empty(self._rows, dtype=self.dtype, device=self.device),
+                   torch.empty(self._cols, **w), torch.empty(self._cols, **w) if self.bias else None)
         else:
-            _need_rows(out[0], "dx", shp, self.dtype, self.device)
+            _need_rows(out[0], "dx", self._rows, self.dtype, self.device)
             self._check_params(out[1], out[2], "d")
         dx, dweight, dbias = out
         B.mm_moe_norm_backward(self.shape, dy, x, weight, self.mean, self.rstd, dx_add, dx,
-                               dweight, dbias, self.workspace, stream)
+                               dweight, dbias, self.workspace, _stream(stream, self.device))
         return dx, dweight, dbias
 
 
@@ -151,7 +159,7 @@ class MoEBalanceLoss:
         _need(topk_idx, "topk_idx", (self.T, self.k), torch.int32, self.device)
         B.mm_moe_balance_forward(self.shape, logits, topk_idx, seq_offsets, mask, self.losses,
                                  self.seq_loss, self.counts, self.tokens, self.lse,
-                                 self.workspace, stream)
+                                 self.workspace, _stream(stream, self.device))
         return self.losses, self.counts
 
     def backward(self, logits, dlosses, seq_offsets=None, mask=None,
@@ -166,7 +174,8 @@ class MoEBalanceLoss:
         else:
             _need(dlogits, "dlogits", (self.T, self.E), self.dtype, self.device)
         B.mm_moe_balance_backward(self.shape, logits, seq_offsets, mask, self.counts, self.tokens,
-                                  dlosses, dlogits, self.workspace, stream)
+                                  dlosses, dlogits, self.workspace,
+                                  _stream(stream, self.device))
         return dlogits
 
 
@@ -182,34 +191,36 @@ class MoEGradClip:
         self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def _entries(self, grads: Sequence[torch.Tensor], out):
+        """The call's mm_moe_grad array: four 64-bit words a tensor."""
         if len(grads) > self.max_tensors:
             raise ValueError(f"grads: {len(grads)} tensors, made for at most {self.max_tensors}")
         if out is not None and len(out) != len(grads):
             raise ValueError(f"out: expected {len(grads)} tensors, got {len(out)}")
-        dev, code = self.device, _CODE
-        entries = []
+        where = -1 if self.device.index is None else self.device.index
+        words = []
         for i, g in enumerate(grads):
-            d = code.get(g.dtype)
-            if d is None or g.device != dev or not g.is_contiguous():
+            d = _CODE.get(g.dtype)
+            if d is None or g.get_device() != where or not g.is_contiguous():
                 raise ValueError(f"grads[{i}]: expected a contiguous bf16, fp16 or fp32 tensor "
-                                 f"on {dev}")
+                                 f"on {self.device}")
             p = g.data_ptr()
-            entries.append((p, p, g.numel(), d, d))
-        if out is not None:
-            f32 = B.MM_MOE_DT_F32
-            for i, (o, g) in enumerate(zip(out, grads)):
-                od, (p, _, n, d, _) = code.get(o.dtype), entries[i]
-                if (od != d and od != f32) or o.device != dev or not o.is_contiguous() \
-                        or o.shape != g.shape:
-                    raise ValueError(f"out[{i}]: expected a contiguous tensor like grads[{i}], of "
-                                     "its dtype or fp32")
-                entries[i] = (p, o.data_ptr(), n, d, od)
-        return entries
+            if out is None:
+                words += (p, p, g.numel(), d | d << 32)
+                continue
+            o = out[i]
+            od = _CODE.get(o.dtype)
+            if (od != d and od != B.MM_MOE_DT_F32) or o.get_device() != where \
+                    or not o.is_contiguous() or o.shape != g.shape:
+                raise ValueError(f"out[{i}]: expected a contiguous tensor like grads[{i}], of "
+                                 "its dtype or fp32")
+            words += (p, o.data_ptr(), g.numel(), d | od << 32)
+        return array("Q", words)
 
     def norm(self, grads: Sequence[torch.Tensor], stream=None) -> torch.Tensor:
         """The norm as a 0-d fp32 tensor on the device (no synchronisation)."""
         norm = torch.empty((), dtype=torch.float32, device=self.device)
-        B.mm_moe_grad_norm(self._entries(grads, None), norm, self.workspace, stream)
+        B.mm_moe_grad_norm(self._entries(grads, None), norm, self.workspace,
+                           _stream(stream, self.device))
         return norm
 
     def clip(self, grads: Sequence[torch.Tensor], max_norm: float, out=None,
@@ -220,5 +231,5 @@ class MoEGradClip:
             raise ValueError(f"max_norm must be >= 0, got {max_norm}")
         norm = torch.empty((), dtype=torch.float32, device=self.device)
         B.mm_moe_grad_clip(self._entries(grads, out), max_norm, self.eps, norm, self.workspace,
-                           stream)
+                           _stream(stream, self.device))
         return norm

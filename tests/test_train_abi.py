@@ -84,7 +84,7 @@ def test_balance_pointers(lib):
 
 def test_grad_arguments(lib):
     def call(entries, n=None, max_norm=1.0, eps=1e-6, norm=P[10], ws=P[11], clip=True):
-        flat = B._grad_array(entries)
+        flat = B.grad_array(entries)
         n = len(entries) if n is None else n
         p = flat.buffer_info()[0] if entries else None
         if clip:
