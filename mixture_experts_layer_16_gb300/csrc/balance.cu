@@ -23,38 +23,125 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "dtype.cuh"
 #include "internal.h"
 
 namespace mmmoe {
 
-constexpr int BAL_THREADS = 256;
-constexpr int BAL_WARPS = BAL_THREADS / 32;
+// Threads of a token kernel's CTA at most: few large CTAs leave few pieces to join; with
+// many short sequences, each of which ends with a barrier, smaller CTAs run side by side.
+constexpr int BAL_THREADS = 384;
+constexpr int BAL_SMALL = 128;
+constexpr int BAL_WARPS = BAL_THREADS / 32;  // at most
 
-// Four consecutive logits; past E they read as -inf.
-template <typename T>
-__device__ __forceinline__ void load4(const T* row, int e0, int E, bool vec, float (&v)[4]) {
-  if (vec) {
-    if (e0 < E) {
-      if constexpr (sizeof(T) == 4) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(row + e0));
-        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-      } else {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(row + e0));
-        const T* h = reinterpret_cast<const T*>(&q);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = to_f32(h[i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = -INFINITY;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = e0 + i < E ? to_f32(row[e0 + i]) : -INFINITY;
+// A token's row reaches its lanes through a ring in shared memory, STAGES - 1 tokens ahead,
+// by cp.async: a lane copies its own four-logit quads (and its share of topk_idx) and reads
+// nothing but what it copied, so no barrier guards the ring.  A quad past the last expert
+// holds -inf from the start.
+constexpr int BAL_STAGES = 3;
+
+template <typename T, int L, int NV>
+struct Ring {
+  static constexpr int QUAD = 4 * static_cast<int>(sizeof(T));
+  static constexpr int KS = L >= 8 ? 1 : 8 / L;  // topk_idx entries per lane (k <= 8; else read directly)
+  static constexpr int BYTES = BAL_STAGES * (NV * QUAD + KS * 4);  // per thread
+  unsigned char* quads;  // this thread's; a quad lies blockDim quads before the next
+  int* idx;
+  __device__ __forceinline__ void init(unsigned char* smem) {
+    quads = smem + threadIdx.x * QUAD;
+    idx = reinterpret_cast<int*>(smem + BAL_STAGES * NV * QUAD * blockDim.x) + threadIdx.x;
   }
-}
+  __device__ __forceinline__ T* quad(int st, int i) const {
+    return reinterpret_cast<T*>(quads + (st * NV + i) * (QUAD * blockDim.x));
+  }
+  __device__ __forceinline__ int& slot(int st, int j) const {
+    return idx[(st * KS + j) * blockDim.x];
+  }
+  template <int B>
+  __device__ __forceinline__ static void copy(void* dst, const void* src) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (B == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(B)
+                   : "memory");
+  }
+  // whether quad i of lane l holds expert 4 (l + i L) + j
+  __device__ __forceinline__ void blank(int l, int E) const {
+#pragma unroll
+    for (int st = 0; st < BAL_STAGES; ++st)
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (4 * (l + i * L) + j >= E) quad(st, i)[j] = from_f32<T>(-INFINITY);
+  }
+  // The row's quads (vec: whole and aligned).  16-bit rows that are not come by plain loads.
+  __device__ __forceinline__ void load(int st, const T* row, int l, int E, bool vec) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e0 = 4 * (l + i * L);
+      if (vec) {
+        if (e0 < E) copy<QUAD>(quad(st, i), row + e0);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (e0 + j < E) {
+            if constexpr (sizeof(T) == 4)
+              copy<4>(quad(st, i) + j, row + e0 + j);
+            else
+              quad(st, i)[j] = row[e0 + j];
+          }
+      }
+    }
+  }
+  __device__ __forceinline__ void load_idx(int st, const int32_t* row, int l, int k) const {
+#pragma unroll
+    for (int j = 0; j < KS; ++j)
+      if (l + j * L < k) copy<4>(&slot(st, j), row + l + j * L);
+  }
+  __device__ __forceinline__ static void commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ static void wait() {  // the oldest of STAGES rows has landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(BAL_STAGES - 1) : "memory");
+  }
+  __device__ __forceinline__ static void drain() {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+  __device__ __forceinline__ void get(int st, f2 (&v)[2 * NV]) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(quad(st, i));
+        v[2 * i] = q.x;
+        v[2 * i + 1] = q.y;
+      } else {
+        const uint2 q = *reinterpret_cast<const uint2*>(quad(st, i));
+        const T* h = reinterpret_cast<const T*>(&q);
+        v[2 * i] = f2_make(to_f32(h[0]), to_f32(h[1]));
+        v[2 * i + 1] = f2_make(to_f32(h[2]), to_f32(h[3]));
+      }
+    }
+  }
+};
+
+// Mask bytes of a group's next L tokens, one a lane, read once for all of them.
+template <int L>
+struct MaskAhead {
+  uint32_t mine = 1;
+  __device__ __forceinline__ bool get(const uint8_t* mask, int64_t t, int64_t end, int stride, int l,
+                                      int it) {
+    if (mask == nullptr) return true;
+    if (it % L == 0) {
+      const int64_t mt = t + static_cast<int64_t>(l) * stride;
+      mine = mt < end ? __ldg(mask + mt) : 0;
+    }
+    return __shfl_sync(0xffffffffu, mine, it % L, L) != 0;
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ void store4(T* row, int e0, int E, bool vec, const float (&v)[4]) {
@@ -83,6 +170,45 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// Largest and sum of a lane's values, in two chains.
+template <int N>
+__device__ __forceinline__ float pairs_max(const f2 (&v)[N]) {
+  float m[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float a, b;
+    f2_split(v[i], a, b);
+    m[i & 1] = max_nan(m[i & 1], max_nan(a, b));
+  }
+  return max_nan(m[0], m[1]);
+}
+template <int N>
+__device__ __forceinline__ float pairs_sum(const f2 (&v)[N]) {
+  f2 a = v[0], b = v[1];
+#pragma unroll
+  for (int i = 2; i < N; i += 2) {
+    a = f2_add(a, v[i]);
+    b = f2_add(b, v[i + 1]);
+  }
+  return f2_sum(f2_add(a, b));
+}
+
+// 2^x; below 2^-126 zero (FLUSH) or the subnormal
+template <bool FLUSH>
+__device__ __forceinline__ float pow2(float x) {
+  float r;
+  if constexpr (FLUSH)
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  else
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 template <int L>
 __device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
@@ -97,32 +223,48 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 
 // Walks a CTA's range [t0, t1) of tokens sequence by sequence.  Offsets may hold empty
-// sequences and may leave tokens before the first or after the last one in none.
+// sequences and may leave tokens before the first or after the last one in none.  The
+// offsets around the range come into shared memory; every thread of the CTA walks along.
 struct SeqWalk {
+  static constexpr int WINDOW = BAL_SMALL;
   const int32_t* off;  // [G + 1], or null: one sequence of all tokens
+  int* win;            // shared [WINDOW + 1]: offsets from off[base] on
   int G;
   int s;               // sequence of the current piece, or -1: in none
   int64_t a, b;        // the current piece [a, b)
   int64_t t1;
-  __device__ __forceinline__ int64_t at(int g) const { return __ldg(off + g); }
-  __device__ __forceinline__ void start(const int32_t* off_, int G_, int64_t t0, int64_t t1_) {
+  int next_seq, base;
+
+  __device__ __forceinline__ void fill() {
+    __syncthreads();
+    base = next_seq;
+    for (int i = threadIdx.x; i <= WINDOW; i += blockDim.x)
+      if (base + i <= G) win[i] = __ldg(off + base + i);
+    __syncthreads();
+  }
+  __device__ __forceinline__ void start(const int32_t* off_, int* win_, int G_, int64_t t0,
+                                        int64_t t1_) {
     off = off_;
+    win = win_;
     G = G_;
     t1 = t1_;
     b = t0;
     s = 0;
     if (off == nullptr) return;
-    int lo = 0, hi = G;  // the first sequence that ends past t0
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (at(mid + 1) > t0)
-        hi = mid;
-      else
-        lo = mid + 1;
+    // the first sequence that ends past t0: each round, the threads test as many
+    // sequences at equal distances and leave one distance to search
+    int lo = 0, n = G;  // it is in [lo, lo + n], lo + n = G: none
+    while (n > 0) {
+      const int threads = blockDim.x, d = (n + threads - 1) / threads;
+      const int g = lo + static_cast<int>(threadIdx.x + 1) * d - 1;  // last of my distance
+      const int before = __syncthreads_count(g < lo + n && __ldg(off + g + 1) <= t0);
+      const int nlo = lo + before * d;
+      n = d == 1 ? 0 : min(d - 1, lo + n - nlo);
+      lo = nlo;
     }
-    next_seq = lo;
+    next_seq = min(lo, G);
+    fill();
   }
-  int next_seq;
   // false when the range is done
   __device__ __forceinline__ bool next() {
     a = b;
@@ -132,7 +274,9 @@ struct SeqWalk {
       return true;
     }
     for (; next_seq < G; ++next_seq) {
-      const int64_t lo = at(next_seq), hi = min(at(next_seq + 1), t1);
+      if (next_seq - base >= WINDOW) fill();
+      const int64_t lo = win[next_seq - base], 
+                    hi = min(static_cast<int64_t>(win[next_seq - base + 1]), t1);
       if (hi <= a) continue;
       if (lo > a) {  // a gap in front of it
         b = min(lo, t1);
@@ -149,6 +293,20 @@ struct SeqWalk {
   }
 };
 
+// e^(l - m) as 2^((l - m) log2(e)): the difference comes first, so that rows of the type's
+// lowest value, whose product with log2(e) overflows, keep their (even) distribution.
+constexpr float LOG2_E = 1.44269504088896340736f;
+template <bool FLUSH, int N>
+__device__ __forceinline__ void pairs_exp(f2 (&v)[N], float m) {
+  const f2 nm = f2_make(-m, -m), s = f2_make(LOG2_E, LOG2_E);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float a, b;
+    f2_split(f2_mul(f2_add(v[i], nm), s), a, b);
+    v[i] = f2_make(pow2<FLUSH>(a), pow2<FLUSH>(b));
+  }
+}
+
 // Partial results of one (CTA, sequence) piece, at row CTA + sequence of each array
 // (unique: the next piece has a larger CTA or a larger sequence).
 struct BalParts {
@@ -158,77 +316,84 @@ struct BalParts {
   int32_t* n;     // [pieces]
   float* z;       // [pieces]
   float* seq_z;   // [G]
+  float* dot;     // [G, expert blocks of the joining kernel]
+  int* arrived;   // CTAs of the joining kernel that are done
+  float* cta_f;   // [CTAs of balance_join_many_kernel, 2]: sums of sequence losses, of lse^2
+  int* cta_n;     // [.., 2]: tokens, sequences with a token
 };
 
 template <typename T, int L, int NV>
-__global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(
+__global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_fwd_kernel(
     const T* __restrict__ logits, const int32_t* __restrict__ topk_idx,
     const int32_t* __restrict__ off, const uint8_t* __restrict__ mask, int64_t T_, int E, int k,
     int G, int chunk, bool vec, float* __restrict__ lse_out, BalParts parts) {
-  extern __shared__ char smem[];
-  float* s_p = reinterpret_cast<float*>(smem);              // [BAL_WARPS][E]
-  int* s_cnt = reinterpret_cast<int*>(s_p + BAL_WARPS * E);  // [E]
+  using R = Ring<T, L, NV>;
+  const int nt = blockDim.x, warps = nt / 32;
+  extern __shared__ __align__(16) unsigned char smem[];
+  float* s_p = reinterpret_cast<float*>(smem + R::BYTES * nt);  // [warps][E]
+  int* s_cnt = reinterpret_cast<int*>(s_p + warps * E);  // [E]
   __shared__ float s_z[BAL_WARPS];
   __shared__ int s_n[BAL_WARPS];
+  __shared__ int s_win[SeqWalk::WINDOW + 1];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int l = lane % L;                    // lane within its token's group
-  constexpr int GROUPS = BAL_THREADS / L;
+  const int l = lane % L;  // lane within its token's group
+  const int GROUPS = nt / L;
   const int grp = tid / L;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * chunk;
   const int64_t t1 = min(T_, t0 + chunk);
-  for (int e = tid; e < E; e += BAL_THREADS) s_cnt[e] = 0;
+  R ring;
+  ring.init(smem);
+  ring.blank(l, E);
+  if (blockIdx.x == 0 && tid == 0) *parts.arrived = 0;
+  for (int e = tid; e < E; e += nt) s_cnt[e] = 0;
   __syncthreads();
   SeqWalk w;
-  w.start(off, G, t0, t1);
+  w.start(off, s_win, G, t0, t1);
   while (w.next()) {
     if (w.s < 0) {  // tokens in no sequence
-      for (int64_t t = w.a + tid; t < w.b; t += BAL_THREADS) lse_out[t] = 0.f;
+      for (int64_t t = w.a + tid; t < w.b; t += nt) lse_out[t] = 0.f;
       continue;
     }
-    float acc[NV * 4];
-#pragma unroll
-    for (int i = 0; i < NV * 4; ++i) acc[i] = 0.f;
+    f2 acc[2 * NV] = {};
     float z = 0.f;
     int n = 0;
-    for (int64_t base = w.a; base < w.b; base += GROUPS) {
-      const int64_t t = base + grp;
-      bool on = t < w.b;
-      if (on && mask != nullptr) on = __ldg(mask + t) != 0;
-      float v[NV][4];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (on) {
-          load4(logits + t * E, 4 * (l + i * L), E, vec, v[i]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[i][j] = -INFINITY;
-        }
+    MaskAhead<L> ahead;
+    const int rounds = static_cast<int>((w.b - w.a + GROUPS - 1) / GROUPS);
+    int64_t t = w.a + grp, tn = t;
+    const auto issue = [&](int st) {
+      if (tn < w.b) {  // (a masked row is read like any other: no load waits for another)
+        ring.load(st, logits + tn * E, l, E, vec);
+        ring.load_idx(st, topk_idx + tn * k, l, k);
       }
-      float m = -INFINITY;
+      R::commit();
+      tn += GROUPS;
+    };
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m = max_nan(m, v[i][j]);
-      m = lanes_max<L>(m);
+    for (int i = 0; i < BAL_STAGES - 1; ++i) issue(i);
+    int st = 0;
+    for (int it = 0; it < rounds; ++it, t += GROUPS) {
+      issue(st == 0 ? BAL_STAGES - 1 : st - 1);
+      bool on = ahead.get(mask, t, w.b, GROUPS, l, it) && t < w.b;
+      R::wait();
+      f2 v[2 * NV];
+      ring.get(st, v);
+      const float m = lanes_max<L>(pairs_max(v));
       on = on && m != -INFINITY;  // (a NaN counts, and shows in the losses)
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[i][j] = on ? expf(v[i][j] - m) : 0.f;
-          sum += v[i][j];
-        }
-      sum = lanes_sum<L>(sum);
+      pairs_exp<true>(v, m);
+      const float sum = lanes_sum<L>(pairs_sum(v));
       if (on) {
-        const float inv = 1.f / sum;
+        const float inv = reciprocal(sum);
+        const f2 inv2 = f2_make(inv, inv);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < 2 * NV; ++i) acc[i] = f2_fma(v[i], inv2, acc[i]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[4 * i + j] = fmaf(v[i][j], inv, acc[4 * i + j]);
-        for (int j = l; j < k; j += L) {
+        for (int j = 0; j < R::KS; ++j) {
+          const int e = l + j * L < k ? ring.slot(st, j) : -1;
+          if (e >= 0 && e < E) atomicAdd(s_cnt + e, 1);
+        }
+        for (int j = l + R::KS * L; j < k; j += L) {
           const int e = __ldg(topk_idx + t * k + j);
           if (e >= 0 && e < E) atomicAdd(s_cnt + e, 1);
         }
@@ -239,22 +404,24 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(
         z = fmaf(lse, lse, z);
         n += on ? 1 : 0;
       }
+      st = st + 1 == BAL_STAGES ? 0 : st + 1;
     }
+    R::drain();
     // join the groups of the warp, then the warps (in order)
-#pragma unroll
-    for (int i = 0; i < NV * 4; ++i)
-#pragma unroll
-      for (int o = 16; o >= L; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
     z = warp_sum(z);
     n = warp_sum(n);
-    if (lane < L) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      float q[4];
+      f2_split(acc[2 * i], q[0], q[1]);
+      f2_split(acc[2 * i + 1], q[2], q[3]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int e = 4 * (l + i * L) + j;
-          if (e < E) s_p[wid * E + e] = acc[4 * i + j];
-        }
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int o = 16; o >= L; o >>= 1) q[j] += __shfl_xor_sync(0xffffffffu, q[j], o);
+        const int e = 4 * (l + i * L) + j;
+        if (lane < L && e < E) s_p[wid * E + e] = q[j];
+      }
     }
     if (lane == 0) {
       s_z[wid] = z;
@@ -262,10 +429,10 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(
     }
     __syncthreads();
     const int64_t piece = static_cast<int64_t>(blockIdx.x) + w.s;
-    for (int e = tid; e < E; e += BAL_THREADS) {
+    for (int e = tid; e < E; e += nt) {
       float t = s_p[e];
-#pragma unroll
-      for (int i = 1; i < BAL_WARPS; ++i) t += s_p[i * E + e];
+#pragma unroll 4
+      for (int i = 1; i < warps; ++i) t += s_p[i * E + e];
       parts.p[piece * E + e] = t;
       parts.cnt[piece * E + e] = s_cnt[e];
       s_cnt[e] = 0;
@@ -273,7 +440,7 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(
     if (tid == 0) {
       float tz = 0.f;
       int tn = 0;
-      for (int i = 0; i < BAL_WARPS; ++i) {
+      for (int i = 0; i < warps; ++i) {
         tz += s_z[i];
         tn += s_n[i];
       }
@@ -284,169 +451,372 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(
   }
 }
 
-// One CTA per sequence: its pieces joined in order.
-__global__ void __launch_bounds__(256) balance_seq_kernel(const int32_t* __restrict__ off,
-                                                          int64_t T_, int E, int k, int chunk,
-                                                          BalParts parts,
-                                                          float* __restrict__ seq_loss,
-                                                          int32_t* __restrict__ counts,
-                                                          int32_t* __restrict__ tokens) {
-  __shared__ float s[8];
-  pdl_wait();
-  pdl_trigger();
-  const int g = blockIdx.x;
-  const int64_t a = off != nullptr ? max(0, __ldg(off + g)) : 0;
-  const int64_t b = off != nullptr ? min(T_, static_cast<int64_t>(__ldg(off + g + 1))) : T_;
-  const int64_t c0 = a / chunk, c1 = b > a ? (b - 1) / chunk + 1 : c0;
-  float dot = 0.f;
-  for (int e = threadIdx.x; e < E; e += 256) {
-    float p = 0.f;
-    int cnt = 0;
-    for (int64_t c = c0; c < c1; ++c) {
-      p += parts.p[(c + g) * E + e];
-      cnt += parts.cnt[(c + g) * E + e];
-    }
-    counts[static_cast<int64_t>(g) * E + e] = cnt;
-    dot = fmaf(static_cast<float>(cnt), p, dot);
+// ---------------------------------------------------------------- joining the pieces
+// The CTAs whose tokens sequence g reaches: [c0, c1).
+struct PieceRange {
+  int64_t c0, c1;
+  __device__ __forceinline__ PieceRange(const int32_t* off, int g, int64_t T_, int chunk) {
+    const int64_t a = off != nullptr ? max(0, __ldg(off + g)) : 0;
+    const int64_t b = off != nullptr ? min(T_, static_cast<int64_t>(__ldg(off + g + 1))) : T_;
+    c0 = a / chunk;
+    c1 = b > a ? (b - 1) / chunk + 1 : c0;
   }
-  dot = block_sum(dot, s);
-  float z = 0.f, n = 0.f;
-  int ni = 0;
-  for (int64_t c = c0 + threadIdx.x; c < c1; c += 256) {
-    z += parts.z[c + g];
-    ni += parts.n[c + g];
-  }
-  z = block_sum(z, s);
-  ni = block_sum(ni, reinterpret_cast<int*>(s));
-  n = static_cast<float>(ni);
+};
+
+// Counts a CTA (whose results thread 0 wrote) in; true in all threads of the last one, with
+// the others' results visible.  What is then added, and in which order, does not depend on
+// which CTA that is.
+__device__ __forceinline__ bool last_cta(int* arrived) {
+  __shared__ int s_before;
   if (threadIdx.x == 0) {
-    tokens[g] = ni;
-    seq_loss[g] = ni > 0 ? dot * (static_cast<float>(E) / static_cast<float>(k)) / (n * n) : 0.f;
-    parts.seq_z[g] = z;
+    int before = 0;
+    if (gridDim.x > 1)
+      asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                   : "=r"(before)
+                   : "l"(arrived)
+                   : "memory");
+    s_before = before;
   }
+  __syncthreads();
+  return s_before == static_cast<int>(gridDim.x) - 1;
 }
 
-__global__ void __launch_bounds__(256) balance_total_kernel(int G, BalParts parts,
-                                                            const float* __restrict__ seq_loss,
-                                                            const int32_t* __restrict__ tokens,
-                                                            float* __restrict__ losses) {
-  __shared__ float s[8];
+// What the sequences of a thread, a CTA or the whole call add up to.
+struct BalTotals {
+  float sum, z;
+  int n, live;
+  __device__ __forceinline__ void add(float v, float zg, int ng) {
+    sum += v;
+    z += zg;
+    n += ng;
+    live += ng > 0 ? 1 : 0;
+  }
+  // the CTA's threads together (`one_warp`: the others have nothing), then the results
+  __device__ __forceinline__ void finish(bool one_warp, const BalParts& parts, float* losses) {
+    __shared__ float s_f[32][2];
+    __shared__ int s_i[32][2];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    sum = warp_sum(sum);
+    z = warp_sum(z);
+    n = warp_sum(n);
+    live = warp_sum(live);
+    if (!one_warp) {
+      if (lane == 0) {
+        s_f[wid][0] = sum;
+        s_f[wid][1] = z;
+        s_i[wid][0] = n;
+        s_i[wid][1] = live;
+      }
+      __syncthreads();
+      const bool in = lane < static_cast<int>(blockDim.x) / 32;
+      sum = warp_sum(in ? s_f[lane][0] : 0.f);
+      z = warp_sum(in ? s_f[lane][1] : 0.f);
+      n = warp_sum(in ? s_i[lane][0] : 0);
+      live = warp_sum(in ? s_i[lane][1] : 0);
+    }
+    if (threadIdx.x == 0) {
+      losses[0] = live > 0 ? sum / static_cast<float>(live) : 0.f;
+      losses[1] = n > 0 ? z / static_cast<float>(n) : 0.f;
+      parts.stats[0] = static_cast<float>(live);
+      parts.stats[1] = static_cast<float>(n);
+    }
+  }
+};
+__device__ __forceinline__ float sequence_loss(float dot, int n, float per) {
+  const float nf = static_cast<float>(n);
+  return n > 0 ? dot * per / (nf * nf) : 0.f;
+}
+
+// Few sequences: a CTA per sequence and 32 experts; its warps take every 32nd piece, ten
+// loads of each kind in flight.
+constexpr int JOIN_THREADS = 1024;
+constexpr int JOIN_WARPS = JOIN_THREADS / 32;
+__global__ void __launch_bounds__(JOIN_THREADS, 1) balance_join_few_kernel(
+    const int32_t* __restrict__ off, int64_t T_, int E, int k, int G, int chunk, BalParts parts,
+    float* __restrict__ losses, float* __restrict__ seq_loss, int32_t* __restrict__ counts,
+    int32_t* __restrict__ tokens) {
+  constexpr int BATCH = 10;
+  __shared__ float s_p[JOIN_WARPS][33], s_z[JOIN_WARPS];
+  __shared__ int s_c[JOIN_WARPS][33], s_n[JOIN_WARPS];
   pdl_wait();
   pdl_trigger();
-  float a = 0.f, z = 0.f;
-  int n = 0, live = 0;
-  for (int g = threadIdx.x; g < G; g += 256) {
-    a += seq_loss[g];
-    z += parts.seq_z[g];
-    n += tokens[g];
-    live += tokens[g] > 0 ? 1 : 0;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int blocks = (E + 31) / 32;
+  const int g = blockIdx.x / blocks, eb = blockIdx.x - g * blocks;
+  const int e = eb * 32 + lane;
+  const PieceRange r(off, g, T_, chunk);
+  float p = 0.f, z = 0.f;
+  int cnt = 0, n = 0;
+  // (the first of these loads are in flight beside the pieces' own)
+  const int64_t cz = r.c0 + threadIdx.x;
+  const bool first = eb == 0 && cz < r.c1;
+  const float z0 = first ? __ldcg(parts.z + cz + g) : 0.f;
+  const int n0 = first ? __ldcg(parts.n + cz + g) : 0;
+  if (e < E) {
+    const float* pp = parts.p + static_cast<int64_t>(g) * E + e;
+    const int32_t* pc = parts.cnt + static_cast<int64_t>(g) * E + e;
+    for (int64_t c = r.c0 + wid; c < r.c1; c += BATCH * JOIN_WARPS) {
+      float fp[BATCH];
+      int fc[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const bool in = c + i * JOIN_WARPS < r.c1;
+        fp[i] = in ? __ldcg(pp + (c + i * JOIN_WARPS) * E) : 0.f;
+        fc[i] = in ? __ldcg(pc + (c + i * JOIN_WARPS) * E) : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        p += fp[i];
+        cnt += fc[i];
+      }
+    }
   }
-  a = block_sum(a, s);
-  z = block_sum(z, s);
-  n = block_sum(n, reinterpret_cast<int*>(s));
-  live = block_sum(live, reinterpret_cast<int*>(s));
+  s_p[wid][lane] = p;
+  s_c[wid][lane] = cnt;
+  if (eb == 0) {
+    z = z0;
+    n = n0;
+    for (int64_t c = cz + JOIN_THREADS; c < r.c1; c += JOIN_THREADS) {
+      z += __ldcg(parts.z + c + g);
+      n += __ldcg(parts.n + c + g);
+    }
+    z = warp_sum(z);
+    n = warp_sum(n);
+    if (lane == 0) {
+      s_z[wid] = z;
+      s_n[wid] = n;
+    }
+  }
+  __syncthreads();
+  // a warp per expert: lanes are the pieces' warps
+  p = warp_sum(s_p[lane][wid]);
+  cnt = warp_sum(s_c[lane][wid]);
+  if (eb == 0 && wid == 0) {
+    z = warp_sum(s_z[lane]);
+    n = warp_sum(s_n[lane]);
+  }
+  __syncthreads();
+  if (lane == 0) {
+    s_p[0][wid] = static_cast<float>(cnt) * p;
+    if (eb * 32 + wid < E) counts[static_cast<int64_t>(g) * E + eb * 32 + wid] = cnt;
+  }
+  __syncthreads();
+  if (wid == 0) {
+    const float dot = warp_sum(s_p[0][lane]);
+    if (lane == 0) {
+      parts.dot[blockIdx.x] = dot;
+      if (eb == 0) {
+        parts.seq_z[g] = z;
+        tokens[g] = n;
+      }
+    }
+  }
+  if (!last_cta(parts.arrived)) return;
+  const float per = static_cast<float>(E) / static_cast<float>(k);
+  BalTotals all{};
+  for (int i = threadIdx.x; i < G; i += JOIN_THREADS) {
+    const int ni = __ldcg(tokens + i);
+    const float zi = __ldcg(parts.seq_z + i);
+    const float* dots = parts.dot + static_cast<int64_t>(i) * blocks;
+    float q[4];  // (beside the loads above)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = j < blocks ? __ldcg(dots + j) : 0.f;
+    float d = (q[0] + q[1]) + (q[2] + q[3]);
+    for (int j = 4; j < blocks; ++j) d += __ldcg(dots + j);
+    const float v = sequence_loss(d, ni, per);
+    seq_loss[i] = v;
+    all.add(v, zi, ni);
+  }
+  all.finish(G <= 32, parts, losses);
+}
+
+// Many sequences, with few pieces each: a CTA of up to 8 warps takes a sequence at a time, an
+// expert a thread, eight pieces at once.
+constexpr int JOIN_MANY_THREADS = 256;
+constexpr int JOIN_MANY_CTAS = 152 * 4;
+__global__ void __launch_bounds__(JOIN_MANY_THREADS) balance_join_many_kernel(
+    const int32_t* __restrict__ off, int64_t T_, int E, int k, int G, int chunk, BalParts parts,
+    float* __restrict__ losses, float* __restrict__ seq_loss, int32_t* __restrict__ counts,
+    int32_t* __restrict__ tokens) {
+  constexpr int BATCH = 8;
+  __shared__ float s_dot[JOIN_MANY_THREADS / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nt = blockDim.x;
+  const float per = static_cast<float>(E) / static_cast<float>(k);
+  BalTotals mine{};
+  for (int g = blockIdx.x; g < G; g += gridDim.x) {
+    const PieceRange r(off, g, T_, chunk);
+    float dot = 0.f, z = 0.f;
+    int n = 0;
+    if (wid == 0 && r.c0 + lane < r.c1) {
+      z = __ldcg(parts.z + r.c0 + lane + g);
+      n = __ldcg(parts.n + r.c0 + lane + g);
+    }
+    for (int e = threadIdx.x; e < E; e += nt) {
+      float p = 0.f;
+      int cnt = 0;
+      for (int64_t c = r.c0; c < r.c1; c += BATCH) {
+        float fp[BATCH];
+        int fc[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const bool in = c + i < r.c1;
+          fp[i] = in ? __ldcg(parts.p + (c + i + g) * E + e) : 0.f;
+          fc[i] = in ? __ldcg(parts.cnt + (c + i + g) * E + e) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          p += fp[i];
+          cnt += fc[i];
+        }
+      }
+      counts[static_cast<int64_t>(g) * E + e] = cnt;
+      dot = fmaf(static_cast<float>(cnt), p, dot);
+    }
+    dot = warp_sum(dot);
+    if (lane == 0) s_dot[wid] = dot;
+    if (wid == 0) {
+      for (int64_t c = r.c0 + 32 + lane; c < r.c1; c += 32) {
+        z += __ldcg(parts.z + c + g);
+        n += __ldcg(parts.n + c + g);
+      }
+      z = warp_sum(z);
+      n = warp_sum(n);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < nt / 32; ++i) dot += s_dot[i];
+      const float v = sequence_loss(dot, n, per);
+      tokens[g] = n;
+      seq_loss[g] = v;
+      mine.add(v, z, n);
+    }
+    __syncthreads();  // (s_dot is read)
+  }
   if (threadIdx.x == 0) {
-    losses[0] = live > 0 ? a / static_cast<float>(live) : 0.f;
-    losses[1] = n > 0 ? z / static_cast<float>(n) : 0.f;
-    parts.stats[0] = static_cast<float>(live);
-    parts.stats[1] = static_cast<float>(n);
+    parts.cta_f[2 * blockIdx.x] = mine.sum;
+    parts.cta_f[2 * blockIdx.x + 1] = mine.z;
+    parts.cta_n[2 * blockIdx.x] = mine.n;
+    parts.cta_n[2 * blockIdx.x + 1] = mine.live;
   }
+  if (!last_cta(parts.arrived)) return;
+  BalTotals all{};
+  for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += nt) {
+    all.sum += __ldcg(parts.cta_f + 2 * i);
+    all.z += __ldcg(parts.cta_f + 2 * i + 1);
+    all.n += __ldcg(parts.cta_n + 2 * i);
+    all.live += __ldcg(parts.cta_n + 2 * i + 1);
+  }
+  all.finish(false, parts, losses);
 }
 
 template <typename T, int L, int NV>
-__global__ void __launch_bounds__(BAL_THREADS) balance_bwd_kernel(
+__global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_bwd_kernel(
     const T* __restrict__ logits, const int32_t* __restrict__ off,
     const uint8_t* __restrict__ mask, const int32_t* __restrict__ counts,
     const int32_t* __restrict__ tokens, const float* __restrict__ stats,
     const float* __restrict__ dlosses, int64_t T_, int E, int k, int G, int chunk, bool vec,
     T* __restrict__ dlogits) {
+  using R = Ring<T, L, NV>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ int s_win[SeqWalk::WINDOW + 1];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31;
   const int l = lane % L;
-  constexpr int GROUPS = BAL_THREADS / L;
+  const int GROUPS = blockDim.x / L;
   const int grp = tid / L;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * chunk;
   const int64_t t1 = min(T_, t0 + chunk);
+  R ring;
+  ring.init(smem);
+  ring.blank(l, E);
   const float live = __ldg(stats), n_all = __ldg(stats + 1);
   const float db = __ldg(dlosses);
   const float dz = n_all > 0.f ? __ldg(dlosses + 1) * 2.f / n_all : 0.f;
   SeqWalk w;
-  w.start(off, G, t0, t1);
+  w.start(off, s_win, G, t0, t1);
   while (w.next()) {
-    float c[NV][4];
+    MaskAhead<L> ahead;
+    const int rounds = static_cast<int>((w.b - w.a + GROUPS - 1) / GROUPS);
+    int64_t t = w.a + grp, tn = t;
+    const auto issue = [&](int st) {
+      if (tn < w.b) ring.load(st, logits + tn * E, l, E, vec);
+      R::commit();
+      tn += GROUPS;
+    };
+#pragma unroll
+    for (int i = 0; i < BAL_STAGES - 1; ++i) issue(i);
+    f2 c[2 * NV];
     const float ns = w.s >= 0 ? static_cast<float>(__ldg(tokens + w.s)) : 0.f;
     const float scale =
         ns > 0.f ? db * (static_cast<float>(E) / static_cast<float>(k)) / (ns * ns * live) : 0.f;
+    const auto coef = [&](int e) {
+      return w.s >= 0 && e < E
+                 ? scale * static_cast<float>(__ldg(counts + static_cast<int64_t>(w.s) * E + e))
+                 : 0.f;
+    };
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int e = 4 * (l + i * L) + j;
-        c[i][j] = ns > 0.f && e < E
-                      ? scale * static_cast<float>(__ldg(counts + static_cast<int64_t>(w.s) * E + e))
-                      : 0.f;
-      }
-    for (int64_t base = w.a; base < w.b; base += GROUPS) {
-      const int64_t t = base + grp;
-      bool on = t < w.b && ns > 0.f;
-      if (on && mask != nullptr) on = __ldg(mask + t) != 0;
-      float v[NV][4];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (on) {
-          load4(logits + t * E, 4 * (l + i * L), E, vec, v[i]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[i][j] = -INFINITY;
-        }
-      }
-      float m = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m = max_nan(m, v[i][j]);
-      m = lanes_max<L>(m);
+    for (int i = 0; i < 2 * NV; ++i) {
+      const int e = 4 * (l + i / 2 * L) + i % 2 * 2;
+      c[i] = f2_make(coef(e), coef(e + 1));
+    }
+    int st = 0;
+    for (int it = 0; it < rounds; ++it, t += GROUPS) {
+      issue(st == 0 ? BAL_STAGES - 1 : st - 1);
+      bool on = ahead.get(mask, t, w.b, GROUPS, l, it) && t < w.b && ns > 0.f;
+      R::wait();
+      f2 v[2 * NV];
+      ring.get(st, v);
+      const float m = lanes_max<L>(pairs_max(v));
       on = on && m != -INFINITY;
-      float sum = 0.f, dot = 0.f;
+      pairs_exp<false>(v, m);
+      const float sum = lanes_sum<L>(pairs_sum(v));
+      f2 dot2 = 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[i][j] = on ? expf(v[i][j] - m) : 0.f;
-          sum += v[i][j];
-          dot = fmaf(v[i][j], c[i][j], dot);
-        }
-      sum = lanes_sum<L>(sum);
-      dot = lanes_sum<L>(dot);
-      const float inv = on ? 1.f / sum : 0.f;
-      const float shift = on ? dz * (m + logf(sum)) - dot * inv : 0.f;
+      for (int i = 0; i < 2 * NV; ++i) dot2 = f2_fma(v[i], c[i], dot2);
+      const float dot = lanes_sum<L>(f2_sum(dot2));
+      const float inv = reciprocal(sum);
+      const float shift = dz * (m + logf(sum)) - dot * inv;
+      const f2 inv2 = f2_make(inv, inv), shift2 = f2_make(shift, shift);
       if (t < w.b) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          float d[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) d[j] = on ? v[i][j] * inv * (c[i][j] + shift) : 0.f;
+          float d[4] = {};
+          if (on) {
+            f2_split(f2_mul(f2_mul(v[2 * i], inv2), f2_add(c[2 * i], shift2)), d[0], d[1]);
+            f2_split(f2_mul(f2_mul(v[2 * i + 1], inv2), f2_add(c[2 * i + 1], shift2)), d[2], d[3]);
+          }
           store4(dlogits + t * E, 4 * (l + i * L), E, vec, d);
         }
       }
+      st = st + 1 == BAL_STAGES ? 0 : st + 1;
     }
+    R::drain();
   }
 }
 
 // The split of T tokens over CTAs, and the workspace's arrays.
 struct BalPlan {
-  int chunk, nb;
-  size_t stats, seq_z, n, z, cnt, p, bytes;
+  int threads, chunk, nb;
+  size_t stats, arrived, seq_z, dot, cta_f, cta_n, n, z, cnt, p, bytes;
 };
 
 // Lanes per token (L) and 4-element vectors per lane (NV) by the number of experts.
-static int bal_lanes(int E) { return E <= 128 ? 8 : E <= 256 ? 16 : 32; }
+static int bal_lanes(int E) {
+  return E <= 8 ? 2 : E <= 16 ? 4 : E <= 128 ? 8 : E <= 256 ? 16 : 32;
+}
 
 static BalPlan bal_plan(int64_t T, int E, int G) {
   BalPlan b{};
-  const int groups = BAL_THREADS / bal_lanes(E);
-  const int64_t per = (T + 607) / 608;  // about four CTAs on each of 152 SMs
+  // (131072 tokens, 128 experts: 4096 sequences 125 us forward in large CTAs, one sequence
+  // 27.7 us in small ones against 25.0)
+  b.threads = T / G < 1024 && G > 152 ? BAL_SMALL : BAL_THREADS;
+  // (above 512 experts the registers allow one large CTA on an SM)
+  const int ctas = 152 * (E <= 512 ? 2 : 1) * (BAL_THREADS / b.threads);
+  const int groups = b.threads / bal_lanes(E);
+  const int64_t per = (T + ctas - 1) / ctas;
   b.chunk = static_cast<int>((per + groups - 1) / groups * groups);
   b.nb = static_cast<int>((T + b.chunk - 1) / b.chunk);
   const size_t pieces = static_cast<size_t>(b.nb) + G;
@@ -456,6 +826,10 @@ static BalPlan bal_plan(int64_t T, int E, int G) {
     return at;
   };
   b.stats = take(8);
+  b.arrived = take(4);
+  b.cta_f = take(8 * JOIN_MANY_CTAS);
+  b.cta_n = take(8 * JOIN_MANY_CTAS);
+  b.dot = take(4 * static_cast<size_t>(G) * ((E + 31) / 32));
   b.seq_z = take(4 * static_cast<size_t>(G));
   b.n = take(4 * pieces);
   b.z = take(4 * pieces);
@@ -466,9 +840,11 @@ static BalPlan bal_plan(int64_t T, int E, int G) {
 
 static BalParts bal_parts(const BalPlan& b, void* ws) {
   char* p = static_cast<char*>(ws);
-  return BalParts{reinterpret_cast<float*>(p + b.stats),   reinterpret_cast<float*>(p + b.p),
-                  reinterpret_cast<int32_t*>(p + b.cnt),   reinterpret_cast<int32_t*>(p + b.n),
-                  reinterpret_cast<float*>(p + b.z),       reinterpret_cast<float*>(p + b.seq_z)};
+  return BalParts{reinterpret_cast<float*>(p + b.stats),  reinterpret_cast<float*>(p + b.p),
+                  reinterpret_cast<int32_t*>(p + b.cnt),  reinterpret_cast<int32_t*>(p + b.n),
+                  reinterpret_cast<float*>(p + b.z),      reinterpret_cast<float*>(p + b.seq_z),
+                  reinterpret_cast<float*>(p + b.dot),    reinterpret_cast<int*>(p + b.arrived),
+                  reinterpret_cast<float*>(p + b.cta_f),  reinterpret_cast<int*>(p + b.cta_n)};
 }
 
 static bool bal_shape_ok(const mm_moe_balance_shape* s) {
@@ -485,6 +861,8 @@ static bool al(const void* p, uintptr_t a) {
 template <typename F>
 static cudaError_t with_lanes(int E, F f) {
   using std::integral_constant;
+  if (E <= 8) return f(integral_constant<int, 2>{}, integral_constant<int, 1>{});
+  if (E <= 16) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
   if (E <= 32) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
   if (E <= 64) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
   if (E <= 128) return f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
@@ -526,27 +904,33 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_balance_forward(
             G = static_cast<int>(shape->G);
   const BalPlan b = bal_plan(shape->T, E, G);
   const BalParts parts = bal_parts(b, workspace);
-  const size_t smem = static_cast<size_t>(BAL_WARPS + 1) * E * 4;
   prof_begin(c, K_BALANCE_FWD);
   cudaError_t e = with_dtype(shape->dtype, [&](auto* tag) {
     using T = std::remove_pointer_t<decltype(tag)>;
     const T* lg = static_cast<const T*>(logits);
     return with_lanes(E, [&](auto l, auto nv) {
-      return launch_k(c.stream, balance_fwd_kernel<T, decltype(l)::value, decltype(nv)::value>,
-                      dim3(b.nb), dim3(BAL_THREADS), smem, lg, topk_idx, seq_offsets, mask,
-                      shape->T, E, k, G, b.chunk, bal_vec<T>(lg, E), lse, parts);
+      constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
+      auto* kern = balance_fwd_kernel<T, L, NV>;
+      const size_t smem = static_cast<size_t>(Ring<T, L, NV>::BYTES) * b.threads +
+                          static_cast<size_t>(b.threads / 32 + 1) * E * 4;
+      const cudaError_t r = allow_smem(kern, smem);
+      if (r != cudaSuccess) return r;
+      return launch_k(c.stream, kern, dim3(b.nb), dim3(b.threads), smem, lg, topk_idx,
+                      seq_offsets, mask, shape->T, E, k, G, b.chunk, bal_vec<T>(lg, E), lse,
+                      parts);
     });
   });
   prof_end(c, K_BALANCE_FWD);
   if (e != cudaSuccess) return MM_MOE_ECUDA;
+  // one wave of the first kernel's CTAs, else a CTA per sequence (131072 tokens, 256 experts,
+  // 96 sequences, 768 of the first kernel's CTAs: 82 us forward against 44)
+  const int64_t units = static_cast<int64_t>(G) * ((E + 31) / 32);
+  const bool few = units <= 2 * c.num_sms;
   prof_begin(c, K_BALANCE_FINISH);
-  e = launch_k(c.stream, balance_seq_kernel, dim3(G), dim3(256), 0, seq_offsets, shape->T, E, k,
-               b.chunk, parts, seq_loss, counts, tokens);
-  prof_end(c, K_BALANCE_FINISH);
-  if (e != cudaSuccess) return MM_MOE_ECUDA;
-  prof_begin(c, K_BALANCE_FINISH);
-  e = launch_k(c.stream, balance_total_kernel, dim3(1), dim3(256), 0, G, parts,
-               static_cast<const float*>(seq_loss), static_cast<const int32_t*>(tokens), losses);
+  e = launch_k(c.stream, few ? balance_join_few_kernel : balance_join_many_kernel,
+               dim3(static_cast<unsigned>(few ? units : std::min(G, JOIN_MANY_CTAS))),
+               dim3(few ? JOIN_THREADS : std::min(JOIN_MANY_THREADS, (E + 31) / 32 * 32)), 0,
+               seq_offsets, shape->T, E, k, G, b.chunk, parts, losses, seq_loss, counts, tokens);
   prof_end(c, K_BALANCE_FINISH);
   return e == cudaSuccess ? MM_MOE_OK : MM_MOE_ECUDA;
 }
@@ -575,9 +959,13 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_balance_backward(
     const T* lg = static_cast<const T*>(logits);
     T* out = static_cast<T*>(dlogits);
     return with_lanes(E, [&](auto l, auto nv) {
-      return launch_k(c.stream, balance_bwd_kernel<T, decltype(l)::value, decltype(nv)::value>,
-                      dim3(b.nb), dim3(BAL_THREADS), 0, lg, seq_offsets, mask, counts, tokens,
-                      stats, dlosses, shape->T, E, k, G, b.chunk,
+      constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
+      auto* kern = balance_bwd_kernel<T, L, NV>;
+      const size_t smem = static_cast<size_t>(Ring<T, L, NV>::BYTES) * b.threads;
+      const cudaError_t r = allow_smem(kern, smem);
+      if (r != cudaSuccess) return r;
+      return launch_k(c.stream, kern, dim3(b.nb), dim3(b.threads), smem, lg, seq_offsets, mask,
+                      counts, tokens, stats, dlosses, shape->T, E, k, G, b.chunk,
                       bal_vec<T>(lg, E) && bal_vec<T>(out, E), out);
     });
   });

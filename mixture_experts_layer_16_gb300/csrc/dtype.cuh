@@ -79,6 +79,38 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8], const __half*) {
   return v;
 }
 
+// ------------------------------------------------------------------ two fp32 in a pair
+// Packed fp32 arithmetic: one instruction for two values (add, mul, fma .f32x2).
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 f2_make(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_split(f2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float f2_sum(f2 v) {
+  float a, b;
+  f2_split(v, a, b);
+  return a + b;
+}
+
 inline bool dtype_ok(int32_t d) { return d >= MM_MOE_DT_BF16 && d <= MM_MOE_DT_F32; }
 inline size_t dtype_bytes(int32_t d) { return d == MM_MOE_DT_F32 ? 4 : 2; }
 
@@ -104,6 +136,14 @@ inline int sm_count_103() {
   const int n = major == 10 && minor == 3 ? sms : 0;
   if (dev < 64) known[dev].store(n + 1, std::memory_order_relaxed);
   return n;
+}
+
+// Lets `kern` be launched with so much dynamic shared memory.
+template <typename K>
+inline cudaError_t allow_smem(K* kern, size_t bytes) {
+  if (bytes <= 40 * 1024) return cudaSuccess;  // within the default 48 KB, static part included
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(bytes));
 }
 
 template <typename V>

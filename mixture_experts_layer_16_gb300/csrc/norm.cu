@@ -27,38 +27,6 @@ struct Rows {
   __device__ __forceinline__ T* row(int64_t t) const { return p + t * ld; }
 };
 
-// ------------------------------------------------------------------ two fp32 in a pair
-// Packed fp32 arithmetic: one instruction for two values (add, mul, fma .f32x2).
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 f2_make(float a, float b) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void f2_split(f2 v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ float f2_sum(f2 v) {
-  float a, b;
-  f2_split(v, a, b);
-  return a + b;
-}
-
 // The elements of 16 bytes as fp32 pairs, and back.
 template <typename T>
 __device__ __forceinline__ void unpack2(const uint4& q, f2 (&v)[VN<T> / 2]) {
@@ -733,13 +701,6 @@ static NormGrid norm_grid(int GT, int T, int sms, int most_groups = NORM_THREADS
   int groups = std::min(most, (T + sms - 1) / sms);
   groups = (groups + per_warp - 1) / per_warp * per_warp;
   return NormGrid{GT, groups, std::min(sms, (T + groups - 1) / groups)};
-}
-
-template <typename K>
-static cudaError_t allow_smem(K* kern, size_t bytes) {
-  if (bytes <= 40 * 1024) return cudaSuccess;  // (48 KB with the static part)
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(bytes));
 }
 
 template <typename T>
