@@ -10,3 +10,4 @@ from .binding import (Shape, Workspace, MoEError, make_shape, mm_moe_workspace_s
                       mm_moe_kernel_name, mm_moe_kernel_count)
 from .layer import MoELayer, MoERouter  # noqa: F401,E402
 from .train import MoEBalanceLoss, MoEGradClip, MoELayerNorm  # noqa: F401,E402
+from .block import MoEBlock  # noqa: F401,E402
