@@ -56,11 +56,11 @@ __device__ __forceinline__ uint4 pack2(const f2 (&v)[VN<T> / 2]) {
 // copies its own units and reads nothing but what it copied, so no barrier guards the ring.
 constexpr int NORM_THREADS = 512;
 
-// Rows in the ring: what keeps 128 KB (forward) or 96 to 192 KB (backward) of it.
-template <int NU>
-constexpr int norm_fwd_stages = NU <= 4 ? 4 : 2;
-template <int NU>
-constexpr int norm_bwd_stages = NU <= 2 ? 4 : 2;
+// Steps of ROWS rows in the ring: 64 to 192 KB of it.
+template <int NU, int ROWS>
+constexpr int norm_fwd_steps = ROWS == 2 ? 3 : NU <= 4 ? 4 : 2;
+template <int NU, bool ADD, int ROWS>
+constexpr int norm_bwd_steps = (NU <= 2 ? 4 : 2) / ROWS + (NU <= 2 && !ADD && ROWS == 2 ? 1 : 0);
 // Parameters stay in registers up to 16 columns a thread, else in shared memory.
 template <typename T, int NU>
 constexpr bool norm_params_shared = NU * VN<T> > 16;
@@ -97,9 +97,12 @@ __device__ __forceinline__ void group_bar(int g, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(threads) : "memory");
 }
 
-// A thread's place: its group and its columns.  EVEN: every row is whole units (it starts
-// on a 16-byte boundary and ends on one), so nothing is masked or cut short.
-template <typename T, int NU, bool EVEN>
+// What a row is like: ANY; whole units (EVEN: it starts and ends on a 16-byte boundary, so
+// nothing is masked or cut short); FULL: whole units, NU of them for every thread.
+enum Cut { ANY, EVEN, FULL };
+
+// A thread's place: its group and its columns.
+template <typename T, int NU, Cut CUT>
 struct Place {
   static constexpr int U = VN<T>;
   int GT, g, j, groups, H;
@@ -112,18 +115,22 @@ struct Place {
     j = threadIdx.x - g * GT;
     groups = blockDim.x / GT;
   }
+  // the first row of the warp's groups (they loop together)
+  __device__ __forceinline__ uint32_t first_of_warp(uint32_t t) const {
+    return GT < 32 ? t - (g & (32 / GT - 1)) : t;
+  }
   template <typename V>
   __device__ __forceinline__ void cut(const Rows<V>& r, int64_t t) {
-    shift = EVEN ? 0
-                 : static_cast<int>((reinterpret_cast<uintptr_t>(r.p + t * r.ld) & 15) / sizeof(T));
-    units = EVEN ? H / U : (H + shift + U - 1) / U;
+    shift = CUT != ANY ? 0
+                       : static_cast<int>((reinterpret_cast<uintptr_t>(r.p + t * r.ld) & 15) / sizeof(T));
+    units = CUT != ANY ? H / U : (H + shift + U - 1) / U;
   }
   // first column of unit i (may be negative, or past the row)
   __device__ __forceinline__ int col(int i) const { return (j + i * GT) * U - shift; }
-  __device__ __forceinline__ bool has(int i) const { return j + i * GT < units; }
+  __device__ __forceinline__ bool has(int i) const { return CUT == FULL || j + i * GT < units; }
   // the whole unit lies in the row
   __device__ __forceinline__ bool whole(int i) const {
-    return EVEN ? has(i) : col(i) >= 0 && col(i) + U <= H;
+    return CUT != ANY ? has(i) : col(i) >= 0 && col(i) + U <= H;
   }
   __device__ __forceinline__ bool in(int c) const { return c >= 0 && c < H; }
   // The thread's first unit of a row (unit i lies i GT units further on).
@@ -134,14 +141,14 @@ struct Place {
   // unit i of the row whose first unit of this thread is at p; what lies past the row
   // arrives as zero
   __device__ __forceinline__ void copy(uint32_t slot, const T* p, int i) const {
-    if constexpr (EVEN)
+    if constexpr (CUT != ANY)
       async_copy(slot, p + i * GT * U);
     else
       async_copy(slot, p + i * GT * U, min(U, H - col(i)) * static_cast<int>(sizeof(T)));
   }
   // zero in front of the row
   __device__ __forceinline__ void mask(uint4& q, int i) const {
-    if (EVEN || i != 0) return;
+    if (CUT != ANY || i != 0) return;
     if (j == 0 && shift != 0) {
       T* h = reinterpret_cast<T*>(&q);
 #pragma unroll
@@ -153,7 +160,7 @@ struct Place {
     T* o = p + i * GT * U;
     if (whole(i)) {
       *reinterpret_cast<uint4*>(o) = q;
-    } else if constexpr (!EVEN) {
+    } else if constexpr (CUT == ANY) {
       const T* h = reinterpret_cast<const T*>(&q);
 #pragma unroll
       for (int k = 0; k < U; ++k)
@@ -195,71 +202,85 @@ __device__ __forceinline__ float lanes_sum(float v, int GT) {
   for (int o = GT >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ float group_sum(float v, float* s, int g, int GT) {
-  v = lanes_sum(v, GT);
-  if (GT <= 32) return v;
+template <int N>
+struct alignas(4 * N) Sums {  // one shared-memory access
+  float v[N];
+};
+template <int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], Sums<N>* s, int g, int GT) {
+#pragma unroll
+  for (int q = 0; q < N; ++q) v[q] = lanes_sum(v[q], GT);
+  if (GT <= 32) return;
   const int gw = GT >> 5;
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) {
+    Sums<N> mine;
+#pragma unroll
+    for (int q = 0; q < N; ++q) mine.v[q] = v[q];
+    s[threadIdx.x >> 5] = mine;
+  }
   group_bar(g, GT);
   s += g * gw;
-  float t = s[0];
-  for (int i = 1; i < gw; ++i) t += s[i];
-  return t;
+  Sums<N> t = s[0];
+  for (int i = 1; i < gw; ++i) {
+    const Sums<N> o = s[i];
+#pragma unroll
+    for (int q = 0; q < N; ++q) t.v[q] += o.v[q];
+  }
+#pragma unroll
+  for (int q = 0; q < N; ++q) v[q] = t.v[q];
 }
 
 // ------------------------------------------------------------------------- forward
 // A thread with up to 16 columns holds its parameters in registers; with more columns a
 // row needs fewer threads, so fewer sums across warps (none up to 2048 columns of 16 bits:
-// 16384 x 2048 bf16 takes 31.8 us with 128 threads a row, 16 columns each), and the
-// parameters come from shared memory.
-template <typename T, typename P, int NU, bool EVEN>
+// 16384 x 2048 bf16 takes 31.8 us with 128 threads a row, 16 columns each, 22.6 us with a
+// warp a row), and the parameters come from shared memory.  Where several warps share a
+// row and registers allow it, a group takes two rows at a time (ROWS), so that two share
+// the two barriers.
+template <typename T, typename P, int NU, Cut CUT, int ROWS>
 __global__ void __launch_bounds__(NORM_THREADS, 1) norm_fwd_kernel(
     Rows<const T> x, Rows<T> y, int T_, int H, int GT, const P* __restrict__ w,
     const P* __restrict__ b, float eps, float* __restrict__ mean, float* __restrict__ rstd) {
-  constexpr int U = VN<T>, C2 = NU * U / 2, S = norm_fwd_stages<NU>;
+  constexpr int U = VN<T>, C2 = NU * U / 2, S = norm_fwd_steps<NU, ROWS>;
   constexpr bool PS = norm_params_shared<T, NU>;
-  static_assert(EVEN || !PS, "a shifted row's columns do not line up with the parameters");
+  static_assert(CUT != ANY || !PS, "a shifted row's columns do not line up with the parameters");
   extern __shared__ __align__(16) unsigned char ring_bytes[];
-  __shared__ float s_sum[2][NORM_THREADS / 32];
+  __shared__ Sums<ROWS> s_sum[2][NORM_THREADS / 32];
   const int nt = blockDim.x;
   const uint32_t ring =
       static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)) + threadIdx.x * 16;
-  const uint32_t unit_bytes = nt * 16, stage_bytes = NU * unit_bytes;
+  const uint32_t unit_bytes = nt * 16, row_bytes = NU * unit_bytes, step_bytes = ROWS * row_bytes;
   pdl_wait();
   pdl_trigger();
-  Place<T, NU, EVEN> p;
+  Place<T, NU, CUT> p;
   p.init(GT, H);
   const float inv = 1.f / static_cast<float>(H);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * p.groups;
-  int64_t t = static_cast<int64_t>(blockIdx.x) * p.groups + p.g;
-  // the first row of the warp: its groups loop together
-  int64_t tw = GT < 32 ? t - (p.g & (32 / GT - 1)) : t;
+  const uint32_t n = T_, step = gridDim.x * p.groups;
+  uint32_t t = blockIdx.x * p.groups + p.g;
+  uint32_t tw = p.first_of_warp(t);
   p.cut(x, t);
-  const int64_t step_x = step * x.ld, step_y = step * y.ld;
-  const T* px = p.at(x, t);  // the row to copy next
-  T* py = p.at(y, t);
-  int64_t ta = t;
-  const auto issue = [&](uint32_t stage) {
-    if (ta < T_) {
+  uint32_t ta = t;  // the row to copy next
+  const auto issue = [&](uint32_t at) {
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r, ta += step) {
+      if (ta >= n) continue;
+      const T* px = p.at(x, ta);
 #pragma unroll
       for (int i = 0; i < NU; ++i)
-        if (p.has(i)) p.copy(stage + i * unit_bytes, px, i);
+        if (p.has(i)) p.copy(at + r * row_bytes + i * unit_bytes, px, i);
     }
     async_commit();
-    ta += step;
-    px += step_x;
   };
-#pragma unroll
-  for (int i = 0; i < S * NU; ++i)
+  for (int i = 0; i < S * ROWS * NU; ++i)
     if (!p.has(i % NU)) sts16_zero(ring + i * unit_bytes);
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(ring + i * stage_bytes);
+  for (int i = 0; i < S - 1; ++i) issue(ring + i * step_bytes);
   f2 wv[PS ? 1 : C2], bv[PS ? 1 : C2];
   // shared: weight then bias in fp32, the two halves of the units apart (16-byte reads of
   // consecutive units then meet no bank twice)
-  const uint32_t sw = ring - threadIdx.x * 16 + S * stage_bytes;
+  const uint32_t sw = ring - threadIdx.x * 16 + S * step_bytes;
   if constexpr (PS) {
-    float* s = reinterpret_cast<float*>(ring_bytes + S * stage_bytes);
+    float* s = reinterpret_cast<float*>(ring_bytes + S * step_bytes);
     for (int c = threadIdx.x; c < H; c += nt) {
       const int at = ((c % U / 4) * p.units + c / U) * 4 + c % 4;
       s[at] = to_f32(w[c]);
@@ -273,47 +294,62 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_fwd_kernel(
   bool full = true;
 #pragma unroll
   for (int i = 0; i < NU; ++i) full = full && p.whole(i);
-  uint32_t st = ring, st_in = ring + (S - 1) * stage_bytes;
-  const uint32_t ring_end = ring + S * stage_bytes;
-  for (; tw < T_; t += step, tw += step, py += step_y) {
+  uint32_t st = ring, st_in = ring + (S - 1) * step_bytes;
+  const uint32_t ring_end = ring + S * step_bytes;
+  for (; tw < n; t += ROWS * step, tw += ROWS * step) {
     issue(st_in);
     async_wait<S - 1>();
-    f2 v[C2];
-    f2 a2 = 0;
+    f2 v[ROWS][C2];
+    float mu[ROWS], q[ROWS];
 #pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      uint4 q = lds16(st + i * unit_bytes);
-      p.mask(q, i);
-      f2 u[U / 2];
-      unpack2<T>(q, u);
+    for (int r = 0; r < ROWS; ++r) {
+      f2 a2 = 0;
 #pragma unroll
-      for (int k = 0; k < U / 2; ++k) {
-        v[i * U / 2 + k] = u[k];
-        a2 = f2_add(a2, u[k]);
+      for (int i = 0; i < NU; ++i) {
+        uint4 raw = lds16(st + r * row_bytes + i * unit_bytes);
+        p.mask(raw, i);
+        f2 u[U / 2];
+        unpack2<T>(raw, u);
+#pragma unroll
+        for (int k = 0; k < U / 2; ++k) {
+          v[r][i * U / 2 + k] = u[k];
+          a2 = f2_add(a2, u[k]);
+        }
       }
+      mu[r] = f2_sum(a2);
     }
     st_in = st;
-    st += stage_bytes;
+    st += step_bytes;
     if (st == ring_end) st = ring;
-    const float mu = group_sum(f2_sum(a2), s_sum[0], p.g, GT) * inv;
-    const f2 nmu = f2_make(-mu, -mu);
+    group_sum<ROWS>(mu, s_sum[0], p.g, GT);
 #pragma unroll
-    for (int k = 0; k < C2; ++k) v[k] = f2_add(v[k], nmu);
-    if (!full) {  // what is not in the row has no deviation either
+    for (int r = 0; r < ROWS; ++r) {
+      mu[r] *= inv;
+      const f2 nmu = f2_make(-mu[r], -mu[r]);
 #pragma unroll
-      for (int k = 0; k < C2; ++k) {
-        const int c = p.col(2 * k / U) + 2 * k % U;
-        float lo, hi;
-        f2_split(v[k], lo, hi);
-        v[k] = f2_make(p.in(c) ? lo : 0.f, p.in(c + 1) ? hi : 0.f);
+      for (int k = 0; k < C2; ++k) v[r][k] = f2_add(v[r][k], nmu);
+      if (!full) {  // what is not in the row has no deviation either
+#pragma unroll
+        for (int k = 0; k < C2; ++k) {
+          const int c = p.col(2 * k / U) + 2 * k % U;
+          float lo, hi;
+          f2_split(v[r][k], lo, hi);
+          v[r][k] = f2_make(p.in(c) ? lo : 0.f, p.in(c + 1) ? hi : 0.f);
+        }
       }
-    }
-    a2 = 0;
+      f2 a2 = 0;
 #pragma unroll
-    for (int k = 0; k < C2; ++k) a2 = f2_fma(v[k], v[k], a2);
-    const float r = rsqrtf(group_sum(f2_sum(a2), s_sum[1], p.g, GT) * inv + eps);
-    const f2 r2 = f2_make(r, r);
-    if (t < T_) {
+      for (int k = 0; k < C2; ++k) a2 = f2_fma(v[r][k], v[r][k], a2);
+      q[r] = f2_sum(a2);
+    }
+    group_sum<ROWS>(q, s_sum[1], p.g, GT);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const uint32_t tr = t + r * step;
+      if (tr >= n) continue;
+      T* const py = p.at(y, tr);
+      const float rs = rsqrtf(q[r] * inv + eps);
+      const f2 r2 = f2_make(rs, rs);
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         if (!p.has(i)) break;
@@ -325,21 +361,21 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_fwd_kernel(
             const ulonglong2 w4 = lds16_f2(at + h * p.units * 16),
                              b4 = lds16_f2(at + H * 4 + h * p.units * 16);
             const int e = i * U / 2 + 2 * h;
-            u[2 * h] = f2_fma(f2_mul(v[e], r2), w4.x, b4.x);
-            u[2 * h + 1] = f2_fma(f2_mul(v[e + 1], r2), w4.y, b4.y);
+            u[2 * h] = f2_fma(f2_mul(v[r][e], r2), w4.x, b4.x);
+            u[2 * h + 1] = f2_fma(f2_mul(v[r][e + 1], r2), w4.y, b4.y);
           }
         } else {
 #pragma unroll
           for (int k = 0; k < U / 2; ++k) {
             const int e = i * U / 2 + k;
-            u[k] = f2_fma(f2_mul(v[e], r2), wv[e], bv[e]);
+            u[k] = f2_fma(f2_mul(v[r][e], r2), wv[e], bv[e]);
           }
         }
         p.store(py, i, pack2<T>(u));
       }
       if (p.j == 0) {
-        mean[t] = mu;
-        rstd[t] = r;
+        mean[tr] = mu[r];
+        rstd[tr] = rs;
       }
     }
   }
@@ -348,55 +384,57 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_fwd_kernel(
 
 // ------------------------------------------------------------------------ backward
 // dx and the CTA's column sums in one read of x, dy (and dx_add): the column sums stay
-// in the registers of the threads that own the columns, and a row needs one barrier, that
-// of its two sums.
-template <typename T, int NU, bool EVEN>
+// in the registers of the threads that own the columns.  A group takes ROWS rows at a time,
+// whose sums meet at one barrier: two where shared memory holds two steps of them.  Their
+// x and dy are then read from the ring and unpacked a second time, which costs fewer
+// cycles than the barrier's wait with one row in flight.
+template <typename T, int NU, Cut CUT, bool ADD, int ROWS>
 __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
     Rows<const T> dy, Rows<const T> x, Rows<const T> add, Rows<T> dx, const void* __restrict__ w,
     bool w32, const float* __restrict__ mean, const float* __restrict__ rstd, int T_, int H, int GT,
     float* __restrict__ part) {
-  constexpr int U = VN<T>, C2 = NU * U / 2, S = norm_bwd_stages<NU>;
+  constexpr int U = VN<T>, C2 = NU * U / 2, S = norm_bwd_steps<NU, ADD, ROWS>;
+  constexpr int ARRAYS = ADD ? 3 : 2;
   extern __shared__ __align__(16) unsigned char ring_bytes[];
-  __shared__ f2 s_sum[2][NORM_THREADS / 32];
+  __shared__ Sums<2 * ROWS> s_sum[2][NORM_THREADS / 32];
   const int tid = threadIdx.x, nt = blockDim.x;
-  const bool with_add = add.p != nullptr;
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)) + tid * 16;
   const uint32_t unit_bytes = nt * 16, array_bytes = NU * unit_bytes,
-                 stage_bytes = (with_add ? 3 : 2) * array_bytes;
+                 row_bytes = ARRAYS * array_bytes, step_bytes = ROWS * row_bytes;
   pdl_wait();
   pdl_trigger();
-  Place<T, NU, EVEN> p;
+  Place<T, NU, CUT> p;
   p.init(GT, H);
   const float inv = 1.f / static_cast<float>(H);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * p.groups;
-  int64_t t = static_cast<int64_t>(blockIdx.x) * p.groups + p.g;
-  int64_t tw = GT < 32 ? t - (p.g & (32 / GT - 1)) : t;
+  const uint32_t n = T_, step = gridDim.x * p.groups;
+  uint32_t t = blockIdx.x * p.groups + p.g;
+  uint32_t tw = p.first_of_warp(t);
   p.cut(x, t);
-  const int64_t step_x = step * x.ld, step_g = step * dy.ld, step_a = step * add.ld,
-                step_d = step * dx.ld;
-  const T *px = p.at(x, t), *pg = p.at(dy, t), *pa = with_add ? p.at(add, t) : nullptr;
-  T* pd = p.at(dx, t);
-  int64_t ta = t;
-  const auto issue = [&](uint32_t stage) {
-    if (ta < T_) {
+  uint32_t ta = t;  // the row to copy next
+  const auto issue = [&](uint32_t at) {
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r, ta += step) {
+      if (ta >= n) continue;
+      const T *px = p.at(x, ta), *pg = p.at(dy, ta);
 #pragma unroll
       for (int i = 0; i < NU; ++i)
         if (p.has(i)) {
-          p.copy(stage + i * unit_bytes, px, i);
-          p.copy(stage + array_bytes + i * unit_bytes, pg, i);
-          if (with_add) p.copy(stage + 2 * array_bytes + i * unit_bytes, pa, i);
+          p.copy(at + r * row_bytes + i * unit_bytes, px, i);
+          p.copy(at + r * row_bytes + array_bytes + i * unit_bytes, pg, i);
         }
+      if constexpr (ADD) {
+        const T* pa = p.at(add, ta);
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+          if (p.has(i)) p.copy(at + r * row_bytes + 2 * array_bytes + i * unit_bytes, pa, i);
+      }
     }
     async_commit();
-    ta += step;
-    px += step_x;
-    pg += step_g;
-    if (with_add) pa += step_a;
   };
-  for (int i = 0; i < S * (with_add ? 3 : 2) * NU; ++i)
+  for (int i = 0; i < S * ROWS * ARRAYS * NU; ++i)
     if (!p.has(i % NU)) sts16_zero(ring + i * unit_bytes);
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(ring + i * stage_bytes);
+  for (int i = 0; i < S - 1; ++i) issue(ring + i * step_bytes);
   f2 wv[C2], dw[C2], db[C2];
   if (w32)
     p.params(static_cast<const float*>(w), wv);
@@ -404,80 +442,103 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
     p.params(static_cast<const T*>(w), wv);
 #pragma unroll
   for (int k = 0; k < C2; ++k) dw[k] = db[k] = 0;
-  float mu_n = 0.f, r_n = 0.f;
-  if (t < T_) {
-    mu_n = __ldg(mean + t);
-    r_n = __ldg(rstd + t);
-  }
-  int buf = 0;
-  const int gw = GT >> 5;
-  uint32_t st = ring, st_in = ring + (S - 1) * stage_bytes;
-  const uint32_t ring_end = ring + S * stage_bytes;
-  for (; tw < T_; t += step, tw += step, pd += step_d) {
-    issue(st_in);
-    const bool on = t < T_;
-    const float r = r_n;
-    const f2 r2 = f2_make(r, r), m2 = f2_make(-mu_n, -mu_n);
-    if (t + step < T_) {
-      mu_n = __ldg(mean + t + step);
-      r_n = __ldg(rstd + t + step);
+  float mu_n[ROWS], r_n[ROWS];
+  const auto stats = [&](uint32_t from) {
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const uint32_t q = from + r * step;
+      mu_n[r] = q < n ? __ldg(mean + q) : 0.f;
+      r_n[r] = q < n ? __ldg(rstd + q) : 0.f;
     }
+  };
+  stats(t);
+  int buf = 0;  // (one barrier a step: two buffers keep the next sums off these)
+  uint32_t st = ring, st_in = ring + (S - 1) * step_bytes;
+  const uint32_t ring_end = ring + S * step_bytes;
+  for (; tw < n; t += ROWS * step, tw += ROWS * step) {
+    issue(st_in);
+    f2 r2[ROWS], m2[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      r2[r] = f2_make(r_n[r], r_n[r]);
+      m2[r] = f2_make(-mu_n[r], -mu_n[r]);
+    }
+    stats(t + ROWS * step);
     async_wait<S - 1>();
-    f2 xh[C2], gv[C2];
-    f2 a2 = 0, c2 = 0;
-    if (on) {
+    // xh and g = w dy of unit i of row r
+    const auto unit = [&](int r, int i, f2 (&xh)[U / 2], f2 (&g)[U / 2], bool sums) {
+      uint4 qx = lds16(st + r * row_bytes + i * unit_bytes),
+            qg = lds16(st + r * row_bytes + array_bytes + i * unit_bytes);
+      p.mask(qx, i);
+      p.mask(qg, i);  // (a zero dy takes the column out of every sum)
+      f2 fx[U / 2], fg[U / 2];
+      unpack2<T>(qx, fx);
+      unpack2<T>(qg, fg);
 #pragma unroll
-      for (int i = 0; i < NU; ++i) {
-        uint4 qx = lds16(st + i * unit_bytes), qg = lds16(st + array_bytes + i * unit_bytes);
-        p.mask(qx, i);
-        p.mask(qg, i);  // (a zero dy takes the column out of every sum)
-        f2 fx[U / 2], fg[U / 2];
-        unpack2<T>(qx, fx);
-        unpack2<T>(qg, fg);
-#pragma unroll
-        for (int k = 0; k < U / 2; ++k) {
-          const int e = i * U / 2 + k;
-          xh[e] = f2_mul(f2_add(fx[k], m2), r2);
-          dw[e] = f2_fma(fg[k], xh[e], dw[e]);
+      for (int k = 0; k < U / 2; ++k) {
+        const int e = i * U / 2 + k;
+        xh[k] = f2_mul(f2_add(fx[k], m2[r]), r2[r]);
+        g[k] = f2_mul(fg[k], wv[e]);
+        if (sums) {
+          dw[e] = f2_fma(fg[k], xh[k], dw[e]);
           db[e] = f2_add(db[e], fg[k]);
-          gv[e] = f2_mul(fg[k], wv[e]);
-          a2 = f2_add(a2, gv[e]);
-          c2 = f2_fma(gv[e], xh[e], c2);
         }
       }
+    };
+    f2 xh1[ROWS == 1 ? NU : 1][U / 2], g1[ROWS == 1 ? NU : 1][U / 2];
+    float ac[2 * ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      f2 a2 = 0, c2 = 0;
+      if (t + r * step < n) {
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+          f2 xh[U / 2], g[U / 2];
+          unit(r, i, xh, g, true);
+#pragma unroll
+          for (int k = 0; k < U / 2; ++k) {
+            a2 = f2_add(a2, g[k]);
+            c2 = f2_fma(g[k], xh[k], c2);
+            if constexpr (ROWS == 1) {
+              xh1[i][k] = xh[k];
+              g1[i][k] = g[k];
+            }
+          }
+        }
+      }
+      ac[2 * r] = f2_sum(a2);
+      ac[2 * r + 1] = f2_sum(c2);
     }
-    float a = lanes_sum(f2_sum(a2), GT), c = lanes_sum(f2_sum(c2), GT);
-    if (GT > 32) {
-      f2* const m = s_sum[buf] + p.g * gw;
-      if ((tid & 31) == 0) m[(tid >> 5) - p.g * gw] = f2_make(a, c);
-      group_bar(p.g, GT);
-      f2 t2 = m[0];
-      for (int i = 1; i < gw; ++i) t2 = f2_add(t2, m[i]);
-      f2_split(t2, a, c);
-      buf ^= 1;
-    }
-    if (on) {
-      const f2 na = f2_make(-a * inv, -a * inv), nc = f2_make(-c * inv, -c * inv);
+    group_sum<2 * ROWS>(ac, s_sum[buf], p.g, GT);
+    buf ^= 1;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      if (t + r * step >= n) continue;
+      T* const pd = p.at(dx, t + r * step);
+      const float a = -ac[2 * r] * inv, c = -ac[2 * r + 1] * inv;
+      const f2 na = f2_make(a, a), nc = f2_make(c, c);
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         if (!p.has(i)) break;
-        f2 u[U / 2];
-        if (with_add) {
-          unpack2<T>(lds16(st + 2 * array_bytes + i * unit_bytes), u);
+        f2 xh[U / 2], g[U / 2], u[U / 2];
+        if constexpr (ROWS > 1) unit(r, i, xh, g, false);
+        if constexpr (ADD) {
+          unpack2<T>(lds16(st + r * row_bytes + 2 * array_bytes + i * unit_bytes), u);
         } else {
 #pragma unroll
           for (int k = 0; k < U / 2; ++k) u[k] = 0;
         }
 #pragma unroll
         for (int k = 0; k < U / 2; ++k) {
-          const int e = i * U / 2 + k;
-          u[k] = f2_fma(f2_fma(xh[e], nc, f2_add(gv[e], na)), r2, u[k]);
+          const f2 h = ROWS > 1 ? xh[k] : xh1[ROWS > 1 ? 0 : i][k];
+          const f2 gg = ROWS > 1 ? g[k] : g1[ROWS > 1 ? 0 : i][k];
+          u[k] = f2_fma(f2_fma(h, nc, f2_add(gg, na)), r2[r], u[k]);
         }
         p.store(pd, i, pack2<T>(u));
       }
     }
     st_in = st;
-    st += stage_bytes;
+    st += step_bytes;
     if (st == ring_end) st = ring;
   }
   async_wait<0>();
@@ -492,7 +553,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
   // Groups may cut their rows differently, so the sums meet by column.
   float* const sj = reinterpret_cast<float*>(ring_bytes);  // [groups][2][H]
   __syncthreads();
-  if constexpr (EVEN) {
+  if constexpr (CUT != ANY) {
     float* const q = sj + 2 * p.g * H;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
@@ -708,21 +769,22 @@ static bool even_rows(const Rows<T>& r, int64_t rows) {
   return rows == 1 || r.ld * sizeof(T) % 16 == 0;
 }
 
-template <typename T, typename P, int NU>
+template <typename T, typename P, int NU, int ROWS>
 static cudaError_t fwd_launch(const Ctx& c, Rows<const T> x, Rows<T> y, int T_, int H, const P* w,
                               const P* b, float eps, float* mean, float* rstd) {
   const int GT = group_threads<T, NU>(H, even_rows(x, T_));
-  constexpr int RING = norm_fwd_stages<NU> * NU * 16;  // bytes per thread
+  constexpr int RING = norm_fwd_steps<NU, ROWS> * ROWS * NU * 16;  // bytes per thread
   // the ring and shared parameters have to fit beside each other (H above 8192: one group)
   const int fit = norm_params_shared<T, NU> ? (224 * 1024 - 8 * H) / (RING * GT) : NORM_THREADS;
   const NormGrid n = norm_grid(GT, T_, c.num_sms, fit);
   const int nt = n.GT * n.groups;
   size_t smem = static_cast<size_t>(RING) * nt;
-  auto* kern = norm_fwd_kernel<T, P, NU, true>;
+  const bool even = even_rows(x, T_) && H % VN<T> == 0;
+  auto* kern = norm_fwd_kernel<T, P, NU, EVEN, ROWS>;
   if constexpr (norm_params_shared<T, NU>)
     smem += sizeof(float) * 2 * H;
-  else if (!(even_rows(x, T_) && H % VN<T> == 0))
-    kern = norm_fwd_kernel<T, P, NU, false>;
+  else if (!even)
+    kern = norm_fwd_kernel<T, P, NU, ANY, ROWS>;
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
   return launch_k(c.stream, kern, dim3(n.ctas), dim3(nt), smem, x, y, T_, H, n.GT, w, b, eps, mean,
@@ -740,19 +802,25 @@ static mm_moe_status norm_forward(const Ctx& c, const mm_moe_norm_shape* s, cons
   const P* b = static_cast<const P*>(b_);
   constexpr int MOST = 16 / VN<T>;  // units of 16 columns
   const bool even = even_rows(x, T_);
-  const auto go = [&](auto nu) {
-    return fwd_launch<T, P, decltype(nu)::value>(c, x, y, T_, H, w, b, s->eps, mean, rstd);
+  const auto go = [&](auto nu, auto rows) {
+    return fwd_launch<T, P, decltype(nu)::value, decltype(rows)::value>(c, x, y, T_, H, w, b,
+                                                                        s->eps, mean, rstd);
   };
   const auto pick = [&]() -> cudaError_t {
-    using std::integral_constant;
+    constexpr std::integral_constant<int, 1> one{};
+    constexpr std::integral_constant<int, 2> two{};
+    constexpr std::integral_constant<int, MOST> most{};
     if (same_cut(x, y, T_)) {
       if (T_ <= c.num_sms && group_threads<T, 1>(H, even) != 0)
-        return go(integral_constant<int, 1>{});  // one row a CTA: spread it wide
+        return go(one, one);  // one row a CTA: spread it wide
       if constexpr (sizeof(T) == 2) {
         if (even && H % VN<T> == 0 && H > 512 && H <= 16384)
-          return H <= 1024 ? go(integral_constant<int, 4>{}) : go(integral_constant<int, 8>{});
+          return H <= 1024 ? go(std::integral_constant<int, 4>{}, one)
+                           : go(std::integral_constant<int, 8>{}, one);
       }
-      if (group_threads<T, MOST>(H, even) != 0) return go(integral_constant<int, MOST>{});
+      const int GT = group_threads<T, MOST>(H, even);
+      if (GT > 32) return go(most, two);
+      if (GT != 0) return go(most, one);
     }
     return launch_k(c.stream, norm_fwd_loop_kernel<T, P>, dim3(std::min(T_, c.num_sms * 8)),
                     dim3(256), 0, x, y, T_, H, w, b, s->eps, mean, rstd);
@@ -775,15 +843,23 @@ struct BwdArgs {
   float* part;
 };
 
-template <typename T, int NU>
+template <typename T, int NU, int ROWS>
 static cudaError_t bwd_launch(const Ctx& c, const BwdArgs<T>& a, int* n_part) {
   const NormGrid n = norm_grid(group_threads<T, NU>(a.H, even_rows(a.x, a.T_)), a.T_, c.num_sms);
   const int nt = n.GT * n.groups;
-  size_t smem =
-      static_cast<size_t>(norm_bwd_stages<NU>) * (a.add.p != nullptr ? 3 : 2) * NU * 16 * nt;
+  size_t smem = static_cast<size_t>(ROWS) * NU * 16 * nt *
+                (a.add.p != nullptr ? 3 * norm_bwd_steps<NU, true, ROWS>
+                                    : 2 * norm_bwd_steps<NU, false, ROWS>);
   if (n.groups > 1) smem = std::max(smem, sizeof(float) * 2 * n.groups * a.H);
-  auto* kern = even_rows(a.x, a.T_) && a.H % VN<T> == 0 ? norm_bwd_kernel<T, NU, true>
-                                                        : norm_bwd_kernel<T, NU, false>;
+  const bool even = even_rows(a.x, a.T_) && a.H % VN<T> == 0;
+  const Cut cut = !even ? ANY : NU <= 2 && a.H == n.GT * NU * VN<T> ? FULL : EVEN;
+  auto* kern = a.add.p != nullptr
+                   ? (cut == ANY    ? norm_bwd_kernel<T, NU, ANY, true, ROWS>
+                      : cut == EVEN ? norm_bwd_kernel<T, NU, EVEN, true, ROWS>
+                                    : norm_bwd_kernel<T, NU, FULL, true, ROWS>)
+                   : (cut == ANY    ? norm_bwd_kernel<T, NU, ANY, false, ROWS>
+                      : cut == EVEN ? norm_bwd_kernel<T, NU, EVEN, false, ROWS>
+                                    : norm_bwd_kernel<T, NU, FULL, false, ROWS>);
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
   *n_part = n.ctas;
@@ -816,12 +892,20 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
   if (same_cut(a.dy, a.x, T_) && same_cut(a.add, a.x, T_) && same_cut(a.dx, a.x, T_) &&
       group_threads<T, MOST>(H, even) != 0) {
     prof_begin(c, K_NORM_BWD);
-    if (T_ <= c.num_sms && group_threads<T, 1>(H, even) != 0)
-      e = bwd_launch<T, 1>(c, a, &n);
-    else if (MOST == 4 && group_threads<T, 2>(H, even) != 0)
-      e = bwd_launch<T, 2>(c, a, &n);
-    else
-      e = bwd_launch<T, MOST>(c, a, &n);
+    const auto pick = [&]() -> cudaError_t {
+      if (T_ <= c.num_sms && group_threads<T, 1>(H, even) != 0) return bwd_launch<T, 1, 1>(c, a, &n);
+      if constexpr (sizeof(T) == 2) {
+        // 16 bits: two rows a barrier where more than two warps share a row (8191 x 4096
+        // 43.8 -> 40.2 us, 20011 x 1111 47.5 -> 41.0 us; 30000 x 1000, two warps a row, 44.5
+        // -> 46.3 us)
+        return group_threads<T, 2>(H, even) > 64 ? bwd_launch<T, 2, 2>(c, a, &n)
+                                                 : bwd_launch<T, 2, 1>(c, a, &n);
+      } else {
+        return group_threads<T, 2>(H, even) != 0 ? bwd_launch<T, 2, 1>(c, a, &n)
+                                                 : bwd_launch<T, 4, 1>(c, a, &n);
+      }
+    };
+    e = pick();
     prof_end(c, K_NORM_BWD);
     if (e != cudaSuccess) return MM_MOE_ECUDA;
   } else {
