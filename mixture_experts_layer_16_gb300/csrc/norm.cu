@@ -392,7 +392,7 @@ template <typename T, int NU, Cut CUT, bool ADD, int ROWS>
 __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
     Rows<const T> dy, Rows<const T> x, Rows<const T> add, Rows<T> dx, const void* __restrict__ w,
     bool w32, const float* __restrict__ mean, const float* __restrict__ rstd, int T_, int H, int GT,
-    float* __restrict__ part) {
+    float* __restrict__ part, void* __restrict__ dweight, void* __restrict__ dbias) {
   constexpr int U = VN<T>, C2 = NU * U / 2, S = norm_bwd_steps<NU, ADD, ROWS>;
   constexpr int ARRAYS = ADD ? 3 : 2;
   extern __shared__ __align__(16) unsigned char ring_bytes[];
@@ -543,11 +543,24 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
   }
   async_wait<0>();
 
-  // the groups' column sums, added in order
+  // the groups' column sums, added in order: the CTA's partial ones, or from the only CTA
+  // the gradients themselves
   float* const p0 = part + static_cast<int64_t>(blockIdx.x) * 2 * H;
+  const auto put = [&](int which, int c, float v) {
+    if (gridDim.x > 1) {
+      p0[which * H + c] = v;
+    } else {
+      void* const o = which == 0 ? dweight : dbias;
+      if (o == nullptr) return;
+      if (w32)
+        static_cast<float*>(o)[c] = v;
+      else
+        static_cast<T*>(o)[c] = from_f32<T>(v);
+    }
+  };
   if (p.groups == 1) {
-    p.each(dw, [&](int c, float v) { p0[c] = v; });
-    p.each(db, [&](int c, float v) { p0[H + c] = v; });
+    p.each(dw, [&](int c, float v) { put(0, c, v); });
+    p.each(db, [&](int c, float v) { put(1, c, v); });
     return;
   }
   // Groups may cut their rows differently, so the sums meet by column.
@@ -575,7 +588,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
     float v = sj[i];
 #pragma unroll 4
     for (int k = 1; k < p.groups; ++k) v += sj[2 * k * H + i];
-    p0[i] = v;
+    put(i >= H, i < H ? i : i - H, v);
   }
 }
 
@@ -841,11 +854,20 @@ struct BwdArgs {
   const float *mean, *rstd;
   int T_, H;
   float* part;
+  void *dw, *db;
 };
+
+// So few rows that a single CTA's groups hold them in two rounds (rows of differing cuts: in
+// one, see Place): nothing is left to join after it.
+static bool one_cta(int GT, int T, bool even) {
+  return T <= (even ? 2 : 1) * (NORM_THREADS / GT);
+}
 
 template <typename T, int NU, int ROWS>
 static cudaError_t bwd_launch(const Ctx& c, const BwdArgs<T>& a, int* n_part) {
-  const NormGrid n = norm_grid(group_threads<T, NU>(a.H, even_rows(a.x, a.T_)), a.T_, c.num_sms);
+  const int GT = group_threads<T, NU>(a.H, even_rows(a.x, a.T_));
+  NormGrid n = norm_grid(GT, a.T_, c.num_sms);
+  if (one_cta(GT, a.T_, even_rows(a.x, a.T_))) n = NormGrid{GT, NORM_THREADS / GT, 1};
   const int nt = n.GT * n.groups;
   size_t smem = static_cast<size_t>(ROWS) * NU * 16 * nt *
                 (a.add.p != nullptr ? 3 * norm_bwd_steps<NU, true, ROWS>
@@ -864,7 +886,7 @@ static cudaError_t bwd_launch(const Ctx& c, const BwdArgs<T>& a, int* n_part) {
   if (e != cudaSuccess) return e;
   *n_part = n.ctas;
   return launch_k(c.stream, kern, dim3(n.ctas), dim3(nt), smem, a.dy, a.x, a.add,
-                  a.dx, a.w, a.w32, a.mean, a.rstd, a.T_, a.H, n.GT, a.part);
+                  a.dx, a.w, a.w32, a.mean, a.rstd, a.T_, a.H, n.GT, a.part, a.dw, a.db);
 }
 
 template <typename T, typename P>
@@ -884,7 +906,9 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
                      rstd,
                      T_,
                      H,
-                     part};
+                     part,
+                     dw,
+                     db};
   constexpr int MOST = 16 / VN<T>;
   const bool even = even_rows(a.x, T_);
   cudaError_t e;
@@ -893,7 +917,10 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
       group_threads<T, MOST>(H, even) != 0) {
     prof_begin(c, K_NORM_BWD);
     const auto pick = [&]() -> cudaError_t {
-      if (T_ <= c.num_sms && group_threads<T, 1>(H, even) != 0) return bwd_launch<T, 1, 1>(c, a, &n);
+      constexpr int WIDE = sizeof(T) == 2 ? 2 : 4;
+      if (T_ <= c.num_sms && !one_cta(group_threads<T, WIDE>(H, even), T_, even) &&
+          group_threads<T, 1>(H, even) != 0)
+        return bwd_launch<T, 1, 1>(c, a, &n);
       if constexpr (sizeof(T) == 2) {
         // 16 bits: two rows a barrier where more than two warps share a row (8191 x 4096
         // 43.8 -> 40.2 us, 20011 x 1111 47.5 -> 41.0 us; 30000 x 1000, two warps a row, 44.5
@@ -908,6 +935,7 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
     e = pick();
     prof_end(c, K_NORM_BWD);
     if (e != cudaSuccess) return MM_MOE_ECUDA;
+    if (n == 1) return MM_MOE_OK;  // (the only CTA has written them)
   } else {
     prof_begin(c, K_NORM_BWD);
     e = launch_k(c.stream, norm_dx_loop_kernel<T, P>, dim3(std::min(T_, c.num_sms * 8)), dim3(256),
