@@ -124,7 +124,8 @@ class MoEBalanceLoss:
     balance and the z loss; counts [sequences, E] int32).  seq_offsets [sequences + 1]
     int32 (ascending, on the device) splits the tokens; a token whose mask is 0 does not
     count.  self.seq_loss, self.tokens, self.lse hold each sequence's balance loss, its
-    counting tokens and each token's log-sum-exp."""
+    counting tokens and each token's log-sum-exp.  All of these are the handle's own
+    tensors, which the next forward overwrites."""
 
     def __init__(self, T: int, E: int, k: int, sequences: int = 1, dtype: str = "fp32",
                  device: Optional[torch.device] = None):

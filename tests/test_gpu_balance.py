@@ -140,6 +140,24 @@ def test_balance_large_and_masked_logits():
     assert not d[7].any() and float(h.lse[7]) == 0.0 and not d[:, 5].any()
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_balance_rows_of_the_lowest_value(dtype):
+    """A row masked throughout with its type's lowest value is an even distribution."""
+    c = case(40, 24, 3, 2, dtype=dtype)
+    c["logits"][5] = torch.finfo(DT[dtype]).min
+    c["logits"][6, 2:] = torch.finfo(DT[dtype]).min
+    h, losses, counts, d = run(c, dl=(1.0, 0.0))
+    f = ot.balance_forward(f64(c["logits"]), c["idx"].cpu().numpy(), 2, c["off"].cpu().numpy())
+    assert np.array_equal(counts.cpu().numpy(), f["counts"]) and int(h.tokens.sum()) == 40
+    assert abs(float(losses[0]) - f["losses"][0]) <= 1420 * E32 * f["losses"][0]
+    assert abs(float(h.lse[5]) - f["lse"][5]) <= 4 * E32 * abs(f["lse"][5])
+    want = ot.balance_backward(f64(c["logits"]), c["idx"].cpu().numpy(), (1.0, 0.0), 2,
+                               c["off"].cpu().numpy())
+    # the terms' size: p (c + <p, c>) <= 2 max c = 2 E counts / (k n^2 S)
+    cmax = 2 * 24 * f["counts"].max() / (3 * max(f["tokens"].min(), 1) ** 2)
+    assert np.abs(f64(d) - want).max() <= 100 * E32 * cmax + U[dtype] * np.abs(want).max()
+
+
 def test_balance_nothing_counts():
     for n_seq in (1, 4):
         c = case(50, 8, 2, n_seq)
