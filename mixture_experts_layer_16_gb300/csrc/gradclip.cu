@@ -15,8 +15,8 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "dtype.cuh"
 #include "internal.h"
+#include "ops.cuh"
 
 namespace mmmoe {
 

@@ -147,15 +147,6 @@ enum KernelId {
   K_DENSE_TN,
   K_ROUTER_TOPK,
   K_ROUTER_DLOGITS,
-  K_NORM_FWD,
-  K_NORM_BWD,
-  K_NORM_BWD_FINISH,
-  K_BALANCE_FWD,
-  K_BALANCE_FINISH,
-  K_BALANCE_BWD,
-  K_GRAD_SQ,
-  K_GRAD_NORM,
-  K_GRAD_SCALE,
   K_COUNT
 };
 

@@ -14,8 +14,8 @@
 #include <algorithm>
 #include <cstdint>
 
-#include "dtype.cuh"
 #include "internal.h"
+#include "ops.cuh"
 
 namespace mmmoe {
 

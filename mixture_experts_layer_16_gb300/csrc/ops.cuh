@@ -1,6 +1,6 @@
-// dtype.cuh -- typed element access shared by the operators around the layer (norm.cu,
-// balance.cu, gradclip.cu): bf16, fp16 and fp32 in memory, fp32 in registers.  A value
-// is rounded (to nearest even) only where it is stored.
+// ops.cuh -- what the operators around the layer (norm.cu, balance.cu, gradclip.cu) share:
+// their kernel ids and typed element access, bf16, fp16 and fp32 in memory, fp32 in
+// registers.  A value is rounded (to nearest even) only where it is stored.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -9,9 +9,23 @@
 #include <atomic>
 #include <cstdint>
 
-#include "../../include/mm_moe.h"
+#include "internal.h"
 
 namespace mmmoe {
+
+// Kernel ids of these operators, after the layer's (per-kernel timing).
+enum OpKernelId {
+  K_NORM_FWD = K_COUNT,
+  K_NORM_BWD,
+  K_NORM_BWD_FINISH,
+  K_BALANCE_FWD,
+  K_BALANCE_FINISH,
+  K_BALANCE_BWD,
+  K_GRAD_SQ,
+  K_GRAD_NORM,
+  K_GRAD_SCALE,
+  K_ALL_COUNT
+};
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }

@@ -6,10 +6,11 @@
 #include <vector>
 
 #include "internal.h"
+#include "ops.cuh"
 
 namespace mmmoe {
 
-static const char* const kKernelNames[K_COUNT] = {
+static const char* const kKernelNames[K_ALL_COUNT] = {
     "route_count", "route_scan", "route_place", "permute_x", "gemm_gateup_swiglu",
     "gemm_down_weighted", "combine", "permute_dy", "gemm_dgrad_down_dswiglu",
     "gemm_dgrad_gateup", "unpermute_reduce", "gemm_wgrad_down", "gemm_wgrad_gateup", "gemm_wgrad",
@@ -30,8 +31,8 @@ struct Prof {
   size_t used = 0;
   cudaEvent_t pending = nullptr;
   std::vector<Rec> recs;
-  double total_ms[K_COUNT] = {};
-  int count[K_COUNT] = {};
+  double total_ms[K_ALL_COUNT] = {};
+  int count[K_ALL_COUNT] = {};
   cudaEvent_t take() {
     if (used == pool.size()) {
       cudaEvent_t e = nullptr;
@@ -72,7 +73,7 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_profile_start(void) {
   p.recs.clear();
   p.used = 0;
   p.pending = nullptr;
-  for (int i = 0; i < K_COUNT; ++i) {
+  for (int i = 0; i < K_ALL_COUNT; ++i) {
     p.total_ms[i] = 0.0;
     p.count[i] = 0;
   }
@@ -95,7 +96,7 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_profile_stop(float* total_ms, int* la
   }
   p.recs.clear();
   p.used = 0;
-  for (int i = 0; i < n && i < K_COUNT; ++i) {
+  for (int i = 0; i < n && i < K_ALL_COUNT; ++i) {
     if (total_ms) total_ms[i] = static_cast<float>(p.total_ms[i]);
     if (launches) launches[i] = p.count[i];
   }
@@ -103,7 +104,7 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_profile_stop(float* total_ms, int* la
 }
 
 extern "C" MM_MOE_API const char* mm_moe_kernel_name(int id) {
-  return (id >= 0 && id < K_COUNT) ? kKernelNames[id] : nullptr;
+  return (id >= 0 && id < K_ALL_COUNT) ? kKernelNames[id] : nullptr;
 }
 
-extern "C" MM_MOE_API int mm_moe_kernel_count(void) { return K_COUNT; }
+extern "C" MM_MOE_API int mm_moe_kernel_count(void) { return K_ALL_COUNT; }
