@@ -42,65 +42,81 @@ constexpr int BAL_WARPS = BAL_THREADS / 32;  // at most
 // holds -inf from the start.
 constexpr int BAL_STAGES = 3;
 
-template <typename T, int L, int NV>
+template <typename T, int L, int NV, bool VEC>
 struct Ring {
   static constexpr int QUAD = 4 * static_cast<int>(sizeof(T));
   static constexpr int KS = L >= 8 ? 1 : 8 / L;  // topk_idx entries per lane (k <= 8; else read directly)
   static constexpr int BYTES = BAL_STAGES * (NV * QUAD + KS * 4);  // per thread
-  unsigned char* quads;  // this thread's; a quad lies blockDim quads before the next
-  int* idx;
-  __device__ __forceinline__ void init(unsigned char* smem) {
-    quads = smem + threadIdx.x * QUAD;
-    idx = reinterpret_cast<int*>(smem + BAL_STAGES * NV * QUAD * blockDim.x) + threadIdx.x;
-  }
-  __device__ __forceinline__ T* quad(int st, int i) const {
-    return reinterpret_cast<T*>(quads + (st * NV + i) * (QUAD * blockDim.x));
-  }
-  __device__ __forceinline__ int& slot(int st, int j) const {
-    return idx[(st * KS + j) * blockDim.x];
-  }
-  template <int B>
-  __device__ __forceinline__ static void copy(void* dst, const void* src) {
-    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    if constexpr (B == 16)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-    else
-      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(B)
-                   : "memory");
-  }
-  // whether quad i of lane l holds expert 4 (l + i L) + j
-  __device__ __forceinline__ void blank(int l, int E) const {
+  // This thread's; its next one lies a quad (an int) of every thread further on, as a warp's
+  // quads come from memory.  (A thread's quads side by side, which takes fewer address
+  // instructions, cost 25% more time: the copies then scatter each line they bring.)
+  uint32_t quads, idx, unit, idx_unit;
+  int l, E, k;
+  __device__ __forceinline__ void init(unsigned char* smem, int l_, int E_, int k_) {
+    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    unit = blockDim.x * QUAD;
+    idx_unit = blockDim.x * 4;
+    quads = base + threadIdx.x * QUAD;
+    idx = base + BAL_STAGES * NV * unit + threadIdx.x * 4;
+    l = l_;
+    E = E_;
+    k = k_;
+    // what lies past the last expert
 #pragma unroll
     for (int st = 0; st < BAL_STAGES; ++st)
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (4 * (l + i * L) + j >= E) quad(st, i)[j] = from_f32<T>(-INFINITY);
+          if (expert(i) + j >= E) put(st, i, j, from_f32<T>(-INFINITY));
   }
-  // The row's quads (vec: whole and aligned).  16-bit rows that are not come by plain loads.
-  __device__ __forceinline__ void load(int st, const T* row, int l, int E, bool vec) const {
+  __device__ __forceinline__ int expert(int i) const { return 4 * (l + i * L); }
+  __device__ __forceinline__ uint32_t quad(int st, int i) const { return quads + (st * NV + i) * unit; }
+  __device__ __forceinline__ void put(int st, int i, int j, T v) const {
+    const uint32_t at = quad(st, i) + j * static_cast<int>(sizeof(T));
+    if constexpr (sizeof(T) == 4)
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+    else
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(*reinterpret_cast<const uint16_t*>(&v))
+                   : "memory");
+  }
+  template <int B>
+  __device__ __forceinline__ static void copy(uint32_t dst, const void* src) {
+    if constexpr (B == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(B)
+                   : "memory");
+  }
+  // A token's quads; p is its row from this lane's first expert on.  VEC: rows are whole
+  // quads on their boundaries; others come element by element, 16-bit ones by plain loads.
+  __device__ __forceinline__ void load(int st, const T* p) const {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e0 = 4 * (l + i * L);
-      if (vec) {
-        if (e0 < E) copy<QUAD>(quad(st, i), row + e0);
+      if constexpr (VEC) {
+        if (expert(i) < E) copy<QUAD>(quad(st, i), p + 4 * i * L);
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (e0 + j < E) {
+          if (expert(i) + j < E) {
             if constexpr (sizeof(T) == 4)
-              copy<4>(quad(st, i) + j, row + e0 + j);
+              copy<4>(quad(st, i) + 4 * j, p + 4 * i * L + j);
             else
-              quad(st, i)[j] = row[e0 + j];
+              put(st, i, j, p[4 * i * L + j]);
           }
       }
     }
   }
-  __device__ __forceinline__ void load_idx(int st, const int32_t* row, int l, int k) const {
+  // and of topk_idx; p is the row from this lane's first slot on
+  __device__ __forceinline__ void load_idx(int st, const int32_t* p) const {
 #pragma unroll
     for (int j = 0; j < KS; ++j)
-      if (l + j * L < k) copy<4>(&slot(st, j), row + l + j * L);
+      if (l + j * L < k) copy<4>(idx + (st * KS + j) * idx_unit, p + j * L);
+  }
+  __device__ __forceinline__ int slot(int st, int j) const {
+    int e;
+    asm volatile("ld.shared.s32 %0, [%1];" : "=r"(e) : "r"(idx + (st * KS + j) * idx_unit) : "memory");
+    return e;
   }
   __device__ __forceinline__ static void commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -115,11 +131,16 @@ struct Ring {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if constexpr (sizeof(T) == 4) {
-        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(quad(st, i));
-        v[2 * i] = q.x;
-        v[2 * i + 1] = q.y;
+        asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];"
+                     : "=l"(v[2 * i]), "=l"(v[2 * i + 1])
+                     : "r"(quad(st, i))
+                     : "memory");
       } else {
-        const uint2 q = *reinterpret_cast<const uint2*>(quad(st, i));
+        uint2 q;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                     : "=r"(q.x), "=r"(q.y)
+                     : "r"(quad(st, i))
+                     : "memory");
         const T* h = reinterpret_cast<const T*>(&q);
         v[2 * i] = f2_make(to_f32(h[0]), to_f32(h[1]));
         v[2 * i + 1] = f2_make(to_f32(h[2]), to_f32(h[3]));
@@ -128,38 +149,35 @@ struct Ring {
   }
 };
 
-// Mask bytes of a group's next L tokens, one a lane, read once for all of them.
+// Mask bytes of a group's next L tokens, one a lane, read once for all of them.  p is the
+// group's token of round `it`, of which `left` rounds' tokens remain.
 template <int L>
 struct MaskAhead {
   uint32_t mine = 1;
-  __device__ __forceinline__ bool get(const uint8_t* mask, int64_t t, int64_t end, int stride, int l,
-                                      int it) {
-    if (mask == nullptr) return true;
-    if (it % L == 0) {
-      const int64_t mt = t + static_cast<int64_t>(l) * stride;
-      mine = mt < end ? __ldg(mask + mt) : 0;
-    }
+  __device__ __forceinline__ bool get(const uint8_t* p, int stride, int l, int it, int left) {
+    if (it % L == 0) mine = l < left ? __ldg(p + static_cast<int64_t>(l) * stride) : 0;
     return __shfl_sync(0xffffffffu, mine, it % L, L) != 0;
   }
 };
 
-template <typename T>
-__device__ __forceinline__ void store4(T* row, int e0, int E, bool vec, const float (&v)[4]) {
-  if (vec) {
-    if (e0 >= E) return;
+// Four values to o, where j < n of them exist (VEC: all or none).
+template <bool VEC, typename T>
+__device__ __forceinline__ void store4(T* o, int n, const float (&v)[4]) {
+  if constexpr (VEC) {
+    if (n <= 0) return;
     if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(row + e0) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
       uint2 q;
       T* h = reinterpret_cast<T*>(&q);
 #pragma unroll
       for (int i = 0; i < 4; ++i) h[i] = from_f32<T>(v[i]);
-      *reinterpret_cast<uint2*>(row + e0) = q;
+      *reinterpret_cast<uint2*>(o) = q;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (e0 + i < E) row[e0 + i] = from_f32<T>(v[i]);
+      if (i < n) o[i] = from_f32<T>(v[i]);
   }
 }
 
@@ -202,6 +220,12 @@ __device__ __forceinline__ float pow2(float x) {
   else
     asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// ln x for x >= 1 (a softmax's sum), to 2^-22
+__device__ __forceinline__ float ln_sum(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r * 0.69314718055994530942f;
 }
 __device__ __forceinline__ float reciprocal(float x) {
   float r;
@@ -322,12 +346,12 @@ struct BalParts {
   int* cta_n;     // [.., 2]: tokens, sequences with a token
 };
 
-template <typename T, int L, int NV>
+template <typename T, int L, int NV, bool VEC>
 __global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_fwd_kernel(
     const T* __restrict__ logits, const int32_t* __restrict__ topk_idx,
     const int32_t* __restrict__ off, const uint8_t* __restrict__ mask, int64_t T_, int E, int k,
-    int G, int chunk, bool vec, float* __restrict__ lse_out, BalParts parts) {
-  using R = Ring<T, L, NV>;
+    int G, int chunk, float* __restrict__ lse_out, BalParts parts) {
+  using R = Ring<T, L, NV, VEC>;
   const int nt = blockDim.x, warps = nt / 32;
   extern __shared__ __align__(16) unsigned char smem[];
   float* s_p = reinterpret_cast<float*>(smem + R::BYTES * nt);  // [warps][E]
@@ -344,8 +368,7 @@ __global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_fwd_kern
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * chunk;
   const int64_t t1 = min(T_, t0 + chunk);
   R ring;
-  ring.init(smem);
-  ring.blank(l, E);
+  ring.init(smem, l, E, k);
   if (blockIdx.x == 0 && tid == 0) *parts.arrived = 0;
   for (int e = tid; e < E; e += nt) s_cnt[e] = 0;
   __syncthreads();
@@ -360,22 +383,36 @@ __global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_fwd_kern
     float z = 0.f;
     int n = 0;
     MaskAhead<L> ahead;
-    const int rounds = static_cast<int>((w.b - w.a + GROUPS - 1) / GROUPS);
-    int64_t t = w.a + grp, tn = t;
+    // rounds of the CTA, and those in which this group has a token
+    const int len = static_cast<int>(w.b - w.a), rounds = (len + GROUPS - 1) / GROUPS;
+    const int mine = grp < len ? (len - 1 - grp) / GROUPS + 1 : 0;
+    const int64_t first = w.a + grp;
+    const T* row = logits + first * E + 4 * l;   // of the token to copy next
+    const int32_t* idx = topk_idx + first * k + l;
+    const int64_t row_step = static_cast<int64_t>(GROUPS) * E, idx_step = static_cast<int64_t>(GROUPS) * k;
+    int left = mine;
     const auto issue = [&](int st) {
-      if (tn < w.b) {  // (a masked row is read like any other: no load waits for another)
-        ring.load(st, logits + tn * E, l, E, vec);
-        ring.load_idx(st, topk_idx + tn * k, l, k);
+      if (left > 0) {  // (a masked row is read like any other: no load waits for another)
+        ring.load(st, row);
+        ring.load_idx(st, idx);
       }
       R::commit();
-      tn += GROUPS;
+      --left;
+      row += row_step;
+      idx += idx_step;
     };
 #pragma unroll
     for (int i = 0; i < BAL_STAGES - 1; ++i) issue(i);
+    float* lse_at = lse_out + first;
+    const uint8_t* mask_at = mask != nullptr ? mask + first : nullptr;
     int st = 0;
-    for (int it = 0; it < rounds; ++it, t += GROUPS) {
+    for (int it = 0; it < rounds; ++it) {
       issue(st == 0 ? BAL_STAGES - 1 : st - 1);
-      bool on = ahead.get(mask, t, w.b, GROUPS, l, it) && t < w.b;
+      bool on = it < mine;
+      if (mask != nullptr) {
+        on = ahead.get(mask_at, GROUPS, l, it, mine - it) && on;
+        mask_at += GROUPS;
+      }
       R::wait();
       f2 v[2 * NV];
       ring.get(st, v);
@@ -391,19 +428,23 @@ __global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_fwd_kern
 #pragma unroll
         for (int j = 0; j < R::KS; ++j) {
           const int e = l + j * L < k ? ring.slot(st, j) : -1;
-          if (e >= 0 && e < E) atomicAdd(s_cnt + e, 1);
+          if (static_cast<uint32_t>(e) < static_cast<uint32_t>(E)) atomicAdd(s_cnt + e, 1);
         }
-        for (int j = l + R::KS * L; j < k; j += L) {
-          const int e = __ldg(topk_idx + t * k + j);
-          if (e >= 0 && e < E) atomicAdd(s_cnt + e, 1);
+        if (k > R::KS * L) {
+          const int32_t* rest = topk_idx + (first + static_cast<int64_t>(it) * GROUPS) * k;
+          for (int j = l + R::KS * L; j < k; j += L) {
+            const int e = __ldg(rest + j);
+            if (static_cast<uint32_t>(e) < static_cast<uint32_t>(E)) atomicAdd(s_cnt + e, 1);
+          }
         }
       }
-      if (l == 0 && t < w.b) {
-        const float lse = on ? m + logf(sum) : 0.f;
-        lse_out[t] = lse;
+      if (l == 0 && it < mine) {
+        const float lse = on ? m + ln_sum(sum) : 0.f;
+        *lse_at = lse;
         z = fmaf(lse, lse, z);
         n += on ? 1 : 0;
       }
+      lse_at += GROUPS;
       st = st + 1 == BAL_STAGES ? 0 : st + 1;
     }
     R::drain();
@@ -711,14 +752,14 @@ __global__ void __launch_bounds__(JOIN_MANY_THREADS) balance_join_many_kernel(
   all.finish(false, parts, losses);
 }
 
-template <typename T, int L, int NV>
+template <typename T, int L, int NV, bool VEC>
 __global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_bwd_kernel(
     const T* __restrict__ logits, const int32_t* __restrict__ off,
     const uint8_t* __restrict__ mask, const int32_t* __restrict__ counts,
     const int32_t* __restrict__ tokens, const float* __restrict__ stats,
-    const float* __restrict__ dlosses, int64_t T_, int E, int k, int G, int chunk, bool vec,
+    const float* __restrict__ dlosses, int64_t T_, int E, int k, int G, int chunk,
     T* __restrict__ dlogits) {
-  using R = Ring<T, L, NV>;
+  using R = Ring<T, L, NV, VEC>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int s_win[SeqWalk::WINDOW + 1];
   pdl_wait();
@@ -730,8 +771,7 @@ __global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_bwd_kern
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * chunk;
   const int64_t t1 = min(T_, t0 + chunk);
   R ring;
-  ring.init(smem);
-  ring.blank(l, E);
+  ring.init(smem, l, E, 0);
   const float live = __ldg(stats), n_all = __ldg(stats + 1);
   const float db = __ldg(dlosses);
   const float dz = n_all > 0.f ? __ldg(dlosses + 1) * 2.f / n_all : 0.f;
@@ -739,15 +779,21 @@ __global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_bwd_kern
   w.start(off, s_win, G, t0, t1);
   while (w.next()) {
     MaskAhead<L> ahead;
-    const int rounds = static_cast<int>((w.b - w.a + GROUPS - 1) / GROUPS);
-    int64_t t = w.a + grp, tn = t;
+    const int len = static_cast<int>(w.b - w.a), rounds = (len + GROUPS - 1) / GROUPS;
+    const int mine = grp < len ? (len - 1 - grp) / GROUPS + 1 : 0;
+    const int64_t first = w.a + grp, row_step = static_cast<int64_t>(GROUPS) * E;
+    const T* row = logits + first * E + 4 * l;
+    int left = mine;
     const auto issue = [&](int st) {
-      if (tn < w.b) ring.load(st, logits + tn * E, l, E, vec);
+      if (left > 0) ring.load(st, row);
       R::commit();
-      tn += GROUPS;
+      --left;
+      row += row_step;
     };
 #pragma unroll
     for (int i = 0; i < BAL_STAGES - 1; ++i) issue(i);
+    T* out = dlogits + first * E + 4 * l;
+    const uint8_t* mask_at = mask != nullptr ? mask + first : nullptr;
     f2 c[2 * NV];
     const float ns = w.s >= 0 ? static_cast<float>(__ldg(tokens + w.s)) : 0.f;
     const float scale =
@@ -763,9 +809,13 @@ __global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_bwd_kern
       c[i] = f2_make(coef(e), coef(e + 1));
     }
     int st = 0;
-    for (int it = 0; it < rounds; ++it, t += GROUPS) {
+    for (int it = 0; it < rounds; ++it, out += row_step) {
       issue(st == 0 ? BAL_STAGES - 1 : st - 1);
-      bool on = ahead.get(mask, t, w.b, GROUPS, l, it) && t < w.b && ns > 0.f;
+      bool on = it < mine && ns > 0.f;
+      if (mask != nullptr) {
+        on = ahead.get(mask_at, GROUPS, l, it, mine - it) && on;
+        mask_at += GROUPS;
+      }
       R::wait();
       f2 v[2 * NV];
       ring.get(st, v);
@@ -778,9 +828,9 @@ __global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_bwd_kern
       for (int i = 0; i < 2 * NV; ++i) dot2 = f2_fma(v[i], c[i], dot2);
       const float dot = lanes_sum<L>(f2_sum(dot2));
       const float inv = reciprocal(sum);
-      const float shift = dz * (m + logf(sum)) - dot * inv;
+      const float shift = dz * (m + ln_sum(sum)) - dot * inv;
       const f2 inv2 = f2_make(inv, inv), shift2 = f2_make(shift, shift);
-      if (t < w.b) {
+      if (it < mine) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           float d[4] = {};
@@ -788,7 +838,7 @@ __global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_bwd_kern
             f2_split(f2_mul(f2_mul(v[2 * i], inv2), f2_add(c[2 * i], shift2)), d[0], d[1]);
             f2_split(f2_mul(f2_mul(v[2 * i + 1], inv2), f2_add(c[2 * i + 1], shift2)), d[2], d[3]);
           }
-          store4(dlogits + t * E, 4 * (l + i * L), E, vec, d);
+          store4<VEC>(out + 4 * i * L, E - 4 * (l + i * L), d);
         }
       }
       st = st + 1 == BAL_STAGES ? 0 : st + 1;
@@ -910,14 +960,14 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_balance_forward(
     const T* lg = static_cast<const T*>(logits);
     return with_lanes(E, [&](auto l, auto nv) {
       constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
-      auto* kern = balance_fwd_kernel<T, L, NV>;
-      const size_t smem = static_cast<size_t>(Ring<T, L, NV>::BYTES) * b.threads +
+      auto* kern = bal_vec<T>(lg, E) ? balance_fwd_kernel<T, L, NV, true>
+                                     : balance_fwd_kernel<T, L, NV, false>;
+      const size_t smem = static_cast<size_t>(Ring<T, L, NV, true>::BYTES) * b.threads +
                           static_cast<size_t>(b.threads / 32 + 1) * E * 4;
       const cudaError_t r = allow_smem(kern, smem);
       if (r != cudaSuccess) return r;
       return launch_k(c.stream, kern, dim3(b.nb), dim3(b.threads), smem, lg, topk_idx,
-                      seq_offsets, mask, shape->T, E, k, G, b.chunk, bal_vec<T>(lg, E), lse,
-                      parts);
+                      seq_offsets, mask, shape->T, E, k, G, b.chunk, lse, parts);
     });
   });
   prof_end(c, K_BALANCE_FWD);
@@ -960,13 +1010,13 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_balance_backward(
     T* out = static_cast<T*>(dlogits);
     return with_lanes(E, [&](auto l, auto nv) {
       constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
-      auto* kern = balance_bwd_kernel<T, L, NV>;
-      const size_t smem = static_cast<size_t>(Ring<T, L, NV>::BYTES) * b.threads;
+      auto* kern = bal_vec<T>(lg, E) && bal_vec<T>(out, E) ? balance_bwd_kernel<T, L, NV, true>
+                                                           : balance_bwd_kernel<T, L, NV, false>;
+      const size_t smem = static_cast<size_t>(Ring<T, L, NV, true>::BYTES) * b.threads;
       const cudaError_t r = allow_smem(kern, smem);
       if (r != cudaSuccess) return r;
       return launch_k(c.stream, kern, dim3(b.nb), dim3(b.threads), smem, lg, seq_offsets, mask,
-                      counts, tokens, stats, dlosses, shape->T, E, k, G, b.chunk,
-                      bal_vec<T>(lg, E) && bal_vec<T>(out, E), out);
+                      counts, tokens, stats, dlosses, shape->T, E, k, G, b.chunk, out);
     });
   });
   prof_end(c, K_BALANCE_BWD);
