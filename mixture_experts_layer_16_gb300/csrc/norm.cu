@@ -593,33 +593,86 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
 }
 
 // --------------------------------------------------------------- looped, any width
+// For rows that no CTA holds in its ring, and operands whose rows are cut differently.  VEC:
+// every row is whole 16-byte units and the parameters lie on 16-byte boundaries; else
+// element by element.
+constexpr int LOOP_THREADS = 512;
+template <typename T, bool VEC>
+constexpr int loop_unit = VEC ? VN<T> : 1;
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_unit(const T* p, int u, float (&f)[loop_unit<T, VEC>]) {
+  if constexpr (VEC)
+    unpack(reinterpret_cast<const uint4*>(p)[u], f, p);
+  else
+    f[0] = to_f32(p[u]);
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_unit(T* p, int u, const float (&f)[loop_unit<T, VEC>]) {
+  if constexpr (VEC)
+    reinterpret_cast<uint4*>(p)[u] = pack(f, p);
+  else
+    p[u] = from_f32<T>(f[0]);
+}
+// U parameters from column c on
+template <typename P, int U>
+__device__ __forceinline__ void load_params(const P* p, int c, float (&f)[U]) {
+  if constexpr (U == 1) {
+    f[0] = to_f32(p[c]);
+  } else {
+    constexpr int N = VN<P> < U ? VN<P> : U;  // (fp32 parameters of 16-bit rows: two loads)
+#pragma unroll
+    for (int i = 0; i < U; i += N) {
+      float t[VN<P>];
+      unpack(__ldg(reinterpret_cast<const uint4*>(p + c + i)), t, p);
+#pragma unroll
+      for (int j = 0; j < N; ++j) f[i + j] = t[j];
+    }
+  }
+}
+
 // One CTA per row; the row is read three times (sum, centred squares, output), the
 // second and third time from L1/L2.
-template <typename T, typename P>
-__global__ void __launch_bounds__(256) norm_fwd_loop_kernel(Rows<const T> x, Rows<T> y, int T_,
-                                                            int H, const P* __restrict__ w,
-                                                            const P* __restrict__ b, float eps,
-                                                            float* __restrict__ mean,
-                                                            float* __restrict__ rstd) {
-  __shared__ float s[8];
+template <typename T, typename P, bool VEC>
+__global__ void __launch_bounds__(LOOP_THREADS) norm_fwd_loop_kernel(
+    Rows<const T> x, Rows<T> y, int T_, int H, const P* __restrict__ w, const P* __restrict__ b,
+    float eps, float* __restrict__ mean, float* __restrict__ rstd) {
+  constexpr int U = loop_unit<T, VEC>;
+  __shared__ float s[LOOP_THREADS / 32];
   pdl_wait();
   pdl_trigger();
   const float inv = 1.f / static_cast<float>(H);
+  const int units = H / U;
   for (int64_t t = blockIdx.x; t < T_; t += gridDim.x) {
     const T* xr = x.row(t);
     float a = 0.f;
-    for (int i = threadIdx.x; i < H; i += 256) a += to_f32(xr[i]);
+#pragma unroll 4
+    for (int u = threadIdx.x; u < units; u += LOOP_THREADS) {
+      float f[U];
+      load_unit<T, VEC>(xr, u, f);
+#pragma unroll
+      for (int k = 0; k < U; ++k) a += f[k];
+    }
     const float mu = block_sum(a, s) * inv;
     a = 0.f;
-    for (int i = threadIdx.x; i < H; i += 256) {
-      const float d = to_f32(xr[i]) - mu;
-      a = fmaf(d, d, a);
+#pragma unroll 4
+    for (int u = threadIdx.x; u < units; u += LOOP_THREADS) {
+      float f[U];
+      load_unit<T, VEC>(xr, u, f);
+#pragma unroll
+      for (int k = 0; k < U; ++k) a = fmaf(f[k] - mu, f[k] - mu, a);
     }
     const float r = rsqrtf(block_sum(a, s) * inv + eps);
     T* yr = y.row(t);
-    for (int i = threadIdx.x; i < H; i += 256) {
-      const float v = (to_f32(xr[i]) - mu) * r;
-      yr[i] = from_f32<T>(fmaf(v, to_f32(w[i]), b != nullptr ? to_f32(b[i]) : 0.f));
+#pragma unroll 2
+    for (int u = threadIdx.x; u < units; u += LOOP_THREADS) {
+      float f[U], wf[U], bf[U] = {};
+      load_unit<T, VEC>(xr, u, f);
+      load_params(w, u * U, wf);
+      if (b != nullptr) load_params(b, u * U, bf);
+#pragma unroll
+      for (int k = 0; k < U; ++k) f[k] = fmaf((f[k] - mu) * r, wf[k], bf[k]);
+      store_unit<T, VEC>(yr, u, f);
     }
     if (threadIdx.x == 0) {
       mean[t] = mu;
@@ -628,62 +681,85 @@ __global__ void __launch_bounds__(256) norm_fwd_loop_kernel(Rows<const T> x, Row
   }
 }
 
-template <typename T, typename P>
-__global__ void __launch_bounds__(256) norm_dx_loop_kernel(Rows<const T> dy, Rows<const T> x,
-                                                           const P* __restrict__ w,
-                                                           const float* __restrict__ mean,
-                                                           const float* __restrict__ rstd,
-                                                           Rows<const T> add, Rows<T> dx, int T_,
-                                                           int H) {
-  __shared__ float s[8];
+template <typename T, typename P, bool VEC>
+__global__ void __launch_bounds__(LOOP_THREADS) norm_dx_loop_kernel(
+    Rows<const T> dy, Rows<const T> x, const P* __restrict__ w, const float* __restrict__ mean,
+    const float* __restrict__ rstd, Rows<const T> add, Rows<T> dx, int T_, int H) {
+  constexpr int U = loop_unit<T, VEC>;
+  __shared__ float s[LOOP_THREADS / 32];
   pdl_wait();
   pdl_trigger();
   const float inv = 1.f / static_cast<float>(H);
+  const int units = H / U;
   for (int64_t t = blockIdx.x; t < T_; t += gridDim.x) {
     const T* xr = x.row(t);
     const T* gr = dy.row(t);
     const float mu = mean[t], r = rstd[t];
     float a = 0.f, c = 0.f;
-    for (int i = threadIdx.x; i < H; i += 256) {
-      const float g = to_f32(gr[i]) * to_f32(w[i]);
-      a += g;
-      c = fmaf(g, (to_f32(xr[i]) - mu) * r, c);
+#pragma unroll 2
+    for (int u = threadIdx.x; u < units; u += LOOP_THREADS) {
+      float fx[U], fg[U], wf[U];
+      load_unit<T, VEC>(xr, u, fx);
+      load_unit<T, VEC>(gr, u, fg);
+      load_params(w, u * U, wf);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        a = fmaf(fg[k], wf[k], a);
+        c = fmaf(fg[k] * wf[k], (fx[k] - mu) * r, c);
+      }
     }
     a = block_sum(a, s) * inv;
     c = block_sum(c, s) * inv;
     T* o = dx.row(t);
-    for (int i = threadIdx.x; i < H; i += 256) {
-      const float g = to_f32(gr[i]) * to_f32(w[i]);
-      const float xh = (to_f32(xr[i]) - mu) * r;
-      float d = (g - a - xh * c) * r;
-      if (add.p != nullptr) d += to_f32(add.row(t)[i]);
-      o[i] = from_f32<T>(d);
+#pragma unroll 2
+    for (int u = threadIdx.x; u < units; u += LOOP_THREADS) {
+      float fx[U], fg[U], wf[U], d[U] = {};
+      load_unit<T, VEC>(xr, u, fx);
+      load_unit<T, VEC>(gr, u, fg);
+      load_params(w, u * U, wf);
+      if (add.p != nullptr) load_unit<T, VEC>(add.row(t), u, d);
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        d[k] = fmaf(fg[k] * wf[k] - a - (fx[k] - mu) * r * c, r, d[k]);
+      store_unit<T, VEC>(o, u, d);
     }
   }
 }
 
-// Column sums of one range of rows per blockIdx.y: a thread owns a column.
+// Column sums of one range of rows per blockIdx.y: a thread owns a unit's columns.
 // part[(blockIdx.y * 2 + {0, 1}) * H + i] = {sum dy xh, sum dy} over the range.
-template <typename T>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) norm_cols_loop_kernel(Rows<const T> dy, Rows<const T> x,
                                                              const float* __restrict__ mean,
                                                              const float* __restrict__ rstd,
                                                              int T_, int H, int rows,
                                                              float* __restrict__ part) {
+  constexpr int U = loop_unit<T, VEC>;
   pdl_wait();
   pdl_trigger();
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= H) return;
+  const int u = blockIdx.x * 256 + threadIdx.x;
+  if (u >= H / U) return;
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * rows;
   const int64_t t1 = min(static_cast<int64_t>(T_), t0 + rows);
-  float a = 0.f, c = 0.f;
+  float a[U] = {}, c[U] = {};
+#pragma unroll 4
   for (int64_t t = t0; t < t1; ++t) {
-    const float g = to_f32(dy.row(t)[i]);
-    a = fmaf(g, (to_f32(x.row(t)[i]) - mean[t]) * rstd[t], a);
-    c += g;
+    float fx[U], fg[U];
+    load_unit<T, VEC>(x.row(t), u, fx);
+    load_unit<T, VEC>(dy.row(t), u, fg);
+    const float mu = __ldg(mean + t), r = __ldg(rstd + t);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      a[k] = fmaf(fg[k], (fx[k] - mu) * r, a[k]);
+      c[k] += fg[k];
+    }
   }
-  part[(static_cast<int64_t>(blockIdx.y) * 2) * H + i] = a;
-  part[(static_cast<int64_t>(blockIdx.y) * 2 + 1) * H + i] = c;
+  float* const p = part + static_cast<int64_t>(blockIdx.y) * 2 * H + u * U;
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    p[k] = a[k];
+    p[H + k] = c[k];
+  }
 }
 
 // dweight (blockIdx.y 0) / dbias (1) from n partial rows: 16 warps take every 16th row of
@@ -740,12 +816,14 @@ static bool vec_ok(const void* p, size_t a) {
   return p != nullptr && reinterpret_cast<uintptr_t>(p) % a == 0;
 }
 
+static bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
 // The cut of an operand's rows (see Place): the same for rows that start on a 16-byte
 // boundary and lie equally far apart modulo 16 bytes.
 template <typename A, typename B>
 static bool same_cut(const Rows<A>& a, const Rows<B>& b, int64_t rows) {
   if (a.p == nullptr) return true;
-  return reinterpret_cast<uintptr_t>(a.p) % 16 == 0 && reinterpret_cast<uintptr_t>(b.p) % 16 == 0 &&
+  return al16(a.p) && al16(b.p) &&
          (rows == 1 || (a.ld - b.ld) * sizeof(A) % 16 == 0);
 }
 
@@ -835,8 +913,12 @@ static mm_moe_status norm_forward(const Ctx& c, const mm_moe_norm_shape* s, cons
       if (GT > 32) return go(most, two);
       if (GT != 0) return go(most, one);
     }
-    return launch_k(c.stream, norm_fwd_loop_kernel<T, P>, dim3(std::min(T_, c.num_sms * 8)),
-                    dim3(256), 0, x, y, T_, H, w, b, s->eps, mean, rstd);
+    const bool vec = even && even_rows(y, T_) && H % VN<T> == 0 && al16(x.p) && al16(y.p) &&
+                     al16(w) && (b == nullptr || al16(b));
+    return launch_k(c.stream,
+                    vec ? norm_fwd_loop_kernel<T, P, true> : norm_fwd_loop_kernel<T, P, false>,
+                    dim3(std::min(T_, c.num_sms * 4)), dim3(LOOP_THREADS), 0, x, y, T_, H, w, b,
+                    s->eps, mean, rstd);
   };
   prof_begin(c, K_NORM_FWD);
   const cudaError_t e = pick();
@@ -937,17 +1019,23 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
     if (e != cudaSuccess) return MM_MOE_ECUDA;
     if (n == 1) return MM_MOE_OK;  // (the only CTA has written them)
   } else {
+    const bool vec = even && even_rows(a.dy, T_) && even_rows(a.dx, T_) && H % VN<T> == 0 &&
+                     al16(x) && al16(dy) && al16(dx) && al16(w) &&
+                     (add == nullptr || (al16(add) && even_rows(a.add, T_)));
     prof_begin(c, K_NORM_BWD);
-    e = launch_k(c.stream, norm_dx_loop_kernel<T, P>, dim3(std::min(T_, c.num_sms * 8)), dim3(256),
-                 0, a.dy, a.x, static_cast<const P*>(w), mean, rstd, a.add, a.dx, T_, H);
+    e = launch_k(c.stream,
+                 vec ? norm_dx_loop_kernel<T, P, true> : norm_dx_loop_kernel<T, P, false>,
+                 dim3(std::min(T_, c.num_sms * 4)), dim3(LOOP_THREADS), 0, a.dy, a.x,
+                 static_cast<const P*>(w), mean, rstd, a.add, a.dx, T_, H);
     prof_end(c, K_NORM_BWD);
     if (e != cudaSuccess) return MM_MOE_ECUDA;
-    const int want = std::min(norm_parts(T_), std::max(1, c.num_sms * 8 / ((H + 255) / 256)));
+    const int cols = (H / (vec ? VN<T> : 1) + 255) / 256;
+    const int want = std::min(norm_parts(T_), std::max(1, c.num_sms * 8 / cols));
     const int rows = (T_ + want - 1) / want;
     n = (T_ + rows - 1) / rows;
     prof_begin(c, K_NORM_BWD);
-    e = launch_k(c.stream, norm_cols_loop_kernel<T>, dim3((H + 255) / 256, n), dim3(256), 0, a.dy,
-                 a.x, mean, rstd, T_, H, rows, part);
+    e = launch_k(c.stream, vec ? norm_cols_loop_kernel<T, true> : norm_cols_loop_kernel<T, false>,
+                 dim3(cols, n), dim3(256), 0, a.dy, a.x, mean, rstd, T_, H, rows, part);
     prof_end(c, K_NORM_BWD);
     if (e != cudaSuccess) return MM_MOE_ECUDA;
   }
