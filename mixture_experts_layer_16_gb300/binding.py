@@ -302,17 +302,24 @@ def mm_moe_norm_workspace_size(shape: NormShape) -> int:
 
 def mm_moe_norm_forward(shape: NormShape, x, weight, bias, y, mean, rstd, stream=None) -> None:
     """x and y [T, H] with rows stride(0) elements apart."""
-    _check("mm_moe_norm_forward", lib().mm_moe_norm_forward(
-        ctypes.byref(shape), _ptr(x), x.stride(0), _ptr(weight), _ptr(bias), _ptr(y),
-        y.stride(0), _ptr(mean), _ptr(rstd), _stream(stream)))
+    st = lib().mm_moe_norm_forward(
+        shape, x.data_ptr(), x.stride(0), weight.data_ptr(), 0 if bias is None else bias.data_ptr(),
+        y.data_ptr(), y.stride(0), mean.data_ptr(), rstd.data_ptr(),
+        stream if type(stream) is int else _stream(stream))
+    if st:
+        _check("mm_moe_norm_forward", st)
 
 
 def mm_moe_norm_backward(shape: NormShape, dy, x, weight, mean, rstd, dx_add, dx, dweight, dbias,
                          workspace, stream=None) -> None:
-    _check("mm_moe_norm_backward", lib().mm_moe_norm_backward(
-        ctypes.byref(shape), _ptr(dy), dy.stride(0), _ptr(x), x.stride(0), _ptr(weight),
-        _ptr(mean), _ptr(rstd), _ptr(dx_add), 0 if dx_add is None else dx_add.stride(0),
-        _ptr(dx), dx.stride(0), _ptr(dweight), _ptr(dbias), _ptr(workspace), _stream(stream)))
+    st = lib().mm_moe_norm_backward(
+        shape, dy.data_ptr(), dy.stride(0), x.data_ptr(), x.stride(0), weight.data_ptr(),
+        mean.data_ptr(), rstd.data_ptr(), 0 if dx_add is None else dx_add.data_ptr(),
+        0 if dx_add is None else dx_add.stride(0), dx.data_ptr(), dx.stride(0),
+        dweight.data_ptr(), 0 if dbias is None else dbias.data_ptr(), workspace.data_ptr(),
+        stream if type(stream) is int else _stream(stream))
+    if st:
+        _check("mm_moe_norm_backward", st)
 
 
 def mm_moe_balance_workspace_size(shape: BalanceShape) -> int:

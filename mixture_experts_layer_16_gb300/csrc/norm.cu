@@ -865,7 +865,7 @@ static cudaError_t fwd_launch(const Ctx& c, Rows<const T> x, Rows<T> y, int T_, 
                               const P* b, float eps, float* mean, float* rstd) {
   const int GT = group_threads<T, NU>(H, even_rows(x, T_));
   constexpr int RING = norm_fwd_steps<NU, ROWS> * ROWS * NU * 16;  // bytes per thread
-  // the ring and shared parameters have to fit beside each other (H above 8192: one group)
+  // the ring and shared parameters have to fit beside each other
   const int fit = norm_params_shared<T, NU> ? (224 * 1024 - 8 * H) / (RING * GT) : NORM_THREADS;
   const NormGrid n = norm_grid(GT, T_, c.num_sms, fit);
   const int nt = n.GT * n.groups;
@@ -905,7 +905,7 @@ static mm_moe_status norm_forward(const Ctx& c, const mm_moe_norm_shape* s, cons
       if (T_ <= c.num_sms && group_threads<T, 1>(H, even) != 0)
         return go(one, one);  // one row a CTA: spread it wide
       if constexpr (sizeof(T) == 2) {
-        if (even && H % VN<T> == 0 && H > 512 && H <= 16384)
+        if (even && H % VN<T> == 0 && H > 512 && H <= 8192)
           return H <= 1024 ? go(std::integral_constant<int, 4>{}, one)
                            : go(std::integral_constant<int, 8>{}, one);
       }

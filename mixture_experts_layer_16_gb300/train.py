@@ -38,6 +38,15 @@ def _stream(stream, device: torch.device) -> int:
     return int(getattr(stream, "cuda_stream", stream))
 
 
+def _plain(t, shape: torch.Size, dtype, where: int) -> bool:
+    """A contiguous tensor of this shape and dtype on CUDA device `where` (-1: the CPU)."""
+    try:
+        return (t.dtype is dtype and t.shape == shape and t.get_device() == where
+                and t.is_contiguous())
+    except AttributeError:
+        return False
+
+
 def _need_rows(t, name: str, shape, dtype, device) -> None:
     """As _need, but the rows may lie apart (a slice of wider rows)."""
     if not isinstance(t, torch.Tensor):
@@ -73,22 +82,31 @@ class MoELayerNorm:
         self.rstd = torch.empty(T, dtype=torch.float32, device=self.device)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
         self._rows, self._cols = torch.Size((T, H)), torch.Size((H,))
+        self._where = -1 if self.device.index is None else self.device.index
+
+    def _check_rows(self, t, name):
+        if not _plain(t, self._rows, self.dtype, self._where):
+            _need_rows(t, name, self._rows, self.dtype, self.device)
+
+    def _check_param(self, t, name):
+        if not _plain(t, self._cols, self.param_dtype, self._where):
+            _need(t, name, self._cols, self.param_dtype, self.device)
 
     def _check_params(self, weight, bias, prefix=""):
-        _need(weight, prefix + "weight", self._cols, self.param_dtype, self.device)
+        self._check_param(weight, prefix + "weight")
         if self.bias:
-            _need(bias, prefix + "bias", self._cols, self.param_dtype, self.device)
+            self._check_param(bias, prefix + "bias")
         elif bias is not None:
             raise ValueError(f"{prefix}bias: this layer norm has none")
 
     def forward(self, x, weight, bias=None, y: Optional[torch.Tensor] = None,
                 stream=None) -> torch.Tensor:
-        _need_rows(x, "x", self._rows, self.dtype, self.device)
+        self._check_rows(x, "x")
         self._check_params(weight, bias)
         if y is None:
             y = torch.empty(self._rows, dtype=self.dtype, device=self.device)
         else:
-            _need_rows(y, "y", self._rows, self.dtype, self.device)
+            self._check_rows(y, "y")
         B.mm_moe_norm_forward(self.shape, x, weight, bias, y, self.mean, self.rstd,
                               _stream(stream, self.device))
         return y
@@ -98,17 +116,16 @@ class MoELayerNorm:
         """Gradients (dx, dweight, dbias) of the last forward, whose x and weight are given
         again (dbias None without a bias).  dx_add: a gradient that joins dx (the residual
         path's); dx may be written over it (out)."""
-        _need_rows(dy, "dy", self._rows, self.dtype, self.device)
-        _need_rows(x, "x", self._rows, self.dtype, self.device)
-        _need(weight, "weight", self._cols, self.param_dtype, self.device)
+        self._check_rows(dy, "dy")
+        self._check_rows(x, "x")
+        self._check_param(weight, "weight")
         if dx_add is not None:
-            _need_rows(dx_add, "dx_add", self._rows, self.dtype, self.device)
+            self._check_rows(dx_add, "dx_add")
         if out is None:
-            w = dict(dtype=self.param_dtype, device=self.device)
             out = (torch.empty(self._rows, dtype=self.dtype, device=self.device),
-                   torch.empty(self._cols, **w), torch.empty(self._cols, **w) if self.bias else None)
+                   torch.empty_like(weight), torch.empty_like(weight) if self.bias else None)
         else:
-            _need_rows(out[0], "dx", self._rows, self.dtype, self.device)
+            self._check_rows(out[0], "dx")
             self._check_params(out[1], out[2], "d")
         dx, dweight, dbias = out
         B.mm_moe_norm_backward(self.shape, dy, x, weight, self.mean, self.rstd, dx_add, dx,
