@@ -328,17 +328,25 @@ def mm_moe_balance_workspace_size(shape: BalanceShape) -> int:
 
 def mm_moe_balance_forward(shape: BalanceShape, logits, topk_idx, seq_offsets, mask, losses,
                            seq_loss, counts, tokens, lse, workspace, stream=None) -> None:
-    _check("mm_moe_balance_forward", lib().mm_moe_balance_forward(
-        ctypes.byref(shape), _ptr(logits), _ptr(topk_idx), _ptr(seq_offsets), _ptr(mask),
-        _ptr(losses), _ptr(seq_loss), _ptr(counts), _ptr(tokens), _ptr(lse), _ptr(workspace),
-        _stream(stream)))
+    st = lib().mm_moe_balance_forward(
+        shape, logits.data_ptr(), topk_idx.data_ptr(),
+        0 if seq_offsets is None else seq_offsets.data_ptr(),
+        0 if mask is None else mask.data_ptr(), losses.data_ptr(), seq_loss.data_ptr(),
+        counts.data_ptr(), tokens.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+        stream if type(stream) is int else _stream(stream))
+    if st:
+        _check("mm_moe_balance_forward", st)
 
 
 def mm_moe_balance_backward(shape: BalanceShape, logits, seq_offsets, mask, counts, tokens,
                             dlosses, dlogits, workspace, stream=None) -> None:
-    _check("mm_moe_balance_backward", lib().mm_moe_balance_backward(
-        ctypes.byref(shape), _ptr(logits), _ptr(seq_offsets), _ptr(mask), _ptr(counts),
-        _ptr(tokens), _ptr(dlosses), _ptr(dlogits), _ptr(workspace), _stream(stream)))
+    st = lib().mm_moe_balance_backward(
+        shape, logits.data_ptr(), 0 if seq_offsets is None else seq_offsets.data_ptr(),
+        0 if mask is None else mask.data_ptr(), counts.data_ptr(), tokens.data_ptr(),
+        dlosses.data_ptr(), dlogits.data_ptr(), workspace.data_ptr(),
+        stream if type(stream) is int else _stream(stream))
+    if st:
+        _check("mm_moe_balance_backward", st)
 
 
 def mm_moe_grad_workspace_size(n_tensors: int) -> int:

@@ -17,6 +17,7 @@ from .layer import _need
 
 TORCH_DTYPE = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 _CODE = {TORCH_DTYPE[n]: c for n, c in B.DTYPE.items()}
+_TWO = torch.Size((2,))
 
 
 def _device(device) -> torch.device:
@@ -158,23 +159,27 @@ class MoEBalanceLoss:
         self.tokens = torch.empty(sequences, dtype=i, device=d)
         self.lse = torch.empty(T, dtype=f, device=d)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=d)
+        self._rows, self._slots = torch.Size((T, E)), torch.Size((T, k))
+        self._tokens, self._offsets = torch.Size((T,)), torch.Size((sequences + 1,))
+        self._where = -1 if d.index is None else d.index
+
+    def _need(self, t, name, shape, dtype):
+        if not _plain(t, shape, dtype, self._where):
+            _need(t, name, shape, dtype, self.device)
 
     def _check(self, logits, seq_offsets, mask):
-        _need(logits, "logits", (self.T, self.E), self.dtype, self.device)
+        self._need(logits, "logits", self._rows, self.dtype)
         if seq_offsets is not None:
-            _need(seq_offsets, "seq_offsets", (self.G + 1,), torch.int32, self.device)
+            self._need(seq_offsets, "seq_offsets", self._offsets, torch.int32)
         elif self.G != 1:
             raise ValueError("seq_offsets: needed for more than one sequence")
-        if mask is not None:
-            if isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
-                mask = mask.view(torch.uint8)
-            _need(mask, "mask", (self.T,), torch.uint8, self.device)
-        return mask
+        if mask is not None and not _plain(mask, self._tokens, torch.bool, self._where):
+            self._need(mask, "mask", self._tokens, torch.uint8)
 
     def forward(self, logits, topk_idx, seq_offsets=None, mask=None, stream=None
                 ) -> Tuple[torch.Tensor, torch.Tensor]:
-        mask = self._check(logits, seq_offsets, mask)
-        _need(topk_idx, "topk_idx", (self.T, self.k), torch.int32, self.device)
+        self._check(logits, seq_offsets, mask)
+        self._need(topk_idx, "topk_idx", self._slots, torch.int32)
         B.mm_moe_balance_forward(self.shape, logits, topk_idx, seq_offsets, mask, self.losses,
                                  self.seq_loss, self.counts, self.tokens, self.lse,
                                  self.workspace, _stream(stream, self.device))
@@ -185,15 +190,14 @@ class MoEBalanceLoss:
         """The logit gradient of dlosses[0] balance + dlosses[1] z (dlosses [2] fp32 on the
         device) of the last forward, whose logits, seq_offsets and mask are given again.
         MoERouter.backward takes it as dlogits_aux."""
-        mask = self._check(logits, seq_offsets, mask)
-        _need(dlosses, "dlosses", (2,), torch.float32, self.device)
+        self._check(logits, seq_offsets, mask)
+        self._need(dlosses, "dlosses", _TWO, torch.float32)
         if dlogits is None:
-            dlogits = torch.empty((self.T, self.E), dtype=self.dtype, device=self.device)
+            dlogits = torch.empty_like(logits)
         else:
-            _need(dlogits, "dlogits", (self.T, self.E), self.dtype, self.device)
+            self._need(dlogits, "dlogits", self._rows, self.dtype)
         B.mm_moe_balance_backward(self.shape, logits, seq_offsets, mask, self.counts, self.tokens,
-                                  dlosses, dlogits, self.workspace,
-                                  _stream(stream, self.device))
+                                  dlosses, dlogits, self.workspace, _stream(stream, self.device))
         return dlogits
 
 
