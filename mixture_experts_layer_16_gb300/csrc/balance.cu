@@ -49,7 +49,7 @@ struct Ring {
   static constexpr int BYTES = BAL_STAGES * (NV * QUAD + KS * 4);  // per thread
   // This thread's; its next one lies a quad (an int) of every thread further on, as a warp's
   // quads come from memory.  (A thread's quads side by side, which takes fewer address
-  // instructions, cost 25% more time: the copies then scatter each line they bring.)
+  // instructions, cost 30% more time: the copies then scatter each line they bring.)
   uint32_t quads, idx, unit, idx_unit;
   int l, E, k;
   __device__ __forceinline__ void init(unsigned char* smem, int l_, int E_, int k_) {
@@ -275,6 +275,13 @@ struct SeqWalk {
     b = t0;
     s = 0;
     if (off == nullptr) return;
+    next_seq = 0;
+    if (G <= WINDOW) {  // all offsets fit: one trip to memory
+      fill();
+      const int i = threadIdx.x;
+      next_seq = __syncthreads_count(i < G && win[i < G ? i + 1 : 0] <= t0);
+      return;
+    }
     // the first sequence that ends past t0: each round, the threads test as many
     // sequences at equal distances and leave one distance to search
     int lo = 0, n = G;  // it is in [lo, lo + n], lo + n = G: none
@@ -860,14 +867,17 @@ static int bal_lanes(int E) {
 
 static BalPlan bal_plan(int64_t T, int E, int G) {
   BalPlan b{};
-  // (131072 tokens, 128 experts: 4096 sequences 125 us forward in large CTAs, one sequence
-  // 27.7 us in small ones against 25.0)
+  // (131072 tokens, 128 experts: 4096 sequences 83.8 us forward in large CTAs, 52.4 in small
+  // ones; one sequence 22.3 and 25.4)
   b.threads = T / G < 1024 && G > 152 ? BAL_SMALL : BAL_THREADS;
   // (above 512 experts the registers allow one large CTA on an SM)
   const int ctas = 152 * (E <= 512 ? 2 : 1) * (BAL_THREADS / b.threads);
   const int groups = b.threads / bal_lanes(E);
   const int64_t per = (T + ctas - 1) / ctas;
   b.chunk = static_cast<int>((per + groups - 1) / groups * groups);
+  // a CTA takes its sequences one after the other: where whole rounds of it would hold
+  // several, and there are CTAs to spare, about one each
+  if (b.chunk > T / G) b.chunk = static_cast<int>(std::max(per, T / G));
   b.nb = static_cast<int>((T + b.chunk - 1) / b.chunk);
   const size_t pieces = static_cast<size_t>(b.nb) + G;
   const auto take = [&](size_t bytes) {
@@ -972,10 +982,11 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_balance_forward(
   });
   prof_end(c, K_BALANCE_FWD);
   if (e != cudaSuccess) return MM_MOE_ECUDA;
-  // one wave of the first kernel's CTAs, else a CTA per sequence (131072 tokens, 256 experts,
-  // 96 sequences, 768 of the first kernel's CTAs: 82 us forward against 44)
+  // by how many pieces a sequence has on average (131072 tokens, 128 experts: 16 sequences,
+  // 19 pieces each, 23.6 us forward with the first kernel, 32.5 with the second; 64 sequences,
+  // 5 pieces, 28.3 and 27.5; 64 x 8, one piece, 6.0 and 5.0)
+  const bool few = b.nb > 6 * static_cast<int64_t>(G);
   const int64_t units = static_cast<int64_t>(G) * ((E + 31) / 32);
-  const bool few = units <= 2 * c.num_sms;
   prof_begin(c, K_BALANCE_FINISH);
   e = launch_k(c.stream, few ? balance_join_few_kernel : balance_join_many_kernel,
                dim3(static_cast<unsigned>(few ? units : std::min(G, JOIN_MANY_CTAS))),
