@@ -170,6 +170,21 @@ struct Place {
   // parameters of the thread's columns as pairs, zero outside the row
   template <typename P>
   __device__ __forceinline__ void params(const P* p, f2 (&v)[NU * U / 2]) const {
+    if constexpr (CUT != ANY) {
+      if (p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {  // whole vectors
+        constexpr int N = VN<P> < U ? VN<P> : U;
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+#pragma unroll
+          for (int k = 0; k < U; k += N) {
+            f2 t[VN<P> / 2] = {};
+            if (has(i)) unpack2<P>(__ldg(reinterpret_cast<const uint4*>(p + col(i) + k)), t);
+#pragma unroll
+            for (int q = 0; q < N / 2; ++q) v[(i * U + k) / 2 + q] = t[q];
+          }
+        return;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < NU; ++i)
 #pragma unroll
@@ -273,8 +288,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_fwd_kernel(
   };
   for (int i = 0; i < S * ROWS * NU; ++i)
     if (!p.has(i % NU)) sts16_zero(ring + i * unit_bytes);
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(ring + i * step_bytes);
+  issue(ring);
   f2 wv[PS ? 1 : C2], bv[PS ? 1 : C2];
   // shared: weight then bias in fp32, the two halves of the units apart (16-byte reads of
   // consecutive units then meet no bank twice)
@@ -291,6 +305,9 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_fwd_kernel(
     p.params(w, wv);
     p.params(b, bv);
   }
+  // (behind the parameters, which the first row already needs)
+#pragma unroll
+  for (int i = 1; i < S - 1; ++i) issue(ring + i * step_bytes);
   bool full = true;
 #pragma unroll
   for (int i = 0; i < NU; ++i) full = full && p.whole(i);
@@ -433,13 +450,15 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
   };
   for (int i = 0; i < S * ROWS * ARRAYS * NU; ++i)
     if (!p.has(i % NU)) sts16_zero(ring + i * unit_bytes);
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(ring + i * step_bytes);
+  // the parameters' loads stand behind the first step's, not behind the whole ring's
+  issue(ring);
   f2 wv[C2], dw[C2], db[C2];
   if (w32)
     p.params(static_cast<const float*>(w), wv);
   else
     p.params(static_cast<const T*>(w), wv);
+#pragma unroll
+  for (int i = 1; i < S - 1; ++i) issue(ring + i * step_bytes);
 #pragma unroll
   for (int k = 0; k < C2; ++k) dw[k] = db[k] = 0;
   float mu_n[ROWS], r_n[ROWS];
