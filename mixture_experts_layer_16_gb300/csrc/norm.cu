@@ -58,7 +58,7 @@ constexpr int NORM_THREADS = 512;
 
 // Steps of ROWS rows in the ring: 64 to 192 KB of it.
 template <int NU, int ROWS>
-constexpr int norm_fwd_steps = ROWS == 2 ? 3 : NU <= 4 ? 4 : 2;
+constexpr int norm_fwd_steps = ROWS == 2 ? 3 : NU <= 4 ? 4 : NU <= 5 ? 3 : 2;
 template <int NU, bool ADD, int ROWS>
 constexpr int norm_bwd_steps = (NU <= 2 ? 4 : 2) / ROWS + (NU <= 2 && !ADD && ROWS == 2 ? 1 : 0);
 // Parameters stay in registers up to 16 columns a thread, else in shared memory.
@@ -924,9 +924,20 @@ static mm_moe_status norm_forward(const Ctx& c, const mm_moe_norm_shape* s, cons
       if (T_ <= c.num_sms && group_threads<T, 1>(H, even) != 0)
         return go(one, one);  // one row a CTA: spread it wide
       if constexpr (sizeof(T) == 2) {
-        if (even && H % VN<T> == 0 && H > 512 && H <= 8192)
-          return H <= 1024 ? go(std::integral_constant<int, 4>{}, one)
-                           : go(std::integral_constant<int, 8>{}, one);
+        if (even && H % VN<T> == 0 && H > 512 && H <= 8192) {
+          // as few warps as hold the row in 8 units a thread, and as few units as they need
+          // (12000 x 2560 in five units 23.9 us, in eight 31.3; 8192 x 4096 in eight units
+          // 25.2 us, in four, two rows a barrier, 26.8)
+          const int units = H / VN<T>, lanes = (units + 255) / 256 * 32;
+          switch ((units + lanes - 1) / lanes) {
+            case 3: return go(std::integral_constant<int, 3>{}, one);
+            case 4: return go(std::integral_constant<int, 4>{}, one);
+            case 5: return go(std::integral_constant<int, 5>{}, one);
+            case 6: return go(std::integral_constant<int, 6>{}, one);
+            case 7: return go(std::integral_constant<int, 7>{}, one);
+            default: return go(std::integral_constant<int, 8>{}, one);
+          }
+        }
       }
       const int GT = group_threads<T, MOST>(H, even);
       if (GT > 32) return go(most, two);
