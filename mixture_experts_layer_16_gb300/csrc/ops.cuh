@@ -1,4 +1,4 @@
-// ops.cuh -- what the operators around the layer (norm.cu, balance.cu, gradclip.cu) share:
+// ops.cuh -- what the operators around the layer (norm.cuh, balance.cu, gradclip.cu) share:
 // their kernel ids and typed element access, bf16, fp16 and fp32 in memory, fp32 in
 // registers.  A value is rounded (to nearest even) only where it is stored.
 #pragma once
