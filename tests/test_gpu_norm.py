@@ -130,6 +130,23 @@ def test_norm_many_rows(T):
     go(T, 100, "fp32", "fp32", bias=False)
 
 
+@pytest.mark.parametrize("H", [24, 520, 640, 768, 1016, 1272, 1536, 1792, 2056, 2560, 3333, 4100,
+                               5120, 6144, 7168, 8176, 8191, 8192, 9000, 16384])
+@pytest.mark.parametrize("dtype,param", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp32")])
+def test_norm_widths(H, dtype, param):
+    """More rows than CTAs: every number of units a thread, and both sides of its limits."""
+    go(331, H, dtype, param, bias=H % 3 != 0, add=H % 16 == 0)
+
+
+def test_norm_operands_cut_differently():
+    """Rows of x lie apart, y and dx are dense with an odd width: no common cut."""
+    T, H = 300, 333
+    d = data(T, H, "bf16", "bf16", pad=3)
+    n = MoELayerNorm(T, H, eps=EPS)
+    y = n.forward(d["x"], d["w"], d["b"])
+    check_all(d, "bf16", "bf16", n, y, n.backward(d["dy"], d["x"], d["w"], dx_add=d["add"]))
+
+
 def test_norm_unaligned_pointers():
     # a row that starts on its element only (2 bytes past a 16-byte boundary)
     T, H = 19, 256
