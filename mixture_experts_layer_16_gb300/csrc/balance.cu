@@ -353,17 +353,71 @@ struct BalParts {
   int* cta_n;     // [.., 2]: tokens, sequences with a token
 };
 
+// What the sequences of a thread, a CTA or the whole call add up to.
+struct BalTotals {
+  float sum, z;
+  int n, live;
+  __device__ __forceinline__ void add(float v, float zg, int ng) {
+    sum += v;
+    z += zg;
+    n += ng;
+    live += ng > 0 ? 1 : 0;
+  }
+  // the CTA's threads together (`one_warp`: the others have nothing), then the results
+  __device__ __forceinline__ void finish(bool one_warp, const BalParts& parts, float* losses) {
+    __shared__ float s_f[32][2];
+    __shared__ int s_i[32][2];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    sum = warp_sum(sum);
+    z = warp_sum(z);
+    n = warp_sum(n);
+    live = warp_sum(live);
+    if (!one_warp) {
+      if (lane == 0) {
+        s_f[wid][0] = sum;
+        s_f[wid][1] = z;
+        s_i[wid][0] = n;
+        s_i[wid][1] = live;
+      }
+      __syncthreads();
+      const bool in = lane < static_cast<int>(blockDim.x) / 32;
+      sum = warp_sum(in ? s_f[lane][0] : 0.f);
+      z = warp_sum(in ? s_f[lane][1] : 0.f);
+      n = warp_sum(in ? s_i[lane][0] : 0);
+      live = warp_sum(in ? s_i[lane][1] : 0);
+    }
+    if (threadIdx.x == 0) {
+      losses[0] = live > 0 ? sum / static_cast<float>(live) : 0.f;
+      losses[1] = n > 0 ? z / static_cast<float>(n) : 0.f;
+      parts.stats[0] = static_cast<float>(live);
+      parts.stats[1] = static_cast<float>(n);
+    }
+  }
+};
+__device__ __forceinline__ float sequence_loss(float dot, int n, float per) {
+  const float nf = static_cast<float>(n);
+  return n > 0 ? dot * per / (nf * nf) : 0.f;
+}
+
+// What the call returns.
+struct BalOut {
+  float* losses;     // [2]
+  float* seq_loss;   // [G]
+  int32_t* counts;   // [G, E]
+  int32_t* tokens;   // [G]
+};
+
 template <typename T, int L, int NV, bool VEC>
 __global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_fwd_kernel(
     const T* __restrict__ logits, const int32_t* __restrict__ topk_idx,
     const int32_t* __restrict__ off, const uint8_t* __restrict__ mask, int64_t T_, int E, int k,
-    int G, int chunk, float* __restrict__ lse_out, BalParts parts) {
+    int G, int chunk, float* __restrict__ lse_out, BalParts parts, BalOut out) {
   using R = Ring<T, L, NV, VEC>;
   const int nt = blockDim.x, warps = nt / 32;
   extern __shared__ __align__(16) unsigned char smem[];
   float* s_p = reinterpret_cast<float*>(smem + R::BYTES * nt);  // [warps][E]
   int* s_cnt = reinterpret_cast<int*>(s_p + warps * E);  // [E]
-  __shared__ float s_z[BAL_WARPS];
+  __shared__ float s_z[BAL_WARPS], s_dot[BAL_WARPS];
   __shared__ int s_n[BAL_WARPS];
   __shared__ int s_win[SeqWalk::WINDOW + 1];
   pdl_wait();
@@ -376,8 +430,20 @@ __global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_fwd_kern
   const int64_t t1 = min(T_, t0 + chunk);
   R ring;
   ring.init(smem, l, E, k);
+  const bool alone = gridDim.x == 1;  // (then its results are the call's)
+  const float per = static_cast<float>(E) / static_cast<float>(k);
+  BalTotals all{};
   if (blockIdx.x == 0 && tid == 0) *parts.arrived = 0;
   for (int e = tid; e < E; e += nt) s_cnt[e] = 0;
+  if (alone && off != nullptr)  // sequences without tokens
+    for (int i = tid; i < G * (E + 1); i += nt) {
+      if (i < G) {
+        out.seq_loss[i] = 0.f;
+        out.tokens[i] = 0;
+      } else {
+        out.counts[i - G] = 0;
+      }
+    }
   __syncthreads();
   SeqWalk w;
   w.start(off, s_win, G, t0, t1);
@@ -477,13 +543,21 @@ __global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_fwd_kern
     }
     __syncthreads();
     const int64_t piece = static_cast<int64_t>(blockIdx.x) + w.s;
+    int32_t* cnt_at = alone ? out.counts + static_cast<int64_t>(w.s) * E : parts.cnt + piece * E;
+    float dot = 0.f;
     for (int e = tid; e < E; e += nt) {
       float t = s_p[e];
 #pragma unroll 4
       for (int i = 1; i < warps; ++i) t += s_p[i * E + e];
-      parts.p[piece * E + e] = t;
-      parts.cnt[piece * E + e] = s_cnt[e];
+      if (!alone) parts.p[piece * E + e] = t;
+      cnt_at[e] = s_cnt[e];
+      dot = fmaf(static_cast<float>(s_cnt[e]), t, dot);
       s_cnt[e] = 0;
+    }
+    if (alone) {
+      dot = warp_sum(dot);
+      if (lane == 0) s_dot[wid] = dot;
+      __syncthreads();
     }
     if (tid == 0) {
       float tz = 0.f;
@@ -492,11 +566,20 @@ __global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_fwd_kern
         tz += s_z[i];
         tn += s_n[i];
       }
-      parts.z[piece] = tz;
-      parts.n[piece] = tn;
+      if (alone) {
+        for (int i = 1; i < warps; ++i) dot += s_dot[i];
+        const float v = sequence_loss(dot, tn, per);
+        out.seq_loss[w.s] = v;
+        out.tokens[w.s] = tn;
+        all.add(v, tz, tn);
+      } else {
+        parts.z[piece] = tz;
+        parts.n[piece] = tn;
+      }
     }
     __syncthreads();
   }
+  if (alone && wid == 0) all.finish(true, parts, out.losses);
 }
 
 // ---------------------------------------------------------------- joining the pieces
@@ -529,60 +612,13 @@ __device__ __forceinline__ bool last_cta(int* arrived) {
   return s_before == static_cast<int>(gridDim.x) - 1;
 }
 
-// What the sequences of a thread, a CTA or the whole call add up to.
-struct BalTotals {
-  float sum, z;
-  int n, live;
-  __device__ __forceinline__ void add(float v, float zg, int ng) {
-    sum += v;
-    z += zg;
-    n += ng;
-    live += ng > 0 ? 1 : 0;
-  }
-  // the CTA's threads together (`one_warp`: the others have nothing), then the results
-  __device__ __forceinline__ void finish(bool one_warp, const BalParts& parts, float* losses) {
-    __shared__ float s_f[32][2];
-    __shared__ int s_i[32][2];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    sum = warp_sum(sum);
-    z = warp_sum(z);
-    n = warp_sum(n);
-    live = warp_sum(live);
-    if (!one_warp) {
-      if (lane == 0) {
-        s_f[wid][0] = sum;
-        s_f[wid][1] = z;
-        s_i[wid][0] = n;
-        s_i[wid][1] = live;
-      }
-      __syncthreads();
-      const bool in = lane < static_cast<int>(blockDim.x) / 32;
-      sum = warp_sum(in ? s_f[lane][0] : 0.f);
-      z = warp_sum(in ? s_f[lane][1] : 0.f);
-      n = warp_sum(in ? s_i[lane][0] : 0);
-      live = warp_sum(in ? s_i[lane][1] : 0);
-    }
-    if (threadIdx.x == 0) {
-      losses[0] = live > 0 ? sum / static_cast<float>(live) : 0.f;
-      losses[1] = n > 0 ? z / static_cast<float>(n) : 0.f;
-      parts.stats[0] = static_cast<float>(live);
-      parts.stats[1] = static_cast<float>(n);
-    }
-  }
-};
-__device__ __forceinline__ float sequence_loss(float dot, int n, float per) {
-  const float nf = static_cast<float>(n);
-  return n > 0 ? dot * per / (nf * nf) : 0.f;
-}
-
 // Few sequences: a CTA per sequence and 32 experts; its warps take every 32nd piece, ten
 // loads of each kind in flight.
 constexpr int JOIN_THREADS = 1024;
 constexpr int JOIN_WARPS = JOIN_THREADS / 32;
 __global__ void __launch_bounds__(JOIN_THREADS, 1) balance_join_few_kernel(
     const int32_t* __restrict__ off, int64_t T_, int E, int k, int G, int chunk, BalParts parts,
-    float* __restrict__ losses, float* __restrict__ seq_loss, int32_t* __restrict__ counts,
-    int32_t* __restrict__ tokens) {
+    BalOut out) {
   constexpr int BATCH = 10;
   __shared__ float s_p[JOIN_WARPS][33], s_z[JOIN_WARPS];
   __shared__ int s_c[JOIN_WARPS][33], s_n[JOIN_WARPS];
@@ -646,7 +682,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 1) balance_join_few_kernel(
   __syncthreads();
   if (lane == 0) {
     s_p[0][wid] = static_cast<float>(cnt) * p;
-    if (eb * 32 + wid < E) counts[static_cast<int64_t>(g) * E + eb * 32 + wid] = cnt;
+    if (eb * 32 + wid < E) out.counts[static_cast<int64_t>(g) * E + eb * 32 + wid] = cnt;
   }
   __syncthreads();
   if (wid == 0) {
@@ -655,7 +691,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 1) balance_join_few_kernel(
       parts.dot[blockIdx.x] = dot;
       if (eb == 0) {
         parts.seq_z[g] = z;
-        tokens[g] = n;
+        out.tokens[g] = n;
       }
     }
   }
@@ -663,7 +699,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 1) balance_join_few_kernel(
   const float per = static_cast<float>(E) / static_cast<float>(k);
   BalTotals all{};
   for (int i = threadIdx.x; i < G; i += JOIN_THREADS) {
-    const int ni = __ldcg(tokens + i);
+    const int ni = __ldcg(out.tokens + i);
     const float zi = __ldcg(parts.seq_z + i);
     const float* dots = parts.dot + static_cast<int64_t>(i) * blocks;
     float q[4];  // (beside the loads above)
@@ -672,10 +708,10 @@ __global__ void __launch_bounds__(JOIN_THREADS, 1) balance_join_few_kernel(
     float d = (q[0] + q[1]) + (q[2] + q[3]);
     for (int j = 4; j < blocks; ++j) d += __ldcg(dots + j);
     const float v = sequence_loss(d, ni, per);
-    seq_loss[i] = v;
+    out.seq_loss[i] = v;
     all.add(v, zi, ni);
   }
-  all.finish(G <= 32, parts, losses);
+  all.finish(G <= 32, parts, out.losses);
 }
 
 // Many sequences, with few pieces each: a CTA of up to 8 warps takes a sequence at a time, an
@@ -684,8 +720,7 @@ constexpr int JOIN_MANY_THREADS = 256;
 constexpr int JOIN_MANY_CTAS = 152 * 4;
 __global__ void __launch_bounds__(JOIN_MANY_THREADS) balance_join_many_kernel(
     const int32_t* __restrict__ off, int64_t T_, int E, int k, int G, int chunk, BalParts parts,
-    float* __restrict__ losses, float* __restrict__ seq_loss, int32_t* __restrict__ counts,
-    int32_t* __restrict__ tokens) {
+    BalOut out) {
   constexpr int BATCH = 8;
   __shared__ float s_dot[JOIN_MANY_THREADS / 32];
   pdl_wait();
@@ -719,7 +754,7 @@ __global__ void __launch_bounds__(JOIN_MANY_THREADS) balance_join_many_kernel(
           cnt += fc[i];
         }
       }
-      counts[static_cast<int64_t>(g) * E + e] = cnt;
+      out.counts[static_cast<int64_t>(g) * E + e] = cnt;
       dot = fmaf(static_cast<float>(cnt), p, dot);
     }
     dot = warp_sum(dot);
@@ -736,8 +771,8 @@ __global__ void __launch_bounds__(JOIN_MANY_THREADS) balance_join_many_kernel(
     if (threadIdx.x == 0) {
       for (int i = 1; i < nt / 32; ++i) dot += s_dot[i];
       const float v = sequence_loss(dot, n, per);
-      tokens[g] = n;
-      seq_loss[g] = v;
+      out.tokens[g] = n;
+      out.seq_loss[g] = v;
       mine.add(v, z, n);
     }
     __syncthreads();  // (s_dot is read)
@@ -756,7 +791,7 @@ __global__ void __launch_bounds__(JOIN_MANY_THREADS) balance_join_many_kernel(
     all.n += __ldcg(parts.cta_n + 2 * i);
     all.live += __ldcg(parts.cta_n + 2 * i + 1);
   }
-  all.finish(false, parts, losses);
+  all.finish(false, parts, out.losses);
 }
 
 template <typename T, int L, int NV, bool VEC>
@@ -865,7 +900,7 @@ static int bal_lanes(int E) {
   return E <= 8 ? 2 : E <= 16 ? 4 : E <= 128 ? 8 : E <= 256 ? 16 : 32;
 }
 
-static BalPlan bal_plan(int64_t T, int E, int G) {
+static BalPlan bal_plan(int64_t T, int E, int G, bool forward) {
   BalPlan b{};
   // (131072 tokens, 128 experts: 4096 sequences 83.8 us forward in large CTAs, 52.4 in small
   // ones; one sequence 22.3 and 25.4)
@@ -878,6 +913,11 @@ static BalPlan bal_plan(int64_t T, int E, int G) {
   // a CTA takes its sequences one after the other: where whole rounds of it would hold
   // several, and there are CTAs to spare, about one each
   if (b.chunk > T / G) b.chunk = static_cast<int>(std::max(per, T / G));
+  // few tokens: one CTA takes them all and no launch follows (us, two launches and one: 64 x 8
+  // 5.1 and 3.0, 192 x 128 6.4 and 5.7, 288 x 128 6.3 and 6.9; two sequences in 64 x 128 9.1
+  // and 7.2, three in 128 x 128 9.2 and 9.6).  Gradients have no second launch to save.
+  if (forward && T <= static_cast<int64_t>(std::max(0, 6 - 2 * G)) * groups)
+    b.chunk = static_cast<int>(T);
   b.nb = static_cast<int>((T + b.chunk - 1) / b.chunk);
   const size_t pieces = static_cast<size_t>(b.nb) + G;
   const auto take = [&](size_t bytes) {
@@ -943,7 +983,7 @@ using namespace mmmoe;
 extern "C" MM_MOE_API mm_moe_status mm_moe_balance_workspace_size(
     const mm_moe_balance_shape* shape, size_t* bytes) {
   if (!bal_shape_ok(shape) || bytes == nullptr) return MM_MOE_EINVAL;
-  *bytes = bal_plan(shape->T, static_cast<int>(shape->E), static_cast<int>(shape->G)).bytes;
+  *bytes = bal_plan(shape->T, static_cast<int>(shape->E), static_cast<int>(shape->G), false).bytes;
   return MM_MOE_OK;
 }
 
@@ -962,8 +1002,9 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_balance_forward(
   const Ctx c{static_cast<cudaStream_t>(stream), sms, &launches};
   const int E = static_cast<int>(shape->E), k = static_cast<int>(shape->k),
             G = static_cast<int>(shape->G);
-  const BalPlan b = bal_plan(shape->T, E, G);
+  const BalPlan b = bal_plan(shape->T, E, G, true);
   const BalParts parts = bal_parts(b, workspace);
+  const BalOut out{losses, seq_loss, counts, tokens};
   prof_begin(c, K_BALANCE_FWD);
   cudaError_t e = with_dtype(shape->dtype, [&](auto* tag) {
     using T = std::remove_pointer_t<decltype(tag)>;
@@ -977,21 +1018,22 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_balance_forward(
       const cudaError_t r = allow_smem(kern, smem);
       if (r != cudaSuccess) return r;
       return launch_k(c.stream, kern, dim3(b.nb), dim3(b.threads), smem, lg, topk_idx,
-                      seq_offsets, mask, shape->T, E, k, G, b.chunk, lse, parts);
+                      seq_offsets, mask, shape->T, E, k, G, b.chunk, lse, parts, out);
     });
   });
   prof_end(c, K_BALANCE_FWD);
   if (e != cudaSuccess) return MM_MOE_ECUDA;
+  if (b.nb == 1) return MM_MOE_OK;
   // by how many pieces a sequence has on average (131072 tokens, 128 experts: 16 sequences,
   // 19 pieces each, 23.6 us forward with the first kernel, 32.5 with the second; 64 sequences,
-  // 5 pieces, 28.3 and 27.5; 64 x 8, one piece, 6.0 and 5.0)
+  // 5 pieces, 28.3 and 27.5)
   const bool few = b.nb > 6 * static_cast<int64_t>(G);
   const int64_t units = static_cast<int64_t>(G) * ((E + 31) / 32);
   prof_begin(c, K_BALANCE_FINISH);
   e = launch_k(c.stream, few ? balance_join_few_kernel : balance_join_many_kernel,
                dim3(static_cast<unsigned>(few ? units : std::min(G, JOIN_MANY_CTAS))),
                dim3(few ? JOIN_THREADS : std::min(JOIN_MANY_THREADS, (E + 31) / 32 * 32)), 0,
-               seq_offsets, shape->T, E, k, G, b.chunk, parts, losses, seq_loss, counts, tokens);
+               seq_offsets, shape->T, E, k, G, b.chunk, parts, out);
   prof_end(c, K_BALANCE_FINISH);
   return e == cudaSuccess ? MM_MOE_OK : MM_MOE_ECUDA;
 }
@@ -1012,7 +1054,7 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_balance_backward(
   const Ctx c{static_cast<cudaStream_t>(stream), sms, &launches};
   const int E = static_cast<int>(shape->E), k = static_cast<int>(shape->k),
             G = static_cast<int>(shape->G);
-  const BalPlan b = bal_plan(shape->T, E, G);
+  const BalPlan b = bal_plan(shape->T, E, G, false);
   const float* stats = bal_parts(b, const_cast<void*>(workspace)).stats;
   prof_begin(c, K_BALANCE_BWD);
   const cudaError_t e = with_dtype(shape->dtype, [&](auto* tag) {

@@ -118,6 +118,40 @@ def test_balance_16_bit_logits(dtype, T, E, k, n_seq):
     check(c, *run(c))
 
 
+@pytest.mark.parametrize("T,E,k,n_seq", [
+    (768, 8, 2, 1), (769, 8, 2, 1), (384, 8, 2, 2), (385, 8, 2, 2), (192, 128, 8, 1),
+    (193, 128, 8, 1), (96, 256, 8, 2), (48, 512, 8, 1), (49, 1000, 8, 1), (384, 16, 3, 1)])
+def test_balance_around_one_cta(T, E, k, n_seq):
+    """Sizes up to which one CTA takes every token, and above."""
+    c = case(T, E, k, n_seq, True)
+    check(c, *run(c))
+
+
+@pytest.mark.parametrize("off", [[0, 0, 90], [0, 90, 90], [20, 20, 20], [7, 40, 83], [0, 90]])
+@pytest.mark.parametrize("stale", [0x00, 0xff])
+def test_balance_few_tokens_and_empty_sequences(off, stale):
+    """One CTA: sequences without tokens and tokens in no sequence, over old results."""
+    c = case(90, 24, 3, len(off) - 1, True)
+    h = MoEBalanceLoss(90, 24, 3, len(off) - 1)
+    for t in (h.losses, h.seq_loss, h.counts, h.tokens, h.lse, h.workspace):
+        t.view(torch.uint8).fill_(stale)
+    c["off"] = torch.tensor(off, dtype=torch.int32, device="cuda")
+    losses, counts = h.forward(c["logits"], c["idx"], c["off"], c["mask"])
+    d = h.backward(c["logits"], torch.tensor(DL, device="cuda"), c["off"], c["mask"])
+    a, b = off[0], off[-1]
+    idx, mask, o = c["idx"].cpu().numpy()[a:b], c["mask"].cpu().numpy()[a:b], np.array(off) - a
+    if a == b:
+        assert not losses.any() and not counts.any() and not h.tokens.any()
+        assert not h.seq_loss.any() and not h.lse.any() and not d.any()
+        return
+    f = ot.balance_forward(f64(c["logits"])[a:b], idx, c["G"], o, mask)
+    assert np.array_equal(counts.cpu().numpy(), f["counts"])
+    assert np.array_equal(h.tokens.cpu().numpy(), f["tokens"])
+    assert np.all(np.abs(f64(h.seq_loss) - f["seq_loss"]) <= 1420 * E32 * f["seq_loss"])
+    assert np.all(np.abs(f64(losses) - f["losses"]) <= 1420 * E32 * f["losses"])
+    assert not h.lse[:a].any() and not h.lse[b:].any() and not d[:a].any() and not d[b:].any()
+
+
 def test_balance_many_tokens():
     c = case(20000, 16, 2, 9, True)
     check(c, *run(c))
