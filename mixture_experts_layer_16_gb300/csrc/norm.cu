@@ -24,7 +24,6 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_fwd_kernel(
     const P* __restrict__ b, float eps, float* __restrict__ mean, float* __restrict__ rstd) {
   constexpr int U = VN<T>, C2 = NU * U / 2, S = norm_fwd_steps<NU, ROWS>;
   constexpr bool PS = norm_params_shared<T, NU>;
-  static_assert(CUT != ANY || !PS, "a shifted row's columns do not line up with the parameters");
   extern __shared__ __align__(16) unsigned char ring_bytes[];
   __shared__ Sums<ROWS> s_sum[2][NORM_THREADS / 32];
   const int nt = blockDim.x;
@@ -56,10 +55,21 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_fwd_kernel(
     if (!p.has(i % NU)) sts16_zero(ring + i * unit_bytes);
   issue(ring);
   f2 wv[PS ? 1 : C2], bv[PS ? 1 : C2];
-  // shared: weight then bias in fp32, the two halves of the units apart (16-byte reads of
-  // consecutive units then meet no bank twice)
+  // shared, rows of whole units: weight then bias in fp32, the two halves of the units apart
+  // (16-byte reads of consecutive units then meet no bank twice); others, whose units begin at
+  // any column: (weight, bias) by column modulo U, so that the k-th columns of consecutive
+  // units are neighbours whatever the shift, with zeros around the row
   const uint32_t sw = ring - threadIdx.x * 16 + S * step_bytes;
-  if constexpr (PS) {
+  const int pitch = H / U + 3;  // of a residue
+  if constexpr (PS && CUT == ANY) {
+    float2* s = reinterpret_cast<float2*>(ring_bytes + S * step_bytes);
+    for (int c = static_cast<int>(threadIdx.x) - U; c < (pitch - 1) * U; c += nt) {
+      const bool in = p.in(c);
+      s[(c + U) % U * pitch + (c + U) / U] = make_float2(
+          in ? to_f32(w[c]) : 0.f, in && b != nullptr ? to_f32(b[c]) : 0.f);
+    }
+    __syncthreads();
+  } else if constexpr (PS) {
     float* s = reinterpret_cast<float*>(ring_bytes + S * step_bytes);
     for (int c = threadIdx.x; c < H; c += nt) {
       const int at = ((c % U / 4) * p.units + c / U) * 4 + c % 4;
@@ -75,8 +85,19 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_fwd_kernel(
 #pragma unroll
   for (int i = 1; i < S - 1; ++i) issue(ring + i * step_bytes);
   bool full = true;
+  uint32_t cut = 0;  // units that lie in the row in part, or not at all
 #pragma unroll
-  for (int i = 0; i < NU; ++i) full = full && p.whole(i);
+  for (int i = 0; i < NU; ++i) {
+    full = full && p.whole(i);
+    cut |= p.whole(i) ? 0u : 1u << i;
+  }
+  uint32_t sk[PS && CUT == ANY ? U : 1];  // the k-th column of this thread's unit 0
+  if constexpr (PS && CUT == ANY)
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int c = k - p.shift + U;
+      sk[k] = sw + (c % U * pitch + c / U + p.j) * 8;
+    }
   uint32_t st = ring, st_in = ring + (S - 1) * step_bytes;
   const uint32_t ring_end = ring + S * step_bytes;
   for (; tw < n; t += ROWS * step, tw += ROWS * step) {
@@ -111,7 +132,20 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_fwd_kernel(
       const f2 nmu = f2_make(-mu[r], -mu[r]);
 #pragma unroll
       for (int k = 0; k < C2; ++k) v[r][k] = f2_add(v[r][k], nmu);
-      if (!full) {  // what is not in the row has no deviation either
+      // what is not in the row has no deviation either
+      if constexpr (CUT == ANY) {
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+          if (cut & 1u << i) {
+#pragma unroll
+            for (int k = i * U / 2; k < (i + 1) * U / 2; ++k) {
+              const int c = p.col(i) + 2 * k % U;
+              float lo, hi;
+              f2_split(v[r][k], lo, hi);
+              v[r][k] = f2_make(p.in(c) ? lo : 0.f, p.in(c + 1) ? hi : 0.f);
+            }
+          }
+      } else if (!full) {
 #pragma unroll
         for (int k = 0; k < C2; ++k) {
           const int c = p.col(2 * k / U) + 2 * k % U;
@@ -137,7 +171,15 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_fwd_kernel(
       for (int i = 0; i < NU; ++i) {
         if (!p.has(i)) break;
         f2 u[U / 2];
-        if constexpr (PS) {
+        if constexpr (PS && CUT == ANY) {
+#pragma unroll
+          for (int k = 0; k < U / 2; ++k) {
+            float lo, hi;
+            f2_split(f2_mul(v[r][i * U / 2 + k], r2), lo, hi);
+            const float2 a = lds8(sk[2 * k] + i * GT * 8), c = lds8(sk[2 * k + 1] + i * GT * 8);
+            u[k] = f2_make(fmaf(lo, a.x, a.y), fmaf(hi, c.x, c.y));
+          }
+        } else if constexpr (PS) {
           const uint32_t at = sw + (p.j + i * GT) * 16;
 #pragma unroll
           for (int h = 0; h < U / 4; ++h) {
@@ -221,16 +263,15 @@ static cudaError_t fwd_launch(const Ctx& c, Rows<const T> x, Rows<T> y, int T_, 
   const int GT = group_threads<T, NU>(H, even_rows(x, T_));
   constexpr int RING = norm_fwd_steps<NU, ROWS> * ROWS * NU * 16;  // bytes per thread
   // the ring and shared parameters have to fit beside each other
-  const int fit = norm_params_shared<T, NU> ? (224 * 1024 - 8 * H) / (RING * GT) : NORM_THREADS;
+  constexpr int U = VN<T>;
+  const int shared = norm_params_shared<T, NU> ? 8 * (H + 4 * U) : 0;
+  const int fit = (224 * 1024 - shared) / (RING * GT);
   const NormGrid n = norm_grid(GT, T_, c.num_sms, fit);
   const int nt = n.GT * n.groups;
-  size_t smem = static_cast<size_t>(RING) * nt;
+  const size_t smem = static_cast<size_t>(RING) * nt + shared;
   const bool even = even_rows(x, T_) && H % VN<T> == 0;
-  auto* kern = norm_fwd_kernel<T, P, NU, EVEN, ROWS>;
-  if constexpr (norm_params_shared<T, NU>)
-    smem += sizeof(float) * 2 * H;
-  else if (!even)
-    kern = norm_fwd_kernel<T, P, NU, ANY, ROWS>;
+  auto* kern =
+      even ? norm_fwd_kernel<T, P, NU, EVEN, ROWS> : norm_fwd_kernel<T, P, NU, ANY, ROWS>;
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
   return launch_k(c.stream, kern, dim3(n.ctas), dim3(nt), smem, x, y, T_, H, n.GT, w, b, eps, mean,
@@ -246,26 +287,43 @@ static mm_moe_status norm_forward(const Ctx& c, const mm_moe_norm_shape* s, cons
   const Rows<T> y{static_cast<T*>(y_), ldy};
   const P* w = static_cast<const P*>(w_);
   const P* b = static_cast<const P*>(b_);
-  constexpr int MOST = 16 / VN<T>;  // units of 16 columns
-  const bool even = even_rows(x, T_);
+  constexpr int U = VN<T>, MOST = 16 / U;  // units of 16 columns
+  const bool even = even_rows(x, T_), any = !even || H % U != 0;
   const auto go = [&](auto nu, auto rows) {
     return fwd_launch<T, P, decltype(nu)::value, decltype(rows)::value>(c, x, y, T_, H, w, b,
                                                                         s->eps, mean, rstd);
+  };
+  // every group has one row at most
+  const auto one_round = [&](int GT) {
+    return GT != 0 && T_ <= c.num_sms / 8 * 8 * (NORM_THREADS / GT);
   };
   const auto pick = [&]() -> cudaError_t {
     constexpr std::integral_constant<int, 1> one{};
     constexpr std::integral_constant<int, 2> two{};
     constexpr std::integral_constant<int, MOST> most{};
     if (same_cut(x, y, T_)) {
-      if (T_ <= c.num_sms && group_threads<T, 1>(H, even) != 0)
-        return go(one, one);  // one row a CTA: spread it wide
+      // few rows: as many threads for each as there are (300 x 2048 bf16 2.6 us, with a warp a
+      // row 4.0; two units a thread where they spare a second warp: 300 x 512 bf16 2.0 and 2.1)
+      const int g1 = group_threads<T, 1>(H, even);
+      if (one_round(g1) && !(sizeof(T) == 2 && g1 == 64)) return go(one, one);
+      if (T_ <= 4 * c.num_sms && one_round(group_threads<T, 2>(H, even))) return go(two, one);
+      const int GT = group_threads<T, MOST>(H, even);
+      // the units a row may have, whatever its cut
+      const int units = any ? (H + 2 * (U - 1)) / U : H / U;
       if constexpr (sizeof(T) == 2) {
-        if (even && H % VN<T> == 0 && H > 512 && H <= 8192) {
-          // as few warps as hold the row in 8 units a thread, and as few units as they need
-          // (12000 x 2560 in five units 23.9 us, in eight 31.3; 8192 x 4096 in eight units
-          // 25.2 us, in four, two rows a barrier, 26.8)
-          const int units = H / VN<T>, lanes = (units + 255) / 256 * 32;
+        // As few warps as hold the row in 8 units a thread, and as few units as they need
+        // (12000 x 2560 in five units 23.9 us, in eight 31.3; 8192 x 4096 in eight units
+        // 25.2 us, in four, two rows a barrier, 26.8).  Rows on no boundary: also parts of a
+        // warp, for what their ends cost is paid once for all rows of a warp (65536 x 511 in
+        // 16 lanes 34.3 us, in 64 60.6; 8192 x 4095 31.8 and 50.1), once there are rows
+        // enough for the parameters' way into shared memory (1216 x 1001 4.6 and 4.6, 600 x
+        // 1001 5.3 and 3.7).
+        if (H <= 8192 && (any ? H > 128 && T_ > 8 * c.num_sms : H > 512)) {
+          int lanes = (units + 255) / 256 * 32;
+          while (any && lanes <= 32 && lanes > 8 && units <= 4 * lanes) lanes /= 2;
           switch ((units + lanes - 1) / lanes) {
+            case 1:
+            case 2: break;
             case 3: return go(std::integral_constant<int, 3>{}, one);
             case 4: return go(std::integral_constant<int, 4>{}, one);
             case 5: return go(std::integral_constant<int, 5>{}, one);
@@ -274,9 +332,25 @@ static mm_moe_status norm_forward(const Ctx& c, const mm_moe_norm_shape* s, cons
             default: return go(std::integral_constant<int, 8>{}, one);
           }
         }
+      } else if (any && H > 64 && H <= 8192) {
+        // Where groups of four units a thread would leave over 30% of a CTA's slots empty: up to
+        // 12 units a thread, with many rows, or where that makes a warp of two or more (us, in
+        // four units and so: 65536 x 511 57.6 and 45.2, 30202 x 1111 49.8 and 45.3, 8192 x 4095
+        // 55.2 and 46.9, 2000 x 511 4.6 and 3.7; but 5000 x 333 5.7 and 6.9, 4000 x 1111 10.5
+        // and 10.9, and without empty slots 43690 x 767 44.7 and 46.8).
+        const int slots = NORM_THREADS * MOST, used = GT == 0 ? 0 : NORM_THREADS / GT * units;
+        if (used * 10 < slots * 7 &&
+            ((units > 128 && units <= 256) || GT == 0 || T_ > 48 * c.num_sms)) {
+          int lanes = (units + 383) / 384 * 32;
+          while (lanes <= 32 && lanes > 8 && units <= 4 * lanes) lanes /= 2;
+          const int n = (units + lanes - 1) / lanes;
+          if (n <= 6) return go(std::integral_constant<int, 6>{}, one);
+          if (n <= 8) return go(std::integral_constant<int, 8>{}, one);
+          if (n <= 10) return go(std::integral_constant<int, 10>{}, one);
+          return go(std::integral_constant<int, 12>{}, one);
+        }
       }
-      const int GT = group_threads<T, MOST>(H, even);
-      if (GT > 32) return go(most, two);
+      if (GT > 32 && !one_round(GT)) return go(most, two);
       if (GT != 0) return go(most, one);
     }
     const bool vec = even && even_rows(y, T_) && H % VN<T> == 0 && al16(x.p) && al16(y.p) &&

@@ -138,6 +138,30 @@ def test_norm_widths(H, dtype, param):
     go(331, H, dtype, param, bias=H % 3 != 0, add=H % 16 == 0)
 
 
+@pytest.mark.parametrize("T,H,dtype,param", [
+    *[(1300, H, "bf16", "bf16") for H in (129, 207, 250, 333, 511, 767, 1001, 1201, 1500, 1780,
+                                          2047, 2049, 3333, 4095, 7001, 8191)],
+    (1300, 1001, "fp16", "fp16"), (1300, 511, "fp16", "fp32"), (1300, 6001, "bf16", "fp32"),
+    *[(7400, H, "fp32", "fp32") for H in (66, 67, 129, 255, 511, 1023, 1111, 1153, 1537)],
+    (1300, 511, "fp32", "fp32"), (1300, 8191, "fp32", "fp32"), (1300, 8190, "fp32", "fp32")])
+def test_norm_many_rows_on_no_boundary(T, H, dtype, param):
+    """Forward: every number of units a thread, parts of a warp and several warps a row."""
+    d = data(T, H, dtype, param, pad=0 if H % 2 else 8)
+    n = MoELayerNorm(T, H, dtype, param, eps=EPS, bias=H % 3 != 0)
+    y = n.forward(d["x"], d["w"], d["b"] if n.bias else None)
+    check_all(d, dtype, param, n, y, None, n.bias)
+
+
+@pytest.mark.parametrize("T", [152, 153, 304, 305, 608, 609, 1216, 1217])
+@pytest.mark.parametrize("H,dtype", [(256, "bf16"), (1000, "bf16"), (2048, "fp16"), (1001, "bf16"),
+                                     (128, "fp32"), (515, "fp32"), (1024, "fp32")])
+def test_norm_one_row_a_group(T, H, dtype):
+    """Few rows, up to one for every group of threads of the grid, and one more."""
+    d = data(T, H, dtype, dtype)
+    n = MoELayerNorm(T, H, dtype, eps=EPS)
+    check_all(d, dtype, dtype, n, n.forward(d["x"], d["w"], d["b"]), None)
+
+
 def test_norm_operands_cut_differently():
     """Rows of x lie apart, y and dx are dense with an odd width: no common cut."""
     T, H = 300, 333
