@@ -190,16 +190,8 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
         static_cast<T*>(o)[c] = from_f32<T>(v);
     }
   };
-  if (p.groups == 1) {
-    p.each(dw, [&](int c, float v) { put(0, c, v); });
-    p.each(db, [&](int c, float v) { put(1, c, v); });
-    return;
-  }
-  // Groups may cut their rows differently, so the sums meet by column.
-  float* const sj = reinterpret_cast<float*>(ring_bytes);  // [groups][2][H]
-  __syncthreads();
-  if constexpr (CUT != ANY) {
-    float* const q = sj + 2 * p.g * H;
+  // a thread's sums by whole units, dw's columns from q on and db's from q + H
+  const auto put_units = [&](float* q) {
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       if (!p.has(i)) break;
@@ -211,6 +203,23 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
         ob[k] = make_ulonglong2(db[i * U / 2 + 2 * k], db[i * U / 2 + 2 * k + 1]);
       }
     }
+  };
+  if (p.groups == 1) {
+    if constexpr (CUT != ANY) {
+      if (gridDim.x > 1) {
+        put_units(p0);
+        return;
+      }
+    }
+    p.each(dw, [&](int c, float v) { put(0, c, v); });
+    p.each(db, [&](int c, float v) { put(1, c, v); });
+    return;
+  }
+  // Groups may cut their rows differently, so the sums meet by column.
+  float* const sj = reinterpret_cast<float*>(ring_bytes);  // [groups][2][H]
+  __syncthreads();
+  if constexpr (CUT != ANY) {
+    put_units(sj + 2 * p.g * H);
   } else {
     p.each(dw, [&](int c, float v) { sj[2 * p.g * H + c] = v; });
     p.each(db, [&](int c, float v) { sj[(2 * p.g + 1) * H + c] = v; });
@@ -414,8 +423,12 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
     prof_begin(c, K_NORM_BWD);
     const auto pick = [&]() -> cudaError_t {
       constexpr int WIDE = sizeof(T) == 2 ? 2 : 4;
-      if (T_ <= c.num_sms && !one_cta(group_threads<T, WIDE>(H, even), T_, even) &&
-          group_threads<T, 1>(H, even) != 0)
+      // few rows: one unit a thread, in up to half of a CTA's groups (us, in two units and so:
+      // 153 x 1024 bf16 5.1 and 4.3, 300 x 512 5.0 and 4.2; in all of them 300 x 2048 6.2 and
+      // 6.6, 1200 x 512 5.1 and 6.2)
+      const int g1 = group_threads<T, 1>(H, even);
+      if (g1 != 0 && T_ <= c.num_sms / 8 * 8 * std::max(1, NORM_THREADS / g1 / 2) &&
+          !one_cta(group_threads<T, WIDE>(H, even), T_, even))
         return bwd_launch<T, 1, 1>(c, a, &n);
       if constexpr (sizeof(T) == 2) {
         // 16 bits: two rows a barrier where more than two warps share a row (8191 x 4096

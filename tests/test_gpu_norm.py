@@ -162,6 +162,14 @@ def test_norm_one_row_a_group(T, H, dtype):
     check_all(d, dtype, dtype, n, n.forward(d["x"], d["w"], d["b"]), None)
 
 
+@pytest.mark.parametrize("T", [20, 152, 153, 304, 305])
+@pytest.mark.parametrize("H,dtype", [(520, "bf16"), (1000, "bf16"), (1001, "fp16"), (8192, "bf16"),
+                                     (515, "fp32"), (4096, "fp32")])
+def test_norm_backward_few_rows(T, H, dtype):
+    """One row a CTA (whole rows of partial sums), some groups of a CTA, and one more."""
+    go(T, H, dtype, dtype, bias=T % 2 == 0, add=T % 3 == 0)
+
+
 def test_norm_operands_cut_differently():
     """Rows of x lie apart, y and dx are dense with an odd width: no common cut."""
     T, H = 300, 333
