@@ -318,7 +318,11 @@ static mm_moe_status norm_forward(const Ctx& c, const mm_moe_norm_shape* s, cons
         // 16 lanes 34.3 us, in 64 60.6; 8192 x 4095 31.8 and 50.1), once there are rows
         // enough for the parameters' way into shared memory (1216 x 1001 4.6 and 4.6, 600 x
         // 1001 5.3 and 3.7).
-        if (H <= 8192 && (any ? H > 128 && T_ > 8 * c.num_sms : H > 512)) {
+        // The same for rows above 8192 columns, up to what fits beside the parameters and
+        // pays (row by row and so: 2600 x 12288 39.4 and 31.0, 2100 x 16001 69.4 and 53.1;
+        // but 2048 x 16384 34.0 and 39.4, 600 x 9000 10.2 and 14.4).
+        const bool many = T_ > 8 * c.num_sms;
+        if (any || H > 8192 ? many && H > 128 && H <= (any ? 16384 : 12288) : H > 512) {
           int lanes = (units + 255) / 256 * 32;
           while (any && lanes <= 32 && lanes > 8 && units <= 4 * lanes) lanes /= 2;
           switch ((units + lanes - 1) / lanes) {

@@ -25,6 +25,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
     float* __restrict__ part, void* __restrict__ dweight, void* __restrict__ dbias) {
   constexpr int U = VN<T>, C2 = NU * U / 2, S = norm_bwd_steps<NU, ADD, ROWS>;
   constexpr int ARRAYS = ADD ? 3 : 2;
+  constexpr bool KEEP = ROWS == 1 && NU * U <= 16;  // xh and g stay in registers
   extern __shared__ __align__(16) unsigned char ring_bytes[];
   __shared__ Sums<2 * ROWS> s_sum[2][NORM_THREADS / 32];
   const int tid = threadIdx.x, nt = blockDim.x;
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
         }
       }
     };
-    f2 xh1[ROWS == 1 ? NU : 1][U / 2], g1[ROWS == 1 ? NU : 1][U / 2];
+    f2 xh1[KEEP ? NU : 1][U / 2], g1[KEEP ? NU : 1][U / 2];
     float ac[2 * ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
           for (int k = 0; k < U / 2; ++k) {
             a2 = f2_add(a2, g[k]);
             c2 = f2_fma(g[k], xh[k], c2);
-            if constexpr (ROWS == 1) {
+            if constexpr (KEEP) {
               xh1[i][k] = xh[k];
               g1[i][k] = g[k];
             }
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
       for (int i = 0; i < NU; ++i) {
         if (!p.has(i)) break;
         f2 xh[U / 2], g[U / 2], u[U / 2];
-        if constexpr (ROWS > 1) unit(r, i, xh, g, false);
+        if constexpr (!KEEP) unit(r, i, xh, g, false);
         if constexpr (ADD) {
           unpack2<T>(lds16(st + r * row_bytes + 2 * array_bytes + i * unit_bytes), u);
         } else {
@@ -162,8 +163,8 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
         }
 #pragma unroll
         for (int k = 0; k < U / 2; ++k) {
-          const f2 h = ROWS > 1 ? xh[k] : xh1[ROWS > 1 ? 0 : i][k];
-          const f2 gg = ROWS > 1 ? g[k] : g1[ROWS > 1 ? 0 : i][k];
+          const f2 h = KEEP ? xh1[KEEP ? i : 0][k] : xh[k];
+          const f2 gg = KEEP ? g1[KEEP ? i : 0][k] : g[k];
           u[k] = f2_fma(f2_fma(h, nc, f2_add(gg, na)), r2[r], u[k]);
         }
         p.store(pd, i, pack2<T>(u));
@@ -380,13 +381,14 @@ static cudaError_t bwd_launch(const Ctx& c, const BwdArgs<T>& a, int* n_part) {
   if (n.groups > 1) smem = std::max(smem, sizeof(float) * 2 * n.groups * a.H);
   const bool even = even_rows(a.x, a.T_) && a.H % VN<T> == 0;
   const Cut cut = !even ? ANY : NU <= 2 && a.H == n.GT * NU * VN<T> ? FULL : EVEN;
+  constexpr Cut WHOLE = NU <= 2 ? FULL : EVEN;
   auto* kern = a.add.p != nullptr
                    ? (cut == ANY    ? norm_bwd_kernel<T, NU, ANY, true, ROWS>
                       : cut == EVEN ? norm_bwd_kernel<T, NU, EVEN, true, ROWS>
-                                    : norm_bwd_kernel<T, NU, FULL, true, ROWS>)
+                                    : norm_bwd_kernel<T, NU, WHOLE, true, ROWS>)
                    : (cut == ANY    ? norm_bwd_kernel<T, NU, ANY, false, ROWS>
                       : cut == EVEN ? norm_bwd_kernel<T, NU, EVEN, false, ROWS>
-                                    : norm_bwd_kernel<T, NU, FULL, false, ROWS>);
+                                    : norm_bwd_kernel<T, NU, WHOLE, false, ROWS>);
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
   *n_part = n.ctas;
@@ -414,7 +416,7 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
                      part,
                      dw,
                      db};
-  constexpr int MOST = 16 / VN<T>;
+  constexpr int MOST = sizeof(T) == 2 ? 3 : 4;  // units a thread
   const bool even = even_rows(a.x, T_);
   cudaError_t e;
   int n = 0;
@@ -431,11 +433,18 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
           !one_cta(group_threads<T, WIDE>(H, even), T_, even))
         return bwd_launch<T, 1, 1>(c, a, &n);
       if constexpr (sizeof(T) == 2) {
-        // 16 bits: two rows a barrier where more than two warps share a row (8191 x 4096
+        // 16 bits: three units a thread where that doubles the CTA's groups, or no CTA holds the
+        // row in two (us: 65536 x 511 101.8 and 65.2, 100000 x 333 81.5 and 58.5, 50000 x 600
+        // 52.4 and 44.6; with 8 groups for 5, 5000 x 1111 18.4 and 21.5; narrow rows, 20000 x
+        // 72 9.1 and 10.3; row by row and so 4096 x 8191 207.6 and 69.9, 2600 x 12288 106.2
+        // and 48.5)
+        const int g2 = group_threads<T, 2>(H, even), g3 = group_threads<T, 3>(H, even);
+        if (g2 == 0 || (H > 128 && NORM_THREADS / g3 >= 2 * (NORM_THREADS / g2)))
+          return bwd_launch<T, 3, 1>(c, a, &n);
+        // two rows a barrier where more than two warps share a row (8191 x 4096
         // 43.8 -> 40.2 us, 20011 x 1111 47.5 -> 41.0 us; 30000 x 1000, two warps a row, 44.5
         // -> 46.3 us)
-        return group_threads<T, 2>(H, even) > 64 ? bwd_launch<T, 2, 2>(c, a, &n)
-                                                 : bwd_launch<T, 2, 1>(c, a, &n);
+        return g2 > 64 ? bwd_launch<T, 2, 2>(c, a, &n) : bwd_launch<T, 2, 1>(c, a, &n);
       } else {
         return group_threads<T, 2>(H, even) != 0 ? bwd_launch<T, 2, 1>(c, a, &n)
                                                  : bwd_launch<T, 4, 1>(c, a, &n);

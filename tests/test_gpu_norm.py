@@ -170,6 +170,17 @@ def test_norm_backward_few_rows(T, H, dtype):
     go(T, H, dtype, dtype, bias=T % 2 == 0, add=T % 3 == 0)
 
 
+@pytest.mark.parametrize("T,H,dtype,param", [
+    (700, 136, "bf16", "bf16"), (700, 207, "fp16", "fp32"), (700, 250, "bf16", "bf16"),
+    (700, 300, "bf16", "fp32"), (700, 333, "bf16", "bf16"), (700, 511, "fp16", "fp16"),
+    (700, 600, "bf16", "bf16"), (400, 4095, "bf16", "bf16"), (330, 8190, "bf16", "bf16"),
+    (330, 8191, "fp16", "fp32"), (330, 10007, "bf16", "bf16"), (330, 12274, "bf16", "bf16"),
+    (330, 12275, "bf16", "bf16"), (330, 12288, "fp16", "fp16"), (1300, 12288, "bf16", "bf16"),
+    (1300, 9001, "bf16", "fp32"), (1220, 16383, "bf16", "bf16"), (330, 12296, "bf16", "bf16")])
+def test_norm_three_units_and_wide_rows(T, H, dtype, param):
+    go(T, H, dtype, param, bias=H % 3 != 0, add=H % 2 == 0)
+
+
 def test_norm_operands_cut_differently():
     """Rows of x lie apart, y and dx are dense with an odd width: no common cut."""
     T, H = 300, 333
