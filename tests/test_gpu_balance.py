@@ -201,6 +201,30 @@ def test_balance_nothing_counts():
         assert not h.seq_loss.any() and not h.tokens.any()
 
 
+def test_balance_offsets_past_32_bits():
+    """4.3e9 logits: the last sequence against a call on its tokens alone.  Probabilities and
+    counts are the same, sums over tokens are added in another order."""
+    E, k, last = 1024, 2, 101
+    T = (1 << 22) + last
+    lg = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    idx = torch.zeros(T, k, dtype=torch.int32, device="cuda")
+    c = case(last, E, k, dtype="bf16")
+    lg[-last:], idx[-last:] = c["logits"], c["idx"]
+    off = torch.tensor([0, T - last, T], dtype=torch.int32, device="cuda")
+    dl = torch.tensor([1.0, 0.0], device="cuda")
+    one, two = MoEBalanceLoss(last, E, k, 1, "bf16"), MoEBalanceLoss(T, E, k, 2, "bf16")
+    one.forward(c["logits"], c["idx"])
+    two.forward(lg, idx, off)
+    assert torch.equal(two.counts[1], one.counts[0]) and two.tokens.tolist() == [T - last, last]
+    assert torch.equal(two.lse[-last:], one.lse)
+    assert int(two.counts[0, 0]) == k * (T - last)
+    assert abs(float(two.seq_loss[1] - one.seq_loss[0])) <= 400 * E32 * float(one.seq_loss[0])
+    d1 = f64(one.backward(c["logits"], dl))
+    d2 = f64(two.backward(lg, dl, off)[-last:])
+    # (half of it: two sequences; each is rounded once)
+    assert np.all(np.abs(2 * d2 - d1) <= 2.0 ** -7 * np.abs(d1))
+
+
 def test_balance_masked_garbage_does_not_count():
     c = case(120, 24, 3, 5, True)
     want = [t.clone() for t in run(c)[1:]]

@@ -181,6 +181,28 @@ def test_norm_three_units_and_wide_rows(T, H, dtype, param):
     go(T, H, dtype, param, bias=H % 3 != 0, add=H % 2 == 0)
 
 
+@pytest.mark.parametrize("H", [256, 1001])
+def test_norm_offsets_past_32_bits(H):
+    """Rows a million elements apart: the last ones begin past 2^32 elements.  Bit by bit as
+    with dense rows."""
+    T, ld = 4200, (1 << 20) + (8 if H % 8 == 0 else H % 8 + 8)   # (rows are cut alike)
+    d = data(T, H, "bf16", "bf16")
+    n = MoELayerNorm(T, H, eps=EPS)
+    y = n.forward(d["x"], d["w"], d["b"])
+    dx, dw, db = n.backward(d["dy"], d["x"], d["w"], dx_add=d["add"])
+    x2, dy2, y2 = (torch.empty(T * ld, dtype=torch.bfloat16, device="cuda").view(T, ld)[:, :H]
+                   for _ in range(3))
+    x2.copy_(d["x"])
+    dy2.copy_(d["dy"])
+    assert torch.equal(n.forward(x2, d["w"], d["b"], y=y2), y)
+    out = (y2, torch.empty_like(dw), torch.empty_like(db))
+    got = n.backward(dy2, x2, d["w"], dx_add=d["add"] if H % 8 == 0 else None, out=out)
+    if H % 8:
+        dx, dw, db = n.backward(d["dy"], d["x"], d["w"])
+    for a, b in zip(got, (dx, dw, db)):
+        assert torch.equal(a, b)
+
+
 def test_norm_operands_cut_differently():
     """Rows of x lie apart, y and dx are dense with an odd width: no common cut."""
     T, H = 300, 333
