@@ -62,7 +62,8 @@ struct Ring {
     E = E_;
     k = k_;
     // what lies past the last expert
-#pragma unroll
+    if (E == 4 * L * NV) return;
+#pragma unroll 1
     for (int st = 0; st < BAL_STAGES; ++st)
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -585,12 +586,12 @@ __global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_fwd_kern
 // ---------------------------------------------------------------- joining the pieces
 // The CTAs whose tokens sequence g reaches: [c0, c1).
 struct PieceRange {
-  int64_t c0, c1;
+  uint32_t c0, c1;
   __device__ __forceinline__ PieceRange(const int32_t* off, int g, int64_t T_, int chunk) {
-    const int64_t a = off != nullptr ? max(0, __ldg(off + g)) : 0;
-    const int64_t b = off != nullptr ? min(T_, static_cast<int64_t>(__ldg(off + g + 1))) : T_;
-    c0 = a / chunk;
-    c1 = b > a ? (b - 1) / chunk + 1 : c0;
+    const int n = static_cast<int>(T_), a = off != nullptr ? max(0, __ldg(off + g)) : 0;
+    const int b = off != nullptr ? min(n, __ldg(off + g + 1)) : n;
+    c0 = static_cast<uint32_t>(a) / static_cast<uint32_t>(chunk);
+    c1 = b > a ? static_cast<uint32_t>(b - 1) / static_cast<uint32_t>(chunk) + 1 : c0;
   }
 };
 
@@ -632,21 +633,23 @@ __global__ void __launch_bounds__(JOIN_THREADS, 1) balance_join_few_kernel(
   float p = 0.f, z = 0.f;
   int cnt = 0, n = 0;
   // (the first of these loads are in flight beside the pieces' own)
-  const int64_t cz = r.c0 + threadIdx.x;
+  const uint32_t cz = r.c0 + threadIdx.x;
   const bool first = eb == 0 && cz < r.c1;
   const float z0 = first ? __ldcg(parts.z + cz + g) : 0.f;
   const int n0 = first ? __ldcg(parts.n + cz + g) : 0;
   if (e < E) {
-    const float* pp = parts.p + static_cast<int64_t>(g) * E + e;
-    const int32_t* pc = parts.cnt + static_cast<int64_t>(g) * E + e;
-    for (int64_t c = r.c0 + wid; c < r.c1; c += BATCH * JOIN_WARPS) {
+    const int64_t at = static_cast<int64_t>(r.c0 + wid + g) * E + e;
+    const float* pp = parts.p + at;
+    const int32_t* pc = parts.cnt + at;
+    const int step = JOIN_WARPS * E;
+    for (uint32_t c = r.c0 + wid; c < r.c1; c += BATCH * JOIN_WARPS) {
       float fp[BATCH];
       int fc[BATCH];
 #pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
+      for (int i = 0; i < BATCH; ++i, pp += step, pc += step) {
         const bool in = c + i * JOIN_WARPS < r.c1;
-        fp[i] = in ? __ldcg(pp + (c + i * JOIN_WARPS) * E) : 0.f;
-        fc[i] = in ? __ldcg(pc + (c + i * JOIN_WARPS) * E) : 0;
+        fp[i] = in ? __ldcg(pp) : 0.f;
+        fc[i] = in ? __ldcg(pc) : 0;
       }
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
@@ -660,7 +663,8 @@ __global__ void __launch_bounds__(JOIN_THREADS, 1) balance_join_few_kernel(
   if (eb == 0) {
     z = z0;
     n = n0;
-    for (int64_t c = cz + JOIN_THREADS; c < r.c1; c += JOIN_THREADS) {
+#pragma unroll 1
+    for (uint32_t c = cz + JOIN_THREADS; c < r.c1; c += JOIN_THREADS) {
       z += __ldcg(parts.z + c + g);
       n += __ldcg(parts.n + c + g);
     }
@@ -739,14 +743,17 @@ __global__ void __launch_bounds__(JOIN_MANY_THREADS) balance_join_many_kernel(
     for (int e = threadIdx.x; e < E; e += nt) {
       float p = 0.f;
       int cnt = 0;
-      for (int64_t c = r.c0; c < r.c1; c += BATCH) {
+      const int64_t at = static_cast<int64_t>(r.c0 + g) * E + e;
+      const float* pp = parts.p + at;
+      const int32_t* pc = parts.cnt + at;
+      for (uint32_t c = r.c0; c < r.c1; c += BATCH) {
         float fp[BATCH];
         int fc[BATCH];
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
+        for (int i = 0; i < BATCH; ++i, pp += E, pc += E) {
           const bool in = c + i < r.c1;
-          fp[i] = in ? __ldcg(parts.p + (c + i + g) * E + e) : 0.f;
-          fc[i] = in ? __ldcg(parts.cnt + (c + i + g) * E + e) : 0;
+          fp[i] = in ? __ldcg(pp) : 0.f;
+          fc[i] = in ? __ldcg(pc) : 0;
         }
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
@@ -760,7 +767,8 @@ __global__ void __launch_bounds__(JOIN_MANY_THREADS) balance_join_many_kernel(
     dot = warp_sum(dot);
     if (lane == 0) s_dot[wid] = dot;
     if (wid == 0) {
-      for (int64_t c = r.c0 + 32 + lane; c < r.c1; c += 32) {
+#pragma unroll 1
+      for (uint32_t c = r.c0 + 32 + lane; c < r.c1; c += 32) {
         z += __ldcg(parts.z + c + g);
         n += __ldcg(parts.n + c + g);
       }
@@ -1024,11 +1032,12 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_balance_forward(
   prof_end(c, K_BALANCE_FWD);
   if (e != cudaSuccess) return MM_MOE_ECUDA;
   if (b.nb == 1) return MM_MOE_OK;
-  // by how many pieces a sequence has on average (131072 tokens, 128 experts: 16 sequences,
-  // 19 pieces each, 23.6 us forward with the first kernel, 32.5 with the second; 64 sequences,
-  // 5 pieces, 28.3 and 27.5)
-  const bool few = b.nb > 6 * static_cast<int64_t>(G);
+  // The first kernel where a sequence has many pieces and all its CTAs run at once (us, first
+  // and second: 131072 x 128 16 sequences, 19 pieces each, 21.3 and 23.7, 64 sequences, 5
+  // pieces, 26.0 and 23.1; 32768 x 256 in 32, 256 CTAs, 19.8 and 17.6; one sequence, whose
+  // second kernel is one CTA with no other to wait for, 21 pieces 7.0 and 6.4)
   const int64_t units = static_cast<int64_t>(G) * ((E + 31) / 32);
+  const bool few = G == 1 ? b.nb > 24 : b.nb > 6 * static_cast<int64_t>(G) && units <= sms;
   prof_begin(c, K_BALANCE_FINISH);
   e = launch_k(c.stream, few ? balance_join_few_kernel : balance_join_many_kernel,
                dim3(static_cast<unsigned>(few ? units : std::min(G, JOIN_MANY_CTAS))),

@@ -329,12 +329,11 @@ __global__ void __launch_bounds__(512) norm_cols_finish_kernel(const float* __re
   const int i = blockIdx.x * 32 + lane;
   float a = 0.f;
   if (i < H) {
-    const float* p = part + static_cast<int64_t>(blockIdx.y) * H + i;
+    const float* p = part + static_cast<int64_t>(2 * w + blockIdx.y) * H + i;
     for (int j = w; j < n; j += W * B) {
       float v[B];
 #pragma unroll
-      for (int b = 0; b < B; ++b)
-        v[b] = j + b * W < n ? __ldcg(p + static_cast<int64_t>(j + b * W) * 2 * H) : 0.f;
+      for (int b = 0; b < B; ++b, p += 2 * W * H) v[b] = j + b * W < n ? __ldcg(p) : 0.f;
 #pragma unroll
       for (int b = 0; b < B; ++b) a += v[b];
     }

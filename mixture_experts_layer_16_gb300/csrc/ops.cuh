@@ -168,6 +168,8 @@ __device__ __forceinline__ V warp_sum(V v) {
   return v;
 }
 
+__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
+
 // Sum over the CTA's warps, the same value in every thread (warps added in order);
 // `s` holds one V per warp.  The leading barrier frees `s` from an earlier use.
 template <typename V>
