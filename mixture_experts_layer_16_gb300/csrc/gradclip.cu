@@ -22,6 +22,8 @@ namespace mmmoe {
 
 constexpr int GC_THREADS = 256;
 constexpr int GC_CHUNK = 16384;  // elements: 8 16-byte vectors per thread in 16 bits, 16 in fp32
+constexpr int GC_SHORT = 4096;   // of few and small tensors, up to one for every SM (250,000
+                                 // elements 5.4 us in long ones, 4.6 in short ones; 1 M 5.7, 6.4)
 constexpr int GC_MAX = 384;      // tensors per launch (11 KB of parameters) ...
 constexpr int GC_FEW = 32;       // ... and of a launch with few (1 KB)
 constexpr int GC_CTAS = 4;       // CTAs per SM, all resident
@@ -31,8 +33,9 @@ constexpr int GC_KEEP = 2000;
 
 // The tensors of one launch.  Elements [0, head) of a tensor precede its first 16-byte
 // boundary; chunk c covers head + [c, c + 1) CHUNK, the first chunk the head too.
-template <int N>
+template <int N, int CHUNK_>
 struct GradList {
+  static constexpr int CHUNK = CHUNK_;
   const void* in[N];
   void* out[N];
   int64_t n[N];
@@ -41,8 +44,8 @@ struct GradList {
   int count;
 };
 
-template <int N>
-__device__ __forceinline__ int find_tensor(const GradList<N>& g, int chunk) {
+template <typename L>
+__device__ __forceinline__ int find_tensor(const L& g, int chunk) {
   int lo = 0, hi = g.count - 1;  // the last tensor whose first chunk is <= chunk
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -60,14 +63,14 @@ __device__ __forceinline__ int64_t head_of(const T* p, int64_t n) {
   return h < n ? h : n;
 }
 
-
-template <typename T>
+template <int CHUNK, typename T>
 __device__ __forceinline__ double sq_chunk(const T* p, int64_t n, int64_t chunk, bool keep) {
   constexpr int N = VN<T>;
-  constexpr int BATCH = 8;  // vectors in flight per thread
+  constexpr int PER = CHUNK / N / GC_THREADS;
+  constexpr int BATCH = PER < 8 ? PER : 8;  // vectors in flight per thread
   const int64_t head = head_of(p, n);
-  const int64_t a = head + chunk * GC_CHUNK;
-  const int64_t len = n > a ? (n - a < GC_CHUNK ? n - a : GC_CHUNK) : 0;
+  const int64_t a = head + chunk * CHUNK;
+  const int64_t len = n > a ? (n - a < CHUNK ? n - a : CHUNK) : 0;
   const uint4* v = reinterpret_cast<const uint4*>(p + a);
   const int nv = static_cast<int>(len / N);
   double acc = 0.0;
@@ -86,11 +89,12 @@ __device__ __forceinline__ double sq_chunk(const T* p, int64_t n, int64_t chunk,
 #pragma unroll
       for (int j = 0; j < N; ++j) s = fmaf(f[j], f[j], s);
     }
+    constexpr uint32_t MAGNITUDE = sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu;
     bool again = !(s <= 1e36f);
     if (s < 1e-30f) {
       uint32_t bits = 0;  // (all zero: an expert without tokens, nothing to add again)
 #pragma unroll
-      for (int i = 0; i < BATCH; ++i) bits |= (q[i].x | q[i].y | q[i].z | q[i].w) & 0x7fff7fffu;
+      for (int i = 0; i < BATCH; ++i) bits |= (q[i].x | q[i].y | q[i].z | q[i].w) & MAGNITUDE;
       again = bits != 0;
     }
     if (again) {
@@ -118,11 +122,20 @@ __device__ __forceinline__ double sq_chunk(const T* p, int64_t n, int64_t chunk,
   return acc;
 }
 
+// Sums in fp64 go through one warp: the SM adds two doubles a cycle, so an addition by
+// every thread of its CTAs takes half a microsecond (all warps joining the partial sums and
+// taking the root cost the second pass 6 us: 5 M gradients 15.4 us, so 9.1).
+__device__ __forceinline__ double tile_sum(const double* s, int n) {
+  double a = 0.0;
+  for (int i = threadIdx.x; i < n; i += 32) a += s[i];
+  return a;
+}
+
 // part[blockIdx.x] = the CTA's share of the sum of squares.
-template <int N>
+template <typename L>
 __global__ void __launch_bounds__(GC_THREADS, GC_CTAS) grad_sq_kernel(
-    const __grid_constant__ GradList<N> g, double* __restrict__ part) {
-  __shared__ double s[GC_THREADS / 32];
+    const __grid_constant__ L g, double* __restrict__ part) {
+  __shared__ double s[GC_THREADS];
   pdl_wait();
   pdl_trigger();
   const int total = g.first[g.count];
@@ -134,30 +147,47 @@ __global__ void __launch_bounds__(GC_THREADS, GC_CTAS) grad_sq_kernel(
     const int d = g.dt[t] & 15;
     const bool keep = c >= total - GC_KEEP;
     if (d == MM_MOE_DT_BF16)
-      acc += sq_chunk(static_cast<const __nv_bfloat16*>(g.in[t]), g.n[t], k, keep);
+      acc += sq_chunk<L::CHUNK>(static_cast<const __nv_bfloat16*>(g.in[t]), g.n[t], k, keep);
     else if (d == MM_MOE_DT_F16)
-      acc += sq_chunk(static_cast<const __half*>(g.in[t]), g.n[t], k, keep);
+      acc += sq_chunk<L::CHUNK>(static_cast<const __half*>(g.in[t]), g.n[t], k, keep);
     else
-      acc += sq_chunk(static_cast<const float*>(g.in[t]), g.n[t], k, keep);
+      acc += sq_chunk<L::CHUNK>(static_cast<const float*>(g.in[t]), g.n[t], k, keep);
   }
-  acc = block_sum(acc, s);
+  s[threadIdx.x] = acc;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  acc = warp_sum(tile_sum(s, GC_THREADS));
   if (threadIdx.x == 0) part[blockIdx.x] = acc;
 }
 
-// Sum of n partials, the same in every CTA: the norm.
-__device__ __forceinline__ double norm_of(const double* part, int n, double* s) {
+// The norm from n partial sums, the same in every CTA (and in every thread of it).
+__device__ __forceinline__ float norm_of(const double* part, int n) {
+  // (a tile that held all of a launch's sums, 4 KB more a CTA, would leave less of L1 to the
+  // scaling: 604 M gradients 544 us with this one, 624 with that)
+  constexpr int TILE = GC_THREADS;
+  __shared__ double s[TILE];
+  __shared__ float s_norm;
   double a = 0.0;
-  for (int i = threadIdx.x; i < n; i += GC_THREADS) a += part[i];
-  return sqrt(block_sum(a, s));
+  for (int i0 = 0; i0 < n; i0 += TILE) {
+    if (i0 > 0) __syncthreads();
+    if (i0 + static_cast<int>(threadIdx.x) < n) s[threadIdx.x] = __ldcg(part + i0 + threadIdx.x);
+    __syncthreads();
+    if (threadIdx.x < 32) a += tile_sum(s, min(TILE, n - i0));
+  }
+  if (threadIdx.x < 32) {
+    a = warp_sum(a);
+    if (threadIdx.x == 0) s_norm = static_cast<float>(sqrt(a));
+  }
+  __syncthreads();
+  return s_norm;
 }
 
 __global__ void __launch_bounds__(GC_THREADS) grad_norm_kernel(const double* __restrict__ part,
                                                                int n, float* __restrict__ norm) {
-  __shared__ double s[GC_THREADS / 32];
   pdl_wait();
   pdl_trigger();
-  const double v = norm_of(part, n, s);
-  if (threadIdx.x == 0) *norm = static_cast<float>(v);
+  const float v = norm_of(part, n);
+  if (threadIdx.x == 0) *norm = v;
 }
 
 // One vector of TI (16 bytes, or 8 where 16 bits widen to fp32, so that a store is 16).
@@ -178,16 +208,16 @@ __device__ __forceinline__ uint4 scale_vec(const std::conditional_t<sizeof(TI) =
   }
 }
 
-template <typename TI, typename TO>
+template <int CHUNK, typename TI, typename TO>
 __device__ __forceinline__ void scale_chunk(const TI* p, TO* o, int64_t n, int64_t chunk,
                                             float coef) {
   using V = std::conditional_t<sizeof(TI) == sizeof(TO), uint4, uint2>;
   constexpr int N = 16 / static_cast<int>(sizeof(TO));  // elements of a vector
-  constexpr int PER = GC_CHUNK / N / GC_THREADS;
-  constexpr int BATCH = 4;  // vectors in flight per thread (8 measured 1 to 6% slower)
+  constexpr int PER = CHUNK / N / GC_THREADS;
+  constexpr int BATCH = PER < 4 ? PER : 4;  // vectors in flight per thread (8 measured 1 to 6% slower)
   const int64_t head = head_of(p, n);
-  const int64_t a = head + chunk * GC_CHUNK;
-  const int len = static_cast<int>(n > a ? (n - a < GC_CHUNK ? n - a : GC_CHUNK) : 0);
+  const int64_t a = head + chunk * CHUNK;
+  const int len = static_cast<int>(n > a ? (n - a < CHUNK ? n - a : CHUNK) : 0);
   const int tid = threadIdx.x;
   int done = 0;
   if (reinterpret_cast<uintptr_t>(o + a) % 16 == 0) {
@@ -195,7 +225,7 @@ __device__ __forceinline__ void scale_chunk(const TI* p, TO* o, int64_t n, int64
     uint4* w = reinterpret_cast<uint4*>(o + a) + tid;
     const int nv = len / N;
     done = nv * N;
-    if (len == GC_CHUNK) {
+    if (len == CHUNK) {
 #pragma unroll 1
       for (int i0 = 0; i0 < PER; i0 += BATCH, v += BATCH * GC_THREADS, w += BATCH * GC_THREADS) {
         V q[BATCH];
@@ -227,14 +257,13 @@ __device__ __forceinline__ void scale_chunk(const TI* p, TO* o, int64_t n, int64
 // go backwards, from what the first pass left in L2.  The benchmark layer's gradients (604 M
 // bf16, into bf16) take 561 us forwards, 555 backwards, 543 with the first pass's streaming
 // loads: 3.6 GB moved at 6.67 TB/s.
-template <int N>
+template <typename L>
 __global__ void __launch_bounds__(GC_THREADS, GC_CTAS) grad_scale_kernel(
-    const __grid_constant__ GradList<N> g, const double* __restrict__ part, int n_part,
+    const __grid_constant__ L g, const double* __restrict__ part, int n_part,
     float max_norm, float eps, bool all_in_place, float* __restrict__ norm) {
-  __shared__ double s[GC_THREADS / 32];
   pdl_wait();
   pdl_trigger();
-  const float nrm = static_cast<float>(norm_of(part, n_part, s));
+  const float nrm = norm_of(part, n_part);
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = nrm;
   const float ratio = max_norm / (nrm + eps);
   const float coef = ratio > 1.f ? 1.f : ratio;  // a NaN stays one
@@ -250,20 +279,20 @@ __global__ void __launch_bounds__(GC_THREADS, GC_CTAS) grad_scale_kernel(
     const int64_t k = c - g.first[t], n = g.n[t];
     switch (g.dt[t]) {
       case MM_MOE_DT_BF16 | MM_MOE_DT_BF16 << 4:
-        scale_chunk(static_cast<const __nv_bfloat16*>(in), static_cast<__nv_bfloat16*>(out), n, k,
+        scale_chunk<L::CHUNK>(static_cast<const __nv_bfloat16*>(in), static_cast<__nv_bfloat16*>(out), n, k,
                     coef);
         break;
       case MM_MOE_DT_F16 | MM_MOE_DT_F16 << 4:
-        scale_chunk(static_cast<const __half*>(in), static_cast<__half*>(out), n, k, coef);
+        scale_chunk<L::CHUNK>(static_cast<const __half*>(in), static_cast<__half*>(out), n, k, coef);
         break;
       case MM_MOE_DT_BF16 | MM_MOE_DT_F32 << 4:
-        scale_chunk(static_cast<const __nv_bfloat16*>(in), static_cast<float*>(out), n, k, coef);
+        scale_chunk<L::CHUNK>(static_cast<const __nv_bfloat16*>(in), static_cast<float*>(out), n, k, coef);
         break;
       case MM_MOE_DT_F16 | MM_MOE_DT_F32 << 4:
-        scale_chunk(static_cast<const __half*>(in), static_cast<float*>(out), n, k, coef);
+        scale_chunk<L::CHUNK>(static_cast<const __half*>(in), static_cast<float*>(out), n, k, coef);
         break;
       default:
-        scale_chunk(static_cast<const float*>(in), static_cast<float*>(out), n, k, coef);
+        scale_chunk<L::CHUNK>(static_cast<const float*>(in), static_cast<float*>(out), n, k, coef);
     }
   }
 }
@@ -291,8 +320,8 @@ static bool grads_ok(const mm_moe_grad* g, int64_t n, bool clip) {
 }
 
 // Up to N tensors from i on into a list; returns the first one left out.
-template <int N>
-static int64_t fill_list(GradList<N>* l, const mm_moe_grad* g, int64_t i, int64_t n) {
+template <int N, int CHUNK>
+static int64_t fill_list(GradList<N, CHUNK>* l, const mm_moe_grad* g, int64_t i, int64_t n) {
   l->count = 0;
   int chunks = 0;
   for (; i < n && l->count < N; ++i) {
@@ -302,7 +331,7 @@ static int64_t fill_list(GradList<N>* l, const mm_moe_grad* g, int64_t i, int64_
     l->n[l->count] = g[i].numel;
     l->dt[l->count] = static_cast<uint8_t>(g[i].dtype | g[i].out_dtype << 4);
     l->first[l->count++] = chunks;
-    chunks += static_cast<int>((g[i].numel + GC_CHUNK - 1) / GC_CHUNK);
+    chunks += static_cast<int>((g[i].numel + CHUNK - 1) / CHUNK);
   }
   l->first[l->count] = chunks;
   return i;
@@ -313,12 +342,18 @@ static int64_t max_lists(int64_t n) { return n / GC_MAX + 1; }
 // f(list) over lists of all tensors; at least one call when `always`.
 template <typename F>
 static cudaError_t each_list(const mm_moe_grad* g, int64_t n, bool always, F f) {
-  if (n <= GC_FEW) {
-    GradList<GC_FEW> l;
+  const auto once = [&](auto l) {
     fill_list(&l, g, 0, n);
     return l.count > 0 || always ? f(l) : cudaSuccess;
+  };
+  if (n <= GC_FEW) {
+    int64_t total = 0;
+    for (int64_t i = 0; i < n; ++i) total += g[i].numel;
+    // (up to a short chunk for every SM)
+    if (total <= GC_SHORT * 152) return once(GradList<GC_FEW, GC_SHORT>{});
+    return once(GradList<GC_FEW, GC_CHUNK>{});
   }
-  GradList<GC_MAX> l;
+  GradList<GC_MAX, GC_CHUNK> l;
   cudaError_t e = cudaSuccess;
   for (int64_t i = 0; i < n && e == cudaSuccess; always = false) {
     i = fill_list(&l, g, i, n);
@@ -332,10 +367,10 @@ static cudaError_t launch_sq(const Ctx& c, const mm_moe_grad* g, int64_t n, doub
                              int* n_part) {
   *n_part = 0;
   return each_list(g, n, false, [&](const auto& l) {
-    constexpr int N = sizeof(l.in) / sizeof(l.in[0]);
+    using L = std::decay_t<decltype(l)>;
     const int grid = std::min(c.num_sms * GC_CTAS, l.first[l.count]);
     prof_begin(c, K_GRAD_SQ);
-    const cudaError_t e = launch_k(c.stream, grad_sq_kernel<N>, dim3(grid), dim3(GC_THREADS), 0, l,
+    const cudaError_t e = launch_k(c.stream, grad_sq_kernel<L>, dim3(grid), dim3(GC_THREADS), 0, l,
                                    part + *n_part);
     prof_end(c, K_GRAD_SQ);
     *n_part += grid;
@@ -388,11 +423,11 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_grad_clip(const mm_moe_grad* grads, i
   for (int64_t i = 0; i < n_tensors; ++i)
     in_place = in_place && (grads[i].numel == 0 || grads[i].out == grads[i].grad);
   const cudaError_t e = each_list(grads, n_tensors, true, [&](const auto& l) {
-    constexpr int N = sizeof(l.in) / sizeof(l.in[0]);
+    using L = std::decay_t<decltype(l)>;
     const int grid = std::max(1, std::min(c.num_sms * GC_CTAS, l.first[l.count]));
     prof_begin(c, K_GRAD_SCALE);
     const cudaError_t r =
-        launch_k(c.stream, grad_scale_kernel<N>, dim3(grid), dim3(GC_THREADS), 0, l,
+        launch_k(c.stream, grad_scale_kernel<L>, dim3(grid), dim3(GC_THREADS), 0, l,
                  static_cast<const double*>(part), n_part, max_norm, eps, in_place, norm);
     prof_end(c, K_GRAD_SCALE);
     return r;

@@ -177,3 +177,32 @@ def test_clip_tensor_past_32_bits():
     assert float(norm) == 13.0
     assert abs(float(g[-1]) - 1.5) <= 0.01 and abs(float(g[1 << 31]) - 6.0) <= 0.04
     assert int((g != 0).sum()) == 3
+
+
+def test_gradclip_single_low_bits():
+    """Subnormal fp32 values of one low bit each: their squares vanish in fp32."""
+    for bit in (0, 7, 15, 16, 22):
+        g = torch.full((1000,), 1 << bit, dtype=torch.int32, device="cuda").view(torch.float32)
+        want = 2.0 ** (bit - 149) * 1000 ** 0.5
+        got = float(MoEGradClip(1).norm([g]))
+        assert abs(got - want) <= 2.0 ** -149 + 2.0 ** -23 * want, (bit, got, want)
+
+
+@pytest.mark.parametrize("total", [4096 * 608, 4096 * 608 + 1])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp32")])
+def test_gradclip_around_the_short_chunks(total, dtype, out):
+    """Few tensors, in short chunks up to one for every CTA and in long ones above."""
+    dt = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+    sizes = [1, 4095, 4096, 4097, 16385]
+    sizes.append(total - sum(sizes))
+    gen = torch.Generator("cuda").manual_seed(total)
+    g = [torch.randn(n, device="cuda", generator=gen).to(dt[dtype]) for n in sizes]
+    o = [torch.empty(n, dtype=dt[out], device="cuda") for n in sizes]
+    norm = float(MoEGradClip(8).clip(g, 1.0, out=o))
+    want = float(sum((t.double() ** 2).sum() for t in g)) ** 0.5
+    assert abs(norm - want) <= 2.0 ** -20 * want     # fp32 sums of 64, fp64 beyond
+    coef = 1.0 / (want + 1e-6)
+    u = torch.finfo(dt[out]).eps / 2
+    for a, b in zip(o, g):
+        ref = b.double() * coef
+        assert ((a.double() - ref).abs() <= (u + 2.0 ** -19) * ref.abs() + 2.0 ** -25).all()
