@@ -14,8 +14,8 @@ namespace mmmoe {
 // ------------------------------------------------------------------------- forward
 // A thread with up to 16 columns holds its parameters in registers; with more columns a
 // row needs fewer threads, so fewer sums across warps (none up to 2048 columns of 16 bits:
-// 16384 x 2048 bf16 takes 31.8 us with 128 threads a row, 16 columns each, 22.6 us with a
-// warp a row), and the parameters come from shared memory.  Where several warps share a
+// 16384 x 2048 bf16 takes 31.8 us with 128 threads a row, 16 columns each, 22.4 us with a
+// warp a row, 0.88 of the copy rate), and the parameters come from shared memory.  Where several warps share a
 // row and registers allow it, a group takes two rows at a time (ROWS), so that two share
 // the two barriers.
 template <typename T, typename P, int NU, Cut CUT, int ROWS>
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_fwd_kernel(
 }
 
 // One CTA per row; the row is read three times (sum, centred squares, output), the
-// second and third time from L1/L2.
+// second and third time from L1/L2.  2048 x 16384 bf16: 34.0 us, 0.58 of the copy rate.
 template <typename T, typename P, bool VEC>
 __global__ void __launch_bounds__(LOOP_THREADS) norm_fwd_loop_kernel(
     Rows<const T> x, Rows<T> y, int T_, int H, const P* __restrict__ w, const P* __restrict__ b,

@@ -18,6 +18,9 @@ namespace mmmoe {
 // whose sums meet at one barrier: two where shared memory holds two steps of them.  Their
 // x and dy are then read from the ring and unpacked a second time, which costs fewer
 // cycles than the barrier's wait with one row in flight.
+// 16384 x 2048 bf16 with a residual gradient: 45.9 us together with the launch that ends it, 0.86
+// of the copy rate (HBM, 6 us of ramps and that launch); 8191 x 4096 fp16 39.5 us, bound by the
+// barrier of eight warps and by issue.
 template <typename T, int NU, Cut CUT, bool ADD, int ROWS>
 __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
     Rows<const T> dy, Rows<const T> x, Rows<const T> add, Rows<T> dx, const void* __restrict__ w,
@@ -234,6 +237,8 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_bwd_kernel(
   }
 }
 
+// dx, one CTA per row, x and dy read twice; with the column sums below, which read them a third
+// time, 2048 x 16384 bf16 takes 106 us, 0.37 of the copy rate.
 template <typename T, typename P, bool VEC>
 __global__ void __launch_bounds__(LOOP_THREADS) norm_dx_loop_kernel(
     Rows<const T> dy, Rows<const T> x, const P* __restrict__ w, const float* __restrict__ mean,
@@ -316,7 +321,8 @@ __global__ void __launch_bounds__(256) norm_cols_loop_kernel(Rows<const T> dy, R
 }
 
 // dweight (blockIdx.y 0) / dbias (1) from n partial rows: 16 warps take every 16th row of
-// 32 columns, ten loads in flight each, and are added in order.
+// 32 columns, ten loads in flight each, and are added in order.  About 3 us of latency for the
+// 2.5 MB of 152 rows of 2048 columns.
 template <typename P>
 __global__ void __launch_bounds__(512) norm_cols_finish_kernel(const float* __restrict__ part,
                                                                int n, int H, P* __restrict__ dw,
