@@ -270,8 +270,10 @@ static cudaError_t fwd_launch(const Ctx& c, Rows<const T> x, Rows<T> y, int T_, 
   const int nt = n.GT * n.groups;
   const size_t smem = static_cast<size_t>(RING) * nt + shared;
   const bool even = even_rows(x, T_) && H % VN<T> == 0;
+  // (fp32 rows on 16-byte boundaries have at most four units a thread)
+  constexpr Cut WHOLE = sizeof(T) == 4 && NU > 4 ? ANY : EVEN;
   auto* kern =
-      even ? norm_fwd_kernel<T, P, NU, EVEN, ROWS> : norm_fwd_kernel<T, P, NU, ANY, ROWS>;
+      even ? norm_fwd_kernel<T, P, NU, WHOLE, ROWS> : norm_fwd_kernel<T, P, NU, ANY, ROWS>;
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
   return launch_k(c.stream, kern, dim3(n.ctas), dim3(nt), smem, x, y, T_, H, n.GT, w, b, eps, mean,
