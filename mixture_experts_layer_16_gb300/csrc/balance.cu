@@ -400,6 +400,10 @@ __device__ __forceinline__ float sequence_loss(float dot, int n, float per) {
   return n > 0 ? dot * per / (nf * nf) : 0.f;
 }
 
+// Sequences up to which a single CTA gives the call's results by itself.  (One token makes one CTA
+// at any G: with more sequences the joining launch writes their results.)
+constexpr int BAL_ALONE_SEQS = 2;
+
 // What the call returns.
 struct BalOut {
   float* losses;     // [2]
@@ -433,7 +437,7 @@ __global__ void __launch_bounds__(BAL_THREADS, NV >= 8 ? 1 : 2) balance_fwd_kern
   const int64_t t1 = min(T_, t0 + chunk);
   R ring;
   ring.init(smem, l, E, k);
-  const bool alone = gridDim.x == 1;  // (then its results are the call's)
+  const bool alone = gridDim.x == 1 && G <= BAL_ALONE_SEQS;  // (then its results are the call's)
   const float per = static_cast<float>(E) / static_cast<float>(k);
   BalTotals all{};
   if (blockIdx.x == 0 && tid == 0) *parts.arrived = 0;
@@ -1035,7 +1039,7 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_balance_forward(
   });
   prof_end(c, K_BALANCE_FWD);
   if (e != cudaSuccess) return MM_MOE_ECUDA;
-  if (b.nb == 1) return MM_MOE_OK;
+  if (b.nb == 1 && G <= BAL_ALONE_SEQS) return MM_MOE_OK;
   // The first kernel where a sequence has many pieces and all its CTAs run at once (us, first
   // and second: 131072 x 128 16 sequences, 19 pieces each, 21.3 and 23.7, 64 sequences, 5
   // pieces, 26.0 and 23.1; 32768 x 256 in 32, 256 CTAs, 19.8 and 17.6; one sequence, whose
