@@ -99,6 +99,11 @@ __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Lets `kern` be launched with so much dynamic shared memory on the current device.  The limit
+// belongs to the kernel, for all host threads, so it is only ever raised: set back to a smaller
+// call's size, it would refuse a larger launch that another thread is about to make.
+cudaError_t raise_smem_limit(const void* kern, size_t bytes);
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_k(cudaStream_t st, void (*kern)(KArgs...), dim3 grid, dim3 block,
                      size_t smem, Args... args) {

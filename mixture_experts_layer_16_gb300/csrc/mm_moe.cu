@@ -4,7 +4,10 @@
 
 #include <cstdint>
 #include <cstdlib>
+#include <map>
 #include <mutex>
+#include <new>
+#include <utility>
 
 #include "internal.h"
 
@@ -18,6 +21,25 @@ bool sm_pairs_enabled() {
     return !(v != nullptr && v[0] == '0');
   }();
   return on;
+}
+
+cudaError_t raise_smem_limit(const void* kern, size_t bytes) {
+  static std::mutex mu;
+  static std::map<std::pair<int, const void*>, size_t> limits;  // by device and kernel
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  try {
+    const std::lock_guard<std::mutex> lock(mu);
+    size_t& limit = limits[{dev, kern}];
+    if (bytes <= limit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(bytes));
+    if (e == cudaSuccess) limit = bytes;
+    return e;
+  } catch (const std::bad_alloc&) {
+    return cudaErrorMemoryAllocation;
+  }
 }
 
 // Bytes of one quantised copy of a [rows, cols] operand: e4m3 codes (rows * cols bytes)

@@ -157,8 +157,7 @@ inline int sm_count_103() {
 template <typename K>
 inline cudaError_t allow_smem(K* kern, size_t bytes) {
   if (bytes <= 40 * 1024) return cudaSuccess;  // within the default 48 KB, static part included
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(bytes));
+  return raise_smem_limit(reinterpret_cast<const void*>(kern), bytes);
 }
 
 template <typename V>
