@@ -464,7 +464,7 @@ cudaError_t launch_permute(const Ctx& c, const Layout& L, const uint16_t* src, v
   auto* kern = quant == QS_MX      ? permute_rows_kernel<QS_MX>
                : quant == QS_BLOCK ? permute_rows_kernel<QS_BLOCK>
                                    : permute_rows_kernel<QS_NONE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   const int per_sm = std::max(1, std::min(16, (200 * 1024) / (smem + 1024)));
   prof_begin(c, kernel_id);
