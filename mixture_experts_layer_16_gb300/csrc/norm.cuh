@@ -335,6 +335,11 @@ int group_threads(int H, bool even) {
   return g;
 }
 
+// a / b rounded up (the rows go up to 2^31 - 1, so the sum does not fit 32 bits)
+inline int div_up(int a, int b) {
+  return static_cast<int>((static_cast<int64_t>(a) + b - 1) / b);
+}
+
 struct NormGrid {
   int GT, groups, ctas;
 };
@@ -345,9 +350,9 @@ inline NormGrid norm_grid(int GT, int T, int sms, int most_groups = NORM_THREADS
   sms = std::max(8, sms / 8 * 8);
   const int per_warp = GT < 32 ? 32 / GT : 1;
   const int most = std::min(most_groups, NORM_THREADS / GT);
-  int groups = std::min(most, (T + sms - 1) / sms);
+  int groups = std::min(most, div_up(T, sms));
   groups = (groups + per_warp - 1) / per_warp * per_warp;
-  return NormGrid{GT, groups, std::min(sms, (T + groups - 1) / groups)};
+  return NormGrid{GT, groups, std::min(sms, div_up(T, groups))};
 }
 
 template <typename T>

@@ -472,8 +472,8 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
     if (e != cudaSuccess) return MM_MOE_ECUDA;
     const int cols = (H / (vec ? VN<T> : 1) + 255) / 256;
     const int want = std::min(norm_parts(T_), std::max(1, c.num_sms * 8 / cols));
-    const int rows = (T_ + want - 1) / want;
-    n = (T_ + rows - 1) / rows;
+    const int rows = div_up(T_, want);
+    n = div_up(T_, rows);
     prof_begin(c, K_NORM_BWD);
     e = launch_k(c.stream, vec ? norm_cols_loop_kernel<T, true> : norm_cols_loop_kernel<T, false>,
                  dim3(cols, n), dim3(256), 0, a.dy, a.x, mean, rstd, T_, H, rows, part);
