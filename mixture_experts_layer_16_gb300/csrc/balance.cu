@@ -1038,7 +1038,7 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_balance_forward(
     });
   });
   prof_end(c, K_BALANCE_FWD);
-  if (e != cudaSuccess) return MM_MOE_ECUDA;
+  if (e != cudaSuccess) return op_status(e);
   if (b.nb == 1 && G <= BAL_ALONE_SEQS) return MM_MOE_OK;
   // The first kernel where a sequence has many pieces and all its CTAs run at once (us, first
   // and second: 131072 x 128 16 sequences, 19 pieces each, 21.3 and 23.7, 64 sequences, 5
@@ -1052,7 +1052,7 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_balance_forward(
                dim3(few ? JOIN_THREADS : std::min(JOIN_MANY_THREADS, (E + 31) / 32 * 32)), 0,
                seq_offsets, shape->T, E, k, G, b.chunk, parts, out);
   prof_end(c, K_BALANCE_FINISH);
-  return e == cudaSuccess ? MM_MOE_OK : MM_MOE_ECUDA;
+  return op_status(e);
 }
 
 extern "C" MM_MOE_API mm_moe_status mm_moe_balance_backward(
@@ -1090,5 +1090,5 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_balance_backward(
     });
   });
   prof_end(c, K_BALANCE_BWD);
-  return e == cudaSuccess ? MM_MOE_OK : MM_MOE_ECUDA;
+  return op_status(e);
 }

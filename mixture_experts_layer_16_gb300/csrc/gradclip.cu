@@ -399,12 +399,13 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_grad_norm(const mm_moe_grad* grads, i
   const Ctx c{static_cast<cudaStream_t>(stream), sms, &launches};
   double* part = static_cast<double*>(workspace);
   int n_part = 0;
-  if (launch_sq(c, grads, n_tensors, part, &n_part) != cudaSuccess) return MM_MOE_ECUDA;
+  cudaError_t e = launch_sq(c, grads, n_tensors, part, &n_part);
+  if (e != cudaSuccess) return op_status(e);
   prof_begin(c, K_GRAD_NORM);
-  const cudaError_t e = launch_k(c.stream, grad_norm_kernel, dim3(1), dim3(GC_THREADS), 0,
-                                 static_cast<const double*>(part), n_part, norm);
+  e = launch_k(c.stream, grad_norm_kernel, dim3(1), dim3(GC_THREADS), 0,
+               static_cast<const double*>(part), n_part, norm);
   prof_end(c, K_GRAD_NORM);
-  return e == cudaSuccess ? MM_MOE_OK : MM_MOE_ECUDA;
+  return op_status(e);
 }
 
 extern "C" MM_MOE_API mm_moe_status mm_moe_grad_clip(const mm_moe_grad* grads, int64_t n_tensors,
@@ -419,11 +420,12 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_grad_clip(const mm_moe_grad* grads, i
   const Ctx c{static_cast<cudaStream_t>(stream), sms, &launches};
   double* part = static_cast<double*>(workspace);
   int n_part = 0;
-  if (launch_sq(c, grads, n_tensors, part, &n_part) != cudaSuccess) return MM_MOE_ECUDA;
+  cudaError_t e = launch_sq(c, grads, n_tensors, part, &n_part);
+  if (e != cudaSuccess) return op_status(e);
   bool in_place = true;
   for (int64_t i = 0; i < n_tensors; ++i)
     in_place = in_place && (grads[i].numel == 0 || grads[i].out == grads[i].grad);
-  const cudaError_t e = each_list(grads, n_tensors, true, [&](const auto& l) {
+  e = each_list(grads, n_tensors, true, [&](const auto& l) {
     using L = std::decay_t<decltype(l)>;
     const int grid = std::max(1, std::min(c.num_sms * GC_CTAS, l.first[l.count]));
     prof_begin(c, K_GRAD_SCALE);
@@ -433,5 +435,5 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_grad_clip(const mm_moe_grad* grads, i
     prof_end(c, K_GRAD_SCALE);
     return r;
   });
-  return e == cudaSuccess ? MM_MOE_OK : MM_MOE_ECUDA;
+  return op_status(e);
 }

@@ -369,7 +369,7 @@ static mm_moe_status norm_forward(const Ctx& c, const mm_moe_norm_shape* s, cons
   prof_begin(c, K_NORM_FWD);
   const cudaError_t e = pick();
   prof_end(c, K_NORM_FWD);
-  return e == cudaSuccess ? MM_MOE_OK : MM_MOE_ECUDA;
+  return op_status(e);
 }
 
 }  // namespace mmmoe

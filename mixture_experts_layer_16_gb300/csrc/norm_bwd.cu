@@ -457,7 +457,7 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
     };
     e = pick();
     prof_end(c, K_NORM_BWD);
-    if (e != cudaSuccess) return MM_MOE_ECUDA;
+    if (e != cudaSuccess) return op_status(e);
     if (n == 1) return MM_MOE_OK;  // (the only CTA has written them)
   } else {
     const bool vec = even && even_rows(a.dy, T_) && even_rows(a.dx, T_) && H % VN<T> == 0 &&
@@ -469,7 +469,7 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
                  dim3(std::min(T_, c.num_sms * 4)), dim3(LOOP_THREADS), 0, a.dy, a.x,
                  static_cast<const P*>(w), mean, rstd, a.add, a.dx, T_, H);
     prof_end(c, K_NORM_BWD);
-    if (e != cudaSuccess) return MM_MOE_ECUDA;
+    if (e != cudaSuccess) return op_status(e);
     const int cols = (H / (vec ? VN<T> : 1) + 255) / 256;
     const int want = std::min(norm_parts(T_), std::max(1, c.num_sms * 8 / cols));
     const int rows = div_up(T_, want);
@@ -478,14 +478,14 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
     e = launch_k(c.stream, vec ? norm_cols_loop_kernel<T, true> : norm_cols_loop_kernel<T, false>,
                  dim3(cols, n), dim3(256), 0, a.dy, a.x, mean, rstd, T_, H, rows, part);
     prof_end(c, K_NORM_BWD);
-    if (e != cudaSuccess) return MM_MOE_ECUDA;
+    if (e != cudaSuccess) return op_status(e);
   }
   prof_begin(c, K_NORM_BWD_FINISH);
   e = launch_k(c.stream, norm_cols_finish_kernel<P>, dim3((H + 31) / 32, db != nullptr ? 2 : 1),
                dim3(512), 0, static_cast<const float*>(part), n, H, static_cast<P*>(dw),
                static_cast<P*>(db));
   prof_end(c, K_NORM_BWD_FINISH);
-  return e == cudaSuccess ? MM_MOE_OK : MM_MOE_ECUDA;
+  return op_status(e);
 }
 
 }  // namespace mmmoe

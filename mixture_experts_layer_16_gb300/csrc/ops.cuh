@@ -153,6 +153,14 @@ inline int sm_count_103() {
   return n;
 }
 
+// A call's status.  The error of a failed one is taken off the host thread, whose next CUDA call
+// would report it as its own.
+inline mm_moe_status op_status(cudaError_t e) {
+  if (e == cudaSuccess) return MM_MOE_OK;
+  cudaGetLastError();
+  return MM_MOE_ECUDA;
+}
+
 // Lets `kern` be launched with so much dynamic shared memory.
 template <typename K>
 inline cudaError_t allow_smem(K* kern, size_t bytes) {
