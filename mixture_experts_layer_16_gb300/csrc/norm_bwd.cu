@@ -429,13 +429,14 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
       group_threads<T, MOST>(H, even) != 0) {
     prof_begin(c, K_NORM_BWD);
     const auto pick = [&]() -> cudaError_t {
-      constexpr int WIDE = sizeof(T) == 2 ? 2 : 4;
       // few rows: one unit a thread, in up to half of a CTA's groups (us, in two units and so:
       // 153 x 1024 bf16 5.1 and 4.3, 300 x 512 5.0 and 4.2; in all of them 300 x 2048 6.2 and
-      // 6.6, 1200 x 512 5.1 and 6.2)
-      const int g1 = group_threads<T, 1>(H, even);
+      // 6.6, 1200 x 512 5.1 and 6.2), unless a single CTA takes them in two units a thread.  (Not
+      // in fp32's four, in which it would take twice as many rows: 16 x 1024 3.2 us in one unit,
+      // 6.0 in one CTA; 9 x 1000 3.1 and 5.5; 5 x 2048 3.5 and 6.1.)
+      const int g1 = group_threads<T, 1>(H, even), g2 = group_threads<T, 2>(H, even);
       if (g1 != 0 && T_ <= c.num_sms / 8 * 8 * std::max(1, NORM_THREADS / g1 / 2) &&
-          !one_cta(group_threads<T, WIDE>(H, even), T_, even))
+          !one_cta(g2, T_, even))
         return bwd_launch<T, 1, 1>(c, a, &n);
       if constexpr (sizeof(T) == 2) {
         // 16 bits: three units a thread where that doubles the CTA's groups, or no CTA holds the
@@ -443,7 +444,7 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
         // 52.4 and 44.6; with 8 groups for 5, 5000 x 1111 18.4 and 21.5; narrow rows, 20000 x
         // 72 9.1 and 10.3; row by row and so 4096 x 8191 207.6 and 69.9, 2600 x 12288 106.2
         // and 48.5)
-        const int g2 = group_threads<T, 2>(H, even), g3 = group_threads<T, 3>(H, even);
+        const int g3 = group_threads<T, 3>(H, even);
         if (g2 == 0 || (H > 128 && NORM_THREADS / g3 >= 2 * (NORM_THREADS / g2)))
           return bwd_launch<T, 3, 1>(c, a, &n);
         // two rows a barrier where more than two warps share a row (8191 x 4096
@@ -451,8 +452,7 @@ static mm_moe_status norm_backward(const Ctx& c, const mm_moe_norm_shape* s, con
         // -> 46.3 us)
         return g2 > 64 ? bwd_launch<T, 2, 2>(c, a, &n) : bwd_launch<T, 2, 1>(c, a, &n);
       } else {
-        return group_threads<T, 2>(H, even) != 0 ? bwd_launch<T, 2, 1>(c, a, &n)
-                                                 : bwd_launch<T, 4, 1>(c, a, &n);
+        return g2 != 0 ? bwd_launch<T, 2, 1>(c, a, &n) : bwd_launch<T, 4, 1>(c, a, &n);
       }
     };
     e = pick();
