@@ -326,11 +326,12 @@ MM_MOE_API mm_moe_status mm_moe_norm_forward(const mm_moe_norm_shape* shape, con
  *   dx = rstd (g - 1/H sum g - xh 1/H sum g xh)  [+ dx_add]
  *   dweight = sum_t dy xh,  dbias = sum_t dy
  *   dx_add   [T, H] or NULL: a gradient that joins dx (the residual path's), added in fp32
- *   dx       [T, H] out; may equal dx_add when the strides are equal, must not overlap
- *            dy or x
+ *   dx       [T, H] out; may equal dx_add when the strides are equal (and not overlap it
+ *            otherwise), must not overlap dy or x
  *   dweight  [H] out;  dbias [H] out or NULL (overwritten, not accumulated)
  *   workspace  of mm_moe_norm_workspace_size, 16-byte aligned
- * All sums have a fixed order: bitwise deterministic. */
+ * Overlaps of rows equally far apart or dense are refused (MM_MOE_EINVAL) in both calls.  All sums
+ * have a fixed order: bitwise deterministic. */
 MM_MOE_API mm_moe_status mm_moe_norm_backward(
     const mm_moe_norm_shape* shape, const void* dy, int64_t lddy, const void* x, int64_t ldx,
     const void* weight, const float* mean, const float* rstd, const void* dx_add, int64_t ldadd,

@@ -393,6 +393,8 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_norm_forward(const mm_moe_norm_shape*
   if (!rows_ok(x, ldx, shape) || !rows_ok(y, ldy, shape) || !vec_ok(weight, pb) ||
       (bias != nullptr && !vec_ok(bias, pb)) || !vec_ok(mean, 4) || !vec_ok(rstd, 4))
     return MM_MOE_EINVAL;
+  if (!same_rows(x, ldx, y, ldy, shape->T) && rows_overlap(x, ldx, y, ldy, shape))
+    return MM_MOE_EINVAL;
   const int sms = std::min(152, sm_count_103());
   if (sms == 0) return MM_MOE_ENOTSUP;
   int launches = 0;

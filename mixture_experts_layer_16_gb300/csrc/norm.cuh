@@ -15,6 +15,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
+#include <utility>
 
 #include "internal.h"
 #include "ops.cuh"
@@ -307,6 +308,29 @@ inline bool rows_ok(const void* p, int64_t ld, const mm_moe_norm_shape* s) {
   return p != nullptr && reinterpret_cast<uintptr_t>(p) % dtype_bytes(s->dtype) == 0 &&
          (ld >= s->H || s->T == 1) && ld < (int64_t{1} << 40);
 }
+// Whether operands a and b of T rows of H elements share memory: b's rows (a's, where they begin
+// first) against the other's.  Exact for rows equally far apart and for dense ones; of others, the
+// first row of the operand that begins later.
+inline bool rows_overlap(const void* a, int64_t lda, const void* b, int64_t ldb,
+                         const mm_moe_norm_shape* s) {
+  if (s->T == 1) lda = ldb = s->H;
+  if (reinterpret_cast<uintptr_t>(b) < reinterpret_cast<uintptr_t>(a)) {
+    std::swap(a, b);
+    std::swap(lda, ldb);
+  }
+  const int64_t d = static_cast<int64_t>(
+      (reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)) / dtype_bytes(s->dtype));
+  // (2^31 rows 2^40 elements apart leave 64 bits)
+  if (d >= static_cast<__int128>(s->T - 1) * lda + s->H) return false;
+  const int64_t row = d / lda;  // where b begins
+  if (d - row * lda < s->H) return true;
+  return row + 1 < s->T && (row + 1) * lda < d + (ldb == s->H ? s->T * s->H : s->H);
+}
+// the same rows: what is written over them element by element
+inline bool same_rows(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t T) {
+  return a == b && (T == 1 || lda == ldb);
+}
+
 inline bool vec_ok(const void* p, size_t a) {
   return p != nullptr && reinterpret_cast<uintptr_t>(p) % a == 0;
 }

@@ -503,6 +503,11 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_norm_backward(
       !vec_ok(mean, 4) || !vec_ok(rstd, 4) || !vec_ok(dweight, pb) ||
       (dbias != nullptr && !vec_ok(dbias, pb)) || !vec_ok(workspace, 16))
     return MM_MOE_EINVAL;
+  // (dx over dx_add is read and written element by element; x and dy are read again)
+  if (rows_overlap(dx, lddx, x, ldx, shape) || rows_overlap(dx, lddx, dy, lddy, shape) ||
+      (dx_add != nullptr && !same_rows(dx, lddx, dx_add, ldadd, shape->T) &&
+       rows_overlap(dx, lddx, dx_add, ldadd, shape)))
+    return MM_MOE_EINVAL;
   const int sms = std::min(152, sm_count_103());
   if (sms == 0) return MM_MOE_ENOTSUP;
   int launches = 0;

@@ -102,6 +102,7 @@ class MoELayerNorm:
 
     def forward(self, x, weight, bias=None, y: Optional[torch.Tensor] = None,
                 stream=None) -> torch.Tensor:
+        """y may be x itself (in place); rows that overlap otherwise are refused (MoEError)."""
         self._check_rows(x, "x")
         self._check_params(weight, bias)
         if y is None:
@@ -116,7 +117,7 @@ class MoELayerNorm:
                  ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
         """Gradients (dx, dweight, dbias) of the last forward, whose x and weight are given
         again (dbias None without a bias).  dx_add: a gradient that joins dx (the residual
-        path's); dx may be written over it (out)."""
+        path's); dx may be written over it (out), but not over x or dy (MoEError)."""
         self._check_rows(dy, "dy")
         self._check_rows(x, "x")
         self._check_param(weight, "weight")
