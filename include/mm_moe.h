@@ -375,7 +375,8 @@ MM_MOE_API mm_moe_status mm_moe_balance_forward(
  * forward's arguments, its counts, tokens and workspace):
  *   dlosses  [2] fp32 on the device
  *   dlogits  [T, E] out (overwritten; zero where a token does not count); must not
- *            overlap logits.  mm_moe_router_backward_aux takes it (fp32). */
+ *            overlap logits (MM_MOE_EINVAL).  mm_moe_router_backward_aux takes it
+ *            (fp32). */
 MM_MOE_API mm_moe_status mm_moe_balance_backward(
     const mm_moe_balance_shape* shape, const void* logits, const int32_t* seq_offsets,
     const uint8_t* mask, const int32_t* counts, const int32_t* tokens, const float* dlosses,

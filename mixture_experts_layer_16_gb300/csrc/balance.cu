@@ -1065,6 +1065,9 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_balance_backward(
       !al(dlosses, 4) || !al(workspace, 16) ||
       (seq_offsets == nullptr ? shape->G != 1 : !al(seq_offsets, 4)))
     return MM_MOE_EINVAL;
+  const auto lg_at = reinterpret_cast<uintptr_t>(logits), d_at = reinterpret_cast<uintptr_t>(dlogits);
+  const uintptr_t size = static_cast<uintptr_t>(shape->T) * shape->E * es;
+  if (d_at < lg_at + size && lg_at < d_at + size) return MM_MOE_EINVAL;
   const int sms = sm_count_103();
   if (sms == 0) return MM_MOE_ENOTSUP;
   int launches = 0;

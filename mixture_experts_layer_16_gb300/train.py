@@ -190,7 +190,7 @@ class MoEBalanceLoss:
                  dlogits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """The logit gradient of dlosses[0] balance + dlosses[1] z (dlosses [2] fp32 on the
         device) of the last forward, whose logits, seq_offsets and mask are given again.
-        MoERouter.backward takes it as dlogits_aux."""
+        MoERouter.backward takes it as dlogits_aux.  It must not overlap the logits (MoEError)."""
         self._check(logits, seq_offsets, mask)
         self._need(dlosses, "dlosses", _TWO, torch.float32)
         if dlogits is None:

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from mixture_experts_layer_16_gb300 import MoELayerNorm
+from mixture_experts_layer_16_gb300 import MoEBalanceLoss, MoELayerNorm
 from mixture_experts_layer_16_gb300.binding import MoEError
 from tests import gpu_util as G
 
@@ -53,3 +53,20 @@ def test_norm_operands_between_and_over_one_another(T, H):
     n.forward(x, w, b)
     got = n.backward(dy, x, w, dx_add=x2, out=(x2, dw.clone(), db.clone()))
     assert torch.equal(got[0], dx) and torch.equal(got[1], dw)
+
+
+@pytest.mark.parametrize("E", [8, 33])
+def test_balance_gradient_beside_the_logits(E):
+    T, k = 200, 2
+    both = torch.zeros((2 * T + 1, E), device="cuda")
+    lg, d = both[:T], both[T:2 * T]
+    lg.normal_()
+    idx = torch.topk(lg, k, dim=1).indices.to(torch.int32).contiguous()
+    dl = torch.tensor([1.0, 0.5], device="cuda")
+    h = MoEBalanceLoss(T, E, k)
+    h.forward(lg, idx)
+    want = h.backward(lg, dl)
+    assert torch.equal(h.backward(lg, dl, dlogits=d), want) and not both[2 * T].any()
+    for over in (lg, both[T - 1:2 * T - 1], both[1:T + 1]):
+        with pytest.raises(MoEError):
+            h.backward(lg, dl, dlogits=over)

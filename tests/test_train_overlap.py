@@ -37,3 +37,12 @@ def test_norm_overlaps_are_refused(lib, at, ld, ldo):
                                     P[5], P[6], P[7], None) == EI
     assert lib.mm_moe_norm_backward(s, P[0], 8, P[9], ldo, P[2], P[3], P[4], None, 0, other, ld,
                                     P[5], P[6], P[7], None) == EI
+
+
+@pytest.mark.parametrize("dtype,size", [(B.MM_MOE_DT_F32, 4), (B.MM_MOE_DT_F16, 2)])
+@pytest.mark.parametrize("at", [0, 1, -1, 8, 127, -127])
+def test_balance_gradient_over_the_logits_is_refused(lib, at, dtype, size):
+    s = ctypes.byref(B.BalanceShape(16, 8, 2, 1, dtype))
+    P = [A * (i + 1) for i in range(8)]
+    assert lib.mm_moe_balance_backward(s, P[0], None, None, P[1], P[2], P[3], P[0] + size * at, P[4],
+                                       None) == EI
