@@ -83,6 +83,7 @@ class MoELayerNorm:
         self.rstd = torch.empty(T, dtype=torch.float32, device=self.device)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
         self._rows, self._cols = torch.Size((T, H)), torch.Size((H,))
+        self._ran = False  # a forward has left what a backward reads
         self._where = -1 if self.device.index is None else self.device.index
 
     def _check_rows(self, t, name):
@@ -111,6 +112,7 @@ class MoELayerNorm:
             self._check_rows(y, "y")
         B.mm_moe_norm_forward(self.shape, x, weight, bias, y, self.mean, self.rstd,
                               _stream(stream, self.device))
+        self._ran = True
         return y
 
     def backward(self, dy, x, weight, dx_add=None, out=None, stream=None
@@ -129,6 +131,8 @@ class MoELayerNorm:
         else:
             self._check_rows(out[0], "dx")
             self._check_params(out[1], out[2], "d")
+        if not self._ran:
+            raise RuntimeError("backward needs a forward first")
         dx, dweight, dbias = out
         B.mm_moe_norm_backward(self.shape, dy, x, weight, self.mean, self.rstd, dx_add, dx,
                                dweight, dbias, self.workspace, _stream(stream, self.device))
@@ -162,6 +166,7 @@ class MoEBalanceLoss:
         self.workspace = torch.empty(n, dtype=torch.uint8, device=d)
         self._rows, self._slots = torch.Size((T, E)), torch.Size((T, k))
         self._tokens, self._offsets = torch.Size((T,)), torch.Size((sequences + 1,))
+        self._ran = False  # a forward has left what a backward reads
         self._where = -1 if d.index is None else d.index
 
     def _need(self, t, name, shape, dtype):
@@ -184,6 +189,7 @@ class MoEBalanceLoss:
         B.mm_moe_balance_forward(self.shape, logits, topk_idx, seq_offsets, mask, self.losses,
                                  self.seq_loss, self.counts, self.tokens, self.lse,
                                  self.workspace, _stream(stream, self.device))
+        self._ran = True
         return self.losses, self.counts
 
     def backward(self, logits, dlosses, seq_offsets=None, mask=None,
@@ -197,6 +203,8 @@ class MoEBalanceLoss:
             dlogits = torch.empty_like(logits)
         else:
             self._need(dlogits, "dlogits", self._rows, self.dtype)
+        if not self._ran:
+            raise RuntimeError("backward needs a forward first")
         B.mm_moe_balance_backward(self.shape, logits, seq_offsets, mask, self.counts, self.tokens,
                                   dlosses, dlogits, self.workspace, _stream(stream, self.device))
         return dlogits
