@@ -3,7 +3,9 @@ MoEBalanceLoss on the router's logits, MoEGradClip over the step's gradients.
 
 Like MoELayer these are handles that own their small device buffers (torch allocations),
 check tensor dtypes, shapes and devices, and forward every call to the C ABI.  No
-arithmetic happens here.
+arithmetic happens here.  `stream` is the stream a call runs on (a torch stream or a raw handle;
+the current one by default).  The caller orders it after what made the call's tensors, and after
+the current stream, from whose memory the handle's own and the returned ones come.
 """
 from __future__ import annotations
 
@@ -33,10 +35,19 @@ def _dtype(name: str) -> torch.dtype:
     return TORCH_DTYPE[name]
 
 
-def _stream(stream, device: torch.device) -> int:
+def _stream(stream, device: torch.device, *mine: Optional[torch.Tensor]) -> int:
+    """The stream of a call, the current one unless the caller names another.  `mine`: the tensors
+    that the handle holds or made for this call, from the current stream's memory; on another
+    stream they are marked as in use there, so that none of it is handed out again before that
+    stream is done with it."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device.index)
-    return int(getattr(stream, "cuda_stream", stream))
+    raw = int(getattr(stream, "cuda_stream", stream))
+    where = torch.cuda.ExternalStream(raw, device=device)
+    for t in mine:
+        if t is not None:
+            t.record_stream(where)
+    return raw
 
 
 def _plain(t, shape: torch.Size, dtype, where: int) -> bool:
@@ -111,7 +122,7 @@ class MoELayerNorm:
         else:
             self._check_rows(y, "y")
         B.mm_moe_norm_forward(self.shape, x, weight, bias, y, self.mean, self.rstd,
-                              _stream(stream, self.device))
+                              _stream(stream, self.device, y, self.mean, self.rstd))
         self._ran = True
         return y
 
@@ -135,7 +146,9 @@ class MoELayerNorm:
             raise RuntimeError("backward needs a forward first")
         dx, dweight, dbias = out
         B.mm_moe_norm_backward(self.shape, dy, x, weight, self.mean, self.rstd, dx_add, dx,
-                               dweight, dbias, self.workspace, _stream(stream, self.device))
+                               dweight, dbias, self.workspace,
+                               _stream(stream, self.device, dx, dweight, dbias, self.mean,
+                                       self.rstd, self.workspace))
         return dx, dweight, dbias
 
 
@@ -188,7 +201,9 @@ class MoEBalanceLoss:
         self._need(topk_idx, "topk_idx", self._slots, torch.int32)
         B.mm_moe_balance_forward(self.shape, logits, topk_idx, seq_offsets, mask, self.losses,
                                  self.seq_loss, self.counts, self.tokens, self.lse,
-                                 self.workspace, _stream(stream, self.device))
+                                 self.workspace,
+                                 _stream(stream, self.device, self.losses, self.seq_loss,
+                                         self.counts, self.tokens, self.lse, self.workspace))
         self._ran = True
         return self.losses, self.counts
 
@@ -206,7 +221,9 @@ class MoEBalanceLoss:
         if not self._ran:
             raise RuntimeError("backward needs a forward first")
         B.mm_moe_balance_backward(self.shape, logits, seq_offsets, mask, self.counts, self.tokens,
-                                  dlosses, dlogits, self.workspace, _stream(stream, self.device))
+                                  dlosses, dlogits, self.workspace,
+                                  _stream(stream, self.device, dlogits, self.counts, self.tokens,
+                                          self.workspace))
         return dlogits
 
 
@@ -251,7 +268,7 @@ class MoEGradClip:
         """The norm as a 0-d fp32 tensor on the device (no synchronisation)."""
         norm = torch.empty((), dtype=torch.float32, device=self.device)
         B.mm_moe_grad_norm(self._entries(grads, None), norm, self.workspace,
-                           _stream(stream, self.device))
+                           _stream(stream, self.device, norm, self.workspace))
         return norm
 
     def clip(self, grads: Sequence[torch.Tensor], max_norm: float, out=None,
@@ -262,5 +279,5 @@ class MoEGradClip:
             raise ValueError(f"max_norm must be >= 0, got {max_norm}")
         norm = torch.empty((), dtype=torch.float32, device=self.device)
         B.mm_moe_grad_clip(self._entries(grads, out), max_norm, self.eps, norm, self.workspace,
-                           _stream(stream, self.device))
+                           _stream(stream, self.device, norm, self.workspace))
         return norm
