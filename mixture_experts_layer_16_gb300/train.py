@@ -229,7 +229,8 @@ class MoEBalanceLoss:
 
 class MoEGradClip:
     """The global L2 norm of up to max_tensors gradients, and clipping by it: every
-    gradient times min(1, max_norm / (norm + eps))."""
+    gradient times min(1, max_norm / (norm + eps)).  What is clipped must not overlap another
+    gradient or output: in place, each tensor once."""
 
     def __init__(self, max_tensors: int = 1024, eps: float = 1e-6,
                  device: Optional[torch.device] = None):
@@ -244,6 +245,16 @@ class MoEGradClip:
             raise ValueError(f"grads: {len(grads)} tensors, made for at most {self.max_tensors}")
         if out is not None and len(out) != len(grads):
             raise ValueError(f"out: expected {len(grads)} tensors, got {len(out)}")
+        try:
+            return array("Q", self._words(grads, out))
+        except AttributeError:  # (looked for only now: short lists are bound by the host)
+            for name, ts in (("grads", grads), ("out", out or ())):
+                for i, t in enumerate(ts):
+                    if not isinstance(t, torch.Tensor):
+                        raise TypeError(f"{name}[{i}] must be a torch.Tensor") from None
+            raise
+
+    def _words(self, grads, out):
         where = -1 if self.device.index is None else self.device.index
         words = []
         for i, g in enumerate(grads):
@@ -262,7 +273,7 @@ class MoEGradClip:
                 raise ValueError(f"out[{i}]: expected a contiguous tensor like grads[{i}], of "
                                  "its dtype or fp32")
             words += (p, o.data_ptr(), g.numel(), d | od << 32)
-        return array("Q", words)
+        return words
 
     def norm(self, grads: Sequence[torch.Tensor], stream=None) -> torch.Tensor:
         """The norm as a 0-d fp32 tensor on the device (no synchronisation)."""
