@@ -63,11 +63,14 @@ def parse_args():
                     help="activation checkpointing: the backward re-runs the gate/up stage")
     ap.add_argument("--multicast", action="store_true",
                     help="bf16 grouped GEMMs on clusters of two SM pairs sharing A by TMA "
-                         "multicast (MM_MOE_MULTICAST)")
+                         "multicast (MM_MOE_MULTICAST; one GPU only)")
     ap.add_argument("--with-router", action="store_true",
                     help="the step also runs the top-k router (forward before the layer, "
                          "backward after it); topk_idx/topk_w then come from the router")
-    return ap.parse_args()
+    args = ap.parse_args()
+    if args.multicast and max(args.gpus, dist_info()[0]) > 1:
+        ap.error("--multicast is for one GPU")
+    return args
 
 
 # ---------------------------------------------------------------- distributed plumbing

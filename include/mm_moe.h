@@ -108,7 +108,9 @@ typedef enum {
  *                     a GB300 holds 36 four-CTA clusters (144 of its 152 SMs), which
  *                     costs about what the halved A reads gain (benchmark layer 3.10 ->
  *                     3.11 ms, 235B shape 6.23 -> 6.23 ms on one box).  Single-GPU only:
- *                     the copies read this GPU's own memory. */
+ *                     the copies read this GPU's own memory, and only a job of one GPU
+ *                     may set the bit (the Python handle and the benchmark refuse it
+ *                     beside other ranks). */
 #define MM_MOE_MULTICAST 2
 
 /* Problem shape.  T tokens, H hidden, I expert intermediate, E experts, top-k.

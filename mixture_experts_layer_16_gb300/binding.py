@@ -70,8 +70,19 @@ MM_MOE_RECOMPUTE = 1  # activation checkpointing (include/mm_moe.h)
 MM_MOE_MULTICAST = 2  # A-multicast clusters of two SM pairs (include/mm_moe.h)
 
 
+def _ranks() -> int:
+    """Ranks of the job that this process belongs to."""
+    import torch.distributed as dist
+    if dist.is_available() and dist.is_initialized():
+        return dist.get_world_size()
+    return int(os.environ.get("WORLD_SIZE") or 1)
+
+
 def make_shape(T, H, I, E, k, prec="bf16", recompute: bool = False,
                multicast: bool = False) -> Shape:
+    """multicast: in a job of one GPU only (its loads are for code that runs alone)."""
+    if multicast and _ranks() > 1:
+        raise ValueError(f"multicast is for jobs of one GPU, this one has {_ranks()} ranks")
     return Shape(int(T), int(H), int(I), int(E), int(k), PRECISION.get(prec, prec),
                  (MM_MOE_RECOMPUTE if recompute else 0) | (MM_MOE_MULTICAST if multicast else 0))
 
