@@ -1,11 +1,12 @@
-"""MoEBalanceLoss of a single token in many sequences, all but one of which are empty."""
+"""MoEBalanceLoss of sequences of very different lengths: a single token in many, all but one of which
+are empty; one of nearly all tokens among many short ones."""
 import pytest
 import torch
 
 import oracle.train as ot
 from mixture_experts_layer_16_gb300 import MoEBalanceLoss
 from tests import gpu_util as G
-from tests.test_gpu_balance import DL, E32, f64
+from tests.test_gpu_balance import DL, E32, case, check, f64, run
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +42,16 @@ def test_balance_one_token_in_many_sequences(E, n_seq, at):
     assert abs(f64(d) - want).max() <= 200 * E32 * (E + abs(f["lse"][0]))
     counts[at], h.tokens[at], h.seq_loss[at] = 0, 0, 0.0
     assert not counts.any() and not h.tokens.any() and not h.seq_loss.any()
+
+
+@pytest.mark.parametrize("E,k,n_seq", [(16, 2, 64), (130, 4, 60)])
+def test_balance_one_long_sequence_among_short_ones(E, k, n_seq):
+    """One sequence of nearly all tokens, in some hundred pieces, and many of a few tokens."""
+    T, at = 20000, n_seq // 3
+    c = case(T, E, k, mask=True)
+    lengths = torch.arange(n_seq) * 5 % 4
+    lengths[at] = 0
+    lengths[at] = T - int(lengths.sum())
+    off = torch.cat([torch.zeros(1, dtype=torch.int64), lengths.cumsum(0)])
+    c.update(off=off.to(torch.int32).cuda(), G=n_seq)
+    check(c, *run(c))
