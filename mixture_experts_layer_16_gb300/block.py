@@ -4,8 +4,10 @@
   out = x + MoELayer(n, topk)
 
 and its backward: the layer's dx, the router's (with the auxiliary losses' logit gradient)
-added to it, the norm's backward joined with the residual path's gradient.  Every step is one
-of the library's operators; this module holds the buffers that pass between them.
+added to it, the norm's backward joined with the residual path's gradient.  Every step but the
+residual's addition is one of the library's operators; this module holds the buffers that pass
+between them.  The layer gives its output in bf16, so out is rounded twice: where the layer stores
+it and where the residual is added (one half ulp of MoE(n) beside one of out).
 """
 from __future__ import annotations
 
@@ -47,7 +49,8 @@ class MoEBlock:
 
     def forward(self, x: torch.Tensor, params: Dict[str, torch.Tensor], seq_offsets=None,
                 mask=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
-        """(out [T, H], losses [2] fp32: balance and z, counts [sequences, E] int32)."""
+        """(out [T, H], losses [2] fp32: balance and z, counts [sequences, E] int32); losses and
+        counts are the balance loss's own tensors, which the next forward overwrites."""
         p = params
         n = self.norm.forward(x, p["norm_weight"], p["norm_bias"])
         idx, w = self.router.forward(n, p["W_router"])
