@@ -8,7 +8,7 @@ from tests import gpu_util as G
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
-SLEEP = 600_000_000            # cycles: some 0.3 s
+SLEEP = 1_000_000_000          # cycles: some 0.5 s
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -94,3 +94,35 @@ def test_clip_on_another_stream():
         return [c.clip(g, 1.0, out=o, stream=s), c.workspace]
     check(norm)
     check(clip)
+
+
+def test_capture_with_the_stream_named():
+    """A graph captured on a stream that the calls name themselves, with tensors made inside."""
+    T, H, E, k = 300, 256, 16, 2
+    x, dy = (torch.randn((T, H), device="cuda").to(BF) for _ in range(2))
+    w, b = (torch.randn(H, device="cuda").to(BF) for _ in range(2))
+    lg = torch.randn((T, E), device="cuda")
+    idx = torch.topk(lg, k, dim=1).indices.to(torch.int32).contiguous()
+    dl = torch.ones(2, device="cuda")
+    n, h, c = MoELayerNorm(T, H), MoEBalanceLoss(T, E, k), MoEGradClip(4)
+    g = [torch.randn(5000, device="cuda") for _ in range(3)]
+    o = [torch.empty_like(t) for t in g]
+
+    def go(s):
+        y = n.forward(x, w, b, stream=s)
+        grads = n.backward(dy, x, w, stream=s)
+        losses, counts = h.forward(lg, idx, stream=s)
+        d = h.backward(lg, dl, stream=s)
+        return [y, *grads, losses, counts, d, c.clip(g, 1.0, out=o, stream=s), *o]
+    want = [t.clone() for t in go(None)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = go(s)
+    for t in (*got, n.mean, n.rstd, h.workspace):
+        t.zero_()
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, v) for a, v in zip(got, want))
