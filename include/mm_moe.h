@@ -291,8 +291,8 @@ MM_MOE_API mm_moe_status mm_moe_fp8_block_quantize(const uint16_t* in, uint8_t* 
                                                    uint8_t* scales, int64_t rows, int64_t cols,
                                                    int layout, void* stream);
 
-/* Element types of the operators around the layer (layer norm, balance loss,
- * gradient clipping). */
+/* Element types of the operators around the layer (layer norm, balance loss, gradient
+ * clipping, AdamW). */
 typedef enum { MM_MOE_DT_BF16 = 0, MM_MOE_DT_F16 = 1, MM_MOE_DT_F32 = 2 } mm_moe_dtype;
 
 /* Layer normalisation in front of the layer (the source pages start at the layer and
@@ -421,6 +421,67 @@ MM_MOE_API mm_moe_status mm_moe_grad_norm(const mm_moe_grad* grads, int64_t n_te
 MM_MOE_API mm_moe_status mm_moe_grad_clip(const mm_moe_grad* grads, int64_t n_tensors,
                                           float max_norm, float eps, float* norm,
                                           void* workspace, void* stream);
+
+/* One AdamW step over many tensors:
+ *   g = coef grad,  coef = min(1, max_norm / (norm + clip_eps)), 1 without a norm
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   p = p - lr (m / (1 - beta1^t) / ((v / (1 - beta2^t))^(1/2) + eps) + weight_decay p)
+ * where p is the tensor's fp32 master, whose rounding the parameter then holds, or without one
+ * the parameter itself.  t is counted on the device.
+ *   MM_MOE_STATES_F32   m, v: fp32
+ *   MM_MOE_STATES_8BIT  m, v: a byte an element, and one for every 32 elements: blocks of 32
+ *                       share the scale 2^(c - 127) (m_scale, v_scale hold c; 255: the block is
+ *                       NaN), the smallest under which the block's largest value fits; m in e4m3
+ *                       (up to 448), v with 5 exponent bits of bias 15, 3 fraction bits and no
+ *                       sign (up to 1.875 * 2^16).  The step uses the moments before they are
+ *                       rounded; what is kept is rounded up or down at random with the
+ *                       fraction's probability (a v above zero not to zero), by a hash of seed,
+ *                       step, tensor and element.
+ * A value that is not finite spreads to its element, under 8 bits to its block; with a norm that
+ * is not finite the step does nothing and does not count. */
+typedef enum { MM_MOE_STATES_F32 = 0, MM_MOE_STATES_8BIT = 1 } mm_moe_states;
+typedef struct {
+  double beta1, beta2;  /* in [0, 1) */
+  double eps;           /* > 0 (as a float) */
+  float max_norm;       /* >= 0, may be infinite */
+  float clip_eps;       /* >= 0 */
+  int32_t states;       /* mm_moe_states */
+  uint32_t seed;        /* of the 8-bit states' rounding */
+} mm_moe_adamw;
+typedef struct {
+  void* param;         /* device, contiguous, aligned to its element; in and out */
+  float* master;       /* of a 16-bit parameter, or NULL; in and out */
+  const void* grad;
+  int64_t numel;       /* >= 0 (0: the pointers are not looked at); at most 2^41 together */
+  int32_t dtype;       /* mm_moe_dtype of param */
+  int32_t grad_dtype;  /* of grad: dtype, or MM_MOE_DT_F32 */
+  float weight_decay;
+  int32_t reserved;
+} mm_moe_adamw_tensor;
+
+/*   tensors  host array of n_tensors (0 .. MM_MOE_MAX_GRADS) entries, read during the call; no
+ *            two parameters, masters or gradients share memory.  The same tensors in the same
+ *            order at every step
+ *   m, v     moments of all tensors, one after the other, each beginning on a multiple of 32
+ *            elements (zero behind its last one): 32-byte aligned.  m_scale, v_scale: a byte
+ *            for every 32 elements (8-bit states; else NULL)
+ *   counter  32 bytes, 16-byte aligned, which the step advances: int64 steps behind, double
+ *            beta1^steps and beta2^steps, 8 bytes 0 (so {0, 1.0, 1.0, 0} at the start)
+ *   lr_dev   NULL, or the learning rate as one fp32 on the device (lr is then ignored)
+ *   norm     NULL, or one fp32 on the device (mm_moe_grad_norm's)
+ * Deterministic.  Two steps on the same moments or counter must not overlap.  Errors as for the
+ * layer. */
+MM_MOE_API mm_moe_status mm_moe_adamw_step(const mm_moe_adamw* opt,
+                                           const mm_moe_adamw_tensor* tensors, int64_t n_tensors,
+                                           void* m, uint8_t* m_scale, void* v, uint8_t* v_scale,
+                                           void* counter, double lr, const float* lr_dev,
+                                           const float* norm, void* stream);
+
+/* The values that 8-bit moments stand for, in bf16 (exact where bf16 has them): n elements, a
+ * multiple of 32; all but the scales 16-byte aligned. */
+MM_MOE_API mm_moe_status mm_moe_adamw_moments(const uint8_t* m, const uint8_t* m_scale,
+                                              const uint8_t* v, const uint8_t* v_scale, int64_t n,
+                                              uint16_t* m_out, uint16_t* v_out, void* stream);
 
 /* Synchronises `stream`, then returns the device status word of `scratch`
  * (MM_MOE_OK, MM_MOE_EBADIDX or MM_MOE_ETIMEOUT), or MM_MOE_ECUDA when the

@@ -30,7 +30,8 @@ EXPORTS = ("mm_moe_workspace_size", "mm_moe_forward", "mm_moe_backward", "mm_moe
            "mm_moe_fp8_block_quantize", "mm_moe_router_backward_aux",
            "mm_moe_norm_workspace_size", "mm_moe_norm_forward", "mm_moe_norm_backward",
            "mm_moe_balance_workspace_size", "mm_moe_balance_forward", "mm_moe_balance_backward",
-           "mm_moe_grad_workspace_size", "mm_moe_grad_norm", "mm_moe_grad_clip")
+           "mm_moe_grad_workspace_size", "mm_moe_grad_norm", "mm_moe_grad_clip",
+           "mm_moe_adamw_step", "mm_moe_adamw_moments")
 
 
 class MoEError(RuntimeError):
@@ -64,6 +65,24 @@ class BalanceShape(ctypes.Structure):
 class Grad(ctypes.Structure):
     _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+# moments of AdamW (mm_moe_states)
+MM_MOE_STATES_F32, MM_MOE_STATES_8BIT = 0, 1
+STATES = {"fp32": MM_MOE_STATES_F32, "8bit": MM_MOE_STATES_8BIT}
+
+
+class AdamW(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("max_norm", ctypes.c_float), ("clip_eps", ctypes.c_float),
+                ("states", ctypes.c_int32), ("seed", ctypes.c_uint32)]
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("grad", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("weight_decay", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
 
 
 MM_MOE_RECOMPUTE = 1  # activation checkpointing (include/mm_moe.h)
@@ -136,6 +155,9 @@ def lib() -> ctypes.CDLL:
         L.mm_moe_grad_workspace_size.argtypes = [i64, szp]
         L.mm_moe_grad_norm.argtypes = [_vp, i64, _vp, _vp, _vp]
         L.mm_moe_grad_clip.argtypes = [_vp, i64, ctypes.c_float, ctypes.c_float, _vp, _vp, _vp]
+        L.mm_moe_adamw_step.argtypes = [ctypes.POINTER(AdamW), _vp, i64] + [_vp] * 5 + \
+            [ctypes.c_double] + [_vp] * 3
+        L.mm_moe_adamw_moments.argtypes = [_vp] * 4 + [i64] + [_vp] * 3
         for fn in EXPORTS:
             getattr(L, fn).restype = ctypes.c_int
         L.mm_moe_kernel_name.restype = ctypes.c_char_p
@@ -384,6 +406,20 @@ def mm_moe_grad_clip(grads, max_norm: float, eps: float, norm, workspace, stream
     p, n = grads.buffer_info()
     _check("mm_moe_grad_clip", lib().mm_moe_grad_clip(p, n // 4, max_norm, eps, _ptr(norm),
                                                       _ptr(workspace), _stream(stream)))
+
+
+def mm_moe_adamw_step(opt: AdamW, tensors, n: int, m, m_scale, v, v_scale, counter, lr: float,
+                      lr_dev=None, norm=None, stream=None) -> None:
+    """tensors: the address of n packed mm_moe_adamw_tensor."""
+    _check("mm_moe_adamw_step", lib().mm_moe_adamw_step(
+        opt, tensors, n, _ptr(m), _ptr(m_scale), _ptr(v), _ptr(v_scale), _ptr(counter), lr,
+        _ptr(lr_dev), _ptr(norm), _stream(stream)))
+
+
+def mm_moe_adamw_moments(m, m_scale, v, v_scale, m_out, v_out, stream=None) -> None:
+    _check("mm_moe_adamw_moments", lib().mm_moe_adamw_moments(
+        _ptr(m), _ptr(m_scale), _ptr(v), _ptr(v_scale), m.numel(), _ptr(m_out), _ptr(v_out),
+        _stream(stream)))
 
 
 def mm_moe_read_status(scratch, stream=None) -> int:

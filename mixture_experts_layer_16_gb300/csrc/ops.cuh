@@ -1,4 +1,5 @@
-// ops.cuh -- what the operators around the layer (norm.cuh, balance.cu, gradclip.cu) share:
+// ops.cuh -- what the operators around the layer (norm.cuh, balance.cu, gradclip.cu, adamw.cu,
+// select.cu, resnorm.cuh) share:
 // their kernel ids and typed element access, bf16, fp16 and fp32 in memory, fp32 in
 // registers.  A value is rounded (to nearest even) only where it is stored.
 #pragma once
@@ -24,6 +25,8 @@ enum OpKernelId {
   K_GRAD_SQ,
   K_GRAD_NORM,
   K_GRAD_SCALE,
+  K_ADAMW,
+  K_ADAMW_MOMENTS,
   K_ALL_COUNT
 };
 

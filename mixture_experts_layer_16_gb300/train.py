@@ -50,6 +50,14 @@ def _stream(stream, device: torch.device, *mine: Optional[torch.Tensor]) -> int:
     return raw
 
 
+def _on(device: torch.device, fn, *args):
+    """fn(*args) with `device` the current one (the library launches on the current device)."""
+    if device.index is None or torch.cuda.current_device() == device.index:
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
 def _plain(t, shape: torch.Size, dtype, where: int) -> bool:
     """A contiguous tensor of this shape and dtype on CUDA device `where` (-1: the CPU)."""
     try:
