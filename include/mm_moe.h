@@ -392,6 +392,63 @@ MM_MOE_API mm_moe_status mm_moe_router_backward_aux(
     const int32_t* topk_idx, const float* topk_w, const float* dtopk_w, const float* dlogits_aux,
     uint16_t* dlogits, uint16_t* dx, uint16_t* dW_router, void* stream);
 
+/* The choice of experts from a router's logits in its other forms, and its backward:
+ *   s = softmax(logits) over all experts, or sigmoid(logits);  key = s + bias
+ *   of `groups` groups of consecutive experts the best topk_groups, by their largest key or by
+ *   the sum of their two largest; of these the k largest keys in descending order
+ *   topk_w = scale s of the chosen; renormalised: scale times the softmax over the chosen logits,
+ *   or scale s / (sum of the chosen s + 1e-20)
+ * Equal keys (groups) go to the lower index.  The order is that of the keys in exact arithmetic
+ * (in 64 bits where 32 do not tell; sums that 64 bits round apart may fall either way): without
+ * a bias that of the logits.  A NaN ranks as -inf,
+ * indices are always distinct and in [0, E); a NaN among the chosen logits makes the token's weights
+ * NaN (under an unrenormalised softmax, or one with a bias, any NaN of the row does).
+ * 1 <= T < 2^31, 1 <= k <= 32, E <= 1024, groups <= 32 a divisor of E, k <= E / groups *
+ * topk_groups. */
+typedef enum { MM_MOE_SCORE_SOFTMAX = 0, MM_MOE_SCORE_SIGMOID = 1 } mm_moe_score;
+typedef enum { MM_MOE_GROUP_MAX = 0, MM_MOE_GROUP_TOP2 = 1 } mm_moe_group_score;
+typedef struct {
+  int64_t T, E, k;
+  int32_t dtype;        /* mm_moe_dtype of the logits */
+  int32_t grad_dtype;   /* of their gradient: dtype, or MM_MOE_DT_BF16 */
+  int32_t score;        /* mm_moe_score */
+  int32_t groups, topk_groups;
+  int32_t group_score;  /* mm_moe_group_score */
+  int32_t renormalise;  /* 0 or 1 */
+  float scale;          /* finite */
+} mm_moe_select;
+
+/*   logits [T, E], contiguous;  bias [E] fp32 or NULL
+ *   topk_idx [T, k] int32 out;  topk_w [T, k] fp32 out
+ * Pointers aligned to their element; rows on 16-byte boundaries run faster.  Errors as for the
+ * layer. */
+MM_MOE_API mm_moe_status mm_moe_select_forward(const mm_moe_select* select, const void* logits,
+                                               const float* bias, int32_t* topk_idx,
+                                               float* topk_w, void* stream);
+
+/* The gradient of the logits through topk_w, the choice held fixed (the bias has none):
+ *   dtopk_w      [T, k] fp32
+ *   dlogits_aux  [T, E] fp32 or NULL: a further gradient of the logits, added in fp32
+ *   dlogits      [T, E] out (grad_dtype; overwritten), must not overlap logits or dlogits_aux
+ *                (MM_MOE_EINVAL)
+ * An index outside [0, E) is dropped, one that a token has twice counts twice. */
+MM_MOE_API mm_moe_status mm_moe_select_backward(const mm_moe_select* select, const void* logits,
+                                                const int32_t* topk_idx, const float* dtopk_w,
+                                                const float* dlogits_aux, void* dlogits,
+                                                void* stream);
+
+/* mm_moe_router_forward and _backward with this choice in the place of theirs.  select: the
+ * shape's T, E and k, fp32 logits and a bf16 gradient (else MM_MOE_EINVAL); logits: the forward's;
+ * dlogits_aux may be NULL. */
+MM_MOE_API mm_moe_status mm_moe_router_select_forward(
+    const mm_moe_shape* shape, const mm_moe_select* select, const uint16_t* x,
+    const uint16_t* W_router, const float* bias, float* logits, int32_t* topk_idx, float* topk_w,
+    void* stream);
+MM_MOE_API mm_moe_status mm_moe_router_select_backward(
+    const mm_moe_shape* shape, const mm_moe_select* select, const uint16_t* x,
+    const uint16_t* W_router, const float* logits, const int32_t* topk_idx, const float* dtopk_w,
+    const float* dlogits_aux, uint16_t* dlogits, uint16_t* dx, uint16_t* dW_router, void* stream);
+
 /* The global L2 norm of many gradient tensors, and clipping by it:
  *   norm = (sum over all tensors and elements of g^2)^(1/2)
  *   coef = min(1, max_norm / (norm + eps)),  out = coef grad

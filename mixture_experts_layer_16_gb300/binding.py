@@ -31,7 +31,9 @@ EXPORTS = ("mm_moe_workspace_size", "mm_moe_forward", "mm_moe_backward", "mm_moe
            "mm_moe_norm_workspace_size", "mm_moe_norm_forward", "mm_moe_norm_backward",
            "mm_moe_balance_workspace_size", "mm_moe_balance_forward", "mm_moe_balance_backward",
            "mm_moe_grad_workspace_size", "mm_moe_grad_norm", "mm_moe_grad_clip",
-           "mm_moe_adamw_step", "mm_moe_adamw_moments")
+           "mm_moe_adamw_step", "mm_moe_adamw_moments", "mm_moe_select_forward",
+           "mm_moe_select_backward", "mm_moe_router_select_forward",
+           "mm_moe_router_select_backward")
 
 
 class MoEError(RuntimeError):
@@ -83,6 +85,19 @@ class AdamWTensor(ctypes.Structure):
                 ("grad", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("grad_dtype", ctypes.c_int32), ("weight_decay", ctypes.c_float),
                 ("reserved", ctypes.c_int32)]
+
+
+# forms of the choice of experts (mm_moe_score, mm_moe_group_score)
+SCORE = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORE = {"max": 0, "top2": 1}
+
+
+class Select(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 MM_MOE_RECOMPUTE = 1  # activation checkpointing (include/mm_moe.h)
@@ -158,6 +173,11 @@ def lib() -> ctypes.CDLL:
         L.mm_moe_adamw_step.argtypes = [ctypes.POINTER(AdamW), _vp, i64] + [_vp] * 5 + \
             [ctypes.c_double] + [_vp] * 3
         L.mm_moe_adamw_moments.argtypes = [_vp] * 4 + [i64] + [_vp] * 3
+        qp = ctypes.POINTER(Select)
+        L.mm_moe_select_forward.argtypes = [qp] + [_vp] * 5
+        L.mm_moe_select_backward.argtypes = [qp] + [_vp] * 6
+        L.mm_moe_router_select_forward.argtypes = [sp, qp] + [_vp] * 7
+        L.mm_moe_router_select_backward.argtypes = [sp, qp] + [_vp] * 10
         for fn in EXPORTS:
             getattr(L, fn).restype = ctypes.c_int
         L.mm_moe_kernel_name.restype = ctypes.c_char_p
@@ -419,6 +439,39 @@ def mm_moe_adamw_step(opt: AdamW, tensors, n: int, m, m_scale, v, v_scale, count
 def mm_moe_adamw_moments(m, m_scale, v, v_scale, m_out, v_out, stream=None) -> None:
     _check("mm_moe_adamw_moments", lib().mm_moe_adamw_moments(
         _ptr(m), _ptr(m_scale), _ptr(v), _ptr(v_scale), m.numel(), _ptr(m_out), _ptr(v_out),
+        _stream(stream)))
+
+
+def mm_moe_select_forward(select: Select, logits, bias, topk_idx, topk_w, stream=None) -> None:
+    st = lib().mm_moe_select_forward(select, logits.data_ptr(), _ptr(bias), topk_idx.data_ptr(),
+                                     topk_w.data_ptr(),
+                                     stream if type(stream) is int else _stream(stream))
+    if st:
+        _check("mm_moe_select_forward", st)
+
+
+def mm_moe_select_backward(select: Select, logits, topk_idx, dtopk_w, dlogits_aux, dlogits,
+                           stream=None) -> None:
+    st = lib().mm_moe_select_backward(select, logits.data_ptr(), topk_idx.data_ptr(),
+                                      dtopk_w.data_ptr(), _ptr(dlogits_aux), dlogits.data_ptr(),
+                                      stream if type(stream) is int else _stream(stream))
+    if st:
+        _check("mm_moe_select_backward", st)
+
+
+def mm_moe_router_select_forward(shape: Shape, select: Select, x, W_router, bias, logits, topk_idx,
+                                 topk_w, stream=None) -> None:
+    _check("mm_moe_router_select_forward", lib().mm_moe_router_select_forward(
+        ctypes.byref(shape), select, _ptr(x), _ptr(W_router), _ptr(bias), _ptr(logits),
+        _ptr(topk_idx), _ptr(topk_w), _stream(stream)))
+
+
+def mm_moe_router_select_backward(shape: Shape, select: Select, x, W_router, logits, topk_idx,
+                                  dtopk_w, dlogits_aux, dlogits, dx, dW_router,
+                                  stream=None) -> None:
+    _check("mm_moe_router_select_backward", lib().mm_moe_router_select_backward(
+        ctypes.byref(shape), select, _ptr(x), _ptr(W_router), _ptr(logits), _ptr(topk_idx),
+        _ptr(dtopk_w), _ptr(dlogits_aux), _ptr(dlogits), _ptr(dx), _ptr(dW_router),
         _stream(stream)))
 
 

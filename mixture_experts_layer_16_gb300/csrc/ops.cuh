@@ -27,6 +27,8 @@ enum OpKernelId {
   K_GRAD_SCALE,
   K_ADAMW,
   K_ADAMW_MOMENTS,
+  K_SELECT_FWD,
+  K_SELECT_BWD,
   K_ALL_COUNT
 };
 

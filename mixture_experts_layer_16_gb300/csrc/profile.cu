@@ -18,7 +18,8 @@ static const char* const kKernelNames[K_ALL_COUNT] = {
     "fbq_cols", "fbq_tiles", "mxq_rows", "mxq_cols",
     "gemm_dense_nt", "gemm_dense_nn", "gemm_dense_tn", "router_topk", "router_dlogits",
     "norm_fwd", "norm_bwd", "norm_bwd_finish", "balance_fwd", "balance_finish", "balance_bwd",
-    "grad_sq", "grad_norm", "grad_scale", "adamw", "adamw_moments"};
+    "grad_sq", "grad_norm", "grad_scale", "adamw", "adamw_moments",
+    "select_fwd", "select_bwd"};
 
 namespace {
 struct Rec {

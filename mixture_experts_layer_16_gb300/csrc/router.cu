@@ -20,6 +20,8 @@
 #include <cstdint>
 
 #include "internal.h"
+#include "ops.cuh"
+#include "select.cuh"
 
 namespace mmmoe {
 
@@ -242,4 +244,49 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_router_backward_aux(
   if (launch_dense(c, GEMM_DENSE_NN, dlogits, W_router, dx, T, H, E) != cudaSuccess)
     return MM_MOE_ECUDA;
   return MM_MOE_OK;
+}
+
+// The same around the other forms of the choice (select.cu): its logit gradient already holds the
+// auxiliary one and is rounded to bf16 for the two products.
+static bool router_select_ok(const mm_moe_shape* s, const mm_moe_select* q) {
+  return router_shape_ok(s) && select_ok(q) && q->T == s->T && q->E == s->E && q->k == s->k &&
+         q->dtype == MM_MOE_DT_F32 && q->grad_dtype == MM_MOE_DT_BF16;
+}
+
+extern "C" MM_MOE_API mm_moe_status mm_moe_router_select_forward(
+    const mm_moe_shape* shape, const mm_moe_select* select, const uint16_t* x,
+    const uint16_t* W_router, const float* bias, float* logits, int32_t* topk_idx, float* topk_w,
+    void* stream) {
+  if (!router_select_ok(shape, select)) return MM_MOE_EINVAL;
+  if (!al(x, 16) || !al(W_router, 16) || (bias != nullptr && !al(bias, 4)) || !al(logits, 16) ||
+      !al(topk_idx, 4) || !al(topk_w, 4))
+    return MM_MOE_EINVAL;
+  int sms = 0;
+  if (!device_ok(&sms)) return MM_MOE_ENOTSUP;
+  int launches = 0;
+  const Ctx c{static_cast<cudaStream_t>(stream), sms, &launches};
+  const cudaError_t e = launch_dense(c, GEMM_DENSE_NT, x, W_router, logits, shape->T, shape->E,
+                                     shape->H);
+  if (e != cudaSuccess) return op_status(e);
+  return op_status(launch_select_fwd(c, select, logits, bias, topk_idx, topk_w));
+}
+
+extern "C" MM_MOE_API mm_moe_status mm_moe_router_select_backward(
+    const mm_moe_shape* shape, const mm_moe_select* select, const uint16_t* x,
+    const uint16_t* W_router, const float* logits, const int32_t* topk_idx, const float* dtopk_w,
+    const float* dlogits_aux, uint16_t* dlogits, uint16_t* dx, uint16_t* dW_router, void* stream) {
+  if (!router_select_ok(shape, select)) return MM_MOE_EINVAL;
+  if (!al(x, 16) || !al(W_router, 16) || !al(logits, 16) || !al(topk_idx, 4) || !al(dtopk_w, 4) ||
+      (dlogits_aux != nullptr && !al(dlogits_aux, 4)) || !al(dlogits, 16) || !al(dx, 16) ||
+      !al(dW_router, 16))
+    return MM_MOE_EINVAL;
+  int sms = 0;
+  if (!device_ok(&sms)) return MM_MOE_ENOTSUP;
+  int launches = 0;
+  const Ctx c{static_cast<cudaStream_t>(stream), sms, &launches};
+  const int64_t T = shape->T, H = shape->H, E = shape->E;
+  cudaError_t e = launch_select_bwd(c, select, logits, topk_idx, dtopk_w, dlogits_aux, dlogits);
+  if (e == cudaSuccess) e = launch_dense(c, GEMM_DENSE_TN, dlogits, x, dW_router, E, H, T);
+  if (e == cudaSuccess) e = launch_dense(c, GEMM_DENSE_NN, dlogits, W_router, dx, T, H, E);
+  return op_status(e);
 }

@@ -103,9 +103,14 @@ class MoELayer:
 class MoERouter:
     """The top-k router in front of MoELayer: topk_idx, topk_w from x and W_router
     [E, H], and the backward from the layer's dtopk_w (adds its dx, returns
-    dW_router).  Every step runs in the library (mm_moe_router_forward/backward)."""
+    dW_router).  Every step runs in the library (mm_moe_router_forward/backward).
 
-    def __init__(self, T: int, H: int, E: int, k: int, device: Optional[torch.device] = None):
+    select: options of MoESelect (score, groups, topk_groups, group_score, renormalise, scale) as
+    a dict, {} for its defaults with a bias; None: the k largest logits and the softmax over
+    them."""
+
+    def __init__(self, T: int, H: int, E: int, k: int, device: Optional[torch.device] = None,
+                 select: Optional[dict] = None):
         self.T, self.H, self.E, self.k = T, H, E, k
         device = torch.device("cuda" if device is None else device)
         if device.type == "cuda" and device.index is None:
@@ -114,15 +119,28 @@ class MoERouter:
         self.shape = B.make_shape(T, H, 64, E, k)   # I is not used by the router
         self.logits = torch.empty((T, E), dtype=torch.float32, device=device)
         self.dlogits = torch.empty((T, E), dtype=torch.bfloat16, device=device)
+        self.select = None
+        if select is not None:
+            from .selection import MoESelect
+            self.select = MoESelect(T, E, k, dtype="fp32", grad_dtype="bf16", device=device,
+                                    **select)
 
-    def forward(self, x, W_router, stream=None):
-        """(topk_idx [T, k] int32, topk_w [T, k] fp32); the logits stay in self.logits."""
+    def forward(self, x, W_router, stream=None, bias=None):
+        """(topk_idx [T, k] int32, topk_w [T, k] fp32); the logits stay in self.logits.
+        bias [E] fp32 (with select): added to the scores for the choice alone."""
         d, bf = self.device, torch.bfloat16
         _need(x, "x", (self.T, self.H), bf, d)
         _need(W_router, "W_router", (self.E, self.H), bf, d)
         idx = torch.empty((self.T, self.k), dtype=torch.int32, device=d)
         w = torch.empty((self.T, self.k), dtype=torch.float32, device=d)
-        B.mm_moe_router_forward(self.shape, x, W_router, self.logits, idx, w, stream)
+        if self.select is None:
+            if bias is not None:
+                raise ValueError("bias: this router has none (select=None)")
+            B.mm_moe_router_forward(self.shape, x, W_router, self.logits, idx, w, stream)
+        else:
+            self.select._check_bias(bias)
+            B.mm_moe_router_select_forward(self.shape, self.select.shape, x, W_router, bias,
+                                           self.logits, idx, w, stream)
         return idx, w
 
     def backward(self, x, W_router, topk_idx, topk_w, dtopk_w, dx, dW_router=None, stream=None,
@@ -139,7 +157,13 @@ class MoERouter:
         if dW_router is None:
             dW_router = torch.empty((self.E, self.H), dtype=bf, device=d)
         _need(dW_router, "dW_router", (self.E, self.H), bf, d)
-        if dlogits_aux is None:
+        if self.select is not None:
+            if dlogits_aux is not None:
+                _need(dlogits_aux, "dlogits_aux", (self.T, self.E), torch.float32, d)
+            B.mm_moe_router_select_backward(self.shape, self.select.shape, x, W_router,
+                                            self.logits, topk_idx, dtopk_w, dlogits_aux,
+                                            self.dlogits, dx, dW_router, stream)
+        elif dlogits_aux is None:
             B.mm_moe_router_backward(self.shape, x, W_router, topk_idx, topk_w, dtopk_w,
                                      self.dlogits, dx, dW_router, stream)
         else:
