@@ -291,8 +291,8 @@ MM_MOE_API mm_moe_status mm_moe_fp8_block_quantize(const uint16_t* in, uint8_t* 
                                                    uint8_t* scales, int64_t rows, int64_t cols,
                                                    int layout, void* stream);
 
-/* Element types of the operators around the layer (layer norm, balance loss, gradient
- * clipping, AdamW). */
+/* Element types of the operators around the layer (norms, balance loss, choice of experts,
+ * gradient clipping, AdamW). */
 typedef enum { MM_MOE_DT_BF16 = 0, MM_MOE_DT_F16 = 1, MM_MOE_DT_F32 = 2 } mm_moe_dtype;
 
 /* Layer normalisation in front of the layer (the source pages start at the layer and
@@ -338,6 +338,64 @@ MM_MOE_API mm_moe_status mm_moe_norm_backward(
     const mm_moe_norm_shape* shape, const void* dy, int64_t lddy, const void* x, int64_t ldx,
     const void* weight, const float* mean, const float* rstd, const void* dx_add, int64_t ldadd,
     void* dx, int64_t lddx, void* dweight, void* dbias, void* workspace, void* stream);
+
+/* The RMS norms behind a block and in front of the next one, with the block's gate and the
+ * residual addition between them, in one pass over the rows:
+ *   u = post_weight f rstd_f,  rstd_f = (1/H sum f^2 + eps)^(-1/2)       (u = f with post 0)
+ *   out = x + scale gate u
+ *   n = pre_weight out rstd_out,  rstd_out = (1/H sum out^2 + eps)^(-1/2)       (with pre 1)
+ * T rows of H channels as for the layer norm.  dtype: of the block's output f, of n and their
+ * gradients; res_dtype: of the residual stream x, out and its gradient, dtype itself or fp32;
+ * param_dtype: of the weights, the gate and their gradients, dtype itself or fp32.  Everything is
+ * computed in fp32 and rounded once where it is stored (n comes from out before its rounding). */
+typedef enum {
+  MM_MOE_GATE_NONE = 0,
+  MM_MOE_GATE_CHANNEL = 1, /* [H] */
+  MM_MOE_GATE_TOKEN = 2    /* [T] */
+} mm_moe_gate;
+typedef struct {
+  int64_t T, H;
+  int32_t dtype, res_dtype, param_dtype; /* mm_moe_dtype */
+  int32_t post, gate, pre;               /* 0 or 1; mm_moe_gate; 0 or 1 */
+  float scale, eps;                      /* finite; >= 0 */
+} mm_moe_resnorm;
+
+/* Bytes of the backward's working memory. */
+MM_MOE_API mm_moe_status mm_moe_resnorm_workspace_size(const mm_moe_resnorm* shape,
+                                                       size_t* bytes);
+
+/*   x, out  [T, H] rows ldx / ldout elements apart (>= H); out may equal x when the strides are
+ *           equal;  f, n [T, H] likewise (n with pre 1)
+ *   f       may be NULL (with pre 1): n is the norm of x, and out, the gate and the norm behind
+ *           the block are not looked at
+ *   post_weight, pre_weight [H];  gate [H] or [T]; each only where the shape has it
+ *   rstd_f, rstd_out        [T] fp32 out, for the backward; likewise
+ * Outputs over operands or over one another are refused (MM_MOE_EINVAL; rows in one another's gaps
+ * pass where both lie equally far apart in bytes).  Pointers aligned to their element; rows on
+ * 16-byte boundaries of a multiple of 8 channels run faster.  Errors as for the layer. */
+MM_MOE_API mm_moe_status mm_moe_resnorm_forward(
+    const mm_moe_resnorm* shape, const void* x, int64_t ldx, const void* f, int64_t ldf,
+    const void* post_weight, const void* gate, const void* pre_weight, void* out, int64_t ldout,
+    void* n, int64_t ldn, float* rstd_f, float* rstd_out, void* stream);
+
+/* With oh = out rstd_out, fh = f rstd_f, v = pre_weight dn and c = scale gate post_weight:
+ *   D = dout + rstd_out (v - oh 1/H sum oh v),  dx = D
+ *   df = rstd_f (c D - fh 1/H sum fh c D)  (c D with post 0)
+ *   dpost_weight = sum_t scale gate fh D,  dpre_weight = sum_t dn oh
+ *   dgate = sum over the tokens (channels) of scale post_weight fh D
+ *   dout  [T, H] gradient of out, or NULL with pre 1 (zero);  dn [T, H] gradient of n (with pre 1)
+ *   out   the forward's (x where it had no f; with pre 1);  f: the forward's, or NULL
+ *   dx, df [T, H] out;  dpost_weight, dpre_weight [H], dgate as gate: out, each where the shape has
+ *         it (overwritten, not accumulated)
+ *   workspace  of mm_moe_resnorm_workspace_size, 16-byte aligned
+ * Overlaps as for the forward (dx must not lie over dout either).  All sums have a fixed order:
+ * bitwise deterministic. */
+MM_MOE_API mm_moe_status mm_moe_resnorm_backward(
+    const mm_moe_resnorm* shape, const void* dout, int64_t lddout, const void* dn, int64_t lddn,
+    const void* out, int64_t ldout, const void* f, int64_t ldf, const void* post_weight,
+    const void* gate, const void* pre_weight, const float* rstd_f, const float* rstd_out, void* dx,
+    int64_t lddx, void* df, int64_t lddf, void* dpost_weight, void* dgate, void* dpre_weight,
+    void* workspace, void* stream);
 
 /* The router's auxiliary losses and per-expert counts, over T tokens split into G
  * sequences.  A token counts when its mask is set and its logits are not all -inf.

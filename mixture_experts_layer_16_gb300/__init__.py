@@ -11,5 +11,6 @@ from .binding import (Shape, Workspace, MoEError, make_shape, mm_moe_workspace_s
 from .layer import MoELayer, MoERouter  # noqa: F401,E402
 from .train import MoEBalanceLoss, MoEGradClip, MoELayerNorm  # noqa: F401,E402
 from .selection import MoESelect  # noqa: F401,E402
+from .resnorm import MoEResidualNorm  # noqa: F401,E402
 from .adamw import MoEAdamW  # noqa: F401,E402
 from .block import MoEBlock  # noqa: F401,E402

@@ -33,7 +33,8 @@ EXPORTS = ("mm_moe_workspace_size", "mm_moe_forward", "mm_moe_backward", "mm_moe
            "mm_moe_grad_workspace_size", "mm_moe_grad_norm", "mm_moe_grad_clip",
            "mm_moe_adamw_step", "mm_moe_adamw_moments", "mm_moe_select_forward",
            "mm_moe_select_backward", "mm_moe_router_select_forward",
-           "mm_moe_router_select_backward")
+           "mm_moe_router_select_backward", "mm_moe_resnorm_workspace_size",
+           "mm_moe_resnorm_forward", "mm_moe_resnorm_backward")
 
 
 class MoEError(RuntimeError):
@@ -98,6 +99,17 @@ class Select(ctypes.Structure):
                 ("score", ctypes.c_int32), ("groups", ctypes.c_int32),
                 ("topk_groups", ctypes.c_int32), ("group_score", ctypes.c_int32),
                 ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+# gates of the residual norm (mm_moe_gate)
+GATE = {None: 0, "channel": 1, "token": 2}
+
+
+class ResNorm(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("res_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                ("post", ctypes.c_int32), ("gate", ctypes.c_int32), ("pre", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 MM_MOE_RECOMPUTE = 1  # activation checkpointing (include/mm_moe.h)
@@ -178,6 +190,12 @@ def lib() -> ctypes.CDLL:
         L.mm_moe_select_backward.argtypes = [qp] + [_vp] * 6
         L.mm_moe_router_select_forward.argtypes = [sp, qp] + [_vp] * 7
         L.mm_moe_router_select_backward.argtypes = [sp, qp] + [_vp] * 10
+        rp = ctypes.POINTER(ResNorm)
+        L.mm_moe_resnorm_workspace_size.argtypes = [rp, szp]
+        L.mm_moe_resnorm_forward.argtypes = [rp, _vp, i64, _vp, i64] + [_vp] * 4 + \
+            [i64, _vp, i64] + [_vp] * 3
+        L.mm_moe_resnorm_backward.argtypes = [rp] + [_vp, i64] * 4 + [_vp] * 5 + \
+            [_vp, i64] * 2 + [_vp] * 5
         for fn in EXPORTS:
             getattr(L, fn).restype = ctypes.c_int
         L.mm_moe_kernel_name.restype = ctypes.c_char_p
@@ -473,6 +491,37 @@ def mm_moe_router_select_backward(shape: Shape, select: Select, x, W_router, log
         ctypes.byref(shape), select, _ptr(x), _ptr(W_router), _ptr(logits), _ptr(topk_idx),
         _ptr(dtopk_w), _ptr(dlogits_aux), _ptr(dlogits), _ptr(dx), _ptr(dW_router),
         _stream(stream)))
+
+
+def mm_moe_resnorm_workspace_size(shape: ResNorm) -> int:
+    return _size("mm_moe_resnorm_workspace_size", ctypes.byref(shape))
+
+
+def _rows(t) -> Tuple[int, int]:
+    return (0, 0) if t is None else (t.data_ptr(), t.stride(0))
+
+
+def mm_moe_resnorm_forward(shape: ResNorm, x, f, post_weight, gate, pre_weight, out, n, rstd_f,
+                           rstd_out, stream=None) -> None:
+    """x, f, out and n [T, H] with rows stride(0) elements apart."""
+    st = lib().mm_moe_resnorm_forward(
+        shape, *_rows(x), *_rows(f), _ptr(post_weight), _ptr(gate), _ptr(pre_weight), *_rows(out),
+        *_rows(n), _ptr(rstd_f), _ptr(rstd_out),
+        stream if type(stream) is int else _stream(stream))
+    if st:
+        _check("mm_moe_resnorm_forward", st)
+
+
+def mm_moe_resnorm_backward(shape: ResNorm, dout, dn, out, f, post_weight, gate, pre_weight, rstd_f,
+                            rstd_out, dx, df, dpost_weight, dgate, dpre_weight, workspace,
+                            stream=None) -> None:
+    st = lib().mm_moe_resnorm_backward(
+        shape, *_rows(dout), *_rows(dn), *_rows(out), *_rows(f), _ptr(post_weight), _ptr(gate),
+        _ptr(pre_weight), _ptr(rstd_f), _ptr(rstd_out), *_rows(dx), *_rows(df), _ptr(dpost_weight),
+        _ptr(dgate), _ptr(dpre_weight), _ptr(workspace),
+        stream if type(stream) is int else _stream(stream))
+    if st:
+        _check("mm_moe_resnorm_backward", st)
 
 
 def mm_moe_read_status(scratch, stream=None) -> int:

@@ -29,6 +29,9 @@ enum OpKernelId {
   K_ADAMW_MOMENTS,
   K_SELECT_FWD,
   K_SELECT_BWD,
+  K_RESNORM_FWD,
+  K_RESNORM_BWD,
+  K_RESNORM_FINISH,
   K_ALL_COUNT
 };
 

@@ -19,7 +19,7 @@ static const char* const kKernelNames[K_ALL_COUNT] = {
     "gemm_dense_nt", "gemm_dense_nn", "gemm_dense_tn", "router_topk", "router_dlogits",
     "norm_fwd", "norm_bwd", "norm_bwd_finish", "balance_fwd", "balance_finish", "balance_bwd",
     "grad_sq", "grad_norm", "grad_scale", "adamw", "adamw_moments",
-    "select_fwd", "select_bwd"};
+    "select_fwd", "select_bwd", "resnorm_fwd", "resnorm_bwd", "resnorm_finish"};
 
 namespace {
 struct Rec {

@@ -1,0 +1,281 @@
+// resnorm.cu -- the norms before and after a block with its gate and residual scale: the
+// forward (formulas in resnorm.cuh).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "internal.h"
+#include "ops.cuh"
+#include "resnorm.cuh"
+
+namespace mmmoe {
+
+template <typename T, typename R>
+struct FwdOps {
+  Rows<const R> x;
+  Rows<const T> f;  // null: out is x and not stored
+  Rows<R> out;
+  Rows<T> n;  // null: no norm in front of the next block
+  const void *w_post, *gate_c, *gate_t, *w_pre;
+  bool p32;
+  float scale, eps;
+  float *rstd_f, *rstd_out;
+  int T_, H, GT;
+};
+
+template <typename T, typename R, int NU>
+constexpr int rn_fwd_steps =
+    std::max(1, std::min(4, RN_RING / (RN_THREADS * (Operand<T, NU, 8>::BYTES + Operand<R, NU, 8>::BYTES))));
+
+template <typename T, typename R, int NU, int U>
+__global__ void __launch_bounds__(RN_THREADS, 1) resnorm_fwd_kernel(const FwdOps<T, R> a) {
+  constexpr int S = U == 8 ? rn_fwd_steps<T, R, NU> : 1;
+  using OF = Operand<T, NU, U>;
+  using OX = Operand<R, NU, U>;
+  extern __shared__ __align__(16) unsigned char ring_bytes[];
+  __shared__ Sums<1> s_sum[2][RN_THREADS / 32];
+  const uint32_t piece = blockDim.x * 16, step_bytes = (OF::BYTES + OX::BYTES) * blockDim.x;
+  const uint32_t ring =
+      static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)) + threadIdx.x * 16;
+  const uint32_t x_at = OF::BYTES * blockDim.x;
+  pdl_wait();
+  pdl_trigger();
+  Cols<NU, U> c;
+  c.init(a.GT, a.H);
+  const uint32_t n = a.T_, step = gridDim.x * c.groups;
+  uint32_t t = blockIdx.x * c.groups + c.g, tw = c.first_of_warp(t), ta = t;
+  const float inv = 1.f / static_cast<float>(a.H);
+  OF of;
+  OX ox;
+  const auto issue = [&](uint32_t at) {
+    if (ta < n) {
+      if (a.f.p != nullptr) of.issue(c, a.f.row(ta), at, piece);
+      ox.issue(c, a.x.row(ta), at + x_at, piece);
+    }
+    ta += step;
+    if constexpr (U == 8) async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(ring + i * step_bytes);
+  float cf[NU * U], w[NU * U];
+  if (a.f.p != nullptr) load_coef<T, NU, U>(c, a.w_post, a.gate_c, a.p32, a.scale, cf);
+  if (a.n.p != nullptr) load_params<T, NU, U>(c, a.w_pre, a.p32, w);
+  int buf = 0;
+  uint32_t st = ring, st_in = ring + (S - 1) * step_bytes;
+  const uint32_t ring_end = ring + S * step_bytes;
+  for (; tw < n; t += step, tw += step) {
+    issue(st_in);
+    const bool live = t < n;
+    float gt = live && a.gate_t != nullptr ? param<T>(a.gate_t, a.p32, t) : 1.f;
+    if constexpr (U == 8) async_wait<S - 1>();
+    float o[NU * U];
+    if (a.f.p != nullptr) {
+      if (a.w_post != nullptr) {
+        float ss[1] = {0.f};
+        if (live)
+#pragma unroll
+          for (int i = 0; i < NU; ++i)
+            if (c.has(i)) {
+              float f[U];
+              of.get(st, piece, i, f);
+#pragma unroll
+              for (int k = 0; k < U; ++k) ss[0] = fmaf(f[k], f[k], ss[0]);
+            }
+        group_sum<1>(ss, s_sum[buf], c.g, a.GT);
+        buf ^= 1;
+        const float rf = rsqrtf(fmaf(ss[0], inv, a.eps));
+        if (live && c.j == 0) a.rstd_f[t] = rf;
+        gt *= rf;
+      }
+    }
+    float ss[1] = {0.f};
+    if (live)
+#pragma unroll
+      for (int i = 0; i < NU; ++i)
+        if (c.has(i)) {
+          float x[U], f[U];
+          ox.get(st + x_at, piece, i, x);
+          if (a.f.p != nullptr) {
+            of.get(st, piece, i, f);
+#pragma unroll
+            for (int k = 0; k < U; ++k) x[k] = fmaf(cf[i * U + k] * gt, f[k], x[k]);
+            put_unit<R, U>(a.out.row(t) + c.col(i), x);
+          }
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            o[i * U + k] = x[k];
+            ss[0] = fmaf(x[k], x[k], ss[0]);
+          }
+        }
+    if (a.n.p != nullptr) {
+      group_sum<1>(ss, s_sum[buf], c.g, a.GT);
+      buf ^= 1;
+      const float ro = rsqrtf(fmaf(ss[0], inv, a.eps));
+      if (live) {
+        if (c.j == 0) a.rstd_out[t] = ro;
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+          if (c.has(i)) {
+            float y[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) y[k] = o[i * U + k] * ro * w[i * U + k];
+            put_unit<T, U>(a.n.row(t) + c.col(i), y);
+          }
+      }
+    }
+    st_in = st;
+    st += step_bytes;
+    if (st == ring_end) st = ring;
+  }
+  if constexpr (U == 8) async_wait<0>();
+}
+
+// Any width: a CTA a row, read up to three times (from L1 and L2).
+template <typename T, typename R, int U>
+__global__ void __launch_bounds__(LOOP_THREADS) resnorm_fwd_loop_kernel(const FwdOps<T, R> a) {
+  __shared__ float s[LOOP_THREADS / 32];
+  pdl_wait();
+  pdl_trigger();
+  const float inv = 1.f / static_cast<float>(a.H);
+  const bool has_f = a.f.p != nullptr;
+  for (int64_t t = blockIdx.x; t < a.T_; t += gridDim.x) {
+    float k = a.scale * (a.gate_t != nullptr ? param<T>(a.gate_t, a.p32, t) : 1.f);
+    if (has_f && a.w_post != nullptr) {
+      float ss = 0.f;
+      for (int i = threadIdx.x * U; i < a.H; i += LOOP_THREADS * U) {
+        float f[U];
+        loop_get<T, U>(a.f.row(t) + i, f);
+#pragma unroll
+        for (int j = 0; j < U; ++j) ss = fmaf(f[j], f[j], ss);
+      }
+      const float rf = rsqrtf(fmaf(block_sum(ss, s), inv, a.eps));
+      if (threadIdx.x == 0) a.rstd_f[t] = rf;
+      k *= rf;
+    }
+    const auto values = [&](int i, float (&x)[U]) {
+      loop_get<R, U>(a.x.row(t) + i, x);
+      if (!has_f) return;
+      float f[U];
+      loop_get<T, U>(a.f.row(t) + i, f);
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        float cf = k;
+        if (a.w_post != nullptr) cf *= param<T>(a.w_post, a.p32, i + j);
+        if (a.gate_c != nullptr) cf *= param<T>(a.gate_c, a.p32, i + j);
+        x[j] = fmaf(cf, f[j], x[j]);
+      }
+    };
+    float ro = 0.f;
+    if (a.n.p != nullptr) {
+      float ss = 0.f;
+      for (int i = threadIdx.x * U; i < a.H; i += LOOP_THREADS * U) {
+        float x[U];
+        values(i, x);
+#pragma unroll
+        for (int j = 0; j < U; ++j) ss = fmaf(x[j], x[j], ss);
+      }
+      ro = rsqrtf(fmaf(block_sum(ss, s), inv, a.eps));
+      if (threadIdx.x == 0) a.rstd_out[t] = ro;
+    }
+    // (out may lie over x: every element is written by the thread that read it last)
+    for (int i = threadIdx.x * U; i < a.H; i += LOOP_THREADS * U) {
+      float x[U];
+      values(i, x);
+      if (has_f) put_unit<R, U>(a.out.row(t) + i, x);
+      if (a.n.p != nullptr) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) x[j] *= ro * param<T>(a.w_pre, a.p32, i + j);
+        put_unit<T, U>(a.n.row(t) + i, x);
+      }
+    }
+  }
+}
+
+template <typename T, typename R, int NU, int U>
+static cudaError_t fwd_launch(const Ctx& c, FwdOps<T, R> a) {
+  a.GT = rn_group_threads<NU, U>(a.H);
+  const NormGrid g = rn_grid(a.GT, a.T_, c.num_sms);
+  const int nt = g.GT * g.groups;
+  const size_t smem = U == 8 ? static_cast<size_t>(rn_fwd_steps<T, R, NU>) * nt *
+                                   (Operand<T, NU, U>::BYTES + Operand<R, NU, U>::BYTES)
+                             : 0;
+  auto* kern = resnorm_fwd_kernel<T, R, NU, U>;
+  const cudaError_t e = allow_smem(kern, smem);
+  if (e != cudaSuccess) return e;
+  return launch_k(c.stream, kern, dim3(g.ctas), dim3(nt), smem, a);
+}
+
+}  // namespace mmmoe
+
+using namespace mmmoe;
+
+extern "C" MM_MOE_API mm_moe_status mm_moe_resnorm_workspace_size(const mm_moe_resnorm* shape,
+                                                                  size_t* bytes) {
+  if (!resnorm_shape_ok(shape) || bytes == nullptr) return MM_MOE_EINVAL;
+  *bytes = (static_cast<size_t>(norm_parts(shape->T)) * 2 * shape->H + shape->T) * sizeof(float);
+  return MM_MOE_OK;
+}
+
+extern "C" MM_MOE_API mm_moe_status mm_moe_resnorm_forward(
+    const mm_moe_resnorm* shape, const void* x, int64_t ldx, const void* f, int64_t ldf,
+    const void* post_weight, const void* gate, const void* pre_weight, void* out, int64_t ldout,
+    void* n, int64_t ldn, float* rstd_f, float* rstd_out, void* stream) {
+  if (!resnorm_shape_ok(shape)) return MM_MOE_EINVAL;
+  const size_t b = dtype_bytes(shape->dtype), rb = dtype_bytes(shape->res_dtype),
+               pb = dtype_bytes(shape->param_dtype);
+  const RowSpan sx{x, ldx, rb}, sf{f, ldf, b}, so{f != nullptr ? out : nullptr, ldout, rb},
+      sn{shape->pre ? n : nullptr, ldn, b};
+  if (!span_ok(sx, shape) || (f == nullptr && !shape->pre)) return MM_MOE_EINVAL;
+  if (f != nullptr &&
+      (!span_ok(sf, shape) || !span_ok(so, shape) ||
+       (shape->post && (!vec_ok(post_weight, pb) || !vec_ok(rstd_f, 4))) ||
+       (shape->gate != MM_MOE_GATE_NONE && !vec_ok(gate, pb))))
+    return MM_MOE_EINVAL;
+  if (shape->pre && (!span_ok(sn, shape) || !vec_ok(pre_weight, pb) || !vec_ok(rstd_out, 4)))
+    return MM_MOE_EINVAL;
+  const bool in_place = so.p == x && (shape->T == 1 || ldout == ldx);
+  if ((!in_place && spans_meet(so, sx, shape)) || spans_meet(so, sf, shape) ||
+      spans_meet(sn, sx, shape) || spans_meet(sn, sf, shape) || spans_meet(sn, so, shape))
+    return MM_MOE_EINVAL;
+  const int sms = std::min(152, sm_count_103());
+  if (sms == 0) return MM_MOE_ENOTSUP;
+  int launches = 0;
+  const Ctx c{static_cast<cudaStream_t>(stream), sms, &launches};
+  const int T_ = static_cast<int>(shape->T), H = static_cast<int>(shape->H);
+  const bool even = H % 8 == 0 && span_even(sx, shape) && span_even(sf, shape) &&
+                    span_even(so, shape) && span_even(sn, shape);
+  prof_begin(c, K_RESNORM_FWD);
+  const cudaError_t e = with_types(shape, [&](auto* t, auto* r) -> cudaError_t {
+    using T = std::remove_pointer_t<decltype(t)>;
+    using R = std::remove_pointer_t<decltype(r)>;
+    const FwdOps<T, R> a{{static_cast<const R*>(x), ldx},
+                         {static_cast<const T*>(f), ldf},
+                         {static_cast<R*>(out), ldout},
+                         {static_cast<T*>(shape->pre ? n : nullptr), ldn},
+                         shape->post && f != nullptr ? post_weight : nullptr,
+                         shape->gate == MM_MOE_GATE_CHANNEL && f != nullptr ? gate : nullptr,
+                         shape->gate == MM_MOE_GATE_TOKEN && f != nullptr ? gate : nullptr,
+                         pre_weight,
+                         shape->param_dtype == MM_MOE_DT_F32,
+                         shape->scale,
+                         shape->eps,
+                         rstd_f,
+                         rstd_out,
+                         T_,
+                         H,
+                         0};
+    if (even && H <= 16 * RN_THREADS) {
+      const int g1 = rn_group_threads<1, 8>(H);
+      if (g1 != 0 && T_ <= c.num_sms * std::max(1, RN_THREADS / g1))
+        return fwd_launch<T, R, 1, 8>(c, a);
+      return fwd_launch<T, R, 2, 8>(c, a);
+    }
+    if (!even && H <= 8 * RN_THREADS) return fwd_launch<T, R, 8, 1>(c, a);
+    return launch_k(c.stream,
+                    even ? resnorm_fwd_loop_kernel<T, R, 8> : resnorm_fwd_loop_kernel<T, R, 1>,
+                    dim3(std::min(T_, c.num_sms * 4)), dim3(LOOP_THREADS), 0, a);
+  });
+  prof_end(c, K_RESNORM_FWD);
+  return op_status(e);
+}

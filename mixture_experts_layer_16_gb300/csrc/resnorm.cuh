@@ -1,0 +1,285 @@
+// resnorm.cuh -- the norms before and after a block fused with its gate and residual scale: what
+// the forward (resnorm.cu) and the backward (resnorm_bwd.cu) share.
+//
+//   u = w_post f rf,  rf = (1/H sum f^2 + eps)^(-1/2)          (u = f without a norm behind the block)
+//   out = x + scale gate u                                     gate: per channel, per token or none
+//   n = w_pre out ro,  ro = (1/H sum out^2 + eps)^(-1/2)       (the next block's norm)
+// Backward, with oh = out ro, fh = f rf, c = scale gate w_post and v = w_pre dn:
+//   D = dout + ro (v - oh <oh v>),   dx = D,                   <>: mean over the row
+//   q = c D,  df = rf (q - fh <fh q>)                          (df = q without the norm)
+//   dw_pre = sum_t dn oh;  K = sum_t [gate_t] fh D gives dw_post = scale gate_c K and
+//   dgate_c = scale w_post K;  dgate_t = scale sum_h w_post fh D
+// <fh q> needs D, which needs <oh v>; so that a row's sums meet at one barrier, the backward sums
+//   s1 = sum oh v,  s2 = sum c fh (dout + ro v),  s3 = sum c fh oh,   sum c fh D = s2 - ro s1 s3 / H.
+//
+// f, n and their gradients are of one type, x and out (the residual stream) of it or fp32,
+// the parameters and the gate of it or fp32.  Everything is computed in fp32 and rounded once where it
+// is stored; n comes from out before its rounding.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <type_traits>
+
+#include "internal.h"
+#include "norm.cuh"
+#include "ops.cuh"
+
+namespace mmmoe {
+
+constexpr int RN_THREADS = 512;
+constexpr int RN_RING = 196608;  // bytes of the ring at most
+
+// A row is cut into units of U = 8 columns (16 bytes of 16-bit types, 32 of fp32), dealt out to
+// the threads of a group in turn, NU to each; rows on no 16-byte boundary, or of a width that is no
+// multiple of 8, into single columns (U = 1).  Units of 8 come through a ring in shared memory by
+// cp.async, S - 1 rows ahead; a thread reads only what it copied itself.  Single columns are
+// loaded into registers.
+template <int NU, int U>
+struct Cols {
+  static constexpr int N = NU * U;
+  int GT, g, j, groups, H;
+  __device__ __forceinline__ void init(int GT_, int H_) {
+    GT = GT_;
+    H = H_;
+    g = threadIdx.x / GT;
+    j = threadIdx.x - g * GT;
+    groups = blockDim.x / GT;
+  }
+  // the first row of the warp's groups (they loop together)
+  __device__ __forceinline__ uint32_t first_of_warp(uint32_t t) const {
+    return GT < 32 ? t - (g & (32 / GT - 1)) : t;
+  }
+  __device__ __forceinline__ int col(int i) const { return (j + i * GT) * U; }
+  __device__ __forceinline__ bool has(int i) const { return col(i) < H; }
+};
+
+// One row operand of type V on its way to the thread's registers.
+template <typename V, int NU, int U>
+struct Operand {
+  static constexpr int PARTS = U == 8 ? 8 / VN<V> : 0;  // 16-byte pieces of a unit
+  static constexpr int BYTES = PARTS * 16 * NU;         // of a thread's share of a row in the ring
+  float reg[U == 1 ? NU : 1];
+  __device__ __forceinline__ void issue(const Cols<NU, U>& c, const V* row, uint32_t at,
+                                        uint32_t piece) {
+    if constexpr (U == 8) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i)
+        if (c.has(i)) {
+#pragma unroll
+          for (int h = 0; h < PARTS; ++h)
+            async_copy(at + (i * PARTS + h) * piece, row + c.col(i) + h * VN<V>);
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NU; ++i) reg[i] = c.has(i) ? to_f32(row[c.col(i)]) : 0.f;
+    }
+  }
+  // unit i's values (any where the thread has none)
+  __device__ __forceinline__ void get(uint32_t at, uint32_t piece, int i, float (&f)[U]) const {
+    if constexpr (U == 8) {
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h) {
+        float t[VN<V>];
+        unpack(lds16(at + (i * PARTS + h) * piece), t, static_cast<const V*>(nullptr));
+#pragma unroll
+        for (int k = 0; k < VN<V>; ++k) f[h * VN<V> + k] = t[k];
+      }
+    } else {
+      f[0] = reg[i];
+    }
+  }
+};
+
+// U elements of a row from memory
+template <typename V, int U>
+__device__ __forceinline__ void loop_get(const V* p, float (&f)[U]) {
+  if constexpr (U == 8) {
+#pragma unroll
+    for (int h = 0; h < 8 / VN<V>; ++h) {
+      float t[VN<V>];
+      unpack(reinterpret_cast<const uint4*>(p)[h], t, p);
+#pragma unroll
+      for (int k = 0; k < VN<V>; ++k) f[h * VN<V> + k] = t[k];
+    }
+  } else {
+    f[0] = to_f32(*p);
+  }
+}
+
+template <typename V, int U>
+__device__ __forceinline__ void put_unit(V* p, const float (&f)[U]) {
+  if constexpr (U == 8) {
+#pragma unroll
+    for (int h = 0; h < 8 / VN<V>; ++h) {
+      float t[VN<V>];
+#pragma unroll
+      for (int k = 0; k < VN<V>; ++k) t[k] = f[h * VN<V> + k];
+      reinterpret_cast<uint4*>(p)[h] = pack(t, p);
+    }
+  } else {
+    *p = from_f32<V>(f[0]);
+  }
+}
+
+// Parameters (of type T, or fp32) of the thread's columns; zero where it has none.
+template <typename T, int NU, int U>
+__device__ __forceinline__ void load_params(const Cols<NU, U>& c, const void* p, bool p32,
+                                            float (&v)[NU * U]) {
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    float f[U] = {};
+    if (c.has(i)) {
+      const bool whole = U == 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+      if (p32) {
+        const float* q = static_cast<const float*>(p) + c.col(i);
+        if constexpr (U == 8) {
+          if (whole) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float4 t = __ldg(reinterpret_cast<const float4*>(q) + h);
+              f[4 * h] = t.x, f[4 * h + 1] = t.y, f[4 * h + 2] = t.z, f[4 * h + 3] = t.w;
+            }
+          }
+        }
+        if (!whole)
+#pragma unroll
+          for (int k = 0; k < U; ++k) f[k] = __ldg(q + k);
+      } else {
+        const T* q = static_cast<const T*>(p) + c.col(i);
+        if constexpr (U == 8) {
+          if (whole) {
+#pragma unroll
+            for (int h = 0; h < 8 / VN<T>; ++h) {
+              float t[VN<T>];
+              unpack(__ldg(reinterpret_cast<const uint4*>(q) + h), t, q);
+#pragma unroll
+              for (int k = 0; k < VN<T>; ++k) f[h * VN<T> + k] = t[k];
+            }
+          }
+        }
+        if (!whole)
+#pragma unroll
+          for (int k = 0; k < U; ++k) f[k] = to_f32(q[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) v[i * U + k] = f[k];
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float param(const void* p, bool p32, int64_t i) {
+  return p32 ? __ldg(static_cast<const float*>(p) + i) : to_f32(static_cast<const T*>(p)[i]);
+}
+
+// c = scale [gate_c] [w_post] of the thread's columns
+template <typename T, int NU, int U>
+__device__ __forceinline__ void load_coef(const Cols<NU, U>& c, const void* w_post,
+                                          const void* gate_c, bool p32, float scale,
+                                          float (&v)[NU * U]) {
+  if (w_post != nullptr) {
+    load_params<T, NU, U>(c, w_post, p32, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < NU * U; ++k) v[k] = 1.f;
+  }
+#pragma unroll
+  for (int k = 0; k < NU * U; ++k) v[k] *= scale;
+  if (gate_c != nullptr) {
+    float t[NU * U];
+    load_params<T, NU, U>(c, gate_c, p32, t);
+#pragma unroll
+    for (int k = 0; k < NU * U; ++k) v[k] *= t[k];
+  }
+}
+
+// Three sums over a group, as group_sum (a warp's in 16 bytes).
+__device__ __forceinline__ void group_sum3(float (&v)[3], float4* s, int g, int GT) {
+#pragma unroll
+  for (int q = 0; q < 3; ++q) v[q] = lanes_sum(v[q], GT);
+  if (GT <= 32) return;
+  const int gw = GT >> 5;
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = make_float4(v[0], v[1], v[2], 0.f);
+  group_bar(g, GT);
+  s += g * gw;
+  float4 t = s[0];
+  for (int i = 1; i < gw; ++i) {
+    const float4 o = s[i];
+    t.x += o.x, t.y += o.y, t.z += o.z;
+  }
+  v[0] = t.x, v[1] = t.y, v[2] = t.z;
+}
+
+// ------------------------------------------------------------------------ host side
+constexpr int RN_MAX_H = 1 << 20;
+
+inline bool resnorm_shape_ok(const mm_moe_resnorm* s) {
+  return s != nullptr && s->T >= 1 && s->T < (int64_t{1} << 31) && s->H >= 1 && s->H <= RN_MAX_H &&
+         dtype_ok(s->dtype) && (s->res_dtype == s->dtype || s->res_dtype == MM_MOE_DT_F32) &&
+         (s->param_dtype == s->dtype || s->param_dtype == MM_MOE_DT_F32) && s->post >= 0 &&
+         s->post <= 1 && s->pre >= 0 && s->pre <= 1 && s->gate >= MM_MOE_GATE_NONE &&
+         s->gate <= MM_MOE_GATE_TOKEN && s->eps >= 0.f && s->eps <= 3.4028235e38f &&
+         s->scale >= -3.4028235e38f && s->scale <= 3.4028235e38f;
+}
+
+// An operand of T rows, `bytes` an element.
+struct RowSpan {
+  const void* p;
+  int64_t ld;
+  size_t bytes;
+};
+inline bool span_ok(const RowSpan& r, const mm_moe_resnorm* s) {
+  return r.p != nullptr && reinterpret_cast<uintptr_t>(r.p) % r.bytes == 0 &&
+         (r.ld >= s->H || s->T == 1) && r.ld < (int64_t{1} << 40);
+}
+// Whether two operands may share memory: exact for rows equally far apart, else by their extents.
+inline bool spans_meet(const RowSpan& a, const RowSpan& b, const mm_moe_resnorm* s) {
+  if (a.p == nullptr || b.p == nullptr) return false;
+  const auto end = [&](const RowSpan& r) {
+    return reinterpret_cast<uintptr_t>(r.p) +
+           static_cast<unsigned __int128>((s->T - 1) * static_cast<__int128>(s->T == 1 ? 0 : r.ld) + s->H) *
+               r.bytes;
+  };
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  if (pa >= end(b) || pb >= end(a)) return false;
+  const uintptr_t la = static_cast<uintptr_t>(a.ld) * a.bytes, lb = static_cast<uintptr_t>(b.ld) * b.bytes;
+  if (s->T == 1 || la != lb) return true;
+  const uintptr_t ra = s->H * a.bytes, rb = s->H * b.bytes;
+  const uintptr_t d = pb >= pa ? (pb - pa) % la : (la - (pa - pb) % la) % la;  // b's row within a's
+  return d < ra || la - d < rb;
+}
+inline bool span_even(const RowSpan& r, const mm_moe_resnorm* s) {
+  return r.p == nullptr || (al16(r.p) && (s->T == 1 || r.ld * r.bytes % 16 == 0));
+}
+
+// How the rows are spread: GT threads a row, groups of them in a CTA.
+template <int NU, int U>
+int rn_group_threads(int H) {
+  const int units = (H + U - 1) / U;
+  const int n = (units + NU - 1) / NU;
+  if (n > RN_THREADS) return 0;
+  if (n > 32) return (n + 31) / 32 * 32;
+  int g = 1;
+  while (g < n) g *= 2;
+  return g;
+}
+inline NormGrid rn_grid(int GT, int T, int sms) {
+  const int per_warp = GT < 32 ? 32 / GT : 1;
+  int groups = std::min(RN_THREADS / GT, div_up(T, sms));
+  groups = (groups + per_warp - 1) / per_warp * per_warp;
+  return NormGrid{GT, groups, std::min(sms, div_up(T, groups))};
+}
+
+// f(tag of T, tag of R): the types of the block and of the residual stream
+template <typename F>
+auto with_types(const mm_moe_resnorm* s, F f) {
+  return with_dtype(s->dtype, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    if (s->res_dtype == s->dtype) return f(t, static_cast<T*>(nullptr));
+    return f(t, static_cast<float*>(nullptr));
+  });
+}
+
+}  // namespace mmmoe

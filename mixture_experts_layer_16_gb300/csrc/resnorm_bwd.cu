@@ -1,0 +1,456 @@
+// resnorm_bwd.cu -- the norms before and after a block with its gate and residual scale: the
+// backward, with the reduction of the parameters' gradients (formulas in resnorm.cuh).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "internal.h"
+#include "ops.cuh"
+#include "resnorm.cuh"
+
+namespace mmmoe {
+
+template <typename T, typename R>
+struct BwdOps {
+  Rows<const R> dout;  // null: zero
+  Rows<const T> dn;    // null: no norm in front of the next block
+  Rows<const R> out;
+  Rows<const T> f;  // null: neither f nor its gradient
+  Rows<R> dx;
+  Rows<T> df;
+  const void *w_post, *gate_c, *gate_t, *w_pre;
+  bool p32, sums_f;  // sums_f: K is wanted (a norm behind the block, or a gate of its channels)
+  float scale;
+  const float *rstd_f, *rstd_out;
+  void* dgate_t;
+  float* part;  // [CTA][2][H]: K, dw_pre
+  float* mean_ov;  // [T] <oh v> (the looped kernels')
+  int T_, H, GT;
+};
+
+template <typename T, typename R, int NU>
+constexpr int rn_bwd_steps = std::max(
+    1, std::min(4, RN_RING / (RN_THREADS * 2 * (Operand<T, NU, 8>::BYTES + Operand<R, NU, 8>::BYTES))));
+
+template <typename T, typename R, int NU, int U>
+__global__ void __launch_bounds__(RN_THREADS, 1) resnorm_bwd_kernel(const BwdOps<T, R> a) {
+  constexpr int S = U == 8 ? rn_bwd_steps<T, R, NU> : 1;
+  using OT = Operand<T, NU, U>;
+  using OR = Operand<R, NU, U>;
+  extern __shared__ __align__(16) unsigned char ring_bytes[];
+  __shared__ float4 s_sum[2][RN_THREADS / 32];
+  const uint32_t nt = blockDim.x, piece = nt * 16, step_bytes = 2 * (OT::BYTES + OR::BYTES) * nt;
+  const uint32_t ring =
+      static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)) + threadIdx.x * 16;
+  const uint32_t out_at = OR::BYTES * nt, dn_at = 2 * out_at, f_at = dn_at + OT::BYTES * nt;
+  pdl_wait();
+  pdl_trigger();
+  Cols<NU, U> c;
+  c.init(a.GT, a.H);
+  const uint32_t n = a.T_, step = gridDim.x * c.groups;
+  uint32_t t = blockIdx.x * c.groups + c.g, tw = c.first_of_warp(t), ta = t;
+  const float inv = 1.f / static_cast<float>(a.H);
+  const bool pre = a.dn.p != nullptr, has_f = a.f.p != nullptr, has_d = a.dout.p != nullptr;
+  const bool post = a.w_post != nullptr;
+  OR od, oo;
+  OT on, of;
+  const auto issue = [&](uint32_t at) {
+    if (ta < n) {
+      if (has_d) od.issue(c, a.dout.row(ta), at, piece);
+      if (pre) {
+        oo.issue(c, a.out.row(ta), at + out_at, piece);
+        on.issue(c, a.dn.row(ta), at + dn_at, piece);
+      }
+      if (has_f) of.issue(c, a.f.row(ta), at + f_at, piece);
+    }
+    ta += step;
+    if constexpr (U == 8) async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(ring + i * step_bytes);
+  float cf[NU * U], w[NU * U], K[NU * U], dw[NU * U];
+  load_coef<T, NU, U>(c, a.w_post, a.gate_c, a.p32, a.scale, cf);
+  if (pre) load_params<T, NU, U>(c, a.w_pre, a.p32, w);
+#pragma unroll
+  for (int k = 0; k < NU * U; ++k) K[k] = dw[k] = 0.f;
+  int buf = 0;
+  uint32_t st = ring, st_in = ring + (S - 1) * step_bytes;
+  const uint32_t ring_end = ring + S * step_bytes;
+  for (; tw < n; t += step, tw += step) {
+    issue(st_in);
+    const bool live = t < n;
+    const float gt = live && a.gate_t != nullptr ? param<T>(a.gate_t, a.p32, t) : 1.f;
+    const float rf = live && post ? __ldg(a.rstd_f + t) : 1.f;
+    const float ro = live && pre ? __ldg(a.rstd_out + t) : 0.f;
+    if constexpr (U == 8) async_wait<S - 1>();
+    // unit i: dout, oh, dn, fh
+    const auto unit = [&](int i, float (&d)[U], float (&oh)[U], float (&dn)[U], float (&fh)[U]) {
+#pragma unroll
+      for (int k = 0; k < U; ++k) d[k] = oh[k] = dn[k] = fh[k] = 0.f;
+      if (has_d) od.get(st, piece, i, d);
+      if (pre) {
+        oo.get(st + out_at, piece, i, oh);
+        on.get(st + dn_at, piece, i, dn);
+#pragma unroll
+        for (int k = 0; k < U; ++k) oh[k] *= ro;
+      }
+      if (has_f) {
+        of.get(st + f_at, piece, i, fh);
+#pragma unroll
+        for (int k = 0; k < U; ++k) fh[k] *= rf;
+      }
+    };
+    float s[3] = {0.f, 0.f, 0.f};
+    if (live)
+#pragma unroll
+      for (int i = 0; i < NU; ++i)
+        if (c.has(i)) {
+          float d[U], oh[U], dn[U], fh[U];
+          unit(i, d, oh, dn, fh);
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            const int e = i * U + k;
+            const float v = pre ? w[e] * dn[k] : 0.f, cfh = cf[e] * fh[k];
+            s[0] = fmaf(oh[k], v, s[0]);
+            s[1] = fmaf(cfh, fmaf(ro, v, d[k]), s[1]);
+            s[2] = fmaf(cfh, oh[k], s[2]);
+            dw[e] = fmaf(dn[k], oh[k], dw[e]);
+          }
+        }
+    group_sum3(s, s_sum[buf], c.g, a.GT);
+    buf ^= 1;
+    const float m1 = s[0] * inv;
+    const float cfd = s[1] - ro * m1 * s[2];  // sum c fh D
+    if (live) {
+      if (c.j == 0 && a.dgate_t != nullptr) {
+        if (a.p32)
+          static_cast<float*>(a.dgate_t)[t] = cfd;
+        else
+          static_cast<T*>(a.dgate_t)[t] = from_f32<T>(cfd);
+      }
+      const float m2 = post ? gt * cfd * inv : 0.f;
+#pragma unroll
+      for (int i = 0; i < NU; ++i)
+        if (c.has(i)) {
+          float d[U], oh[U], dn[U], fh[U];
+          unit(i, d, oh, dn, fh);
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            const int e = i * U + k;
+            const float v = pre ? w[e] * dn[k] : 0.f;
+            d[k] = fmaf(ro, fmaf(-m1, oh[k], v), d[k]);
+            const float gd = gt * d[k];
+            K[e] = fmaf(fh[k], gd, K[e]);
+            fh[k] = rf * fmaf(-m2, fh[k], cf[e] * gd);
+          }
+          put_unit<R, U>(a.dx.row(t) + c.col(i), d);
+          if (has_f) put_unit<T, U>(a.df.row(t) + c.col(i), fh);
+        }
+    }
+    st_in = st;
+    st += step_bytes;
+    if (st == ring_end) st = ring;
+  }
+  if constexpr (U == 8) async_wait<0>();
+  if (!a.sums_f && !pre) return;
+  // the CTA's groups' column sums, added in order
+  float* const p0 = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
+  float* const sj = reinterpret_cast<float*>(ring_bytes);  // [groups][2][H]
+  float* const q = c.groups == 1 ? p0 : sj + 2 * c.g * a.H;
+  if (c.groups > 1) __syncthreads();  // (the ring is read no more)
+#pragma unroll
+  for (int i = 0; i < NU; ++i)
+    if (c.has(i)) {
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        q[c.col(i) + k] = K[i * U + k];
+        q[a.H + c.col(i) + k] = dw[i * U + k];
+      }
+    }
+  if (c.groups == 1) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * a.H; i += nt) {
+    float v = sj[i];
+    for (int k = 1; k < c.groups; ++k) v += sj[2 * k * a.H + i];
+    p0[i] = v;
+  }
+}
+
+// Any width: dx and df, a CTA a row, read twice; <oh v> is left for the column sums.
+template <typename T, typename R, int U>
+__global__ void __launch_bounds__(LOOP_THREADS) resnorm_dx_loop_kernel(const BwdOps<T, R> a) {
+  __shared__ float s[LOOP_THREADS / 32];
+  pdl_wait();
+  pdl_trigger();
+  const float inv = 1.f / static_cast<float>(a.H);
+  const bool pre = a.dn.p != nullptr, has_f = a.f.p != nullptr, post = a.w_post != nullptr;
+  for (int64_t t = blockIdx.x; t < a.T_; t += gridDim.x) {
+    const float gt = a.gate_t != nullptr ? param<T>(a.gate_t, a.p32, t) : 1.f;
+    const float rf = post ? __ldg(a.rstd_f + t) : 1.f;
+    const float ro = pre ? __ldg(a.rstd_out + t) : 0.f;
+    const auto unit = [&](int i, float (&d)[U], float (&oh)[U], float (&v)[U], float (&fh)[U],
+                          float (&cf)[U]) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) d[j] = oh[j] = v[j] = fh[j] = cf[j] = 0.f;
+      if (a.dout.p != nullptr) loop_get<R, U>(a.dout.row(t) + i, d);
+      if (pre) {
+        loop_get<R, U>(a.out.row(t) + i, oh);
+        loop_get<T, U>(a.dn.row(t) + i, v);
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          oh[j] *= ro;
+          v[j] *= param<T>(a.w_pre, a.p32, i + j);
+        }
+      }
+      if (has_f) {
+        loop_get<T, U>(a.f.row(t) + i, fh);
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          fh[j] *= rf;
+          cf[j] = a.scale;
+          if (post) cf[j] *= param<T>(a.w_post, a.p32, i + j);
+          if (a.gate_c != nullptr) cf[j] *= param<T>(a.gate_c, a.p32, i + j);
+        }
+      }
+    };
+    float s1 = 0.f, s2 = 0.f, s3 = 0.f;
+    for (int i = threadIdx.x * U; i < a.H; i += LOOP_THREADS * U) {
+      float d[U], oh[U], v[U], fh[U], cf[U];
+      unit(i, d, oh, v, fh, cf);
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const float cfh = cf[j] * fh[j];
+        s1 = fmaf(oh[j], v[j], s1);
+        s2 = fmaf(cfh, fmaf(ro, v[j], d[j]), s2);
+        s3 = fmaf(cfh, oh[j], s3);
+      }
+    }
+    const float m1 = block_sum(s1, s) * inv;
+    s2 = block_sum(s2, s);
+    s3 = block_sum(s3, s);
+    const float cfd = s2 - ro * m1 * s3;
+    if (threadIdx.x == 0) {
+      if (a.mean_ov != nullptr) a.mean_ov[t] = m1;
+      if (a.dgate_t != nullptr) {
+        if (a.p32)
+          static_cast<float*>(a.dgate_t)[t] = cfd;
+        else
+          static_cast<T*>(a.dgate_t)[t] = from_f32<T>(cfd);
+      }
+    }
+    const float m2 = post ? gt * cfd * inv : 0.f;
+    for (int i = threadIdx.x * U; i < a.H; i += LOOP_THREADS * U) {
+      float d[U], oh[U], v[U], fh[U], cf[U];
+      unit(i, d, oh, v, fh, cf);
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        d[j] = fmaf(ro, fmaf(-m1, oh[j], v[j]), d[j]);
+        fh[j] = rf * fmaf(-m2, fh[j], cf[j] * (gt * d[j]));
+      }
+      put_unit<R, U>(a.dx.row(t) + i, d);
+      if (has_f) put_unit<T, U>(a.df.row(t) + i, fh);
+    }
+  }
+}
+
+// Column sums of one range of rows per blockIdx.y: a thread owns a column.
+template <typename T, typename R>
+__global__ void __launch_bounds__(256) resnorm_cols_loop_kernel(const BwdOps<T, R> a, int rows) {
+  pdl_wait();
+  pdl_trigger();
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.H) return;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * rows;
+  const int64_t t1 = min(static_cast<int64_t>(a.T_), t0 + rows);
+  const bool pre = a.dn.p != nullptr, post = a.w_post != nullptr;
+  const float w = pre ? param<T>(a.w_pre, a.p32, i) : 0.f;
+  float K = 0.f, dw = 0.f;
+#pragma unroll 2
+  for (int64_t t = t0; t < t1; ++t) {
+    float d = a.dout.p != nullptr ? to_f32(a.dout.row(t)[i]) : 0.f;
+    if (pre) {
+      const float ro = __ldg(a.rstd_out + t), oh = to_f32(a.out.row(t)[i]) * ro;
+      const float dn = to_f32(a.dn.row(t)[i]);
+      dw = fmaf(dn, oh, dw);
+      d = fmaf(ro, fmaf(-__ldcg(a.mean_ov + t), oh, w * dn), d);
+    }
+    if (a.sums_f) {
+      const float gt = a.gate_t != nullptr ? param<T>(a.gate_t, a.p32, t) : 1.f;
+      const float fh = to_f32(a.f.row(t)[i]) * (post ? __ldg(a.rstd_f + t) : 1.f);
+      K = fmaf(fh, gt * d, K);
+    }
+  }
+  float* const p = a.part + static_cast<int64_t>(blockIdx.y) * 2 * a.H + i;
+  p[0] = K;
+  p[a.H] = dw;
+}
+
+// The parameters' gradients from n partial rows: 16 warps take every 16th row of 32 columns
+// and are added in order; blockIdx.y 0: K's (dw_post, dgate_c), 1: dw_pre.
+template <typename P>
+__global__ void __launch_bounds__(512) resnorm_finish_kernel(
+    const float* __restrict__ part, int n, int H, const P* __restrict__ w_post,
+    const P* __restrict__ gate_c, float scale, P* __restrict__ dw_post, P* __restrict__ dgate_c,
+    P* __restrict__ dw_pre) {
+  constexpr int W = 16, B = 10;
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.y == 0 ? dw_post == nullptr && dgate_c == nullptr : dw_pre == nullptr) return;
+  __shared__ float s[W][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int i = blockIdx.x * 32 + lane;
+  float a = 0.f;
+  if (i < H) {
+    const float* p = part + static_cast<int64_t>(2 * w + blockIdx.y) * H + i;
+    for (int j = w; j < n; j += W * B) {
+      float v[B];
+#pragma unroll
+      for (int b = 0; b < B; ++b, p += 2 * W * H) v[b] = j + b * W < n ? __ldcg(p) : 0.f;
+#pragma unroll
+      for (int b = 0; b < B; ++b) a += v[b];
+    }
+  }
+  s[w][lane] = a;
+  __syncthreads();
+  if (w != 0 || i >= H) return;
+  float t = 0.f;
+#pragma unroll
+  for (int j = 0; j < W; ++j) t += s[j][lane];
+  if (blockIdx.y == 1) {
+    dw_pre[i] = from_f32<P>(t);
+    return;
+  }
+  t *= scale;
+  if (dw_post != nullptr) dw_post[i] = from_f32<P>(gate_c != nullptr ? t * to_f32(gate_c[i]) : t);
+  if (dgate_c != nullptr) dgate_c[i] = from_f32<P>(w_post != nullptr ? t * to_f32(w_post[i]) : t);
+}
+
+template <typename T, typename R, int NU, int U>
+static cudaError_t bwd_launch(const Ctx& c, BwdOps<T, R> a, int* parts) {
+  a.GT = rn_group_threads<NU, U>(a.H);
+  const NormGrid g = rn_grid(a.GT, a.T_, c.num_sms);
+  const int nt = g.GT * g.groups;
+  size_t smem = U == 8 ? static_cast<size_t>(rn_bwd_steps<T, R, NU>) * nt * 2 *
+                             (Operand<T, NU, U>::BYTES + Operand<R, NU, U>::BYTES)
+                       : 0;
+  if (g.groups > 1) smem = std::max(smem, sizeof(float) * 2 * g.groups * a.H);
+  auto* kern = resnorm_bwd_kernel<T, R, NU, U>;
+  const cudaError_t e = allow_smem(kern, smem);
+  if (e != cudaSuccess) return e;
+  *parts = g.ctas;
+  return launch_k(c.stream, kern, dim3(g.ctas), dim3(nt), smem, a);
+}
+
+}  // namespace mmmoe
+
+using namespace mmmoe;
+
+extern "C" MM_MOE_API mm_moe_status mm_moe_resnorm_backward(
+    const mm_moe_resnorm* shape, const void* dout, int64_t lddout, const void* dn, int64_t lddn,
+    const void* out, int64_t ldout, const void* f, int64_t ldf, const void* post_weight,
+    const void* gate, const void* pre_weight, const float* rstd_f, const float* rstd_out, void* dx,
+    int64_t lddx, void* df, int64_t lddf, void* dpost_weight, void* dgate, void* dpre_weight,
+    void* workspace, void* stream) {
+  if (!resnorm_shape_ok(shape)) return MM_MOE_EINVAL;
+  const size_t b = dtype_bytes(shape->dtype), rb = dtype_bytes(shape->res_dtype),
+               pb = dtype_bytes(shape->param_dtype);
+  const bool pre = shape->pre != 0, has_f = f != nullptr, post = shape->post != 0 && has_f;
+  const int gk = has_f ? shape->gate : MM_MOE_GATE_NONE;
+  const RowSpan in[4] = {{dout, lddout, rb}, {pre ? dn : nullptr, lddn, b},
+                         {pre ? out : nullptr, ldout, rb}, {f, ldf, b}};
+  const RowSpan res[2] = {{dx, lddx, rb}, {has_f ? df : nullptr, lddf, b}};
+  if ((dout == nullptr && !pre) || (!has_f && !pre) || (dout != nullptr && !span_ok(in[0], shape)) ||
+      (pre && (!span_ok(in[1], shape) || !span_ok(in[2], shape) || !vec_ok(pre_weight, pb) ||
+               !vec_ok(rstd_out, 4) || !vec_ok(dpre_weight, pb))) ||
+      (has_f && (!span_ok(in[3], shape) || !span_ok(res[1], shape))) ||
+      (post && (!vec_ok(post_weight, pb) || !vec_ok(rstd_f, 4) || !vec_ok(dpost_weight, pb))) ||
+      (gk != MM_MOE_GATE_NONE && (!vec_ok(gate, pb) || !vec_ok(dgate, pb))) ||
+      !span_ok(res[0], shape) || !vec_ok(workspace, 16))
+    return MM_MOE_EINVAL;
+  for (const RowSpan& r : res)
+    for (const RowSpan& i : in)
+      if (spans_meet(r, i, shape)) return MM_MOE_EINVAL;
+  if (spans_meet(res[0], res[1], shape)) return MM_MOE_EINVAL;
+  const int sms = std::min(152, sm_count_103());
+  if (sms == 0) return MM_MOE_ENOTSUP;
+  int launches = 0;
+  const Ctx c{static_cast<cudaStream_t>(stream), sms, &launches};
+  const int T_ = static_cast<int>(shape->T), H = static_cast<int>(shape->H);
+  bool even = H % 8 == 0;
+  for (const RowSpan& r : {in[0], in[1], in[2], in[3], res[0], res[1]})
+    even = even && span_even(r, shape);
+  float* const part = static_cast<float*>(workspace);
+  float* const mean_ov = part + static_cast<int64_t>(norm_parts(shape->T)) * 2 * H;
+  const bool sums_f = post || gk == MM_MOE_GATE_CHANNEL;
+  int parts = 0;
+  cudaError_t e = with_types(shape, [&](auto* t, auto* r) -> cudaError_t {
+    using T = std::remove_pointer_t<decltype(t)>;
+    using R = std::remove_pointer_t<decltype(r)>;
+    const BwdOps<T, R> a{{static_cast<const R*>(dout), lddout},
+                         {static_cast<const T*>(pre ? dn : nullptr), lddn},
+                         {static_cast<const R*>(out), ldout},
+                         {static_cast<const T*>(f), ldf},
+                         {static_cast<R*>(dx), lddx},
+                         {static_cast<T*>(df), lddf},
+                         post ? post_weight : nullptr,
+                         gk == MM_MOE_GATE_CHANNEL ? gate : nullptr,
+                         gk == MM_MOE_GATE_TOKEN ? gate : nullptr,
+                         pre_weight,
+                         shape->param_dtype == MM_MOE_DT_F32,
+                         sums_f,
+                         shape->scale,
+                         rstd_f,
+                         rstd_out,
+                         gk == MM_MOE_GATE_TOKEN ? dgate : nullptr,
+                         part,
+                         mean_ov,
+                         T_,
+                         H,
+                         0};
+    cudaError_t err;
+    prof_begin(c, K_RESNORM_BWD);
+    if (even && H <= 16 * RN_THREADS) {
+      const int g1 = rn_group_threads<1, 8>(H);
+      if (g1 != 0 && T_ <= c.num_sms * std::max(1, RN_THREADS / g1))
+        err = bwd_launch<T, R, 1, 8>(c, a, &parts);
+      else
+        err = bwd_launch<T, R, 2, 8>(c, a, &parts);
+      prof_end(c, K_RESNORM_BWD);
+      return err;
+    }
+    if (!even && H <= 8 * RN_THREADS) {
+      err = bwd_launch<T, R, 8, 1>(c, a, &parts);
+      prof_end(c, K_RESNORM_BWD);
+      return err;
+    }
+    err = launch_k(c.stream,
+                   even ? resnorm_dx_loop_kernel<T, R, 8> : resnorm_dx_loop_kernel<T, R, 1>,
+                   dim3(std::min(T_, c.num_sms * 4)), dim3(LOOP_THREADS), 0, a);
+    prof_end(c, K_RESNORM_BWD);
+    if (err != cudaSuccess || (!sums_f && !pre)) return err;
+    const int cols = (H + 255) / 256;
+    const int want = std::min(norm_parts(T_), std::max(1, c.num_sms * 8 / cols));
+    const int rows = div_up(T_, want);
+    parts = div_up(T_, rows);
+    prof_begin(c, K_RESNORM_BWD);
+    err = launch_k(c.stream, resnorm_cols_loop_kernel<T, R>, dim3(cols, parts), dim3(256), 0, a,
+                   rows);
+    prof_end(c, K_RESNORM_BWD);
+    return err;
+  });
+  if (e != cudaSuccess || (!sums_f && !pre)) return op_status(e);
+  prof_begin(c, K_RESNORM_FINISH);
+  e = with_dtype(shape->param_dtype, [&](auto* p) {
+    using P = std::remove_pointer_t<decltype(p)>;
+    return launch_k(c.stream, resnorm_finish_kernel<P>, dim3((H + 31) / 32, pre ? 2 : 1), dim3(512),
+                    0, static_cast<const float*>(part), parts, H,
+                    static_cast<const P*>(post ? post_weight : nullptr),
+                    static_cast<const P*>(gk == MM_MOE_GATE_CHANNEL ? gate : nullptr), shape->scale,
+                    static_cast<P*>(post ? dpost_weight : nullptr),
+                    static_cast<P*>(gk == MM_MOE_GATE_CHANNEL ? dgate : nullptr),
+                    static_cast<P*>(pre ? dpre_weight : nullptr));
+  });
+  prof_end(c, K_RESNORM_FINISH);
+  return op_status(e);
+}
