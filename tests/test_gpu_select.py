@@ -297,6 +297,73 @@ def test_gradient_against_differences(score, renorm):
             assert abs((loss(l + h) - loss(l - h)) / 2e-6 - d[t, e]) < 1e-8
 
 
+@pytest.mark.parametrize("T,E,k,groups,keep,gsc,score,dtype,renorm,with_bias", [
+    (20011, 256, 8, 8, 4, "top2", "sigmoid", "fp32", True, True),
+    (20011, 256, 8, 1, 1, "max", "softmax", "fp32", True, False),
+    (20000, 256, 8, 1, 1, "max", "softmax", "bf16", False, True),
+    (10001, 250, 6, 5, 2, "top2", "softmax", "fp32", True, True),
+    (19999, 128, 8, 1, 1, "max", "softmax", "fp32", True, False),
+    (12345, 128, 8, 8, 2, "max", "sigmoid", "fp16", True, True),
+    (12345, 100, 7, 4, 3, "top2", "sigmoid", "fp32", False, False),
+    (20000, 64, 4, 8, 4, "top2", "sigmoid", "fp32", True, True),
+    (11111, 60, 6, 1, 1, "max", "sigmoid", "fp32", True, True),
+    (30000, 32, 4, 4, 2, "max", "softmax", "bf16", True, False),
+    (30001, 16, 4, 1, 1, "max", "softmax", "fp32", False, True),
+    (40000, 8, 2, 1, 1, "max", "softmax", "fp32", True, False),
+    (40001, 7, 7, 1, 1, "max", "sigmoid", "fp32", True, True),
+    (40000, 12, 3, 4, 2, "top2", "sigmoid", "fp32", True, True),
+    (10007, 256, 12, 16, 8, "top2", "sigmoid", "fp32", True, True),
+    (10007, 128, 16, 1, 1, "max", "softmax", "fp32", True, True),
+    (6000, 512, 8, 8, 3, "top2", "sigmoid", "fp32", True, True),
+    (6001, 500, 10, 1, 1, "max", "softmax", "bf16", True, False),
+    (5000, 1024, 8, 16, 4, "top2", "sigmoid", "fp32", True, True),
+    (10007, 256, 8, 8, 3, "max", "sigmoid", "fp32", True, True)])
+def test_many_tokens(T, E, k, groups, keep, gsc, score, dtype, renorm, with_bias):
+    """As test_forward where the tokens fill the SMs, with fewer lanes a token."""
+    opt = options(score, groups, keep, gsc, renorm, 1.5)
+    h = MoESelect(T, E, k, dtype=dtype, **opt)
+    l = logits_of(T, E, dtype, 1)
+    l[5] = -float("inf")
+    l[6, ::2] = -float("inf")
+    l[7] = 0.25                                     # all alike
+    l[8, : E // 2] = 1.0
+    l[9, 3:] = float("nan")
+    bias = bias_of(E, score) if with_bias else None
+    if not with_bias and dtype == "fp32" and gsc != "top2":   # neighbouring values
+        v = np.float32(0.7).view(np.int32) + np.random.default_rng(0).integers(0, 9, (50, E))
+        l[100:150] = torch.from_numpy(v.astype(np.int32).view(np.float32)).cuda()
+    idx, w = h.forward(l, bias)
+    i, w = idx.cpu().numpy(), f64(w)
+    assert ((i >= 0) & (i < E)).all() and len(set(i[9])) == k
+    L, b = f64(l), None if bias is None else f64(bias)
+    ok = [t for t in range(T) if t not in (9,)]
+    ri, rw = os_.forward(L[ok], b, k, **opt)
+    tied = groups > keep and gsc == "top2"          # (rows 5 to 8: sums that tie, see check_groups)
+    keep_rows = np.array([not (tied and t in (5, 6, 7, 8)) for t in ok])
+    bad = np.argwhere((i[ok] != ri).any(1) & keep_rows)[:, 0]
+    assert len(bad) == 0, (len(bad), ok[bad[0]], i[ok][bad[0]], ri[bad[0]])
+    off = (np.abs(w[ok] - rw) > wtol(E, k) * np.abs(rw) + 1e-37) & keep_rows[:, None]
+    assert not off.any(), np.argwhere(off)[:5]
+
+
+def test_near_keys_of_many_tokens():
+    """Biases that bring score + bias together to 1e-8 and less, in one row in ten."""
+    T, E, k = 20000, 256, 8
+    r = np.random.default_rng(3)
+    l = r.standard_normal((T, E)).astype(np.float32)
+    s = os_.scores(l[0].astype(np.float64), "sigmoid")
+    bias = (0.7 - s + np.where(np.arange(E) % 3 == 0, 1e-8, 1e-3) * r.permutation(E)).astype(np.float32)
+    l[::10] = l[0]
+    for groups, keep in ((1, 1), (8, 4)):
+        opt = options("sigmoid", groups, keep, "top2", True, 1.0)
+        h = MoESelect(T, E, k, **opt)
+        idx = h.forward(torch.from_numpy(l).cuda(), torch.from_numpy(bias).cuda())[0].cpu().numpy()
+        rows = np.concatenate([[0], np.arange(1, 2000)])
+        ri, _ = os_.forward(l[rows], bias.astype(np.float64), k, **opt)
+        assert np.array_equal(idx[rows], ri)
+        assert (idx[::10] == idx[0]).all()
+
+
 def test_rows_on_no_vector_boundary():
     """Logits and gradients whose storage begins between two vectors."""
     T, E, k = 33, 128, 8
