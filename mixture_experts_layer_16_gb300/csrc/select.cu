@@ -45,85 +45,117 @@ __device__ __forceinline__ void load_u(const T* p, float (&f)[U]) {
   }
 }
 
-// The logit gradient's row: `rest` at every expert (0, or the dense softmax's -s_e A) and the chosen
-// experts' own values over it, the auxiliary gradient added to both.  U: elements of 16 bytes of the
-// gradient (1: rows on no 16-byte boundary).
-template <typename T, typename O, int U, bool DENSE>
+// W lanes take a token (k of them its chosen experts), in units of U elements, 32 elements a lane at
+// most.  The logit gradient's row is first filled: with zeros or the auxiliary gradient, or with the
+// dense softmax's -scale s_e A beside it (the row then stays in registers between its three uses);
+// the chosen experts' own values go over it.  U: elements of 16 bytes of the gradient (1: rows on no
+// 16-byte boundary).
+template <typename T, typename O, int U, int W, bool DENSE>
 __global__ void __launch_bounds__(SEL_THREADS) select_bwd_kernel(
     const T* __restrict__ logits, const int32_t* __restrict__ topk_idx,
     const float* __restrict__ dtopk_w, const float* __restrict__ aux, const SelArgs a,
     O* __restrict__ dlogits) {
+  constexpr int NU = 32 / U;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (SEL_THREADS / 32) + (threadIdx.x >> 5);
-  if (t >= a.T) return;
-  const T* const row = logits + t * a.E;
-  O* const out = dlogits + t * a.E;
-  const float* const ax = aux != nullptr ? aux + t * a.E : nullptr;
-  const int e = lane < a.k ? __ldg(topk_idx + t * a.k + lane) : -1;
-  const float g = lane < a.k ? __ldg(dtopk_w + t * a.k + lane) : 0.f;
-  const bool mine = e >= 0 && e < a.E;  // (an index outside is dropped)
-  const float l = mine ? to_f32(row[e]) : -INFINITY;
-  float d;  // of the lane's chosen logit
-  [[maybe_unused]] float m = -INFINITY, rz = 0.f, A = 0.f;
-  if constexpr (DENSE) {
-    for (int i = lane * U; i < a.E; i += 32 * U) {
-      float f[U];
-      load_u<U>(row + i, f);
-#pragma unroll
-      for (int j = 0; j < U; ++j) m = fmaxf(m, f[j]);
-    }
-    m = max_of<32>(m);
-    float z = 0.f;
-    for (int i = lane * U; i < a.E; i += 32 * U) {
-      float f[U];
-      load_u<U>(row + i, f);
-#pragma unroll
-      for (int j = 0; j < U; ++j) z += expf(f[j] - m);
-    }
-    rz = m == -INFINITY ? 0.f : 1.f / warp_sum(z);
-    const float s = mine && m != -INFINITY ? expf(l - m) * rz : 0.f;
-    A = warp_sum(mine ? g * s : 0.f);
-    d = s * g;  // (beside -s A, which every expert has)
-  } else if (a.sigmoid) {
-    const float s = mine ? sigmoid32(l) : 0.f;
-    float ds = g;
-    if (a.renorm) {
-      const float n = warp_sum(s) + SUM_EPS;
-      ds = (g - warp_sum(mine ? g * s : 0.f) / n) / n;
-    }
-    d = mine ? a.scale * ds * s * sigmoid32(-l) : 0.f;
-  } else {
-    const float big = max_of<32>(l);
-    const float ex = mine && big != -INFINITY ? expf(l - big) : 0.f;
-    const float sum = warp_sum(ex);
-    const float q = sum == 0.f ? 0.f : ex / sum;
-    d = a.scale * q * (g - warp_sum(mine ? g * q : 0.f));
-  }
-  for (int i = lane * U; i < a.E; i += 32 * U) {
-    float f[U] = {}, x[U] = {};
-    if constexpr (DENSE) load_u<U>(row + i, f);
-    if (ax != nullptr) load_u<U>(ax + i, x);
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      if constexpr (DENSE) f[j] = m == -INFINITY ? 0.f : -a.scale * A * (expf(f[j] - m) * rz);
-      f[j] += x[j];
-    }
+  const int lane = threadIdx.x & (W - 1), sub = (threadIdx.x & 31) / W;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (SEL_THREADS / W) + threadIdx.x / W;
+  const bool live = t < a.T;  // (a warp's tokens go through it together)
+  const int64_t first = live ? t * a.E : 0;
+  const T* const row = logits + first;
+  O* const out = dlogits + first;
+  const float* const ax = aux != nullptr ? aux + first : nullptr;
+  const bool slot = live && lane < a.k;
+  const int e = slot ? __ldg(topk_idx + t * a.k + lane) : -1;
+  const float g = slot ? __ldg(dtopk_w + t * a.k + lane) : 0.f;
+  const auto put = [&](int i, const float (&f)[U]) {
     if constexpr (U == 1)
       out[i] = from_f32<O>(f[0]);
     else
       *reinterpret_cast<uint4*>(out + i) = pack(f, out);
+  };
+  if constexpr (!DENSE) {
+    if (live)
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        const int i = (u * W + lane) * U;
+        if (i >= a.E) break;
+        float f[U] = {};
+        if (ax != nullptr) load_u<U>(ax + i, f);
+        put(i, f);
+      }
+  }
+  const bool mine = e >= 0 && e < a.E;  // (an index outside is dropped)
+  const float l = mine ? to_f32(__ldg(row + e)) : -INFINITY;
+  float d;  // of the lane's chosen logit
+  [[maybe_unused]] float m = -INFINITY, rz = 0.f, A = 0.f;
+  if constexpr (DENSE) {
+    float v[NU][U];
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const int i = (u * W + lane) * U;
+      if (i < a.E) {
+        load_u<U>(row + i, v[u]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < U; ++j) v[u][j] = -INFINITY;
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j) m = fmaxf(m, v[u][j]);
+    }
+    m = max_of<W>(m);
+    float z = 0.f;
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        v[u][j] = m == -INFINITY ? 0.f : expf(v[u][j] - m);
+        z += v[u][j];
+      }
+    z = sum_of<W>(z);
+    rz = m == -INFINITY ? 0.f : 1.f / z;
+    const float s = mine && m != -INFINITY ? expf(l - m) * rz : 0.f;
+    A = sum_of<W>(mine ? g * s : 0.f);
+    d = s * g;  // (beside -s A, which every expert has)
+    const float c = -a.scale * A * rz;
+    if (live)
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        const int i = (u * W + lane) * U;
+        if (i >= a.E) break;
+        float f[U] = {};
+        if (ax != nullptr) load_u<U>(ax + i, f);
+#pragma unroll
+        for (int j = 0; j < U; ++j) f[j] = fmaf(c, v[u][j], f[j]);
+        put(i, f);
+      }
+  } else if (a.sigmoid) {
+    const float s = mine ? sigmoid32(l) : 0.f;
+    float ds = g;
+    if (a.renorm) {
+      const float n = sum_of<W>(s) + SUM_EPS;
+      ds = (g - sum_of<W>(mine ? g * s : 0.f) / n) / n;
+    }
+    d = mine ? a.scale * ds * s * sigmoid32(-l) : 0.f;
+  } else {
+    const float big = max_of<W>(l);
+    const float ex = mine && big != -INFINITY ? expf(l - big) : 0.f;
+    const float sum = sum_of<W>(ex);
+    const float q = sum == 0.f ? 0.f : ex / sum;
+    d = a.scale * q * (g - sum_of<W>(mine ? g * q : 0.f));
   }
   // the chosen experts' values, an expert that is there twice by its first lane
-  const uint32_t same = __match_any_sync(FULL, mine ? e : -1 - lane);
-  float sum = 0.f;
-  for (int j = 0; j < a.k; ++j) {
-    const float v = __shfl_sync(FULL, d, j);
-    if (same >> j & 1u) sum += v;
+  const uint32_t same = __match_any_sync(FULL, mine ? sub << 16 | e : -1 - static_cast<int>(threadIdx.x & 31));
+  float sum = d;
+  if (__any_sync(FULL, mine && (same & (same - 1)) != 0)) {
+    sum = 0.f;
+    for (int j = 0; j < W; ++j) {
+      const float v = __shfl_sync(FULL, d, sub * W + j);
+      if (same >> (sub * W + j) & 1u) sum += v;
+    }
   }
   __syncwarp();
-  if (mine && __ffs(same) - 1 == lane) {
+  if (mine && __ffs(same) - 1 == sub * W + lane) {
     float f = sum;
     if constexpr (DENSE) {
       const float s = m == -INFINITY ? 0.f : expf(l - m) * rz;
@@ -168,11 +200,6 @@ static SelArgs make_args(const mm_moe_select* s) {
   return a;
 }
 
-static unsigned blocks_of(int T) {
-  return static_cast<unsigned>((static_cast<int64_t>(T) + SEL_THREADS / 32 - 1) /
-                               (SEL_THREADS / 32));
-}
-
 cudaError_t launch_select_fwd(const Ctx& c, const mm_moe_select* s, const void* logits,
                               const float* bias, int32_t* idx, float* w) {
   const SelArgs a = make_args(s);
@@ -185,17 +212,30 @@ cudaError_t launch_select_fwd(const Ctx& c, const mm_moe_select* s, const void* 
   return e;
 }
 
-template <typename T, typename O>
+template <typename T, typename O, int U, int W>
 static cudaError_t launch_bwd(const Ctx& c, const SelArgs& a, const void* logits,
                               const int32_t* idx, const float* dw, const float* aux, void* out) {
+  constexpr int TOKENS = SEL_THREADS / W;
+  auto* kern = !a.sigmoid && !a.renorm ? select_bwd_kernel<T, O, U, W, true>
+                                       : select_bwd_kernel<T, O, U, W, false>;
+  return launch_k(c.stream, kern,
+                  dim3(static_cast<unsigned>((static_cast<int64_t>(a.T) + TOKENS - 1) / TOKENS)),
+                  dim3(SEL_THREADS), 0, static_cast<const T*>(logits), idx, dw, aux, a,
+                  static_cast<O*>(out));
+}
+
+// As few lanes a token as its chosen experts and its row leave.
+template <typename T, typename O>
+static cudaError_t launch_bwd_of(const Ctx& c, const SelArgs& a, const void* logits,
+                                 const int32_t* idx, const float* dw, const float* aux, void* out) {
   constexpr int U = VN<O>;
-  const bool dense = !a.sigmoid && !a.renorm;
   const bool vec = a.E % U == 0 && a.E * sizeof(T) % 16 == 0 && al(logits, 16) && al(out, 16) &&
                    (aux == nullptr || al(aux, 16));
-  auto* kern = vec ? (dense ? select_bwd_kernel<T, O, U, true> : select_bwd_kernel<T, O, U, false>)
-                   : (dense ? select_bwd_kernel<T, O, 1, true> : select_bwd_kernel<T, O, 1, false>);
-  return launch_k(c.stream, kern, dim3(blocks_of(a.T)), dim3(SEL_THREADS), 0,
-                  static_cast<const T*>(logits), idx, dw, aux, a, static_cast<O*>(out));
+  if (!vec) return launch_bwd<T, O, 1, 32>(c, a, logits, idx, dw, aux, out);
+  const int lanes = std::max(a.k, (a.E + 31) / 32);
+  if (lanes <= 8) return launch_bwd<T, O, U, 8>(c, a, logits, idx, dw, aux, out);
+  if (lanes <= 16) return launch_bwd<T, O, U, 16>(c, a, logits, idx, dw, aux, out);
+  return launch_bwd<T, O, U, 32>(c, a, logits, idx, dw, aux, out);
 }
 
 cudaError_t launch_select_bwd(const Ctx& c, const mm_moe_select* s, const void* logits,
@@ -204,8 +244,8 @@ cudaError_t launch_select_bwd(const Ctx& c, const mm_moe_select* s, const void* 
   prof_begin(c, K_SELECT_BWD);
   const cudaError_t e = with_dtype(s->dtype, [&](auto* tag) {
     using T = std::remove_pointer_t<decltype(tag)>;
-    if (s->grad_dtype == s->dtype) return launch_bwd<T, T>(c, a, logits, idx, dw, aux, out);
-    return launch_bwd<T, __nv_bfloat16>(c, a, logits, idx, dw, aux, out);
+    if (s->grad_dtype == s->dtype) return launch_bwd_of<T, T>(c, a, logits, idx, dw, aux, out);
+    return launch_bwd_of<T, __nv_bfloat16>(c, a, logits, idx, dw, aux, out);
   });
   prof_end(c, K_SELECT_BWD);
   return e;
