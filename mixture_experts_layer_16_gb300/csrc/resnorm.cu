@@ -10,6 +10,9 @@
 #include "resnorm.cuh"
 
 namespace mmmoe {
+#ifndef RN_PF
+#define RN_PF 2
+#endif
 
 template <typename T, typename R>
 struct FwdOps {
@@ -26,7 +29,7 @@ struct FwdOps {
 
 template <typename T, typename R, int NU>
 constexpr int rn_fwd_steps =
-    std::max(1, std::min(4, RN_RING / (RN_THREADS * (Operand<T, NU, 8>::BYTES + Operand<R, NU, 8>::BYTES))));
+    std::max(1, std::min(4, RN_SMEM / (RN_THREADS * (Operand<T, NU, 8>::BYTES + Operand<R, NU, 8>::BYTES))));
 
 template <typename T, typename R, int NU, int U>
 __global__ void __launch_bounds__(RN_THREADS, 1) resnorm_fwd_kernel(const FwdOps<T, R> a) {
@@ -53,74 +56,92 @@ __global__ void __launch_bounds__(RN_THREADS, 1) resnorm_fwd_kernel(const FwdOps
       if (a.f.p != nullptr) of.issue(c, a.f.row(ta), at, piece);
       ox.issue(c, a.x.row(ta), at + x_at, piece);
     }
+    if constexpr (U == 8) {
+      if (RN_PF > 0 && c.j == 0) {
+        const int64_t tp = ta + static_cast<int64_t>(RN_PF) * step;
+        if (tp < n) {
+          if (a.f.p != nullptr) prefetch_row(a.f.row(tp), a.H);
+          prefetch_row(a.x.row(tp), a.H);
+        }
+      }
+    }
     ta += step;
     if constexpr (U == 8) async_commit();
   };
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue(ring + i * step_bytes);
-  float cf[NU * U], w[NU * U];
+  constexpr int P = Cols<NU, U>::P, PIECES = Cols<NU, U>::PIECES;
+  f2 cf[NU * U / 2], w[NU * U / 2];
   if (a.f.p != nullptr) load_coef<T, NU, U>(c, a.w_post, a.gate_c, a.p32, a.scale, cf);
   if (a.n.p != nullptr) load_params<T, NU, U>(c, a.w_pre, a.p32, w);
+  float gt_n = 1.f;  // the next row's gate, a row ahead
+  const auto gate = [&](uint32_t q) {
+    if (q < n && a.gate_t != nullptr) gt_n = param<T>(a.gate_t, a.p32, q);
+  };
+  gate(t);
   int buf = 0;
   uint32_t st = ring, st_in = ring + (S - 1) * step_bytes;
   const uint32_t ring_end = ring + S * step_bytes;
   for (; tw < n; t += step, tw += step) {
     issue(st_in);
     const bool live = t < n;
-    float gt = live && a.gate_t != nullptr ? param<T>(a.gate_t, a.p32, t) : 1.f;
+    float gt = gt_n;
+    gate(t + step);
     if constexpr (U == 8) async_wait<S - 1>();
-    float o[NU * U];
-    if (a.f.p != nullptr) {
-      if (a.w_post != nullptr) {
-        float ss[1] = {0.f};
-        if (live)
+    f2 o[NU * U / 2];
+    if (a.f.p != nullptr && a.w_post != nullptr) {
+      f2 s2 = 0;
+      if (live)
 #pragma unroll
-          for (int i = 0; i < NU; ++i)
-            if (c.has(i)) {
-              float f[U];
-              of.get(st, piece, i, f);
-#pragma unroll
-              for (int k = 0; k < U; ++k) ss[0] = fmaf(f[k], f[k], ss[0]);
-            }
-        group_sum<1>(ss, s_sum[buf], c.g, a.GT);
-        buf ^= 1;
-        const float rf = rsqrtf(fmaf(ss[0], inv, a.eps));
-        if (live && c.j == 0) a.rstd_f[t] = rf;
-        gt *= rf;
-      }
-    }
-    float ss[1] = {0.f};
-    if (live)
-#pragma unroll
-      for (int i = 0; i < NU; ++i)
-        if (c.has(i)) {
-          float x[U], f[U];
-          ox.get(st + x_at, piece, i, x);
-          if (a.f.p != nullptr) {
+        for (int i = 0; i < PIECES; ++i)
+          if (c.has_piece(i)) {
+            f2 f[P];
             of.get(st, piece, i, f);
 #pragma unroll
-            for (int k = 0; k < U; ++k) x[k] = fmaf(cf[i * U + k] * gt, f[k], x[k]);
-            put_unit<R, U>(a.out.row(t) + c.col(i), x);
+            for (int k = 0; k < P; ++k) s2 = f2_fma(f[k], f[k], s2);
+          }
+      float ss[1] = {f2_sum(s2)};
+      group_sum<1>(ss, s_sum[buf], c.g, a.GT);
+      buf ^= 1;
+      const float rf = rsqrtf(fmaf(ss[0], inv, a.eps));
+      if (live && c.j == 0) a.rstd_f[t] = rf;
+      gt *= rf;
+    }
+    f2 s2 = 0;
+    const f2 gt2 = f2_of(gt);
+    if (live)
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i)
+        if (c.has_piece(i)) {
+          f2 x[P];
+          ox.get(st + x_at, piece, i, x);
+          if (a.f.p != nullptr) {
+            f2 f[P];
+            of.get(st, piece, i, f);
+#pragma unroll
+            for (int k = 0; k < P; ++k) x[k] = f2_fma(f2_mul(cf[i * P + k], gt2), f[k], x[k]);
+            put_piece<R>(c, a.out.row(t), i, x);
           }
 #pragma unroll
-          for (int k = 0; k < U; ++k) {
-            o[i * U + k] = x[k];
-            ss[0] = fmaf(x[k], x[k], ss[0]);
+          for (int k = 0; k < P; ++k) {
+            o[i * P + k] = x[k];
+            s2 = f2_fma(x[k], x[k], s2);
           }
         }
     if (a.n.p != nullptr) {
+      float ss[1] = {f2_sum(s2)};
       group_sum<1>(ss, s_sum[buf], c.g, a.GT);
       buf ^= 1;
       const float ro = rsqrtf(fmaf(ss[0], inv, a.eps));
       if (live) {
         if (c.j == 0) a.rstd_out[t] = ro;
 #pragma unroll
-        for (int i = 0; i < NU; ++i)
-          if (c.has(i)) {
-            float y[U];
+        for (int i = 0; i < PIECES; ++i)
+          if (c.has_piece(i)) {
+            f2 y[P];
 #pragma unroll
-            for (int k = 0; k < U; ++k) y[k] = o[i * U + k] * ro * w[i * U + k];
-            put_unit<T, U>(a.n.row(t) + c.col(i), y);
+            for (int k = 0; k < P; ++k) y[k] = f2_mul(f2_mul(o[i * P + k], f2_of(ro)), w[i * P + k]);
+            put_piece<T>(c, a.n.row(t), i, y);
           }
       }
     }

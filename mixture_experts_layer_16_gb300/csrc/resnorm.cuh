@@ -10,7 +10,8 @@
 //   dw_pre = sum_t dn oh;  K = sum_t [gate_t] fh D gives dw_post = scale gate_c K and
 //   dgate_c = scale w_post K;  dgate_t = scale sum_h w_post fh D
 // <fh q> needs D, which needs <oh v>; so that a row's sums meet at one barrier, the backward sums
-//   s1 = sum oh v,  s2 = sum c fh (dout + ro v),  s3 = sum c fh oh,   sum c fh D = s2 - ro s1 s3 / H.
+//   s1 = sum out v,  s2 = sum c f x,  s3 = sum c f out   with x = dout + ro v, and has
+//   k = ro^3 s1 / H,  D = x - k out,  sum c fh D = rf (s2 - k s3).
 //
 // f, n and their gradients are of one type, x and out (the residual stream) of it or fp32,
 // the parameters and the gate of it or fp32.  Everything is computed in fp32 and rounded once where it
@@ -29,16 +30,17 @@
 namespace mmmoe {
 
 constexpr int RN_THREADS = 512;
-constexpr int RN_RING = 196608;  // bytes of the ring at most
+constexpr int RN_SMEM = 230400;  // bytes of the ring and the parameters at most (227 KB, less what is static)
 
 // A row is cut into units of U = 8 columns (16 bytes of 16-bit types, 32 of fp32), dealt out to
 // the threads of a group in turn, NU to each; rows on no 16-byte boundary, or of a width that is no
 // multiple of 8, into single columns (U = 1).  Units of 8 come through a ring in shared memory by
 // cp.async, S - 1 rows ahead; a thread reads only what it copied itself.  Single columns are
-// loaded into registers.
+// loaded into registers.  A thread's values are pairs for the packed fp32 arithmetic, in PIECES (its units,
+// or all its single columns) of P pairs.
 template <int NU, int U>
 struct Cols {
-  static constexpr int N = NU * U;
+  static constexpr int N = NU * U, PIECES = U == 8 ? NU : 1, P = N / PIECES / 2;
   int GT, g, j, groups, H;
   __device__ __forceinline__ void init(int GT_, int H_) {
     GT = GT_;
@@ -53,16 +55,30 @@ struct Cols {
   }
   __device__ __forceinline__ int col(int i) const { return (j + i * GT) * U; }
   __device__ __forceinline__ bool has(int i) const { return col(i) < H; }
+  __device__ __forceinline__ bool has_piece(int i) const { return U == 1 || has(i); }
 };
+
+// A whole row on its way to L2 (16-byte aligned, a multiple of 16 bytes), by one thread.
+template <typename V>
+__device__ __forceinline__ void prefetch_row(const V* row, int H) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row),
+               "r"(H * static_cast<int>(sizeof(V)))
+               : "memory");
+}
+
+__device__ __forceinline__ void sts16_f2(uint32_t a, f2 x, f2 y) {
+  asm volatile("st.shared.v2.u64 [%0], {%1, %2};" ::"r"(a), "l"(x), "l"(y) : "memory");
+}
+__device__ __forceinline__ f2 f2_of(float v) { return f2_make(v, v); }
 
 // One row operand of type V on its way to the thread's registers.
 template <typename V, int NU, int U>
 struct Operand {
+  using C = Cols<NU, U>;
   static constexpr int PARTS = U == 8 ? 8 / VN<V> : 0;  // 16-byte pieces of a unit
   static constexpr int BYTES = PARTS * 16 * NU;         // of a thread's share of a row in the ring
   float reg[U == 1 ? NU : 1];
-  __device__ __forceinline__ void issue(const Cols<NU, U>& c, const V* row, uint32_t at,
-                                        uint32_t piece) {
+  __device__ __forceinline__ void issue(const C& c, const V* row, uint32_t at, uint32_t piece) {
     if constexpr (U == 8) {
 #pragma unroll
       for (int i = 0; i < NU; ++i)
@@ -76,18 +92,19 @@ struct Operand {
       for (int i = 0; i < NU; ++i) reg[i] = c.has(i) ? to_f32(row[c.col(i)]) : 0.f;
     }
   }
-  // unit i's values (any where the thread has none)
-  __device__ __forceinline__ void get(uint32_t at, uint32_t piece, int i, float (&f)[U]) const {
+  // piece i's values (single columns: zero where there is none)
+  __device__ __forceinline__ void get(uint32_t at, uint32_t piece, int i, f2 (&f)[C::P]) const {
     if constexpr (U == 8) {
 #pragma unroll
       for (int h = 0; h < PARTS; ++h) {
-        float t[VN<V>];
-        unpack(lds16(at + (i * PARTS + h) * piece), t, static_cast<const V*>(nullptr));
+        f2 t[VN<V> / 2];
+        unpack2<V>(lds16(at + (i * PARTS + h) * piece), t);
 #pragma unroll
-        for (int k = 0; k < VN<V>; ++k) f[h * VN<V> + k] = t[k];
+        for (int k = 0; k < VN<V> / 2; ++k) f[h * (VN<V> / 2) + k] = t[k];
       }
     } else {
-      f[0] = reg[i];
+#pragma unroll
+      for (int k = 0; k < C::P; ++k) f[k] = f2_make(reg[2 * k], reg[2 * k + 1]);
     }
   }
 };
@@ -122,11 +139,35 @@ __device__ __forceinline__ void put_unit(V* p, const float (&f)[U]) {
     *p = from_f32<V>(f[0]);
   }
 }
+// A piece's values to their columns of a row.
+template <typename V, int NU, int U>
+__device__ __forceinline__ void put_piece(const Cols<NU, U>& c, V* row, int i,
+                                          const f2 (&f)[Cols<NU, U>::P]) {
+  if constexpr (U == 8) {
+    uint4* const o = reinterpret_cast<uint4*>(row + c.col(i));
+#pragma unroll
+    for (int h = 0; h < 8 / VN<V>; ++h) {
+      f2 t[VN<V> / 2];
+#pragma unroll
+      for (int k = 0; k < VN<V> / 2; ++k) t[k] = f[h * (VN<V> / 2) + k];
+      o[h] = pack2<V>(t);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < NU; k += 2) {
+      float lo, hi;
+      f2_split(f[k / 2], lo, hi);
+      if (c.has(k)) row[c.col(k)] = from_f32<V>(lo);
+      if (c.has(k + 1)) row[c.col(k + 1)] = from_f32<V>(hi);
+    }
+  }
+}
 
 // Parameters (of type T, or fp32) of the thread's columns; zero where it has none.
 template <typename T, int NU, int U>
 __device__ __forceinline__ void load_params(const Cols<NU, U>& c, const void* p, bool p32,
-                                            float (&v)[NU * U]) {
+                                            f2 (&out)[NU * U / 2]) {
+  float v[NU * U];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     float f[U] = {};
@@ -167,6 +208,8 @@ __device__ __forceinline__ void load_params(const Cols<NU, U>& c, const void* p,
 #pragma unroll
     for (int k = 0; k < U; ++k) v[i * U + k] = f[k];
   }
+#pragma unroll
+  for (int k = 0; k < NU * U / 2; ++k) out[k] = f2_make(v[2 * k], v[2 * k + 1]);
 }
 
 template <typename T>
@@ -178,20 +221,20 @@ __device__ __forceinline__ float param(const void* p, bool p32, int64_t i) {
 template <typename T, int NU, int U>
 __device__ __forceinline__ void load_coef(const Cols<NU, U>& c, const void* w_post,
                                           const void* gate_c, bool p32, float scale,
-                                          float (&v)[NU * U]) {
+                                          f2 (&v)[NU * U / 2]) {
   if (w_post != nullptr) {
     load_params<T, NU, U>(c, w_post, p32, v);
   } else {
 #pragma unroll
-    for (int k = 0; k < NU * U; ++k) v[k] = 1.f;
+    for (int k = 0; k < NU * U / 2; ++k) v[k] = f2_of(1.f);
   }
 #pragma unroll
-  for (int k = 0; k < NU * U; ++k) v[k] *= scale;
+  for (int k = 0; k < NU * U / 2; ++k) v[k] = f2_mul(v[k], f2_of(scale));
   if (gate_c != nullptr) {
-    float t[NU * U];
+    f2 t[NU * U / 2];
     load_params<T, NU, U>(c, gate_c, p32, t);
 #pragma unroll
-    for (int k = 0; k < NU * U; ++k) v[k] *= t[k];
+    for (int k = 0; k < NU * U / 2; ++k) v[k] = f2_mul(v[k], t[k]);
   }
 }
 

@@ -10,6 +10,9 @@
 #include "resnorm.cuh"
 
 namespace mmmoe {
+#ifndef RN_PF
+#define RN_PF 2
+#endif
 
 template <typename T, typename R>
 struct BwdOps {
@@ -29,18 +32,27 @@ struct BwdOps {
   int T_, H, GT;
 };
 
-template <typename T, typename R, int NU>
-constexpr int rn_bwd_steps = std::max(
-    1, std::min(4, RN_RING / (RN_THREADS * 2 * (Operand<T, NU, 8>::BYTES + Operand<R, NU, 8>::BYTES))));
-
+// Bytes of a thread's share of a row in the ring.
 template <typename T, typename R, int NU, int U>
+constexpr int rn_bwd_bytes = 2 * (Operand<T, NU, U>::BYTES + Operand<R, NU, U>::BYTES);
+// Steps of the ring: as many as fit beside so many bytes of parameters.
+template <typename T, typename R, int NU>
+constexpr int rn_bwd_steps(int params) {
+  return std::max(1, std::min(4, (RN_SMEM - params) / (RN_THREADS * rn_bwd_bytes<T, R, NU, 8>)));
+}
+
+// S: steps of the ring (units of 8).  WHOLE: dout, dn and f are all there.
+// Two units a thread leave no registers for c and w beside the column sums: they are read from
+// shared memory, in two planes of four columns' pairs a unit, so that a warp's lanes read 512 bytes in a
+// row (in registers, with 72 bytes of spills: 16384 x 2048 bf16 92 us).
+template <typename T, typename R, int NU, int U, int S, bool WHOLE>
 __global__ void __launch_bounds__(RN_THREADS, 1) resnorm_bwd_kernel(const BwdOps<T, R> a) {
-  constexpr int S = U == 8 ? rn_bwd_steps<T, R, NU> : 1;
+  constexpr bool SHARED = U == 8 && NU > 1;
   using OT = Operand<T, NU, U>;
   using OR = Operand<R, NU, U>;
   extern __shared__ __align__(16) unsigned char ring_bytes[];
   __shared__ float4 s_sum[2][RN_THREADS / 32];
-  const uint32_t nt = blockDim.x, piece = nt * 16, step_bytes = 2 * (OT::BYTES + OR::BYTES) * nt;
+  const uint32_t nt = blockDim.x, piece = nt * 16, step_bytes = rn_bwd_bytes<T, R, NU, U> * nt;
   const uint32_t ring =
       static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)) + threadIdx.x * 16;
   const uint32_t out_at = OR::BYTES * nt, dn_at = 2 * out_at, f_at = dn_at + OT::BYTES * nt;
@@ -51,7 +63,8 @@ __global__ void __launch_bounds__(RN_THREADS, 1) resnorm_bwd_kernel(const BwdOps
   const uint32_t n = a.T_, step = gridDim.x * c.groups;
   uint32_t t = blockIdx.x * c.groups + c.g, tw = c.first_of_warp(t), ta = t;
   const float inv = 1.f / static_cast<float>(a.H);
-  const bool pre = a.dn.p != nullptr, has_f = a.f.p != nullptr, has_d = a.dout.p != nullptr;
+  const bool pre = WHOLE || a.dn.p != nullptr, has_f = WHOLE || a.f.p != nullptr,
+             has_d = WHOLE || a.dout.p != nullptr;
   const bool post = a.w_post != nullptr;
   OR od, oo;
   OT on, of;
@@ -64,64 +77,119 @@ __global__ void __launch_bounds__(RN_THREADS, 1) resnorm_bwd_kernel(const BwdOps
       }
       if (has_f) of.issue(c, a.f.row(ta), at + f_at, piece);
     }
+    if constexpr (U == 8) {
+      if (RN_PF > 0 && c.j == 0) {
+        const int64_t tp = ta + static_cast<int64_t>(RN_PF) * step;
+        if (tp < n) {
+          if (has_d) prefetch_row(a.dout.row(tp), a.H);
+          if (pre) prefetch_row(a.out.row(tp), a.H), prefetch_row(a.dn.row(tp), a.H);
+          if (has_f) prefetch_row(a.f.row(tp), a.H);
+        }
+      }
+    }
     ta += step;
     if constexpr (U == 8) async_commit();
   };
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue(ring + i * step_bytes);
-  float cf[NU * U], w[NU * U], K[NU * U], dw[NU * U];
-  load_coef<T, NU, U>(c, a.w_post, a.gate_c, a.p32, a.scale, cf);
-  if (pre) load_params<T, NU, U>(c, a.w_pre, a.p32, w);
+  constexpr int P = Cols<NU, U>::P, PIECES = Cols<NU, U>::PIECES;
+  constexpr bool KEEP = U == 8 && NU == 1;  // x, out and f stay in registers between the two passes
+  f2 K[NU * U / 2], dw[NU * U / 2];
+  f2 cf1[SHARED ? 1 : NU * U / 2], w1[SHARED ? 1 : NU * U / 2];
+  const uint32_t planes = static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)) + S * step_bytes,
+                 plane = a.H / 8 * 16;
+  {
+    f2 cf[NU * U / 2], w[NU * U / 2];
+    load_coef<T, NU, U>(c, a.w_post, a.gate_c, a.p32, a.scale, cf);
 #pragma unroll
-  for (int k = 0; k < NU * U; ++k) K[k] = dw[k] = 0.f;
+    for (int k = 0; k < NU * U / 2; ++k) w[k] = K[k] = dw[k] = 0;
+    if (pre) load_params<T, NU, U>(c, a.w_pre, a.p32, w);
+    if constexpr (SHARED) {
+      if (c.g == 0)
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+          if (c.has(i)) {
+            const uint32_t at = planes + (c.j + i * a.GT) * 16;
+            sts16_f2(at, cf[4 * i], cf[4 * i + 1]);
+            sts16_f2(at + plane, cf[4 * i + 2], cf[4 * i + 3]);
+            sts16_f2(at + 2 * plane, w[4 * i], w[4 * i + 1]);
+            sts16_f2(at + 3 * plane, w[4 * i + 2], w[4 * i + 3]);
+          }
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int k = 0; k < NU * U / 2; ++k) cf1[k] = cf[k], w1[k] = w[k];
+    }
+  }
+  const auto params = [&](int i, f2 (&cf)[P], f2 (&w)[P]) {
+    if constexpr (SHARED) {
+      const uint32_t at = planes + (c.j + i * a.GT) * 16;
+      const ulonglong2 q = lds16_f2(at), r = lds16_f2(at + plane), u = lds16_f2(at + 2 * plane),
+                       v = lds16_f2(at + 3 * plane);
+      cf[0] = q.x, cf[1] = q.y, cf[2] = r.x, cf[3] = r.y;
+      w[0] = u.x, w[1] = u.y, w[2] = v.x, w[3] = v.y;
+    } else {
+#pragma unroll
+      for (int k = 0; k < P; ++k) cf[k] = cf1[i * P + k], w[k] = w1[i * P + k];
+    }
+  };
+  // the next row's gate and reciprocal norms, a row ahead (loaded in their own row: 144 us for 88 at
+  // 8191 x 4096 fp16 and fp32)
+  float gt_n = 1.f, rf_n = 1.f, ro_n = 0.f;
+  const auto stats = [&](uint32_t q) {
+    if (q >= n) return;
+    if (a.gate_t != nullptr) gt_n = param<T>(a.gate_t, a.p32, q);
+    if (post) rf_n = __ldg(a.rstd_f + q);
+    if (pre) ro_n = __ldg(a.rstd_out + q);
+  };
+  stats(t);
   int buf = 0;
   uint32_t st = ring, st_in = ring + (S - 1) * step_bytes;
   const uint32_t ring_end = ring + S * step_bytes;
   for (; tw < n; t += step, tw += step) {
     issue(st_in);
     const bool live = t < n;
-    const float gt = live && a.gate_t != nullptr ? param<T>(a.gate_t, a.p32, t) : 1.f;
-    const float rf = live && post ? __ldg(a.rstd_f + t) : 1.f;
-    const float ro = live && pre ? __ldg(a.rstd_out + t) : 0.f;
+    const float gt = gt_n, rf = rf_n, ro = ro_n;
+    stats(t + step);
+    const f2 ro2 = f2_of(ro);
     if constexpr (U == 8) async_wait<S - 1>();
-    // unit i: dout, oh, dn, fh
-    const auto unit = [&](int i, float (&d)[U], float (&oh)[U], float (&dn)[U], float (&fh)[U]) {
+    // piece i: x = dout + ro w dn, out, f, dn
+    const auto get = [&](int i, f2 (&x)[P], f2 (&o)[P], f2 (&f)[P], f2 (&dn)[P]) {
 #pragma unroll
-      for (int k = 0; k < U; ++k) d[k] = oh[k] = dn[k] = fh[k] = 0.f;
-      if (has_d) od.get(st, piece, i, d);
+      for (int k = 0; k < P; ++k) x[k] = o[k] = f[k] = dn[k] = 0;
+      if (has_d) od.get(st, piece, i, x);
       if (pre) {
-        oo.get(st + out_at, piece, i, oh);
+        oo.get(st + out_at, piece, i, o);
         on.get(st + dn_at, piece, i, dn);
-#pragma unroll
-        for (int k = 0; k < U; ++k) oh[k] *= ro;
       }
-      if (has_f) {
-        of.get(st + f_at, piece, i, fh);
-#pragma unroll
-        for (int k = 0; k < U; ++k) fh[k] *= rf;
-      }
+      if (has_f) of.get(st + f_at, piece, i, f);
     };
-    float s[3] = {0.f, 0.f, 0.f};
+    f2 x1[KEEP ? P : 1], o1[KEEP ? P : 1], f1[KEEP ? P : 1];
+    f2 a0 = 0, a1 = 0, a2 = 0;
     if (live)
 #pragma unroll
-      for (int i = 0; i < NU; ++i)
-        if (c.has(i)) {
-          float d[U], oh[U], dn[U], fh[U];
-          unit(i, d, oh, dn, fh);
+      for (int i = 0; i < PIECES; ++i)
+        if (c.has_piece(i)) {
+          f2 x[P], o[P], f[P], dn[P], cf[P], w[P];
+          get(i, x, o, f, dn);
+          params(i, cf, w);
 #pragma unroll
-          for (int k = 0; k < U; ++k) {
-            const int e = i * U + k;
-            const float v = pre ? w[e] * dn[k] : 0.f, cfh = cf[e] * fh[k];
-            s[0] = fmaf(oh[k], v, s[0]);
-            s[1] = fmaf(cfh, fmaf(ro, v, d[k]), s[1]);
-            s[2] = fmaf(cfh, oh[k], s[2]);
-            dw[e] = fmaf(dn[k], oh[k], dw[e]);
+          for (int k = 0; k < P; ++k) {
+            const int e = i * P + k;
+            const f2 v = f2_mul(w[k], dn[k]), cfk = f2_mul(cf[k], f[k]);
+            x[k] = f2_fma(ro2, v, x[k]);
+            a0 = f2_fma(o[k], v, a0);
+            a1 = f2_fma(cfk, x[k], a1);
+            a2 = f2_fma(cfk, o[k], a2);
+            dw[e] = f2_fma(f2_mul(dn[k], ro2), o[k], dw[e]);
+            if constexpr (KEEP) x1[k] = x[k], o1[k] = o[k], f1[k] = f[k];
           }
         }
+    float s[3] = {f2_sum(a0), f2_sum(a1), f2_sum(a2)};
     group_sum3(s, s_sum[buf], c.g, a.GT);
     buf ^= 1;
-    const float m1 = s[0] * inv;
-    const float cfd = s[1] - ro * m1 * s[2];  // sum c fh D
+    const float k1 = ro * ro * (ro * s[0] * inv);
+    const float cfd = rf * (s[1] - k1 * s[2]);  // sum c fh D
     if (live) {
       if (c.j == 0 && a.dgate_t != nullptr) {
         if (a.p32)
@@ -129,23 +197,31 @@ __global__ void __launch_bounds__(RN_THREADS, 1) resnorm_bwd_kernel(const BwdOps
         else
           static_cast<T*>(a.dgate_t)[t] = from_f32<T>(cfd);
       }
-      const float m2 = post ? gt * cfd * inv : 0.f;
+      const f2 nk1 = f2_of(-k1), grf = f2_of(gt * rf);
+      const f2 nm2 = f2_of(post ? -(rf * rf) * (gt * cfd * inv) : 0.f);
 #pragma unroll
-      for (int i = 0; i < NU; ++i)
-        if (c.has(i)) {
-          float d[U], oh[U], dn[U], fh[U];
-          unit(i, d, oh, dn, fh);
+      for (int i = 0; i < PIECES; ++i)
+        if (c.has_piece(i)) {
+          f2 x[P], o[P], f[P], dn[P], cf[P], w[P];
+          params(i, cf, w);
+          if constexpr (KEEP) {
 #pragma unroll
-          for (int k = 0; k < U; ++k) {
-            const int e = i * U + k;
-            const float v = pre ? w[e] * dn[k] : 0.f;
-            d[k] = fmaf(ro, fmaf(-m1, oh[k], v), d[k]);
-            const float gd = gt * d[k];
-            K[e] = fmaf(fh[k], gd, K[e]);
-            fh[k] = rf * fmaf(-m2, fh[k], cf[e] * gd);
+            for (int k = 0; k < P; ++k) x[k] = x1[k], o[k] = o1[k], f[k] = f1[k];
+          } else {
+            get(i, x, o, f, dn);
+#pragma unroll
+            for (int k = 0; k < P; ++k) x[k] = f2_fma(ro2, f2_mul(w[k], dn[k]), x[k]);
           }
-          put_unit<R, U>(a.dx.row(t) + c.col(i), d);
-          if (has_f) put_unit<T, U>(a.df.row(t) + c.col(i), fh);
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            const int e = i * P + k;
+            x[k] = f2_fma(nk1, o[k], x[k]);
+            const f2 q = f2_mul(grf, x[k]);
+            K[e] = f2_fma(f[k], q, K[e]);
+            f[k] = f2_fma(cf[k], q, f2_mul(nm2, f[k]));
+          }
+          put_piece<R>(c, a.dx.row(t), i, x);
+          if (has_f) put_piece<T>(c, a.df.row(t), i, f);
         }
     }
     st_in = st;
@@ -160,13 +236,13 @@ __global__ void __launch_bounds__(RN_THREADS, 1) resnorm_bwd_kernel(const BwdOps
   float* const q = c.groups == 1 ? p0 : sj + 2 * c.g * a.H;
   if (c.groups > 1) __syncthreads();  // (the ring is read no more)
 #pragma unroll
-  for (int i = 0; i < NU; ++i)
-    if (c.has(i)) {
+  for (int i = 0; i < PIECES; ++i)
+    if (c.has_piece(i)) {
+      f2 k[P], d[P];
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        q[c.col(i) + k] = K[i * U + k];
-        q[a.H + c.col(i) + k] = dw[i * U + k];
-      }
+      for (int j = 0; j < P; ++j) k[j] = K[i * P + j], d[j] = dw[i * P + j];
+      put_piece<float>(c, q, i, k);
+      put_piece<float>(c, q + a.H, i, d);
     }
   if (c.groups == 1) return;
   __syncthreads();
@@ -326,20 +402,35 @@ __global__ void __launch_bounds__(512) resnorm_finish_kernel(
   if (dgate_c != nullptr) dgate_c[i] = from_f32<P>(w_post != nullptr ? t * to_f32(w_post[i]) : t);
 }
 
-template <typename T, typename R, int NU, int U>
-static cudaError_t bwd_launch(const Ctx& c, BwdOps<T, R> a, int* parts) {
-  a.GT = rn_group_threads<NU, U>(a.H);
-  const NormGrid g = rn_grid(a.GT, a.T_, c.num_sms);
+template <typename T, typename R, int NU, int U, int S>
+static cudaError_t bwd_launch_steps(const Ctx& c, const BwdOps<T, R>& a, const NormGrid& g,
+                                    int params) {
   const int nt = g.GT * g.groups;
-  size_t smem = U == 8 ? static_cast<size_t>(rn_bwd_steps<T, R, NU>) * nt * 2 *
-                             (Operand<T, NU, U>::BYTES + Operand<R, NU, U>::BYTES)
-                       : 0;
+  size_t smem = static_cast<size_t>(S) * nt * rn_bwd_bytes<T, R, NU, U> + params;
   if (g.groups > 1) smem = std::max(smem, sizeof(float) * 2 * g.groups * a.H);
-  auto* kern = resnorm_bwd_kernel<T, R, NU, U>;
+  const bool whole = a.dout.p != nullptr && a.dn.p != nullptr && a.f.p != nullptr;
+  auto* kern = whole ? resnorm_bwd_kernel<T, R, NU, U, S, true>
+                     : resnorm_bwd_kernel<T, R, NU, U, S, false>;
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
-  *parts = g.ctas;
   return launch_k(c.stream, kern, dim3(g.ctas), dim3(nt), smem, a);
+}
+
+template <typename T, typename R, int NU, int U>
+static cudaError_t bwd_launch(const Ctx& c, BwdOps<T, R> a, int* n_part) {
+  a.GT = rn_group_threads<NU, U>(a.H);
+  const NormGrid g = rn_grid(a.GT, a.T_, c.num_sms);
+  *n_part = g.ctas;
+  if constexpr (U == 1) {
+    return bwd_launch_steps<T, R, NU, U, 1>(c, a, g, 0);
+  } else {
+    const int params = NU > 1 ? 4 * (a.H / 8 * 16) : 0;
+    constexpr int MOST = rn_bwd_steps<T, R, NU>(NU > 1 ? 8 * 1024 : 0),
+                  LEAST = rn_bwd_steps<T, R, NU>(NU > 1 ? 64 * 1024 : 0);
+    const int fit = rn_bwd_steps<T, R, NU>(params);
+    if (fit >= MOST) return bwd_launch_steps<T, R, NU, U, MOST>(c, a, g, params);
+    return bwd_launch_steps<T, R, NU, U, LEAST>(c, a, g, params);
+  }
 }
 
 }  // namespace mmmoe
