@@ -58,6 +58,11 @@ struct Cols {
   __device__ __forceinline__ bool has_piece(int i) const { return U == 1 || has(i); }
 };
 
+// Whether rows are sent for into L2 a row ahead of the ring: with an fp32 residual stream, whose ring is
+// short (backward of 16384 x 2048 119.7 -> 100.5 us; all in bf16 68.4 -> 72.6).
+template <typename R>
+constexpr bool rn_prefetch = sizeof(R) == 4;
+
 // A whole row on its way to L2 (16-byte aligned, a multiple of 16 bytes), by one thread.
 template <typename V>
 __device__ __forceinline__ void prefetch_row(const V* row, int H) {
@@ -66,6 +71,15 @@ __device__ __forceinline__ void prefetch_row(const V* row, int H) {
                : "memory");
 }
 
+__device__ __forceinline__ void async_copy_l1(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 32 bytes in one store: whole sectors
+__device__ __forceinline__ void store32(float* p, const f2 (&f)[4]) {
+  asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(f[0]), "l"(f[1]), "l"(f[2]),
+               "l"(f[3])
+               : "memory");
+}
 __device__ __forceinline__ void sts16_f2(uint32_t a, f2 x, f2 y) {
   asm volatile("st.shared.v2.u64 [%0], {%1, %2};" ::"r"(a), "l"(x), "l"(y) : "memory");
 }
@@ -84,8 +98,13 @@ struct Operand {
       for (int i = 0; i < NU; ++i)
         if (c.has(i)) {
 #pragma unroll
-          for (int h = 0; h < PARTS; ++h)
-            async_copy(at + (i * PARTS + h) * piece, row + c.col(i) + h * VN<V>);
+          for (int h = 0; h < PARTS; ++h) {
+            // (the halves of 32 bytes meet in L1: past it each would fetch the whole sector)
+            if constexpr (PARTS == 2)
+              async_copy_l1(at + (i * PARTS + h) * piece, row + c.col(i) + h * VN<V>);
+            else
+              async_copy(at + (i * PARTS + h) * piece, row + c.col(i) + h * VN<V>);
+          }
         }
     } else {
 #pragma unroll
@@ -143,7 +162,9 @@ __device__ __forceinline__ void put_unit(V* p, const float (&f)[U]) {
 template <typename V, int NU, int U>
 __device__ __forceinline__ void put_piece(const Cols<NU, U>& c, V* row, int i,
                                           const f2 (&f)[Cols<NU, U>::P]) {
-  if constexpr (U == 8) {
+  if constexpr (U == 8 && std::is_same_v<V, float>) {
+    store32(row + c.col(i), f);
+  } else if constexpr (U == 8) {
     uint4* const o = reinterpret_cast<uint4*>(row + c.col(i));
 #pragma unroll
     for (int h = 0; h < 8 / VN<V>; ++h) {
@@ -160,6 +181,19 @@ __device__ __forceinline__ void put_piece(const Cols<NU, U>& c, V* row, int i,
       if (c.has(k)) row[c.col(k)] = from_f32<V>(lo);
       if (c.has(k + 1)) row[c.col(k + 1)] = from_f32<V>(hi);
     }
+  }
+}
+
+// The same for fp32 sums, in shared or global memory, on 16-byte boundaries.
+template <int NU, int U>
+__device__ __forceinline__ void put_sums(const Cols<NU, U>& c, float* p, int i,
+                                         const f2 (&f)[Cols<NU, U>::P]) {
+  if constexpr (U == 8) {
+    ulonglong2* const o = reinterpret_cast<ulonglong2*>(p + c.col(i));
+    o[0] = make_ulonglong2(f[0], f[1]);
+    o[1] = make_ulonglong2(f[2], f[3]);
+  } else {
+    put_piece<float>(c, p, i, f);
   }
 }
 
@@ -238,6 +272,39 @@ __device__ __forceinline__ void load_coef(const Cols<NU, U>& c, const void* w_po
   }
 }
 
+// The thread's c and w in shared memory: four planes of H / 8 entries, two pairs of a unit in each, so
+// that a warp's lanes read 512 bytes in a row.
+template <int NU>
+__device__ __forceinline__ void put_planes(const Cols<NU, 8>& c, uint32_t planes, uint32_t plane,
+                                           const f2 (&cf)[NU * 4], const f2 (&w)[NU * 4]) {
+#pragma unroll
+  for (int i = 0; i < NU; ++i)
+    if (c.has(i)) {
+      const uint32_t at = planes + (c.j + i * c.GT) * 16;
+      sts16_f2(at, cf[4 * i], cf[4 * i + 1]);
+      sts16_f2(at + plane, cf[4 * i + 2], cf[4 * i + 3]);
+      sts16_f2(at + 2 * plane, w[4 * i], w[4 * i + 1]);
+      sts16_f2(at + 3 * plane, w[4 * i + 2], w[4 * i + 3]);
+    }
+}
+template <int NU>
+__device__ __forceinline__ void put_planes(const Cols<NU, 1>&, uint32_t, uint32_t,
+                                           const f2 (&)[NU / 2], const f2 (&)[NU / 2]) {}
+// Piece i's values of the two planes from `planes` on (single columns: from the registers).
+template <int NU, int N>
+__device__ __forceinline__ void get_plane(const Cols<NU, 8>& c, uint32_t planes, uint32_t plane, int i,
+                                          const f2 (&)[N], f2 (&v)[4]) {
+  const uint32_t at = planes + (c.j + i * c.GT) * 16;
+  const ulonglong2 q = lds16_f2(at), r = lds16_f2(at + plane);
+  v[0] = q.x, v[1] = q.y, v[2] = r.x, v[3] = r.y;
+}
+template <int NU, int N>
+__device__ __forceinline__ void get_plane(const Cols<NU, 1>&, uint32_t, uint32_t, int,
+                                          const f2 (&own)[N], f2 (&v)[NU / 2]) {
+#pragma unroll
+  for (int k = 0; k < NU / 2; ++k) v[k] = own[k];
+}
+
 // Three sums over a group, as group_sum (a warp's in 16 bytes).
 __device__ __forceinline__ void group_sum3(float (&v)[3], float4* s, int g, int GT) {
 #pragma unroll
@@ -294,7 +361,9 @@ inline bool spans_meet(const RowSpan& a, const RowSpan& b, const mm_moe_resnorm*
   return d < ra || la - d < rb;
 }
 inline bool span_even(const RowSpan& r, const mm_moe_resnorm* s) {
-  return r.p == nullptr || (al16(r.p) && (s->T == 1 || r.ld * r.bytes % 16 == 0));
+  const size_t unit = 8 * r.bytes;  // (fp32 is stored 32 bytes at a time)
+  return r.p == nullptr ||
+         (reinterpret_cast<uintptr_t>(r.p) % unit == 0 && (s->T == 1 || r.ld * r.bytes % unit == 0));
 }
 
 // How the rows are spread: GT threads a row, groups of them in a CTA.

@@ -10,9 +10,6 @@
 #include "resnorm.cuh"
 
 namespace mmmoe {
-#ifndef RN_PF
-#define RN_PF 2
-#endif
 
 template <typename T, typename R>
 struct BwdOps {
@@ -41,13 +38,16 @@ constexpr int rn_bwd_steps(int params) {
   return std::max(1, std::min(4, (RN_SMEM - params) / (RN_THREADS * rn_bwd_bytes<T, R, NU, 8>)));
 }
 
-// S: steps of the ring (units of 8).  WHOLE: dout, dn and f are all there.
-// Two units a thread leave no registers for c and w beside the column sums: they are read from
-// shared memory, in two planes of four columns' pairs a unit, so that a warp's lanes read 512 bytes in a
-// row (in registers, with 72 bytes of spills: 16384 x 2048 bf16 92 us).
+// S: steps of the ring (units of 8).  WHOLE: dout, dn and f are all there.  dx, df and the CTA's column
+// sums in one read; the column sums stay in the registers of the threads that own the columns, which
+// leaves none for c and w: they are read from shared memory (in registers, with 72 bytes of spills:
+// 16384 x 2048 bf16 92 us).
+// 16384 x 2048 with the launch that ends it: 68.4 us in bf16 (0.87 of the copy rate), 100.5 with an fp32
+// residual stream (0.89; its rows in halves of sectors 135, not on their way to L2 a row ahead 120); one
+// unit a thread, eight warps a row: 93 and 130.
 template <typename T, typename R, int NU, int U, int S, bool WHOLE>
 __global__ void __launch_bounds__(RN_THREADS, 1) resnorm_bwd_kernel(const BwdOps<T, R> a) {
-  constexpr bool SHARED = U == 8 && NU > 1;
+  constexpr bool SHARED = U == 8;
   using OT = Operand<T, NU, U>;
   using OR = Operand<R, NU, U>;
   extern __shared__ __align__(16) unsigned char ring_bytes[];
@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(RN_THREADS, 1) resnorm_bwd_kernel(const BwdOps
       if (has_f) of.issue(c, a.f.row(ta), at + f_at, piece);
     }
     if constexpr (U == 8) {
-      if (RN_PF > 0 && c.j == 0) {
-        const int64_t tp = ta + static_cast<int64_t>(RN_PF) * step;
+      if (rn_prefetch<R> && c.j == 0) {
+        const int64_t tp = static_cast<int64_t>(ta) + step;
         if (tp < n) {
           if (has_d) prefetch_row(a.dout.row(tp), a.H);
           if (pre) prefetch_row(a.out.row(tp), a.H), prefetch_row(a.dn.row(tp), a.H);
@@ -105,16 +105,7 @@ __global__ void __launch_bounds__(RN_THREADS, 1) resnorm_bwd_kernel(const BwdOps
     for (int k = 0; k < NU * U / 2; ++k) w[k] = K[k] = dw[k] = 0;
     if (pre) load_params<T, NU, U>(c, a.w_pre, a.p32, w);
     if constexpr (SHARED) {
-      if (c.g == 0)
-#pragma unroll
-        for (int i = 0; i < NU; ++i)
-          if (c.has(i)) {
-            const uint32_t at = planes + (c.j + i * a.GT) * 16;
-            sts16_f2(at, cf[4 * i], cf[4 * i + 1]);
-            sts16_f2(at + plane, cf[4 * i + 2], cf[4 * i + 3]);
-            sts16_f2(at + 2 * plane, w[4 * i], w[4 * i + 1]);
-            sts16_f2(at + 3 * plane, w[4 * i + 2], w[4 * i + 3]);
-          }
+      if (c.g == 0) put_planes(c, planes, plane, cf, w);
       __syncthreads();
     } else {
 #pragma unroll
@@ -122,19 +113,10 @@ __global__ void __launch_bounds__(RN_THREADS, 1) resnorm_bwd_kernel(const BwdOps
     }
   }
   const auto params = [&](int i, f2 (&cf)[P], f2 (&w)[P]) {
-    if constexpr (SHARED) {
-      const uint32_t at = planes + (c.j + i * a.GT) * 16;
-      const ulonglong2 q = lds16_f2(at), r = lds16_f2(at + plane), u = lds16_f2(at + 2 * plane),
-                       v = lds16_f2(at + 3 * plane);
-      cf[0] = q.x, cf[1] = q.y, cf[2] = r.x, cf[3] = r.y;
-      w[0] = u.x, w[1] = u.y, w[2] = v.x, w[3] = v.y;
-    } else {
-#pragma unroll
-      for (int k = 0; k < P; ++k) cf[k] = cf1[i * P + k], w[k] = w1[i * P + k];
-    }
+    get_plane(c, planes, plane, i, cf1, cf);
+    get_plane(c, planes + 2 * plane, plane, i, w1, w);
   };
-  // the next row's gate and reciprocal norms, a row ahead (loaded in their own row: 144 us for 88 at
-  // 8191 x 4096 fp16 and fp32)
+  // the next row's gate and reciprocal norms, a row ahead
   float gt_n = 1.f, rf_n = 1.f, ro_n = 0.f;
   const auto stats = [&](uint32_t q) {
     if (q >= n) return;
@@ -241,8 +223,8 @@ __global__ void __launch_bounds__(RN_THREADS, 1) resnorm_bwd_kernel(const BwdOps
       f2 k[P], d[P];
 #pragma unroll
       for (int j = 0; j < P; ++j) k[j] = K[i * P + j], d[j] = dw[i * P + j];
-      put_piece<float>(c, q, i, k);
-      put_piece<float>(c, q + a.H, i, d);
+      put_sums(c, q, i, k);
+      put_sums(c, q + a.H, i, d);
     }
   if (c.groups == 1) return;
   __syncthreads();
@@ -424,9 +406,9 @@ static cudaError_t bwd_launch(const Ctx& c, BwdOps<T, R> a, int* n_part) {
   if constexpr (U == 1) {
     return bwd_launch_steps<T, R, NU, U, 1>(c, a, g, 0);
   } else {
-    const int params = NU > 1 ? 4 * (a.H / 8 * 16) : 0;
-    constexpr int MOST = rn_bwd_steps<T, R, NU>(NU > 1 ? 8 * 1024 : 0),
-                  LEAST = rn_bwd_steps<T, R, NU>(NU > 1 ? 64 * 1024 : 0);
+    const int params = 4 * (a.H / 8 * 16);
+    constexpr int MOST = rn_bwd_steps<T, R, NU>(8 * 1024),
+                  LEAST = rn_bwd_steps<T, R, NU>(NU * 32 * 1024);
     const int fit = rn_bwd_steps<T, R, NU>(params);
     if (fit >= MOST) return bwd_launch_steps<T, R, NU, U, MOST>(c, a, g, params);
     return bwd_launch_steps<T, R, NU, U, LEAST>(c, a, g, params);
