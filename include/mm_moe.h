@@ -371,8 +371,8 @@ MM_MOE_API mm_moe_status mm_moe_resnorm_workspace_size(const mm_moe_resnorm* sha
  *   post_weight, pre_weight [H];  gate [H] or [T]; each only where the shape has it
  *   rstd_f, rstd_out        [T] fp32 out, for the backward; likewise
  * Outputs over operands or over one another are refused (MM_MOE_EINVAL; rows in one another's gaps
- * pass where both lie equally far apart in bytes).  Pointers aligned to their element; rows on
- * 16-byte boundaries of a multiple of 8 channels run faster.  Errors as for the layer. */
+ * pass where both lie equally far apart in bytes).  Pointers aligned to their element; rows of a
+ * multiple of 8 channels on 16-byte (fp32: 32-byte) boundaries run faster.  Errors as for the layer. */
 MM_MOE_API mm_moe_status mm_moe_resnorm_forward(
     const mm_moe_resnorm* shape, const void* x, int64_t ldx, const void* f, int64_t ldf,
     const void* post_weight, const void* gate, const void* pre_weight, void* out, int64_t ldout,

@@ -35,10 +35,10 @@ constexpr int rn_fwd_steps =
 // rows in 16-byte halves of sectors, and not on their way to L2 a row ahead: 80).  Two CTAs an SM with half
 // of the ring and the parameters in shared memory: 49.9 and 71.6.
 template <typename T, typename R, int NU, int U>
-__global__ void __launch_bounds__(RN_THREADS, 1) resnorm_fwd_kernel(const FwdOps<T, R> a) {
+__global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel(const FwdOps<T, R> a) {
   constexpr int S = U == 8 ? rn_fwd_steps<T, R, NU> : 1;
-  using OF = Operand<T, NU, U>;
-  using OX = Operand<R, NU, U>;
+  using OF = Operand<T, NU, U, true>;
+  using OX = Operand<R, NU, U, true>;
   extern __shared__ __align__(16) unsigned char ring_bytes[];
   __shared__ Sums<1> s_sum[2][RN_THREADS / 32];
   const uint32_t piece = blockDim.x * 16, step_bytes = rn_fwd_bytes<T, R, NU, U> * blockDim.x;
@@ -85,7 +85,10 @@ __global__ void __launch_bounds__(RN_THREADS, 1) resnorm_fwd_kernel(const FwdOps
   int buf = 0;
   uint32_t st = ring, st_in = ring + (S - 1) * step_bytes;
   const uint32_t ring_end = ring + S * step_bytes;
+  if constexpr (U == 1) issue(0);
   for (; tw < n; t += step, tw += step) {
+    of.turn();
+    ox.turn();
     issue(st_in);
     const bool live = t < n;
     float gt = gt_n;
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(LOOP_THREADS) resnorm_fwd_loop_kernel(const Fw
 template <typename T, typename R, int NU, int U>
 static cudaError_t fwd_launch(const Ctx& c, FwdOps<T, R> a) {
   a.GT = rn_group_threads<NU, U>(a.H);
-  const NormGrid g = rn_grid(a.GT, a.T_, c.num_sms);
+  const NormGrid g = rn_grid(a.GT, a.T_, c.num_sms * rn_ctas<NU, U>);
   const int nt = g.GT * g.groups;
   const size_t smem =
       U == 8 ? static_cast<size_t>(rn_fwd_steps<T, R, NU>) * nt * rn_fwd_bytes<T, R, NU, U> : 0;
@@ -294,6 +297,7 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_resnorm_forward(
         return fwd_launch<T, R, 1, 8>(c, a);
       return fwd_launch<T, R, 2, 8>(c, a);
     }
+    if (!even && H <= 4 * RN_THREADS) return fwd_launch<T, R, 4, 1>(c, a);
     if (!even && H <= 8 * RN_THREADS) return fwd_launch<T, R, 8, 1>(c, a);
     return launch_k(c.stream,
                     even ? resnorm_fwd_loop_kernel<T, R, 8> : resnorm_fwd_loop_kernel<T, R, 1>,

@@ -85,13 +85,15 @@ __device__ __forceinline__ void sts16_f2(uint32_t a, f2 x, f2 y) {
 }
 __device__ __forceinline__ f2 f2_of(float v) { return f2_make(v, v); }
 
-// One row operand of type V on its way to the thread's registers.
-template <typename V, int NU, int U>
+// One row operand of type V on its way to the thread's registers.  AHEAD: single columns are loaded a
+// row ahead (the forward's; the backward has no registers for it: 56 us so, 67 ahead).
+template <typename V, int NU, int U, bool AHEAD = false>
 struct Operand {
   using C = Cols<NU, U>;
   static constexpr int PARTS = U == 8 ? 8 / VN<V> : 0;  // 16-byte pieces of a unit
   static constexpr int BYTES = PARTS * 16 * NU;         // of a thread's share of a row in the ring
-  float reg[U == 1 ? NU : 1];
+  float reg[U == 1 ? NU : 1];  // the row's values
+  V next[U == 1 && AHEAD ? NU : 1];
   __device__ __forceinline__ void issue(const C& c, const V* row, uint32_t at, uint32_t piece) {
     if constexpr (U == 8) {
 #pragma unroll
@@ -108,7 +110,20 @@ struct Operand {
         }
     } else {
 #pragma unroll
-      for (int i = 0; i < NU; ++i) reg[i] = c.has(i) ? to_f32(row[c.col(i)]) : 0.f;
+      for (int i = 0; i < NU; ++i) {
+        const V v = c.has(i) ? row[c.col(i)] : from_f32<V>(0.f);
+        if constexpr (AHEAD)
+          next[i] = v;
+        else
+          reg[i] = to_f32(v);
+      }
+    }
+  }
+  // the row that is on its way becomes this one
+  __device__ __forceinline__ void turn() {
+    if constexpr (U == 1 && AHEAD) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i) reg[i] = to_f32(next[i]);
     }
   }
   // piece i's values (single columns: zero where there is none)
@@ -365,6 +380,11 @@ inline bool span_even(const RowSpan& r, const mm_moe_resnorm* s) {
   return r.p == nullptr ||
          (reinterpret_cast<uintptr_t>(r.p) % unit == 0 && (s->T == 1 || r.ld * r.bytes % unit == 0));
 }
+
+// CTAs an SM: two where single columns leave the registers for it (four a thread; 5003 x 1111 bf16
+// forward 61 -> 41 us, backward 64 -> 56).
+template <int NU, int U>
+constexpr int rn_ctas = U == 1 && NU <= 4 ? 2 : 1;
 
 // How the rows are spread: GT threads a row, groups of them in a CTA.
 template <int NU, int U>

@@ -46,7 +46,7 @@ constexpr int rn_bwd_steps(int params) {
 // residual stream (0.89; its rows in halves of sectors 135, not on their way to L2 a row ahead 120); one
 // unit a thread, eight warps a row: 93 and 130.
 template <typename T, typename R, int NU, int U, int S, bool WHOLE>
-__global__ void __launch_bounds__(RN_THREADS, 1) resnorm_bwd_kernel(const BwdOps<T, R> a) {
+__global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_bwd_kernel(const BwdOps<T, R> a) {
   constexpr bool SHARED = U == 8;
   using OT = Operand<T, NU, U>;
   using OR = Operand<R, NU, U>;
@@ -401,7 +401,7 @@ static cudaError_t bwd_launch_steps(const Ctx& c, const BwdOps<T, R>& a, const N
 template <typename T, typename R, int NU, int U>
 static cudaError_t bwd_launch(const Ctx& c, BwdOps<T, R> a, int* n_part) {
   a.GT = rn_group_threads<NU, U>(a.H);
-  const NormGrid g = rn_grid(a.GT, a.T_, c.num_sms);
+  const NormGrid g = rn_grid(a.GT, a.T_, c.num_sms * rn_ctas<NU, U>);
   *n_part = g.ctas;
   if constexpr (U == 1) {
     return bwd_launch_steps<T, R, NU, U, 1>(c, a, g, 0);
@@ -493,7 +493,8 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_resnorm_backward(
       return err;
     }
     if (!even && H <= 8 * RN_THREADS) {
-      err = bwd_launch<T, R, 8, 1>(c, a, &parts);
+      err = H <= 4 * RN_THREADS ? bwd_launch<T, R, 4, 1>(c, a, &parts)
+                                : bwd_launch<T, R, 8, 1>(c, a, &parts);
       prof_end(c, K_RESNORM_BWD);
       return err;
     }
