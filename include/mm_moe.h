@@ -557,7 +557,7 @@ MM_MOE_API mm_moe_status mm_moe_grad_clip(const mm_moe_grad* grads, int64_t n_te
 typedef enum { MM_MOE_STATES_F32 = 0, MM_MOE_STATES_8BIT = 1 } mm_moe_states;
 typedef struct {
   double beta1, beta2;  /* in [0, 1) */
-  double eps;           /* > 0 (as a float) */
+  double eps;           /* at least 2^-126 */
   float max_norm;       /* >= 0, may be infinite */
   float clip_eps;       /* >= 0 */
   int32_t states;       /* mm_moe_states */

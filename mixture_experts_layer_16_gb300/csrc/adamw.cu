@@ -91,6 +91,12 @@ __device__ __forceinline__ float sqrt_approx(float v) {  // within 2^-22 of itse
   return r;
 }
 
+__device__ __forceinline__ float rcp_approx(float v) {  // within 2^-22 of itself (v is a normal number)
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // ------------------------------------------------------------------- eight elements
 struct Raw8 {
   uint32_t w[8];
@@ -186,44 +192,68 @@ struct V8 {
 __device__ __forceinline__ float scale_of(uint32_t c) {  // 2^(c - 127), 255 is a NaN
   return __uint_as_float(c == 0 ? 0x00400000u : c == 255 ? 0x7fffffffu : c << 23);
 }
-// A code's bits are those of an fp32 number whose exponent runs from 0 (subnormals among them):
-// one exact product moves it to the format's own bias, another applies the block's scale.
-template <typename F>
-__device__ __forceinline__ void decode8(uint2 q, float scale, float (&f)[8]) {
-  constexpr float MOVE = F::BIAS == 7 ? 0x1p120f : 0x1p112f;
+// e4m3 is a conversion of the hardware's, exact in f16.  The other format's bits are those of an fp32
+// number whose exponent runs from 0 (subnormals among them): one exact product moves it to the
+// format's own bias, another applies the block's scale.
+__device__ __forceinline__ void decode8(uint2 q, float scale, float (&f)[8], M8) {
+  const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
+        : "=r"(h)
+        : "h"(static_cast<uint16_t>(w[k / 2] >> 16 * (k & 1))));
+    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    f[2 * k] = t.x * scale;
+    f[2 * k + 1] = t.y * scale;
+  }
+}
+__device__ __forceinline__ void decode8(uint2 q, float scale, float (&f)[8], V8) {
   const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const uint32_t c = w[k / 4] >> 8 * (k & 3);
-    const uint32_t mag = (F::SIGNED ? c & 0x7fu : c & 0xffu) << 20;
-    f[k] = __uint_as_float(mag) * MOVE * scale;
-    if (F::SIGNED) f[k] = __uint_as_float(__float_as_uint(f[k]) | (c & 0x80u) << 24);
+    const uint32_t top = __byte_perm(w[k / 4], 0, (k & 3) << 12 | 0x444);  // the code's byte alone, at the top
+    f[k] = __uint_as_float(top >> 4) * 0x1p112f * scale;
   }
 }
 // Codes of a thread's eight values (four neighbouring lanes hold a block), rounded up where the
-// bits that a code drops and the random ones carry.  `c`: the block's scale code.
+// bits that a code drops and the random ones (the first moment's lower, the second's upper 16) carry.  `c`: the block's
+// scale code.
 template <typename F>
-__device__ __forceinline__ uint2 encode8(const float (&f)[8], const uint32_t (&rnd)[8], int shift,
-                                         uint32_t& c) {
+__device__ __forceinline__ uint2 encode8(const float (&f)[8], const uint32_t (&rnd)[8], uint32_t& c) {
   constexpr float MOVE = F::BIAS == 7 ? 0x1p-120f : 0x1p-112f;
-  int top = 0;  // (a NaN's bits lie above infinity's)
+  float largest = 0.f, finite = 0.f;  // (finite becomes a NaN with any value that is not)
 #pragma unroll
-  for (int k = 0; k < 8; ++k) top = max(top, __float_as_int(f[k]) & 0x7fffffff);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  for (int k = 0; k < 8; ++k) {
+    largest = fmaxf(largest, fabsf(f[k]));
+    finite = fmaf(f[k], 0.f, finite);
+  }
+  if (finite != 0.f) largest = INFINITY;
+  largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
+  largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
+  const int top = __float_as_int(largest);
   const int e = max(((top + (0x7fffff - F::TOP)) >> 23) - F::SHIFT, 0);
   c = top >= 0x7f800000 ? 255u : static_cast<uint32_t>(e);
   const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
   uint32_t w[2] = {0, 0};
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float z = fabsf(f[k]) * inv * MOVE;
-    uint32_t code = (__float_as_uint(z) + ((rnd[k] >> shift & 0xffffu) << 4)) >> 20;
-    if (F::SIGNED)
-      code |= __float_as_uint(f[k]) >> 24 & 0x80u;
-    else if (code == 0 && f[k] > 0.f)
-      code = 1;
-    w[k / 4] |= (code & 0xffu) << 8 * (k & 3);
+  for (int k = 7; k >= 0; --k) {
+    const float z = fabsf(f[k]) * inv * MOVE;  // (the code's bits are bits 20 to 27)
+    const uint32_t r = F::SIGNED ? rnd[k] & 0xffffu : rnd[k] >> 16;
+    const uint32_t up = (__float_as_uint(z) + r * 16) * 16;  // ... and now the top byte
+    w[k / 4] = __funnelshift_l(up, w[k / 4], 8);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (F::SIGNED) {
+      const uint32_t* b = reinterpret_cast<const uint32_t*>(f + 4 * h);  // the signs' bytes
+      const uint32_t lo = __byte_perm(b[0], b[1], 0x0073), hi = __byte_perm(b[2], b[3], 0x0073);
+      w[h] |= __byte_perm(lo, hi, 0x5410) & 0x80808080u;
+    } else if (((w[h] - 0x01010101u) & ~w[h] & 0x80808080u) != 0) {  // a zero: only of a zero
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if ((w[h] >> 8 * k & 0xffu) == 0 && f[4 * h + k] > 0.f) w[h] |= 1u << 8 * k;
+    }
   }
   return make_uint2(w[0], w[1]);
 }
@@ -313,8 +343,8 @@ __global__ void __launch_bounds__(AW_THREADS, AW_CTAS) adamw_kernel(const __grid
     widen(rg, gdt, fg);
     widen(rp, wdt, fp);
     if constexpr (BITS8) {
-      decode8<M8>(qm, scale_of(cm), m);
-      decode8<V8>(qv, scale_of(cv), v);
+      decode8(qm, scale_of(cm), m, M8{});
+      decode8(qv, scale_of(cv), v, V8{});
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -328,7 +358,7 @@ __global__ void __launch_bounds__(AW_THREADS, AW_CTAS) adamw_kernel(const __grid
       const float x = fg[k] * coef;
       m[k] = fmaf(m[k], a.b1, x * a.a1);
       v[k] = fmaf(v[k], a.b2, x * x * a.a2);
-      const float u = __fdividef(m[k] * c1, fmaf(sqrt_approx(v[k]), c2, a.eps));
+      const float u = m[k] * c1 * rcp_approx(fmaf(sqrt_approx(v[k]), c2, a.eps));
       fp[k] = fmaf(-lr, fmaf(decay, fp[k], u), fp[k]);
     }
     store8(wide, wdt, i, mine, vec, fp);
@@ -343,8 +373,8 @@ __global__ void __launch_bounds__(AW_THREADS, AW_CTAS) adamw_kernel(const __grid
       const uint32_t key = mix32(s_key ^ g.index[t]) ^ static_cast<uint32_t>(i >> 32) * 0x9E3779B1u;
 #pragma unroll
       for (int k = 0; k < 8; ++k) rnd[k] = mix32(static_cast<uint32_t>(i + k) ^ key);
-      qm = encode8<M8>(m, rnd, 0, cm);
-      qv = encode8<V8>(v, rnd, 16, cv);
+      qm = encode8<M8>(m, rnd, cm);
+      qv = encode8<V8>(v, rnd, cv);
       if (held) {
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + at) = qm;
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + at) = qv;
@@ -373,9 +403,9 @@ __global__ void __launch_bounds__(256) adamw_moments_kernel(
     const uint2 qv = __ldg(reinterpret_cast<const uint2*>(v + i));
     const float sm = scale_of(__ldg(m_scale + (i >> 5))), sv = scale_of(__ldg(v_scale + (i >> 5)));
     float f[8];
-    decode8<M8>(qm, sm, f);
+    decode8(qm, sm, f, M8{});
     *reinterpret_cast<uint4*>(om + i) = pack(f, om);
-    decode8<V8>(qv, sv, f);
+    decode8(qv, sv, f, V8{});
     *reinterpret_cast<uint4*>(ov + i) = pack(f, ov);
   }
 }
@@ -451,7 +481,7 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_adamw_step(
     uint8_t* m_scale, void* v, uint8_t* v_scale, void* counter, double lr, const float* lr_dev,
     const float* norm, void* stream) {
   if (opt == nullptr || !(opt->beta1 >= 0.0 && opt->beta1 < 1.0) ||
-      !(opt->beta2 >= 0.0 && opt->beta2 < 1.0) || !(static_cast<float>(opt->eps) > 0.f) || !std::isfinite(opt->eps) ||
+      !(opt->beta2 >= 0.0 && opt->beta2 < 1.0) || !(static_cast<float>(opt->eps) >= 1.17549435e-38f) || !std::isfinite(opt->eps) ||
       !(opt->max_norm >= 0.f) || !(opt->clip_eps >= 0.f) || opt->states < 0 || opt->states > 1 ||
       !std::isfinite(lr))
     return MM_MOE_EINVAL;
