@@ -20,8 +20,9 @@
 // be divided by eps).  A block with a value that is not finite has the scale's NaN.
 //
 // Bytes bound the step: a bf16 parameter with a master and a bf16 gradient moves 28 bytes with fp32
-// moments, 16 with 8-bit ones.  The benchmark layer's 604 M parameters take 2.65 ms (0.94 of the copy rate), 200 M in 48
-// tensors with 8-bit moments 559 us (0.85): 72 instructions an element, two thirds of the issue slots.
+// moments, 16 with 8-bit ones.  The benchmark layer's 604 M parameters take 2.65 ms (0.94 of the copy
+// rate), 200 M in 48 tensors with 8-bit moments 0.57 (0.84: 75 instructions an element, two thirds of
+// the issue slots).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(AW_THREADS, AW_CTAS) adamw_kernel(const __grid
   if (a.norm != nullptr) {
     const float nrm = __ldcg(a.norm);
     if (!(fabsf(nrm) <= 3.4028235e38f)) return;  // nothing moves, and the step does not count
-    coef = fminf(a.max_norm / (nrm + a.clip_eps), 1.f);
+    coef = fminf(__frcp_rn(nrm + a.clip_eps) * a.max_norm, 1.f);  // (0 inf is a NaN: coef 1)
   }
   const float lr = a.lr_dev != nullptr ? __ldcg(a.lr_dev) : a.lr;
   if (threadIdx.x == 0) {
@@ -359,19 +360,16 @@ __global__ void __launch_bounds__(AW_THREADS, AW_CTAS) adamw_kernel(const __grid
       }
     }
     const float c1 = s_c1, c2 = s_c2, decay = g.decay[t];
-    const auto both = [](float x) { return f2_make(x, x); };
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      const f2 x = f2_mul(f2_make(fg[k], fg[k + 1]), both(coef));
-      const f2 m2 = f2_fma(f2_make(m[k], m[k + 1]), both(a.b1), f2_mul(x, both(a.a1)));
-      const f2 v2 = f2_fma(f2_make(v[k], v[k + 1]), both(a.b2), f2_mul(f2_mul(x, x), both(a.a2)));
-      f2_split(m2, m[k], m[k + 1]);
-      f2_split(v2, v[k], v[k + 1]);
-      float d0, d1;
-      f2_split(f2_fma(f2_make(sqrt_approx(v[k]), sqrt_approx(v[k + 1])), both(c2), both(a.eps)), d0, d1);
-      const f2 u = f2_mul(f2_mul(m2, both(c1)), f2_make(rcp_approx(d0), rcp_approx(d1)));
-      const f2 p = f2_make(fp[k], fp[k + 1]);
-      f2_split(f2_fma(both(-lr), f2_fma(both(decay), p, u), p), fp[k], fp[k + 1]);
+    for (int k = 0; k < 8; ++k) {
+      // Under 8 bits each product is rounded by itself, as elementwise fp32 arithmetic does: a value
+      // beside the border between two codes falls to the same side wherever the step is computed.
+      const float x = fg[k] * coef;
+      m[k] = BITS8 ? __fadd_rn(__fmul_rn(m[k], a.b1), __fmul_rn(x, a.a1)) : fmaf(m[k], a.b1, x * a.a1);
+      v[k] = BITS8 ? __fadd_rn(__fmul_rn(v[k], a.b2), __fmul_rn(__fmul_rn(x, x), a.a2))
+                   : fmaf(v[k], a.b2, x * x * a.a2);
+      const float u = m[k] * c1 * rcp_approx(fmaf(sqrt_approx(v[k]), c2, a.eps));
+      fp[k] = fmaf(-lr, fmaf(decay, fp[k], u), fp[k]);
     }
     store8(wide, wdt, i, mine, vec, fp);
     if (has_master) store8(g.param[t], dt, i, mine, vec, fp);
