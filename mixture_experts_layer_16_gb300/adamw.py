@@ -45,8 +45,8 @@ class MoEAdamW:
         b1, b2 = (float(b) for b in betas)
         if not (0.0 <= b1 < 1.0 and 0.0 <= b2 < 1.0):
             raise ValueError(f"betas must lie in [0, 1), got {betas}")
-        if not 0.0 < eps < float("inf"):
-            raise ValueError(f"eps must be > 0, got {eps}")
+        if not 2.0 ** -126 <= eps < float("inf"):
+            raise ValueError(f"eps must be at least 2^-126, got {eps}")
         decay = [float(weight_decay)] * len(params) if isinstance(weight_decay, (int, float)) \
             else [float(w) for w in weight_decay]
         if len(decay) != len(params):

@@ -629,7 +629,162 @@ __global__ void __launch_bounds__(32 * sel_warps<PL>, sel_ctas<PL>) select_fwd_k
   }
 }
 
+// ------------------------------------------------------------------------ few experts
+// Whether expert j's key (bias and all) lies above expert i's, for keys that fp32 does not tell apart: by
+// the difference of the logits (as in select_fwd_kernel), else in 64 bits.
+template <typename T>
+__device__ __noinline__ bool above(const T* __restrict__ row, const float* __restrict__ bias,
+                                   const SelArgs a, float m, float rz, int i, int j) {
+  const float li = to_f32(__ldg(row + i)), lj = to_f32(__ldg(row + j)), dl = lj - li;
+  const float db = __ldg(bias + j) - __ldg(bias + i);
+  if (dl == 0.f && db == 0.f) return false;
+  const float d = a.sigmoid ? sigmoid32(lj) * sigmoid32(-li) * -expm1f(-dl)
+                            : (m == -INFINITY ? 0.f : expf(li - m) * rz) * expm1f(dl);
+  const float far = a.sigmoid ? 64.f + fabsf(dl) : 128.f + fabsf(dl) + fabsf(li - m);
+  const float tol = far * 0x1p-24f * fabsf(d) + 0x1p-23f * fabsf(db);
+  if (fabsf(d + db) > tol) return d + db > 0.f;
+  double s[2], dm = -INFINITY, z = 0.0;
+  if (!a.sigmoid) {
+    for (int e = 0; e < a.E; ++e) dm = fmax(dm, static_cast<double>(to_f32(row[e])));
+    for (int e = 0; e < a.E; ++e) z += exp(static_cast<double>(to_f32(row[e])) - dm);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const double x = h == 0 ? li : lj;
+    s[h] = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : dm == -INFINITY ? 0.0 : exp(x - dm) / z;
+    s[h] += static_cast<double>(__ldg(bias + (h == 0 ? i : j)));
+    if (s[h] != s[h]) s[h] = -INFINITY;
+  }
+  return s[1] > s[0];
+}
+
+// Up to N experts, all groups taking part: a thread a token, its keys in registers, every expert's
+// place the number of keys in front of its own; pairs within each other's errors are compared anew.
+// 131072 x 8 fp32 3.8 us (27 in eight lanes a token), 131072 x 16 9.1.
+template <typename T, int N, bool BIAS>
+__global__ void __launch_bounds__(128) select_small_kernel(
+    const T* __restrict__ logits, const float* __restrict__ bias, const SelArgs a,
+    int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
+  if (t >= a.T) return;
+  const T* const row = logits + t * a.E;
+  float l[N];
+  if (a.vec) {  // (N experts)
+#pragma unroll
+    for (int i = 0; i < N; i += VN<T>) {
+      float f[VN<T>];
+      unpack(__ldg(reinterpret_cast<const uint4*>(row + i)), f, row);
+#pragma unroll
+      for (int j = 0; j < VN<T>; ++j) l[i + j] = f[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) l[i] = i < a.E ? to_f32(__ldg(row + i)) : -INFINITY;
+  }
+  float m = -INFINITY, rz = 0.f;
+  if (!a.sigmoid && (BIAS || !a.renorm)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) z += i < a.E ? expf(l[i] - m) : 0.f;
+    rz = m == -INFINITY ? 0.f : 1.f / z;
+  }
+  const auto score = [&](float x) {
+    return a.sigmoid ? sigmoid32(x) : m == -INFINITY ? 0.f : expf(x - m) * rz;
+  };
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = BIAS ? score(l[i]) + (i < a.E ? __ldg(bias + i) : 0.f) : l[i];
+    v[i] = i < a.E ? low_nan(v[i]) : -INFINITY;
+  }
+  int place[N] = {};
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = i + 1; j < N; ++j) {
+      const bool behind = v[j] > v[i];
+      place[i] += behind;
+      place[j] += !behind;
+    }
+  if constexpr (BIAS) {
+    // the errors of two scores (16 2^-24 of each: a sum of N terms besides), and the sums' own
+    const float bound = (2 * N + 64) * 0x1p-24f * (a.sigmoid ? 1.f : rz);
+    // by expert, those of higher index that are in doubt (all of them, once one bears on the choice: the
+    // places are right together or not at all)
+    uint32_t near[N];
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      near[i] = 0;
+#pragma unroll
+      for (int j = i + 1; j < N; ++j) {
+        const bool apart = fabsf(v[i] - v[j]) > bound + 0x1p-22f * (fabsf(v[i]) + fabsf(v[j]));
+        if (j < a.E && !apart) {
+          near[i] |= 1u << j;
+          any = any || min(place[i], place[j]) < a.k;
+        }
+      }
+    }
+    if (any) {
+      unsigned long long packed = 0;  // the places, four bits each
+#pragma unroll
+      for (int i = 0; i < N; ++i) packed |= static_cast<unsigned long long>(place[i]) << 4 * i;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        while (near[i] != 0) {
+          const int j = __ffs(near[i]) - 1;
+          near[i] &= near[i] - 1;
+          float vj = -INFINITY;
+#pragma unroll
+          for (int h = i + 1; h < N; ++h) vj = h == j ? v[h] : vj;
+          const bool was = vj > v[i], is = above(row, bias, a, m, rz, i, j);
+          if (was != is) {
+            packed += is ? 1ull << 4 * i : 1ull << 4 * j;
+            packed -= is ? 1ull << 4 * j : 1ull << 4 * i;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) place[i] = static_cast<int>(packed >> 4 * i & 15u);
+    }
+  }
+  // (absent experts come behind all: -inf, and of higher index)
+  float big = -INFINITY, sum = 0.f;
+  float w[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (place[i] < a.k) big = fmaxf(big, l[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const bool in = place[i] < a.k;
+    w[i] = !in ? 0.f
+           : a.renorm && !a.sigmoid ? (big == -INFINITY ? 0.f : expf(l[i] - big))
+                                    : score(l[i]);
+    sum += w[i];
+  }
+  const float c = !a.renorm ? a.scale : a.sigmoid ? 1.f / (sum + SUM_EPS) : sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (place[i] < a.k) {
+      topk_idx[t * a.k + place[i]] = i;
+      topk_w[t * a.k + place[i]] = a.renorm ? a.scale * (w[i] * c) : w[i] * c;
+    }
+}
+
 // --------------------------------------------------------------------------- host side
+template <typename T, int N>
+cudaError_t sel_launch_small(const Ctx& c, SelArgs a, const T* logits, const float* bias,
+                             int32_t* idx, float* w) {
+  a.vec = a.E == N && reinterpret_cast<uintptr_t>(logits) % 16 == 0;
+  auto* kern = bias != nullptr ? select_small_kernel<T, N, true> : select_small_kernel<T, N, false>;
+  const int ctas = static_cast<int>((static_cast<int64_t>(a.T) + 127) / 128);
+  return launch_k(c.stream, kern, dim3(ctas), dim3(128), 0, logits, bias, a, idx, w);
+}
+
 // The row over W lanes; false where they do not hold it.
 inline bool sel_split(SelArgs* a, int W) {
   const auto up = [](int n) {
@@ -676,6 +831,9 @@ cudaError_t launch_select_fwd_of(const Ctx& c, const SelArgs& args, const T* log
   const auto fills = [&](int W) {
     return static_cast<int64_t>(a.T) * W >= static_cast<int64_t>(c.num_sms) * 32 * SEL_FILL;
   };
+  if (a.G == 1 && a.E <= 16)
+    return a.E <= 8 ? sel_launch_small<T, 8>(c, a, logits, bias, idx, w)
+                    : sel_launch_small<T, 16>(c, a, logits, bias, idx, w);
   if (fills(8) && sel_split(&a, 8) && a.c <= 32) {
     if (a.c <= 4) return sel_launch<T, 8, 4>(c, a, logits, bias, idx, w);
     if (a.c <= 8) return sel_launch<T, 8, 8>(c, a, logits, bias, idx, w);

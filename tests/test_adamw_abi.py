@@ -44,7 +44,7 @@ def test_layout():
 
 @pytest.mark.parametrize("bad", [
     dict(beta1=-0.1), dict(beta1=1.0), dict(beta2=1.0), dict(beta2=float("nan")), dict(eps=0.0),
-    dict(eps=1e-60), dict(eps=-1e-8), dict(eps=float("inf")), dict(max_norm=-1.0),
+    dict(eps=1e-60), dict(eps=1e-39), dict(eps=-1e-8), dict(eps=float("inf")), dict(max_norm=-1.0),
     dict(max_norm=float("nan")), dict(clip_eps=-1.0), dict(states=2), dict(states=-1)])
 def test_options(lib, bad):
     assert call(lib, opt=bad.items()) == EI
@@ -109,7 +109,7 @@ def test_handle(lib):
     two = MoEAdamW([p[1], p[1]], device="cpu")
     with pytest.raises(ValueError):                   # the same tensor twice
         two.step([p[1], p[1]], [g[1], g[1]], 1e-3)
-    for kw in (dict(states="int8"), dict(betas=(1.0, 0.9)), dict(betas=(0.9, -0.1)), dict(eps=0.0),
+    for kw in (dict(states="int8"), dict(betas=(1.0, 0.9)), dict(betas=(0.9, -0.1)), dict(eps=0.0), dict(eps=1e-39),
                dict(weight_decay=[0.1])):
         with pytest.raises(ValueError):
             MoEAdamW(p, device="cpu", **kw)

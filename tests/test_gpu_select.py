@@ -464,3 +464,45 @@ def test_captured_and_repeated():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, v) for a, v in zip(got, want))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(8, 2), (8, 8), (5, 3), (16, 4), (13, 13)])
+def test_near_keys_of_few_experts(score, E, k):
+    """Keys 1e-3 to 1e-10 apart, several together, in every other row; equal ones and -inf as well."""
+    T = 4000
+    r = np.random.default_rng(E + k)
+    l = r.standard_normal((T, E)).astype(np.float32)
+    l[::2] = l[0]
+    l[3], l[5, ::2], l[7] = 0.5, -np.inf, -np.inf
+    s = os_.scores(l[0].astype(np.float64), score)
+    for gap in (1e-3, 1e-6, 1e-8, 1e-10):
+        bias = (0.7 - s + gap * r.permutation(E)).astype(np.float32)
+        bias[0] = bias[1] = bias[0]
+        h = MoESelect(T, E, k, score)
+        idx = h.forward(torch.from_numpy(l).cuda(), torch.from_numpy(bias).cuda())[0].cpu().numpy()
+        ri, _ = os_.forward(l, bias.astype(np.float64), k, score)
+        bad = np.argwhere((idx != ri).any(1))[:, 0]
+        assert len(bad) == 0, (gap, len(bad), idx[bad[0]], ri[bad[0]])
+
+
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_more_candidates_than_there_is_room_for(with_bias):
+    """Few kept lanes and a large k leave no bound below the k-th key, and rows of equal keys none
+    that helps: the whole row is ranked."""
+    for T, E, k, groups, keep in ((20, 1024, 32, 32, 12), (33, 512, 20, 1, 1), (12000, 256, 8, 1, 1),
+                                  (12000, 256, 8, 8, 4)):
+        opt = options("sigmoid", groups, keep, "max", True, 1.0)
+        l = logits_of(T, E, "fp32", 2)
+        l[1::2] = 0.5
+        l[3, E // 2:] = 0.25
+        bias = None
+        if with_bias:
+            bias = bias_of(E, "sigmoid")
+            bias[E // 4:] = 0.125
+        rows = slice(0, 400)
+        h = MoESelect(T, E, k, **opt)
+        idx, w = h.forward(l, bias)
+        ri, _ = os_.forward(f64(l[rows]), None if bias is None else f64(bias), k, **opt)
+        assert np.array_equal(idx[rows].cpu().numpy(), ri)
+        assert torch.equal(idx[5::2], idx[5].expand_as(idx[5::2]))
