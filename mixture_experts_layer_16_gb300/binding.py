@@ -504,9 +504,14 @@ def _rows(t) -> Tuple[int, int]:
 def mm_moe_resnorm_forward(shape: ResNorm, x, f, post_weight, gate, pre_weight, out, n, rstd_f,
                            rstd_out, stream=None) -> None:
     """x, f, out and n [T, H] with rows stride(0) elements apart."""
+    # (written out: short calls are bound by the host)
     st = lib().mm_moe_resnorm_forward(
-        shape, *_rows(x), *_rows(f), _ptr(post_weight), _ptr(gate), _ptr(pre_weight), *_rows(out),
-        *_rows(n), _ptr(rstd_f), _ptr(rstd_out),
+        shape, x.data_ptr(), x.stride(0), 0 if f is None else f.data_ptr(),
+        0 if f is None else f.stride(0), 0 if post_weight is None else post_weight.data_ptr(),
+        0 if gate is None else gate.data_ptr(), 0 if pre_weight is None else pre_weight.data_ptr(),
+        out.data_ptr(), out.stride(0), 0 if n is None else n.data_ptr(),
+        0 if n is None else n.stride(0), 0 if rstd_f is None else rstd_f.data_ptr(),
+        0 if rstd_out is None else rstd_out.data_ptr(),
         stream if type(stream) is int else _stream(stream))
     if st:
         _check("mm_moe_resnorm_forward", st)

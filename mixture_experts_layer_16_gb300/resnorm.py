@@ -56,16 +56,17 @@ class MoEResidualNorm:
         if not _plain(t, self._rows, dtype, self._where):
             _need_rows(t, name, self._rows, dtype, self.device)
 
-    def _check_params(self, has_f, post_weight, gate, pre_weight, prefix=""):
-        for t, name, has, shape in (
-                (post_weight, "post_weight", self.post and has_f, self._cols),
-                (gate, "gate", self.gate is not None and has_f, self._gates),
-                (pre_weight, "pre_weight", self.pre, self._cols)):
-            if not has:
-                if t is not None:
-                    raise ValueError(f"{prefix}{name}: this call has none")
-            elif not _plain(t, shape, self.param_dtype, self._where):
-                _need(t, prefix + name, shape, self.param_dtype, self.device)
+    def _check_param(self, t, name, has, shape):
+        if not has:
+            if t is not None:
+                raise ValueError(f"{name}: this call has none")
+        elif not _plain(t, shape, self.param_dtype, self._where):
+            _need(t, name, shape, self.param_dtype, self.device)
+
+    def _check_params(self, has_f, post_weight, gate, pre_weight):
+        self._check_param(post_weight, "post_weight", self.post and has_f, self._cols)
+        self._check_param(gate, "gate", self.gate is not None and has_f, self._gates)
+        self._check_param(pre_weight, "pre_weight", self.pre, self._cols)
 
     def forward(self, x, f=None, post_weight=None, gate=None, pre_weight=None,
                 out: Optional[torch.Tensor] = None, stream=None
