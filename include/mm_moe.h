@@ -574,9 +574,9 @@ typedef struct {
   int32_t reserved;
 } mm_moe_adamw_tensor;
 
-/*   tensors  host array of n_tensors (0 .. MM_MOE_MAX_GRADS) entries, read during the call; no
- *            two parameters, masters or gradients share memory.  The same tensors in the same
- *            order at every step
+/*   tensors  host array of n_tensors (0 .. MM_MOE_MAX_GRADS) entries, read during the call; a
+ *            parameter or master that shares memory with another one or with a gradient is
+ *            refused.  The same tensors in the same order at every step
  *   m, v     moments of all tensors, one after the other, each beginning on a multiple of 32
  *            elements (zero behind its last one): 32-byte aligned.  m_scale, v_scale: a byte
  *            for every 32 elements (8-bit states; else NULL)

@@ -26,8 +26,10 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <new>
 #include <type_traits>
 
 #include "internal.h"
@@ -215,7 +217,9 @@ __device__ __forceinline__ void decode8(uint2 q, float scale, float (&f)[8], M8)
 __device__ __forceinline__ void decode8(uint2 q, float scale, float (&f)[8], V8) {
   const uint32_t w[2] = {q.x, q.y};
   // (a code's byte alone, at the top)
-  const auto bits = [&](int k) { return __uint_as_float(__byte_perm(w[k / 4], 0, (k & 3) << 12 | 0x444) >> 4); };
+  const auto bits = [&](int k) {
+    return __uint_as_float(__byte_perm(w[k / 4], 0, (k & 3) << 12 | 0x444) >> 4);
+  };
 #pragma unroll
   for (int k = 0; k < 8; k += 2) {
     const f2 t = f2_mul(f2_make(bits(k), bits(k + 1)), f2_make(0x1p112f, 0x1p112f));
@@ -438,7 +442,7 @@ static bool tensors_ok(const mm_moe_adamw_tensor* p, int64_t n, int64_t* element
   for (int64_t i = 0; i < n; ++i) {
     const mm_moe_adamw_tensor& t = p[i];
     if (!dtype_ok(t.dtype) || (t.grad_dtype != t.dtype && t.grad_dtype != MM_MOE_DT_F32) ||
-        t.numel < 0 || t.numel > AW_MAX_TOTAL || !(fabsf(t.weight_decay) <= 3.4028235e38f) ||
+        t.numel < 0 || t.numel > AW_MAX_TOTAL || !(std::fabs(t.weight_decay) <= FLT_MAX) ||
         (total += t.numel) > AW_MAX_TOTAL)
       return false;
     if (t.numel == 0) continue;
@@ -446,6 +450,42 @@ static bool tensors_ok(const mm_moe_adamw_tensor* p, int64_t n, int64_t* element
     if (t.master != nullptr && (t.dtype == MM_MOE_DT_F32 || !al(t.master, 4))) return false;
   }
   return true;
+}
+
+// A range of memory that the step reads, or also writes.
+struct Span {
+  uintptr_t begin, end;
+  bool written;
+};
+// Whether what is written lies apart from all the rest (two gradients may be the same).
+static bool apart(Span* s, int64_t n) {
+  std::sort(s, s + n, [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  uintptr_t any = 0, written = 0;  // where those in front end
+  for (int64_t i = 0; i < n; ++i) {
+    if (s[i].begin < (s[i].written ? any : written)) return false;
+    any = std::max(any, s[i].end);
+    if (s[i].written) written = std::max(written, s[i].end);
+  }
+  return true;
+}
+static mm_moe_status check_apart(const mm_moe_adamw_tensor* p, int64_t n) {
+  Span few[3 * AW_FEW];
+  Span* const s = n <= AW_FEW ? few : new (std::nothrow) Span[3 * n];
+  if (s == nullptr) return MM_MOE_ECUDA;
+  int64_t k = 0;
+  const auto add = [&](const void* at, size_t bytes, bool written) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(at);
+    if (bytes != 0 && at != nullptr) s[k++] = Span{a, a + bytes, written};
+  };
+  for (int64_t i = 0; i < n; ++i) {
+    const mm_moe_adamw_tensor& t = p[i];
+    add(t.param, t.numel * dtype_bytes(t.dtype), true);
+    add(t.master, t.numel * 4, true);
+    add(t.grad, t.numel * dtype_bytes(t.grad_dtype), false);
+  }
+  const bool ok = apart(s, k);
+  if (s != few) delete[] s;
+  return ok ? MM_MOE_OK : MM_MOE_EINVAL;
 }
 
 template <int N>
@@ -497,17 +537,19 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_adamw_step(
     uint8_t* m_scale, void* v, uint8_t* v_scale, void* counter, double lr, const float* lr_dev,
     const float* norm, void* stream) {
   if (opt == nullptr || !(opt->beta1 >= 0.0 && opt->beta1 < 1.0) ||
-      !(opt->beta2 >= 0.0 && opt->beta2 < 1.0) || !(static_cast<float>(opt->eps) >= 1.17549435e-38f) || !std::isfinite(opt->eps) ||
+      !(opt->beta2 >= 0.0 && opt->beta2 < 1.0) || !(opt->eps >= FLT_MIN && opt->eps <= FLT_MAX) ||
       !(opt->max_norm >= 0.f) || !(opt->clip_eps >= 0.f) || opt->states < 0 || opt->states > 1 ||
-      !std::isfinite(lr))
+      !(std::fabs(lr) <= FLT_MAX))
     return MM_MOE_EINVAL;
   int64_t elements;
   if (!tensors_ok(tensors, n_tensors, &elements)) return MM_MOE_EINVAL;
   const bool bits8 = opt->states == MM_MOE_STATES_8BIT;
   if ((elements > 0 && (!al(m, 32) || !al(v, 32) || (bits8 && (!m_scale || !v_scale)))) ||
-      !al(counter, 16) ||
-      (norm != nullptr && !al(norm, 4)) || (lr_dev != nullptr && !al(lr_dev, 4)))
+      !al(counter, 16) || (norm != nullptr && !al(norm, 4)) ||
+      (lr_dev != nullptr && !al(lr_dev, 4)))
     return MM_MOE_EINVAL;
+  const mm_moe_status meet = check_apart(tensors, n_tensors);
+  if (meet != MM_MOE_OK) return meet;
   const int sms = std::min(152, sm_count_103());
   if (sms == 0) return MM_MOE_ENOTSUP;
   int launches = 0;

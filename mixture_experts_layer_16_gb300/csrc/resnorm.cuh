@@ -302,9 +302,6 @@ __device__ __forceinline__ void put_planes(const Cols<NU, 8>& c, uint32_t planes
       sts16_f2(at + 3 * plane, w[4 * i + 2], w[4 * i + 3]);
     }
 }
-template <int NU>
-__device__ __forceinline__ void put_planes(const Cols<NU, 1>&, uint32_t, uint32_t,
-                                           const f2 (&)[NU / 2], const f2 (&)[NU / 2]) {}
 // Piece i's values of the two planes from `planes` on (single columns: from the registers).
 template <int NU, int N>
 __device__ __forceinline__ void get_plane(const Cols<NU, 8>& c, uint32_t planes, uint32_t plane, int i,

@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(SEL_THREADS) select_bwd_kernel(
     d = a.scale * q * (g - sum_of<W>(mine ? g * q : 0.f));
   }
   // the chosen experts' values, an expert that is there twice by its first lane
-  const uint32_t same = __match_any_sync(FULL, mine ? sub << 16 | e : -1 - static_cast<int>(threadIdx.x & 31));
+  const int none = -1 - static_cast<int>(threadIdx.x & 31);
+  const uint32_t same = __match_any_sync(FULL, mine ? sub << 16 | e : none);
   float sum = d;
   if (__any_sync(FULL, mine && (same & (same - 1)) != 0)) {
     sum = 0.f;

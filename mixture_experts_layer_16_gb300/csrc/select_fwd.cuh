@@ -16,9 +16,11 @@
 // do not depend on how a kernel rounds.  Without a bias the keys are the logits as they are.
 //
 // 131072 x 256 fp32: 73 us with a bias and four of eight groups, 60 without groups, 47 without a bias
-// (the row's bytes take 20): 350 instructions a token, issued in half of the cycles, the ALU pipe
-// (comparisons, selections) for 40% of them.  By rounds of a warp's largest head over sorted
-// lanes, a warp a token, it took 139; with 16 lanes a token 98.
+// (the row's bytes take 20): 410 instructions a token, issued in 64% of the cycles, the ALU pipe
+// (comparisons, selections) busy in 46%.  By rounds of a warp's largest head over sorted
+// lanes, a warp a token, it took 139; with 16 lanes a token 98; with the next row on its way meanwhile 87
+// (more shared memory, so less L1), in one CTA an SM less 73.  Up to 16 experts without groups have a kernel
+// of their own below.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -147,3 +147,15 @@ def test_random_bits_are_even():
     assert abs(np.corrcoef(m[1:], m[:-1])[0, 1]) < 6 / 1024
     n = oa.random16(3, 18, 2, np.arange(1 << 20))[0]
     assert abs(np.corrcoef(m, n)[0, 1]) < 6 / 1024
+
+
+def test_overlap(lib):
+    """What is written lies apart from all the rest, in part too; two gradients may be the same."""
+    a, b = dict(GOOD), dict(GOOD, param=P[6], master=P[7], grad=P[8])
+    for bad in (dict(param=P[0]), dict(param=P[0] + 18), dict(param=P[1] + 38), dict(master=P[1] - 36),
+                dict(master=P[0] + 16), dict(grad=P[0] + 18), dict(grad=P[1] - 18),
+                dict(param=P[2] + 18), dict(master=P[8] + 16), dict(param=P[7] - 18)):
+        assert call(lib, (a, {**b, **bad})) == EI, bad
+        many = [dict(GOOD, numel=0)] * 40                 # (more than a short list)
+        assert call(lib, (a, *many, {**b, **bad})) == EI, bad
+    assert call(lib, lr=1e300) == EI

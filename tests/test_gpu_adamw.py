@@ -349,3 +349,20 @@ def test_on_another_stream():
     b.step(p2, grads, 1e-3, m2, stream=s)
     s.synchronize()
     assert torch.equal(params[0], p2[0]) and torch.equal(a.m, b.m)
+
+
+def test_side_by_side():
+    """Parts of one buffer next to each other, the same gradient for both: as tensors of their own."""
+    p, g, w = make((1001, 1001), "bf16", "bf16", True, 9)
+    out = []
+    for shared in (False, True):
+        if shared:
+            flat = torch.cat(p)
+            ps = [flat[:1001], flat[1001:]]
+        else:
+            ps = [t.clone() for t in p]
+        ws = [t.clone() for t in w]
+        o = MoEAdamW(ps, BETAS, EPS, 0.1)
+        o.step(ps, [g[0], g[0] if shared else g[0].clone()], 1e-3, ws)
+        out.append([t.clone() for t in (*ps, *ws, o.m, o.v)])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
