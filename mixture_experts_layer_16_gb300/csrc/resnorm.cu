@@ -165,9 +165,9 @@ __global__ void __launch_bounds__(LOOP_THREADS) resnorm_fwd_loop_kernel(const Fw
   pdl_wait();
   pdl_trigger();
   const float inv = 1.f / static_cast<float>(a.H);
-  const bool has_f = a.f.p != nullptr;
+  const bool has_f = a.f.p != nullptr, whole = loop_whole(a.w_post, a.gate_c, a.w_pre);
   for (int64_t t = blockIdx.x; t < a.T_; t += gridDim.x) {
-    float k = a.scale * (a.gate_t != nullptr ? param<T>(a.gate_t, a.p32, t) : 1.f);
+    float k = a.gate_t != nullptr ? param<T>(a.gate_t, a.p32, t) : 1.f;
     if (has_f && a.w_post != nullptr) {
       float ss = 0.f;
       for (int i = threadIdx.x * U; i < a.H; i += LOOP_THREADS * U) {
@@ -183,15 +183,11 @@ __global__ void __launch_bounds__(LOOP_THREADS) resnorm_fwd_loop_kernel(const Fw
     const auto values = [&](int i, float (&x)[U]) {
       loop_get<R, U>(a.x.row(t) + i, x);
       if (!has_f) return;
-      float f[U];
+      float f[U], cf[U];
       loop_get<T, U>(a.f.row(t) + i, f);
+      loop_coef<T, U>(a.w_post, a.gate_c, a.p32, whole, a.scale, i, cf);
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
-        float cf = k;
-        if (a.w_post != nullptr) cf *= param<T>(a.w_post, a.p32, i + j);
-        if (a.gate_c != nullptr) cf *= param<T>(a.gate_c, a.p32, i + j);
-        x[j] = fmaf(cf, f[j], x[j]);
-      }
+      for (int j = 0; j < U; ++j) x[j] = fmaf(cf[j] * k, f[j], x[j]);
     };
     float ro = 0.f;
     if (a.n.p != nullptr) {
@@ -211,8 +207,10 @@ __global__ void __launch_bounds__(LOOP_THREADS) resnorm_fwd_loop_kernel(const Fw
       values(i, x);
       if (has_f) put_unit<R, U>(a.out.row(t) + i, x);
       if (a.n.p != nullptr) {
+        float w[U];
+        loop_params<T, U>(a.w_pre, a.p32, whole, i, w);
 #pragma unroll
-        for (int j = 0; j < U; ++j) x[j] *= ro * param<T>(a.w_pre, a.p32, i + j);
+        for (int j = 0; j < U; ++j) x[j] *= ro * w[j];
         put_unit<T, U>(a.n.row(t) + i, x);
       }
     }

@@ -266,6 +266,42 @@ __device__ __forceinline__ float param(const void* p, bool p32, int64_t i) {
   return p32 ? __ldg(static_cast<const float*>(p) + i) : to_f32(static_cast<const T*>(p)[i]);
 }
 
+// Parameters of columns [i, i + U) (`whole`: in 16-byte accesses).
+template <typename T, int U>
+__device__ __forceinline__ void loop_params(const void* p, bool p32, bool whole, int i, float (&f)[U]) {
+  if (U == 8 && whole) {
+    if (p32)
+      loop_get<float, U>(static_cast<const float*>(p) + i, f);
+    else
+      loop_get<T, U>(static_cast<const T*>(p) + i, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < U; ++j) f[j] = param<T>(p, p32, i + j);
+  }
+}
+__device__ __forceinline__ bool loop_whole(const void* a, const void* b, const void* c) {
+  return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |
+           reinterpret_cast<uintptr_t>(c)) & 15) == 0;
+}
+// c = scale [gate_c] [w_post] there
+template <typename T, int U>
+__device__ __forceinline__ void loop_coef(const void* w_post, const void* gate_c, bool p32, bool whole,
+                                          float scale, int i, float (&c)[U]) {
+  float p[U];
+#pragma unroll
+  for (int j = 0; j < U; ++j) c[j] = scale;
+  if (w_post != nullptr) {
+    loop_params<T, U>(w_post, p32, whole, i, p);
+#pragma unroll
+    for (int j = 0; j < U; ++j) c[j] *= p[j];
+  }
+  if (gate_c != nullptr) {
+    loop_params<T, U>(gate_c, p32, whole, i, p);
+#pragma unroll
+    for (int j = 0; j < U; ++j) c[j] *= p[j];
+  }
+}
+
 // c = scale [gate_c] [w_post] of the thread's columns
 template <typename T, int NU, int U>
 __device__ __forceinline__ void load_coef(const Cols<NU, U>& c, const void* w_post,

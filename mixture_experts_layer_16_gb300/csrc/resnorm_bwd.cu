@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(LOOP_THREADS) resnorm_dx_loop_kernel(const Bwd
   pdl_trigger();
   const float inv = 1.f / static_cast<float>(a.H);
   const bool pre = a.dn.p != nullptr, has_f = a.f.p != nullptr, post = a.w_post != nullptr;
+  const bool whole = loop_whole(a.w_post, a.gate_c, a.w_pre);
   for (int64_t t = blockIdx.x; t < a.T_; t += gridDim.x) {
     const float gt = a.gate_t != nullptr ? param<T>(a.gate_t, a.p32, t) : 1.f;
     const float rf = post ? __ldg(a.rstd_f + t) : 1.f;
@@ -255,21 +256,16 @@ __global__ void __launch_bounds__(LOOP_THREADS) resnorm_dx_loop_kernel(const Bwd
       if (pre) {
         loop_get<R, U>(a.out.row(t) + i, oh);
         loop_get<T, U>(a.dn.row(t) + i, v);
+        float w[U];
+        loop_params<T, U>(a.w_pre, a.p32, whole, i, w);
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-          oh[j] *= ro;
-          v[j] *= param<T>(a.w_pre, a.p32, i + j);
-        }
+        for (int j = 0; j < U; ++j) oh[j] *= ro, v[j] *= w[j];
       }
       if (has_f) {
         loop_get<T, U>(a.f.row(t) + i, fh);
+        loop_coef<T, U>(a.w_post, a.gate_c, a.p32, whole, a.scale, i, cf);
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-          fh[j] *= rf;
-          cf[j] = a.scale;
-          if (post) cf[j] *= param<T>(a.w_post, a.p32, i + j);
-          if (a.gate_c != nullptr) cf[j] *= param<T>(a.gate_c, a.p32, i + j);
-        }
+        for (int j = 0; j < U; ++j) fh[j] *= rf;
       }
     };
     float s1 = 0.f, s2 = 0.f, s3 = 0.f;
@@ -312,36 +308,46 @@ __global__ void __launch_bounds__(LOOP_THREADS) resnorm_dx_loop_kernel(const Bwd
   }
 }
 
-// Column sums of one range of rows per blockIdx.y: a thread owns a column.
-template <typename T, typename R>
+// Column sums of one range of rows per blockIdx.y: a thread owns U columns.
+template <typename T, typename R, int U>
 __global__ void __launch_bounds__(256) resnorm_cols_loop_kernel(const BwdOps<T, R> a, int rows) {
   pdl_wait();
   pdl_trigger();
-  const int i = blockIdx.x * 256 + threadIdx.x;
+  const int i = (blockIdx.x * 256 + threadIdx.x) * U;
   if (i >= a.H) return;
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * rows;
   const int64_t t1 = min(static_cast<int64_t>(a.T_), t0 + rows);
   const bool pre = a.dn.p != nullptr, post = a.w_post != nullptr;
-  const float w = pre ? param<T>(a.w_pre, a.p32, i) : 0.f;
-  float K = 0.f, dw = 0.f;
+  float w[U] = {}, K[U] = {}, dw[U] = {};
+  if (pre) loop_params<T, U>(a.w_pre, a.p32, loop_whole(a.w_pre, nullptr, nullptr), i, w);
 #pragma unroll 2
   for (int64_t t = t0; t < t1; ++t) {
-    float d = a.dout.p != nullptr ? to_f32(a.dout.row(t)[i]) : 0.f;
+    float d[U] = {};
+    if (a.dout.p != nullptr) loop_get<R, U>(a.dout.row(t) + i, d);
     if (pre) {
-      const float ro = __ldg(a.rstd_out + t), oh = to_f32(a.out.row(t)[i]) * ro;
-      const float dn = to_f32(a.dn.row(t)[i]);
-      dw = fmaf(dn, oh, dw);
-      d = fmaf(ro, fmaf(-__ldcg(a.mean_ov + t), oh, w * dn), d);
+      const float ro = __ldg(a.rstd_out + t), m1 = __ldcg(a.mean_ov + t);
+      float oh[U], dn[U];
+      loop_get<R, U>(a.out.row(t) + i, oh);
+      loop_get<T, U>(a.dn.row(t) + i, dn);
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        oh[j] *= ro;
+        dw[j] = fmaf(dn[j], oh[j], dw[j]);
+        d[j] = fmaf(ro, fmaf(-m1, oh[j], w[j] * dn[j]), d[j]);
+      }
     }
     if (a.sums_f) {
       const float gt = a.gate_t != nullptr ? param<T>(a.gate_t, a.p32, t) : 1.f;
-      const float fh = to_f32(a.f.row(t)[i]) * (post ? __ldg(a.rstd_f + t) : 1.f);
-      K = fmaf(fh, gt * d, K);
+      const float rf = post ? __ldg(a.rstd_f + t) : 1.f;
+      float f[U];
+      loop_get<T, U>(a.f.row(t) + i, f);
+#pragma unroll
+      for (int j = 0; j < U; ++j) K[j] = fmaf(f[j] * rf, gt * d[j], K[j]);
     }
   }
   float* const p = a.part + static_cast<int64_t>(blockIdx.y) * 2 * a.H + i;
-  p[0] = K;
-  p[a.H] = dw;
+  put_unit<float, U>(p, K);
+  put_unit<float, U>(p + a.H, dw);
 }
 
 // The parameters' gradients from n partial rows: 16 warps take every 16th row of 32 columns
@@ -503,13 +509,14 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_resnorm_backward(
                    dim3(std::min(T_, c.num_sms * 4)), dim3(LOOP_THREADS), 0, a);
     prof_end(c, K_RESNORM_BWD);
     if (err != cudaSuccess || (!sums_f && !pre)) return err;
-    const int cols = (H + 255) / 256;
+    const int cols = ((even ? H / 8 : H) + 255) / 256;
     const int want = std::min(norm_parts(T_), std::max(1, c.num_sms * 8 / cols));
     const int rows = div_up(T_, want);
     parts = div_up(T_, rows);
     prof_begin(c, K_RESNORM_BWD);
-    err = launch_k(c.stream, resnorm_cols_loop_kernel<T, R>, dim3(cols, parts), dim3(256), 0, a,
-                   rows);
+    err = launch_k(c.stream,
+                   even ? resnorm_cols_loop_kernel<T, R, 8> : resnorm_cols_loop_kernel<T, R, 1>,
+                   dim3(cols, parts), dim3(256), 0, a, rows);
     prof_end(c, K_RESNORM_BWD);
     return err;
   });
