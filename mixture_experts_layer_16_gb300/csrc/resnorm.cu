@@ -31,16 +31,22 @@ template <typename T, typename R, int NU>
 constexpr int rn_fwd_steps =
     std::max(1, std::min(4, RN_SMEM / (RN_THREADS * rn_fwd_bytes<T, R, NU, 8>)));
 
-// us at 16384 x 2048: 46.7 in bf16 (0.85 of the copy rate), 62.0 with an fp32 residual stream (0.96; its
-// rows in 16-byte halves of sectors, and not on their way to L2 a row ahead: 80).  Two CTAs an SM with half
-// of the ring and the parameters in shared memory: 49.9 and 71.6.
-template <typename T, typename R, int NU, int U>
+// JOINT (units of 8): the sum over the next row's f joins this row's over out, one barrier a row for two.
+// That takes a step of the ring's lead, and pays where rows span warps and the lead is long or the warps
+// are many (us at 16384 x 2048, without and with: bf16 47.8, 45.9; with an fp32 residual stream 67.2,
+// 72.4; 32768 x 512, a warp a row, 24.3, 25.0; 6000 x 4608 with an fp32 stream 67.8, 57.3; 4096 x 8192
+// bf16 53.8, 45.4).
+// 16384 x 2048 in bf16 is at 0.86 of the copy rate, with an fp32 residual stream at 0.89 (62.0 to 67.2 us;
+// its rows in 16-byte halves of sectors, and not on their way to L2 a row ahead: 80).  Two CTAs an SM with
+// half of the ring and the parameters in shared memory: 49.9 and 71.6.
+template <typename T, typename R, int NU, int U, bool JOINT>
 __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel(const FwdOps<T, R> a) {
   constexpr int S = U == 8 ? rn_fwd_steps<T, R, NU> : 1;
-  using OF = Operand<T, NU, U, true>;
-  using OX = Operand<R, NU, U, true>;
+  using OF = Operand<T, NU, U, NU <= 8>;
+  using OX = Operand<R, NU, U, NU <= 8>;
   extern __shared__ __align__(16) unsigned char ring_bytes[];
-  __shared__ Sums<1> s_sum[2][RN_THREADS / 32];
+  static_assert(!JOINT || S >= 2);
+  __shared__ Sums<JOINT ? 2 : 1> s_sum[2][RN_THREADS / 32];
   const uint32_t piece = blockDim.x * 16, step_bytes = rn_fwd_bytes<T, R, NU, U> * blockDim.x;
   const uint32_t ring =
       static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)) + threadIdx.x * 16;
@@ -85,7 +91,30 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel
   int buf = 0;
   uint32_t st = ring, st_in = ring + (S - 1) * step_bytes;
   const uint32_t ring_end = ring + S * step_bytes;
-  if constexpr (U == 1) issue(0);
+  if constexpr (U == 1 && NU <= 8) issue(0);
+  const bool post = a.f.p != nullptr && a.w_post != nullptr;
+  const auto sum_f = [&](uint32_t at) {  // the thread's part of a row's sum over f
+    f2 s2 = 0;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+      if (c.has_piece(i)) {
+        f2 f[P];
+        of.get(at, piece, i, f);
+#pragma unroll
+        for (int k = 0; k < P; ++k) s2 = f2_fma(f[k], f[k], s2);
+      }
+    return f2_sum(s2);
+  };
+  float rf_n = 1.f;  // the next row's
+  if constexpr (JOINT) {
+    async_wait<S - 2>();
+    if (post) {
+      float ss[2] = {0.f, t < n ? sum_f(st) : 0.f};
+      group_sum<2>(ss, s_sum[buf], c.g, a.GT);
+      buf ^= 1;
+      rf_n = rsqrtf(fmaf(ss[1], inv, a.eps));
+    }
+  }
   for (; tw < n; t += step, tw += step) {
     of.turn();
     ox.turn();
@@ -93,23 +122,16 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel
     const bool live = t < n;
     float gt = gt_n;
     gate(t + step);
-    if constexpr (U == 8) async_wait<S - 1>();
+    if constexpr (U == 8 && !JOINT) async_wait<S - 1>();
     f2 o[NU * U / 2];
-    if (a.f.p != nullptr && a.w_post != nullptr) {
-      f2 s2 = 0;
-      if (live)
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i)
-          if (c.has_piece(i)) {
-            f2 f[P];
-            of.get(st, piece, i, f);
-#pragma unroll
-            for (int k = 0; k < P; ++k) s2 = f2_fma(f[k], f[k], s2);
-          }
-      float ss[1] = {f2_sum(s2)};
-      group_sum<1>(ss, s_sum[buf], c.g, a.GT);
-      buf ^= 1;
-      const float rf = rsqrtf(fmaf(ss[0], inv, a.eps));
+    if (post) {
+      float rf = rf_n;
+      if constexpr (!JOINT) {
+        float ss[1] = {live ? sum_f(st) : 0.f};
+        group_sum<1>(ss, s_sum[buf], c.g, a.GT);
+        buf ^= 1;
+        rf = rsqrtf(fmaf(ss[0], inv, a.eps));
+      }
       if (live && c.j == 0) a.rstd_f[t] = rf;
       gt *= rf;
     }
@@ -134,11 +156,22 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel
             s2 = f2_fma(x[k], x[k], s2);
           }
         }
-    if (a.n.p != nullptr) {
-      float ss[1] = {f2_sum(s2)};
+    const uint32_t st_next = st + step_bytes == ring_end ? ring : st + step_bytes;
+    float so = f2_sum(s2);
+    if constexpr (JOINT) {
+      async_wait<S - 2>();
+      float ss[2] = {so, post && t + step < n ? sum_f(st_next) : 0.f};
+      if (post || a.n.p != nullptr) group_sum<2>(ss, s_sum[buf], c.g, a.GT);
+      so = ss[0];
+      rf_n = rsqrtf(fmaf(ss[1], inv, a.eps));
+    } else if (a.n.p != nullptr) {
+      float ss[1] = {so};
       group_sum<1>(ss, s_sum[buf], c.g, a.GT);
-      buf ^= 1;
-      const float ro = rsqrtf(fmaf(ss[0], inv, a.eps));
+      so = ss[0];
+    }
+    buf ^= 1;
+    if (a.n.p != nullptr) {
+      const float ro = rsqrtf(fmaf(so, inv, a.eps));
       if (live) {
         if (c.j == 0) a.rstd_out[t] = ro;
 #pragma unroll
@@ -152,8 +185,7 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel
       }
     }
     st_in = st;
-    st += step_bytes;
-    if (st == ring_end) st = ring;
+    st = st_next;
   }
   if constexpr (U == 8) async_wait<0>();
 }
@@ -220,11 +252,13 @@ __global__ void __launch_bounds__(LOOP_THREADS) resnorm_fwd_loop_kernel(const Fw
 template <typename T, typename R, int NU, int U>
 static cudaError_t fwd_launch(const Ctx& c, FwdOps<T, R> a) {
   a.GT = rn_group_threads<NU, U>(a.H);
+  constexpr bool MAY = U == 8 && NU > 1;  // (NU = 1: a row or two a group)
+  const bool joint = MAY && a.GT > (sizeof(R) == 2 ? 32 : 128);
   const NormGrid g = rn_grid(a.GT, a.T_, c.num_sms * rn_ctas<NU, U>);
   const int nt = g.GT * g.groups;
   const size_t smem =
       U == 8 ? static_cast<size_t>(rn_fwd_steps<T, R, NU>) * nt * rn_fwd_bytes<T, R, NU, U> : 0;
-  auto* kern = resnorm_fwd_kernel<T, R, NU, U>;
+  auto* kern = joint ? resnorm_fwd_kernel<T, R, NU, U, MAY> : resnorm_fwd_kernel<T, R, NU, U, false>;
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
   return launch_k(c.stream, kern, dim3(g.ctas), dim3(nt), smem, a);
@@ -297,6 +331,7 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_resnorm_forward(
     }
     if (!even && H <= 4 * RN_THREADS) return fwd_launch<T, R, 4, 1>(c, a);
     if (!even && H <= 8 * RN_THREADS) return fwd_launch<T, R, 8, 1>(c, a);
+    if (!even && H <= 16 * RN_THREADS) return fwd_launch<T, R, 16, 1>(c, a);
     return launch_k(c.stream,
                     even ? resnorm_fwd_loop_kernel<T, R, 8> : resnorm_fwd_loop_kernel<T, R, 1>,
                     dim3(std::min(T_, c.num_sms * 4)), dim3(LOOP_THREADS), 0, a);

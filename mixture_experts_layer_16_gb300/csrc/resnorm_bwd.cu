@@ -498,9 +498,10 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_resnorm_backward(
       prof_end(c, K_RESNORM_BWD);
       return err;
     }
-    if (!even && H <= 8 * RN_THREADS) {
-      err = H <= 4 * RN_THREADS ? bwd_launch<T, R, 4, 1>(c, a, &parts)
-                                : bwd_launch<T, R, 8, 1>(c, a, &parts);
+    if (!even && H <= 16 * RN_THREADS) {
+      err = H <= 4 * RN_THREADS   ? bwd_launch<T, R, 4, 1>(c, a, &parts)
+            : H <= 8 * RN_THREADS ? bwd_launch<T, R, 8, 1>(c, a, &parts)
+                                  : bwd_launch<T, R, 16, 1>(c, a, &parts);
       prof_end(c, K_RESNORM_BWD);
       return err;
     }

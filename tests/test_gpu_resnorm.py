@@ -358,3 +358,12 @@ def test_load_stats_and_refusals():
     a.forward(d["x"], pre_weight=d["pre_weight"])
     with pytest.raises(ValueError):      # that forward had no f
         a.backward(d["dout"], d["dn"], out, d["f"], **p)
+
+
+@pytest.mark.parametrize("T,H", [(1500, 1024), (1101, 2048), (1000, 2304), (700, 4104), (471, 8192),
+                                 (461, 7003), (330, 5000)])
+@pytest.mark.parametrize("types", TYPES)
+def test_many_rows(T, H, types):
+    """Three rows and more to every group of threads, groups without a last row among them."""
+    for form in (FORMS[0], FORMS[3], FORMS[7]):
+        go(T, H, types, form)
