@@ -22,6 +22,7 @@ struct FwdOps {
   float scale, eps;
   float *rstd_f, *rstd_out;
   int T_, H, GT;
+  int steps, step_bytes;  // of the ring of single columns
 };
 
 // Bytes of a thread's share of a row in the ring.
@@ -41,29 +42,29 @@ constexpr int rn_fwd_steps =
 // half of the ring and the parameters in shared memory: 49.9 and 71.6.
 template <typename T, typename R, int NU, int U, bool JOINT>
 __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel(const FwdOps<T, R> a) {
-  constexpr int S = U == 8 ? rn_fwd_steps<T, R, NU> : 1;
-  using OF = Operand<T, NU, U, NU <= 8>;
-  using OX = Operand<R, NU, U, NU <= 8>;
+  constexpr int S = U == 8 ? rn_fwd_steps<T, R, NU> : 0;
+  const int steps = U == 8 ? S : a.steps;
+  using OF = Operand<T, NU, U>;
+  using OX = Operand<R, NU, U>;
   extern __shared__ __align__(16) unsigned char ring_bytes[];
   static_assert(!JOINT || S >= 2);
   __shared__ Sums<JOINT ? 2 : 1> s_sum[2][RN_THREADS / 32];
-  const uint32_t piece = blockDim.x * 16, step_bytes = rn_fwd_bytes<T, R, NU, U> * blockDim.x;
-  const uint32_t ring =
-      static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)) + threadIdx.x * 16;
-  const uint32_t x_at = OF::BYTES * blockDim.x;
+  const uint32_t piece = blockDim.x * 16;
+  const uint32_t step_bytes = U == 8 ? rn_fwd_bytes<T, R, NU, U> * blockDim.x : a.step_bytes;
   pdl_wait();
   pdl_trigger();
   Cols<NU, U> c;
   c.init(a.GT, a.H);
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)) +
+                        (U == 8 ? threadIdx.x * 16 : c.g * (step_bytes / c.groups));
+  const uint32_t x_at = U == 8 ? OF::BYTES * blockDim.x : single_bytes(a.H, sizeof(T));
   const uint32_t n = a.T_, step = gridDim.x * c.groups;
   uint32_t t = blockIdx.x * c.groups + c.g, tw = c.first_of_warp(t), ta = t;
   const float inv = 1.f / static_cast<float>(a.H);
-  OF of;
-  OX ox;
   const auto issue = [&](uint32_t at) {
     if (ta < n) {
-      if (a.f.p != nullptr) of.issue(c, a.f.row(ta), at, piece);
-      ox.issue(c, a.x.row(ta), at + x_at, piece);
+      if (a.f.p != nullptr) OF::issue(c, a.f.row(ta), at, piece);
+      OX::issue(c, a.x.row(ta), at + x_at, piece);
     }
     if constexpr (U == 8) {
       if (rn_prefetch<R> && c.j == 0) {
@@ -75,10 +76,9 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel
       }
     }
     ta += step;
-    if constexpr (U == 8) async_commit();
+    async_commit();
   };
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(ring + i * step_bytes);
+  for (int i = 0; i < steps - 1; ++i) issue(ring + i * step_bytes);
   constexpr int P = Cols<NU, U>::P, PIECES = Cols<NU, U>::PIECES;
   f2 cf[NU * U / 2], w[NU * U / 2];
   if (a.f.p != nullptr) load_coef<T, NU, U>(c, a.w_post, a.gate_c, a.p32, a.scale, cf);
@@ -89,17 +89,17 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel
   };
   gate(t);
   int buf = 0;
-  uint32_t st = ring, st_in = ring + (S - 1) * step_bytes;
-  const uint32_t ring_end = ring + S * step_bytes;
-  if constexpr (U == 1 && NU <= 8) issue(0);
+  uint32_t st = ring, st_in = ring + (steps - 1) * step_bytes;
+  const uint32_t ring_end = ring + steps * step_bytes;
   const bool post = a.f.p != nullptr && a.w_post != nullptr;
-  const auto sum_f = [&](uint32_t at) {  // the thread's part of a row's sum over f
+  const auto sum_f = [&](uint32_t at, uint32_t q) {  // the thread's part of row q's sum over f
+    at = OF::found(at, a.f.row(q));
     f2 s2 = 0;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i)
       if (c.has_piece(i)) {
         f2 f[P];
-        of.get(at, piece, i, f);
+        OF::get(c, at, piece, i, f);
 #pragma unroll
         for (int k = 0; k < P; ++k) s2 = f2_fma(f[k], f[k], s2);
       }
@@ -109,16 +109,17 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel
   if constexpr (JOINT) {
     async_wait<S - 2>();
     if (post) {
-      float ss[2] = {0.f, t < n ? sum_f(st) : 0.f};
+      float ss[2] = {0.f, t < n ? sum_f(st, t) : 0.f};
       group_sum<2>(ss, s_sum[buf], c.g, a.GT);
       buf ^= 1;
       rf_n = rsqrtf(fmaf(ss[1], inv, a.eps));
     }
   }
   for (; tw < n; t += step, tw += step) {
-    of.turn();
-    ox.turn();
-    issue(st_in);
+    if constexpr (U == 8)
+      issue(st_in);
+    else
+      single_turn(c.g, a.GT, steps, [&] { issue(st_in); });
     const bool live = t < n;
     float gt = gt_n;
     gate(t + step);
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel
     if (post) {
       float rf = rf_n;
       if constexpr (!JOINT) {
-        float ss[1] = {live ? sum_f(st) : 0.f};
+        float ss[1] = {live ? sum_f(st, t) : 0.f};
         group_sum<1>(ss, s_sum[buf], c.g, a.GT);
         buf ^= 1;
         rf = rsqrtf(fmaf(ss[0], inv, a.eps));
@@ -137,15 +138,16 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel
     }
     f2 s2 = 0;
     const f2 gt2 = f2_of(gt);
+    const uint32_t at_x = OX::found(st + x_at, a.x.row(t)), at_f = OF::found(st, a.f.row(t));
     if (live)
 #pragma unroll
       for (int i = 0; i < PIECES; ++i)
         if (c.has_piece(i)) {
           f2 x[P];
-          ox.get(st + x_at, piece, i, x);
+          OX::get(c, at_x, piece, i, x);
           if (a.f.p != nullptr) {
             f2 f[P];
-            of.get(st, piece, i, f);
+            OF::get(c, at_f, piece, i, f);
 #pragma unroll
             for (int k = 0; k < P; ++k) x[k] = f2_fma(f2_mul(cf[i * P + k], gt2), f[k], x[k]);
             put_piece<R>(c, a.out.row(t), i, x);
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel
     float so = f2_sum(s2);
     if constexpr (JOINT) {
       async_wait<S - 2>();
-      float ss[2] = {so, post && t + step < n ? sum_f(st_next) : 0.f};
+      float ss[2] = {so, post && t + step < n ? sum_f(st_next, t + step) : 0.f};
       if (post || a.n.p != nullptr) group_sum<2>(ss, s_sum[buf], c.g, a.GT);
       so = ss[0];
       rf_n = rsqrtf(fmaf(ss[1], inv, a.eps));
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel
     st_in = st;
     st = st_next;
   }
-  if constexpr (U == 8) async_wait<0>();
+  async_wait<0>();
 }
 
 // Any width: a CTA a row, read up to three times (from L1 and L2).
@@ -256,8 +258,14 @@ static cudaError_t fwd_launch(const Ctx& c, FwdOps<T, R> a) {
   const bool joint = MAY && a.GT > (sizeof(R) == 2 ? 32 : 128);
   const NormGrid g = rn_grid(a.GT, a.T_, c.num_sms * rn_ctas<NU, U>);
   const int nt = g.GT * g.groups;
-  const size_t smem =
-      U == 8 ? static_cast<size_t>(rn_fwd_steps<T, R, NU>) * nt * rn_fwd_bytes<T, R, NU, U> : 0;
+  size_t smem;
+  if (U == 8) {
+    smem = static_cast<size_t>(rn_fwd_steps<T, R, NU>) * nt * rn_fwd_bytes<T, R, NU, U>;
+  } else {
+    a.step_bytes = g.groups * (single_bytes(a.H, sizeof(T)) + single_bytes(a.H, sizeof(R)));
+    a.steps = single_steps<NU>(a.step_bytes);
+    smem = static_cast<size_t>(a.steps) * a.step_bytes;
+  }
   auto* kern = joint ? resnorm_fwd_kernel<T, R, NU, U, MAY> : resnorm_fwd_kernel<T, R, NU, U, false>;
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;

@@ -21,6 +21,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstring>
 #include <type_traits>
 
 #include "internal.h"
@@ -34,13 +35,15 @@ constexpr int RN_SMEM = 230400;  // bytes of the ring and the parameters at most
 
 // A row is cut into units of U = 8 columns (16 bytes of 16-bit types, 32 of fp32), dealt out to
 // the threads of a group in turn, NU to each; rows on no 16-byte boundary, or of a width that is no
-// multiple of 8, into single columns (U = 1).  Units of 8 come through a ring in shared memory by
-// cp.async, S - 1 rows ahead; a thread reads only what it copied itself.  Single columns are
-// loaded into registers.  A thread's values are pairs for the packed fp32 arithmetic, in PIECES (its units,
-// or all its single columns) of P pairs.
+// multiple of 8, into single columns (U = 1).  Rows come through a ring in shared memory by
+// cp.async, S - 1 rows ahead.  Of units of 8 a thread reads only what it copied itself; of single columns a
+// group copies its row in the 16-byte pieces of memory that it touches, and meets at a barrier before
+// it reads it (9000 x 3001 bf16 forward 113 us, backward 129; loaded into registers a row ahead, 2 bytes at
+// a time, 146 and 226).  A thread's values are pairs for the packed fp32 arithmetic, in PIECES (its units,
+// or four single columns, so that few registers hold the operands) of P pairs.
 template <int NU, int U>
 struct Cols {
-  static constexpr int N = NU * U, PIECES = U == 8 ? NU : 1, P = N / PIECES / 2;
+  static constexpr int N = NU * U, PIECES = U == 8 ? NU : NU / 4, P = N / PIECES / 2;
   int GT, g, j, groups, H;
   __device__ __forceinline__ void init(int GT_, int H_) {
     GT = GT_;
@@ -55,7 +58,7 @@ struct Cols {
   }
   __device__ __forceinline__ int col(int i) const { return (j + i * GT) * U; }
   __device__ __forceinline__ bool has(int i) const { return col(i) < H; }
-  __device__ __forceinline__ bool has_piece(int i) const { return U == 1 || has(i); }
+  __device__ __forceinline__ bool has_piece(int i) const { return has(U == 8 ? i : i * 4); }
 };
 
 // Whether rows are sent for into L2 a row ahead of the ring: with an fp32 residual stream, whose ring is
@@ -85,16 +88,30 @@ __device__ __forceinline__ void sts16_f2(uint32_t a, f2 x, f2 y) {
 }
 __device__ __forceinline__ f2 f2_of(float v) { return f2_make(v, v); }
 
-// One row operand of type V on its way to the thread's registers.  AHEAD: single columns are loaded a
-// row ahead (the forward's; the backward has no registers for it: 56 us so, 67 ahead).
-template <typename V, int NU, int U, bool AHEAD = false>
+template <typename V>
+__device__ __forceinline__ float lds_one(uint32_t a) {
+  if constexpr (sizeof(V) == 4) {
+    float f;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(a) : "memory");
+    return f;
+  } else {
+    uint16_t h;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(a) : "memory");
+    V v;
+    memcpy(&v, &h, 2);
+    return to_f32(v);
+  }
+}
+// Bytes of the ring for one row in single columns: all the 16-byte pieces that it can touch.
+__host__ __device__ inline int single_bytes(int H, int size) { return (H * size + 30) / 16 * 16; }
+
+// One row operand of type V on its way to the thread's registers.
+template <typename V, int NU, int U>
 struct Operand {
   using C = Cols<NU, U>;
   static constexpr int PARTS = U == 8 ? 8 / VN<V> : 0;  // 16-byte pieces of a unit
   static constexpr int BYTES = PARTS * 16 * NU;         // of a thread's share of a row in the ring
-  float reg[U == 1 ? NU : 1];  // the row's values
-  V next[U == 1 && AHEAD ? NU : 1];
-  __device__ __forceinline__ void issue(const C& c, const V* row, uint32_t at, uint32_t piece) {
+  static __device__ __forceinline__ void issue(const C& c, const V* row, uint32_t at, uint32_t piece) {
     if constexpr (U == 8) {
 #pragma unroll
       for (int i = 0; i < NU; ++i)
@@ -109,25 +126,20 @@ struct Operand {
           }
         }
     } else {
-#pragma unroll
-      for (int i = 0; i < NU; ++i) {
-        const V v = c.has(i) ? row[c.col(i)] : from_f32<V>(0.f);
-        if constexpr (AHEAD)
-          next[i] = v;
-        else
-          reg[i] = to_f32(v);
-      }
+      const int head = reinterpret_cast<uintptr_t>(row) & 15;
+      const char* const from = reinterpret_cast<const char*>(row) - head;
+      const int bytes = head + c.H * static_cast<int>(sizeof(V));
+      for (int k = c.j * 16; k < bytes; k += c.GT * 16)
+        async_copy(at + k, from + k, min(16, bytes - k));  // (nothing behind the row's end)
     }
   }
-  // the row that is on its way becomes this one
-  __device__ __forceinline__ void turn() {
-    if constexpr (U == 1 && AHEAD) {
-#pragma unroll
-      for (int i = 0; i < NU; ++i) reg[i] = to_f32(next[i]);
-    }
+  // where a row at p is found that was sent for to `at`
+  static __device__ __forceinline__ uint32_t found(uint32_t at, const V* p) {
+    return U == 8 ? at : at + (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15);
   }
   // piece i's values (single columns: zero where there is none)
-  __device__ __forceinline__ void get(uint32_t at, uint32_t piece, int i, f2 (&f)[C::P]) const {
+  static __device__ __forceinline__ void get(const C& c, uint32_t at, uint32_t piece, int i,
+                                             f2 (&f)[C::P]) {
     if constexpr (U == 8) {
 #pragma unroll
       for (int h = 0; h < PARTS; ++h) {
@@ -137,11 +149,42 @@ struct Operand {
         for (int k = 0; k < VN<V> / 2; ++k) f[h * (VN<V> / 2) + k] = t[k];
       }
     } else {
+      const auto one = [&](int k) {
+        return c.has(k) ? lds_one<V>(at + c.col(k) * static_cast<uint32_t>(sizeof(V))) : 0.f;
+      };
 #pragma unroll
-      for (int k = 0; k < C::P; ++k) f[k] = f2_make(reg[2 * k], reg[2 * k + 1]);
+      for (int k = 0; k < C::P; ++k) f[k] = f2_make(one(i * 4 + 2 * k), one(i * 4 + 2 * k + 1));
     }
   }
 };
+
+__device__ __forceinline__ void group_meet(int g, int GT) {
+  if (GT > 32)
+    group_bar(g, GT);
+  else
+    __syncwarp();
+}
+// Single columns: when it returns the next row of the ring is there for the whole group.  issue() sends for a
+// row in place of the one in front, which all of the group are done with (of a ring of one step: for the
+// row itself).
+template <typename F>
+__device__ __forceinline__ void single_turn(int g, int GT, int steps, F issue) {
+  if (steps == 1) {
+    group_meet(g, GT);
+    issue();
+    async_wait<0>();
+    group_meet(g, GT);
+    return;
+  }
+  if (steps == 4)
+    async_wait<2>();
+  else if (steps == 3)
+    async_wait<1>();
+  else
+    async_wait<0>();
+  group_meet(g, GT);
+  issue();
+}
 
 // U elements of a row from memory
 template <typename V, int U>
@@ -190,11 +233,12 @@ __device__ __forceinline__ void put_piece(const Cols<NU, U>& c, V* row, int i,
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < NU; k += 2) {
+    for (int k = 0; k < Cols<NU, U>::P; ++k) {
+      const int j = i * 4 + 2 * k;
       float lo, hi;
-      f2_split(f[k / 2], lo, hi);
-      if (c.has(k)) row[c.col(k)] = from_f32<V>(lo);
-      if (c.has(k + 1)) row[c.col(k + 1)] = from_f32<V>(hi);
+      f2_split(f[k], lo, hi);
+      if (c.has(j)) row[c.col(j)] = from_f32<V>(lo);
+      if (c.has(j + 1)) row[c.col(j + 1)] = from_f32<V>(hi);
     }
   }
 }
@@ -338,21 +382,14 @@ __device__ __forceinline__ void put_planes(const Cols<NU, 8>& c, uint32_t planes
       sts16_f2(at + 3 * plane, w[4 * i + 2], w[4 * i + 3]);
     }
 }
-// Piece i's values of the two planes from `planes` on (single columns: from the registers).
-template <int NU, int N>
+// Piece i's values of the two planes from `planes` on.
+template <int NU>
 __device__ __forceinline__ void get_plane(const Cols<NU, 8>& c, uint32_t planes, uint32_t plane, int i,
-                                          const f2 (&)[N], f2 (&v)[4]) {
+                                          f2 (&v)[4]) {
   const uint32_t at = planes + (c.j + i * c.GT) * 16;
   const ulonglong2 q = lds16_f2(at), r = lds16_f2(at + plane);
   v[0] = q.x, v[1] = q.y, v[2] = r.x, v[3] = r.y;
 }
-template <int NU, int N>
-__device__ __forceinline__ void get_plane(const Cols<NU, 1>&, uint32_t, uint32_t, int,
-                                          const f2 (&own)[N], f2 (&v)[NU / 2]) {
-#pragma unroll
-  for (int k = 0; k < NU / 2; ++k) v[k] = own[k];
-}
-
 // Three sums over a group, as group_sum (a warp's in 16 bytes).
 __device__ __forceinline__ void group_sum3(float (&v)[3], float4* s, int g, int GT) {
 #pragma unroll
@@ -415,9 +452,15 @@ inline bool span_even(const RowSpan& r, const mm_moe_resnorm* s) {
 }
 
 // CTAs an SM: two where single columns leave the registers for it (four a thread; 5003 x 1111 bf16
-// forward 61 -> 41 us, backward 64 -> 56).
+// forward 33 us, backward 43; one CTA, when columns came through registers, 61 for 41 and 64 for 56).
 template <int NU, int U>
 constexpr int rn_ctas = U == 1 && NU <= 4 ? 2 : 1;
+
+// Steps of the ring of single columns, `step` bytes each.
+template <int NU>
+int single_steps(size_t step) {
+  return static_cast<int>(std::min<size_t>(4, RN_SMEM / rn_ctas<NU, 1> / step));
+}
 
 // How the rows are spread: GT threads a row, groups of them in a CTA.
 template <int NU, int U>

@@ -27,6 +27,7 @@ struct BwdOps {
   float* part;  // [CTA][2][H]: K, dw_pre
   float* mean_ov;  // [T] <oh v> (the looped kernels')
   int T_, H, GT;
+  int steps, step_bytes;  // of the ring of single columns
 };
 
 // Bytes of a thread's share of a row in the ring.
@@ -52,30 +53,31 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_bwd_kernel
   using OR = Operand<R, NU, U>;
   extern __shared__ __align__(16) unsigned char ring_bytes[];
   __shared__ float4 s_sum[2][RN_THREADS / 32];
-  const uint32_t nt = blockDim.x, piece = nt * 16, step_bytes = rn_bwd_bytes<T, R, NU, U> * nt;
-  const uint32_t ring =
-      static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)) + threadIdx.x * 16;
-  const uint32_t out_at = OR::BYTES * nt, dn_at = 2 * out_at, f_at = dn_at + OT::BYTES * nt;
+  const uint32_t nt = blockDim.x, piece = nt * 16;
+  const uint32_t step_bytes = U == 8 ? rn_bwd_bytes<T, R, NU, U> * nt : a.step_bytes;
+  const int steps = U == 8 ? S : a.steps;
   pdl_wait();
   pdl_trigger();
   Cols<NU, U> c;
   c.init(a.GT, a.H);
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)) +
+                        (U == 8 ? threadIdx.x * 16 : c.g * (step_bytes / c.groups));
+  const uint32_t out_at = U == 8 ? OR::BYTES * nt : single_bytes(a.H, sizeof(R)), dn_at = 2 * out_at,
+                 f_at = dn_at + (U == 8 ? OT::BYTES * nt : single_bytes(a.H, sizeof(T)));
   const uint32_t n = a.T_, step = gridDim.x * c.groups;
   uint32_t t = blockIdx.x * c.groups + c.g, tw = c.first_of_warp(t), ta = t;
   const float inv = 1.f / static_cast<float>(a.H);
   const bool pre = WHOLE || a.dn.p != nullptr, has_f = WHOLE || a.f.p != nullptr,
              has_d = WHOLE || a.dout.p != nullptr;
   const bool post = a.w_post != nullptr;
-  OR od, oo;
-  OT on, of;
   const auto issue = [&](uint32_t at) {
     if (ta < n) {
-      if (has_d) od.issue(c, a.dout.row(ta), at, piece);
+      if (has_d) OR::issue(c, a.dout.row(ta), at, piece);
       if (pre) {
-        oo.issue(c, a.out.row(ta), at + out_at, piece);
-        on.issue(c, a.dn.row(ta), at + dn_at, piece);
+        OR::issue(c, a.out.row(ta), at + out_at, piece);
+        OT::issue(c, a.dn.row(ta), at + dn_at, piece);
       }
-      if (has_f) of.issue(c, a.f.row(ta), at + f_at, piece);
+      if (has_f) OT::issue(c, a.f.row(ta), at + f_at, piece);
     }
     if constexpr (U == 8) {
       if (rn_prefetch<R> && c.j == 0) {
@@ -88,15 +90,14 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_bwd_kernel
       }
     }
     ta += step;
-    if constexpr (U == 8) async_commit();
+    async_commit();
   };
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(ring + i * step_bytes);
+  for (int i = 0; i < steps - 1; ++i) issue(ring + i * step_bytes);
   constexpr int P = Cols<NU, U>::P, PIECES = Cols<NU, U>::PIECES;
   constexpr bool KEEP = U == 8 && NU == 1;  // x, out and f stay in registers between the two passes
   f2 K[NU * U / 2], dw[NU * U / 2];
   f2 cf1[SHARED ? 1 : NU * U / 2], w1[SHARED ? 1 : NU * U / 2];
-  const uint32_t planes = static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)) + S * step_bytes,
+  const uint32_t planes = static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)) + steps * step_bytes,
                  plane = a.H / 8 * 16;
   {
     f2 cf[NU * U / 2], w[NU * U / 2];
@@ -113,8 +114,13 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_bwd_kernel
     }
   }
   const auto params = [&](int i, f2 (&cf)[P], f2 (&w)[P]) {
-    get_plane(c, planes, plane, i, cf1, cf);
-    get_plane(c, planes + 2 * plane, plane, i, w1, w);
+    if constexpr (SHARED) {
+      get_plane(c, planes, plane, i, cf);
+      get_plane(c, planes + 2 * plane, plane, i, w);
+    } else {
+#pragma unroll
+      for (int k = 0; k < P; ++k) cf[k] = cf1[i * P + k], w[k] = w1[i * P + k];
+    }
   };
   // the next row's gate and reciprocal norms, a row ahead
   float gt_n = 1.f, rf_n = 1.f, ro_n = 0.f;
@@ -126,25 +132,30 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_bwd_kernel
   };
   stats(t);
   int buf = 0;
-  uint32_t st = ring, st_in = ring + (S - 1) * step_bytes;
-  const uint32_t ring_end = ring + S * step_bytes;
+  uint32_t st = ring, st_in = ring + (steps - 1) * step_bytes;
+  const uint32_t ring_end = ring + steps * step_bytes;
   for (; tw < n; t += step, tw += step) {
-    issue(st_in);
+    if constexpr (U == 8)
+      issue(st_in);
+    else
+      single_turn(c.g, a.GT, steps, [&] { issue(st_in); });
     const bool live = t < n;
     const float gt = gt_n, rf = rf_n, ro = ro_n;
     stats(t + step);
     const f2 ro2 = f2_of(ro);
     if constexpr (U == 8) async_wait<S - 1>();
+    const uint32_t at_d = OR::found(st, a.dout.row(t)), at_o = OR::found(st + out_at, a.out.row(t)),
+                   at_n = OT::found(st + dn_at, a.dn.row(t)), at_f = OT::found(st + f_at, a.f.row(t));
     // piece i: x = dout + ro w dn, out, f, dn
     const auto get = [&](int i, f2 (&x)[P], f2 (&o)[P], f2 (&f)[P], f2 (&dn)[P]) {
 #pragma unroll
       for (int k = 0; k < P; ++k) x[k] = o[k] = f[k] = dn[k] = 0;
-      if (has_d) od.get(st, piece, i, x);
+      if (has_d) OR::get(c, at_d, piece, i, x);
       if (pre) {
-        oo.get(st + out_at, piece, i, o);
-        on.get(st + dn_at, piece, i, dn);
+        OR::get(c, at_o, piece, i, o);
+        OT::get(c, at_n, piece, i, dn);
       }
-      if (has_f) of.get(st + f_at, piece, i, f);
+      if (has_f) OT::get(c, at_f, piece, i, f);
     };
     f2 x1[KEEP ? P : 1], o1[KEEP ? P : 1], f1[KEEP ? P : 1];
     f2 a0 = 0, a1 = 0, a2 = 0;
@@ -210,7 +221,7 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_bwd_kernel
     st += step_bytes;
     if (st == ring_end) st = ring;
   }
-  if constexpr (U == 8) async_wait<0>();
+  async_wait<0>();
   if (!a.sums_f && !pre) return;
   // the CTA's groups' column sums, added in order
   float* const p0 = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
@@ -394,7 +405,8 @@ template <typename T, typename R, int NU, int U, int S>
 static cudaError_t bwd_launch_steps(const Ctx& c, const BwdOps<T, R>& a, const NormGrid& g,
                                     int params) {
   const int nt = g.GT * g.groups;
-  size_t smem = static_cast<size_t>(S) * nt * rn_bwd_bytes<T, R, NU, U> + params;
+  size_t smem = U == 8 ? static_cast<size_t>(S) * nt * rn_bwd_bytes<T, R, NU, U> + params
+                       : static_cast<size_t>(a.steps) * a.step_bytes;
   if (g.groups > 1) smem = std::max(smem, sizeof(float) * 2 * g.groups * a.H);
   const bool whole = a.dout.p != nullptr && a.dn.p != nullptr && a.f.p != nullptr;
   auto* kern = whole ? resnorm_bwd_kernel<T, R, NU, U, S, true>
@@ -410,7 +422,9 @@ static cudaError_t bwd_launch(const Ctx& c, BwdOps<T, R> a, int* n_part) {
   const NormGrid g = rn_grid(a.GT, a.T_, c.num_sms * rn_ctas<NU, U>);
   *n_part = g.ctas;
   if constexpr (U == 1) {
-    return bwd_launch_steps<T, R, NU, U, 1>(c, a, g, 0);
+    a.step_bytes = g.groups * 2 * (single_bytes(a.H, sizeof(T)) + single_bytes(a.H, sizeof(R)));
+    a.steps = single_steps<NU>(a.step_bytes);
+    return bwd_launch_steps<T, R, NU, U, 0>(c, a, g, 0);
   } else {
     const int params = 4 * (a.H / 8 * 16);
     constexpr int MOST = rn_bwd_steps<T, R, NU>(8 * 1024),
