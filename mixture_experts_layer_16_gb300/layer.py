@@ -120,6 +120,7 @@ class MoERouter:
         self.logits = torch.empty((T, E), dtype=torch.float32, device=device)
         self.dlogits = torch.empty((T, E), dtype=torch.bfloat16, device=device)
         self.select = None
+        self._ran = False  # whether self.logits holds what a backward with select reads
         if select is not None:
             from .selection import MoESelect
             self.select = MoESelect(T, E, k, dtype="fp32", grad_dtype="bf16", device=device,
@@ -138,15 +139,18 @@ class MoERouter:
                 raise ValueError("bias: this router has none (select=None)")
             B.mm_moe_router_forward(self.shape, x, W_router, self.logits, idx, w, stream)
         else:
+            from .train import _on, _stream
             self.select._check_bias(bias)
-            B.mm_moe_router_select_forward(self.shape, self.select.shape, x, W_router, bias,
-                                           self.logits, idx, w, stream)
+            _on(d, B.mm_moe_router_select_forward, self.shape, self.select.shape, x, W_router, bias,
+                self.logits, idx, w, _stream(stream, d, self.logits, idx, w))
+            self._ran = True
         return idx, w
 
     def backward(self, x, W_router, topk_idx, topk_w, dtopk_w, dx, dW_router=None, stream=None,
                  dlogits_aux=None):
         """Adds the router's input gradient to dx (in place) and returns dW_router.
-        dlogits_aux [T, E] fp32: a further gradient of the logits (MoEBalanceLoss's)."""
+        dlogits_aux [T, E] fp32: a further gradient of the logits (MoEBalanceLoss's).
+        With select it reads self.logits: those of the last forward."""
         d, bf = self.device, torch.bfloat16
         _need(x, "x", (self.T, self.H), bf, d)
         _need(W_router, "W_router", (self.E, self.H), bf, d)
@@ -160,9 +164,12 @@ class MoERouter:
         if self.select is not None:
             if dlogits_aux is not None:
                 _need(dlogits_aux, "dlogits_aux", (self.T, self.E), torch.float32, d)
-            B.mm_moe_router_select_backward(self.shape, self.select.shape, x, W_router,
-                                            self.logits, topk_idx, dtopk_w, dlogits_aux,
-                                            self.dlogits, dx, dW_router, stream)
+            if not self._ran:
+                raise RuntimeError("backward needs a forward first")
+            from .train import _on, _stream
+            _on(d, B.mm_moe_router_select_backward, self.shape, self.select.shape, x, W_router,
+                self.logits, topk_idx, dtopk_w, dlogits_aux, self.dlogits, dx, dW_router,
+                _stream(stream, d, self.logits, self.dlogits, dW_router))
         elif dlogits_aux is None:
             B.mm_moe_router_backward(self.shape, x, W_router, topk_idx, topk_w, dtopk_w,
                                      self.dlogits, dx, dW_router, stream)

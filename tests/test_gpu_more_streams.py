@@ -5,7 +5,7 @@ import threading
 import pytest
 import torch
 
-from mixture_experts_layer_16_gb300 import MoEAdamW, MoEResidualNorm, MoESelect
+from mixture_experts_layer_16_gb300 import MoEAdamW, MoEResidualNorm, MoERouter, MoESelect
 from tests import gpu_util as G
 from tests.test_gpu_train_streams import check
 
@@ -26,6 +26,23 @@ def test_select_on_another_stream():
     g = torch.randn((T, k), device="cuda")
     check(lambda s: list(h.forward(l, b, stream=s)))
     check(lambda s: [h.backward(l, idx, g, stream=s)])
+
+
+def test_router_on_another_stream():
+    T, H, E, k = 4096, 256, 128, 4
+    x, W = torch.randn((T, H), device="cuda").to(BF), torch.randn((E, H), device="cuda").to(BF)
+    g, dx = torch.randn((T, k), device="cuda"), torch.randn((T, H), device="cuda").to(BF)
+
+    def fwd(s):
+        r = MoERouter(T, H, E, k, select=dict(score="sigmoid"))
+        return [*r.forward(x, W, stream=s), r.logits]
+    check(fwd)
+    kept = MoERouter(T, H, E, k, select=dict(score="sigmoid"))
+    idx, w = kept.forward(x, W)
+
+    def bwd(s):
+        return [kept.backward(x, W, idx, w, g, dx, stream=s)]
+    check(bwd)
 
 
 def test_residual_norm_on_another_stream():

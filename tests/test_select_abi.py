@@ -90,3 +90,13 @@ def test_handle(lib):
             h.backward(**{**dict(logits=l, topk_idx=idx, dtopk_w=g), **kw})
     with pytest.raises(TypeError):
         MoERouter(16, 128, 64, 4, device="cpu", select=dict(top=3))
+
+
+def test_router_backward_needs_a_forward():
+    T, H, E, k = 16, 128, 64, 4
+    r = MoERouter(T, H, E, k, device="cpu", select={})
+    bf = dict(dtype=torch.bfloat16)
+    with pytest.raises(RuntimeError):
+        r.backward(torch.zeros(T, H, **bf), torch.zeros(E, H, **bf),
+                   torch.zeros(T, k, dtype=torch.int32), torch.zeros(T, k), torch.zeros(T, k),
+                   torch.zeros(T, H, **bf))
