@@ -28,9 +28,9 @@ struct FwdOps {
 // Bytes of a thread's share of a row in the ring.
 template <typename T, typename R, int NU, int U>
 constexpr int rn_fwd_bytes = Operand<T, NU, U>::BYTES + Operand<R, NU, U>::BYTES;
-template <typename T, typename R, int NU>
+template <typename T, typename R, int NU, int THREADS>
 constexpr int rn_fwd_steps =
-    std::max(1, std::min(4, RN_SMEM / (RN_THREADS * rn_fwd_bytes<T, R, NU, 8>)));
+    std::max(1, std::min(4, RN_SMEM / (THREADS * rn_fwd_bytes<T, R, NU, 8>)));
 
 // JOINT (units of 8): the sum over the next row's f joins this row's over out, one barrier a row for two.
 // That takes a step of the ring's lead, and pays where rows span warps and the lead is long or the warps
@@ -40,15 +40,15 @@ constexpr int rn_fwd_steps =
 // 16384 x 2048 in bf16 is at 0.86 of the copy rate, with an fp32 residual stream at 0.89 (62.0 to 67.2 us;
 // its rows in 16-byte halves of sectors, and not on their way to L2 a row ahead: 80).  Two CTAs an SM with
 // half of the ring and the parameters in shared memory: 49.9 and 71.6.
-template <typename T, typename R, int NU, int U, bool JOINT>
-__global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel(const FwdOps<T, R> a) {
-  constexpr int S = U == 8 ? rn_fwd_steps<T, R, NU> : 0;
+template <typename T, typename R, int NU, int U, bool JOINT, int THREADS = RN_THREADS>
+__global__ void __launch_bounds__(THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel(const FwdOps<T, R> a) {
+  constexpr int S = U == 8 ? rn_fwd_steps<T, R, NU, THREADS> : 0;
   const int steps = U == 8 ? S : a.steps;
   using OF = Operand<T, NU, U>;
   using OX = Operand<R, NU, U>;
   extern __shared__ __align__(16) unsigned char ring_bytes[];
   static_assert(!JOINT || S >= 2);
-  __shared__ Sums<JOINT ? 2 : 1> s_sum[2][RN_THREADS / 32];
+  __shared__ Sums<JOINT ? 2 : 1> s_sum[2][THREADS / 32];
   const uint32_t piece = blockDim.x * 16;
   const uint32_t step_bytes = U == 8 ? rn_fwd_bytes<T, R, NU, U> * blockDim.x : a.step_bytes;
   pdl_wait();
@@ -256,17 +256,25 @@ static cudaError_t fwd_launch(const Ctx& c, FwdOps<T, R> a) {
   a.GT = rn_group_threads<NU, U>(a.H);
   constexpr bool MAY = U == 8 && NU > 1;  // (NU = 1: a row or two a group)
   const bool joint = MAY && a.GT > (sizeof(R) == 2 ? 32 : 128);
-  const NormGrid g = rn_grid(a.GT, a.T_, c.num_sms * rn_ctas<NU, U>);
+  // two groups of up to 384 threads (in 80 registers) where 512 threads would be one, which waits at its
+  // barrier: 6000 x 5120 bf16 52.5 -> 41.5 us, x 6144 88.7 -> 60.8; where more groups fit anyway 512 threads
+  // are as fast (x 3584) or faster (16384 x 2048 45.9, 47.6 with six groups for four)
+  constexpr int MORE = MAY && sizeof(R) == 2 ? 768 : RN_THREADS;
+  const bool more = a.GT > RN_THREADS / 2 && 2 * a.GT <= MORE;
+  const NormGrid g = rn_grid(a.GT, a.T_, c.num_sms * rn_ctas<NU, U>, more ? MORE : RN_THREADS);
   const int nt = g.GT * g.groups;
   size_t smem;
   if (U == 8) {
-    smem = static_cast<size_t>(rn_fwd_steps<T, R, NU>) * nt * rn_fwd_bytes<T, R, NU, U>;
+    smem = static_cast<size_t>(more ? rn_fwd_steps<T, R, NU, MORE> : rn_fwd_steps<T, R, NU, RN_THREADS>) *
+           nt * rn_fwd_bytes<T, R, NU, U>;
   } else {
     a.step_bytes = g.groups * (single_bytes(a.H, sizeof(T)) + single_bytes(a.H, sizeof(R)));
     a.steps = single_steps<NU>(a.step_bytes);
     smem = static_cast<size_t>(a.steps) * a.step_bytes;
   }
-  auto* kern = joint ? resnorm_fwd_kernel<T, R, NU, U, MAY> : resnorm_fwd_kernel<T, R, NU, U, false>;
+  auto* kern = more    ? resnorm_fwd_kernel<T, R, NU, U, MAY, MORE>
+               : joint ? resnorm_fwd_kernel<T, R, NU, U, MAY>
+                       : resnorm_fwd_kernel<T, R, NU, U, false>;
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
   return launch_k(c.stream, kern, dim3(g.ctas), dim3(nt), smem, a);

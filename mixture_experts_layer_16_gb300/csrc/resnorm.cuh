@@ -473,9 +473,9 @@ int rn_group_threads(int H) {
   while (g < n) g *= 2;
   return g;
 }
-inline NormGrid rn_grid(int GT, int T, int sms) {
+inline NormGrid rn_grid(int GT, int T, int sms, int threads = RN_THREADS) {
   const int per_warp = GT < 32 ? 32 / GT : 1;
-  int groups = std::min(RN_THREADS / GT, div_up(T, sms));
+  int groups = std::min(threads / GT, div_up(T, sms));
   groups = (groups + per_warp - 1) / per_warp * per_warp;
   return NormGrid{GT, groups, std::min(sms, div_up(T, groups))};
 }

@@ -133,8 +133,8 @@ __global__ void __launch_bounds__(SEL_THREADS) select_bwd_kernel(
     const float s = mine ? sigmoid32(l) : 0.f;
     float ds = g;
     if (a.renorm) {
-      const float n = sum_of<W>(s) + SUM_EPS;
-      ds = (g - sum_of<W>(mine ? g * s : 0.f) / n) / n;
+      const float n = sum_of<W>(s) + SUM_EPS, q = s / n;  // (of one expert alone 1: no gradient)
+      ds = (g - sum_of<W>(mine ? g * q : 0.f)) / n;
     }
     d = mine ? a.scale * ds * s * sigmoid32(-l) : 0.f;
   } else {

@@ -506,3 +506,15 @@ def test_more_candidates_than_there_is_room_for(with_bias):
         ri, _ = os_.forward(f64(l[rows]), None if bias is None else f64(bias), k, **opt)
         assert np.array_equal(idx[rows].cpu().numpy(), ri)
         assert torch.equal(idx[5::2], idx[5].expand_as(idx[5::2]))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_one_renormalised_expert(score):
+    """Its weight is `scale` whatever the logits are (but for the sigmoid's 1e-20 beside the sum): the gradient is
+    zero, not what is left of two equal terms."""
+    T, E = 700, 96
+    l = logits_of(T, E, "fp32")
+    h = MoESelect(T, E, 1, score, scale=2.5)
+    idx, w = h.forward(l)
+    assert (w == 2.5).all()
+    assert not h.backward(l, idx, torch.randn((T, 1), device="cuda")).any()
