@@ -48,7 +48,8 @@ __global__ void __launch_bounds__(THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel(co
   using OX = Operand<R, NU, U>;
   extern __shared__ __align__(16) unsigned char ring_bytes[];
   static_assert(!JOINT || S >= 2);
-  __shared__ Sums<JOINT ? 2 : 1> s_sum[2][THREADS / 32];
+  constexpr int NSUM = JOINT ? 2 : 1;
+  __shared__ Sums<NSUM> s_sum[2][THREADS / 32];
   const uint32_t piece = blockDim.x * 16;
   const uint32_t step_bytes = U == 8 ? rn_fwd_bytes<T, R, NU, U> * blockDim.x : a.step_bytes;
   pdl_wait();
@@ -88,7 +89,13 @@ __global__ void __launch_bounds__(THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel(co
     if (q < n && a.gate_t != nullptr) gt_n = param<T>(a.gate_t, a.p32, q);
   };
   gate(t);
+  // Every sum takes the buffer that the one in front of it did not: with one barrier to a sum, a warp that
+  // has its totals writes its part of the next sum while others still read the last one's.
   int buf = 0;
+  const auto add_up = [&](float (&v)[NSUM]) {
+    group_sum<NSUM>(v, s_sum[buf], c.g, a.GT);
+    buf ^= 1;
+  };
   uint32_t st = ring, st_in = ring + (steps - 1) * step_bytes;
   const uint32_t ring_end = ring + steps * step_bytes;
   const bool post = a.f.p != nullptr && a.w_post != nullptr;
@@ -110,8 +117,7 @@ __global__ void __launch_bounds__(THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel(co
     async_wait<S - 2>();
     if (post) {
       float ss[2] = {0.f, t < n ? sum_f(st, t) : 0.f};
-      group_sum<2>(ss, s_sum[buf], c.g, a.GT);
-      buf ^= 1;
+      add_up(ss);
       rf_n = rsqrtf(fmaf(ss[1], inv, a.eps));
     }
   }
@@ -129,8 +135,7 @@ __global__ void __launch_bounds__(THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel(co
       float rf = rf_n;
       if constexpr (!JOINT) {
         float ss[1] = {live ? sum_f(st, t) : 0.f};
-        group_sum<1>(ss, s_sum[buf], c.g, a.GT);
-        buf ^= 1;
+        add_up(ss);
         rf = rsqrtf(fmaf(ss[0], inv, a.eps));
       }
       if (live && c.j == 0) a.rstd_f[t] = rf;
@@ -163,15 +168,14 @@ __global__ void __launch_bounds__(THREADS, rn_ctas<NU, U>) resnorm_fwd_kernel(co
     if constexpr (JOINT) {
       async_wait<S - 2>();
       float ss[2] = {so, post && t + step < n ? sum_f(st_next, t + step) : 0.f};
-      if (post || a.n.p != nullptr) group_sum<2>(ss, s_sum[buf], c.g, a.GT);
+      if (post || a.n.p != nullptr) add_up(ss);
       so = ss[0];
       rf_n = rsqrtf(fmaf(ss[1], inv, a.eps));
     } else if (a.n.p != nullptr) {
       float ss[1] = {so};
-      group_sum<1>(ss, s_sum[buf], c.g, a.GT);
+      add_up(ss);
       so = ss[0];
     }
-    buf ^= 1;
     if (a.n.p != nullptr) {
       const float ro = rsqrtf(fmaf(so, inv, a.eps));
       if (live) {
