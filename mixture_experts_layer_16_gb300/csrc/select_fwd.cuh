@@ -575,9 +575,19 @@ __global__ void __launch_bounds__(32 * sel_warps<PL>, sel_ctas<PL>) select_fwd_k
           swap = d + db < -tol;
           doubt = !(fabsf(d + db) > tol) && !tie;
           // three keys close together: only where they are the same
-          if (close(behind, lane + 2))
+          if (close(behind, lane + 2)) {
             doubt = doubt || !(tie && logit(behind) == ln &&
                                __ldg(bias + behind) == __ldg(bias + after));
+            // ... and behind the last place, where no lane looks further, only where all close ones are
+            if (lane == a.k - 1 && !doubt) {
+              const float b = __ldg(bias + e);
+              for (int i = 0; i < N && !doubt; ++i) {
+                const Cand o = cand[i];
+                doubt = !(fabsf(key - o.key) > bound + 0x1p-22f * (fabsf(key) + fabsf(o.key))) &&
+                        !(logit(o.e) == lj && __ldg(bias + o.e) == b);
+              }
+            }
+          }
         }
         const int other = __shfl_up_sync(FULL, e, 1, W);
         const bool from_above = __shfl_up_sync(FULL, swap, 1, W) && lane > 0;
