@@ -458,9 +458,10 @@ MM_MOE_API mm_moe_status mm_moe_router_backward_aux(
  *   or scale s / (sum of the chosen s + 1e-20)
  * Equal keys (groups) go to the lower index.  The order is that of the keys in exact arithmetic
  * (in 64 bits where 32 do not tell; sums that 64 bits round apart may fall either way): without
- * a bias that of the logits.  A NaN ranks as -inf,
+ * a bias that of the logits.  A key that is NaN ranks as -inf (without a bias the logit does),
  * indices are always distinct and in [0, E); a NaN among the chosen logits makes the token's weights
- * NaN (under an unrenormalised softmax, or one with a bias, any NaN of the row does).
+ * NaN (under an unrenormalised sigmoid its own; under an unrenormalised softmax, or one with a bias,
+ * any NaN of the row does).
  * 1 <= T < 2^31, 1 <= k <= 32, E <= 1024, groups <= 32 a divisor of E, k <= E / groups *
  * topk_groups. */
 typedef enum { MM_MOE_SCORE_SOFTMAX = 0, MM_MOE_SCORE_SIGMOID = 1 } mm_moe_score;

@@ -42,6 +42,12 @@ namespace mmmoe {
 constexpr int SEL_FILL = 4;
 
 __device__ __forceinline__ float low_nan(float f) { return fmaxf(f, -INFINITY); }
+// The largest of a row's logits (a NaN is passed over), in whose place e^(l - m) is finite.  Where all are
+// -inf it is 0: their sum is then 0, for scores of 0, and a NaN among them makes it NaN.
+template <typename F>
+__device__ __forceinline__ F finite_max(F m) {
+  return m == -INFINITY ? F(0) : m;
+}
 // For the choice alone, with the hardware's approximations (each within 2 ulp, the exponential's
 // argument rounded): e^d within (|d| + 4) 2^-23 of itself, the sigmoid within 2^-21 of 1.
 __device__ __forceinline__ float exp_key(float d) {
@@ -163,12 +169,13 @@ __device__ __noinline__ int choose(const T* __restrict__ row, const float* __res
     if (!a.sigmoid) {
       for (int i = 0; i < cnt; ++i) m = fmax(m, static_cast<double>(to_f32(row[x.of(i)])));
       for (int o = W / 2; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(FULL, m, o));
+      m = finite_max(m);
       for (int i = 0; i < cnt; ++i) z += exp(static_cast<double>(to_f32(row[x.of(i)])) - m);
       z = sum_of<W>(z);
     }
     for (int i = 0; i < cnt; ++i) {
       const double l = to_f32(row[x.of(i)]);
-      const double s = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : m == -INFINITY ? 0.0 : exp(l - m) / z;
+      const double s = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : z == 0.0 ? 0.0 : exp(l - m) / z;
       key[i] = s + static_cast<double>(bias[x.of(i)]);
     }
   } else {
@@ -208,13 +215,14 @@ __device__ __noinline__ void places64(const T* __restrict__ row, const float* __
   if (!a.sigmoid) {
     for (int e = lane; e < a.E; e += W) m = fmax(m, static_cast<double>(to_f32(row[e])));
     for (int o = W / 2; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(FULL, m, o));
+    m = finite_max(m);
     z = 0.0;
     for (int e = lane; e < a.E; e += W) z += exp(static_cast<double>(to_f32(row[e])) - m);
     z = sum_of<W>(z);
   }
   for (int c = lane; c < N; c += W) {
     const double l = to_f32(row[cand[c].e]);
-    const double s = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : m == -INFINITY ? 0.0 : exp(l - m) / z;
+    const double s = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : z == 0.0 ? 0.0 : exp(l - m) / z;
     const double key = s + static_cast<double>(bias[cand[c].e]);
     keys[c] = key != key ? -INFINITY : key;
   }
@@ -237,6 +245,7 @@ __device__ __noinline__ bool groups64(const T* __restrict__ row, const float* __
   if (!a.sigmoid) {
     for (int e = lane; e < a.E; e += W) m = fmax(m, static_cast<double>(to_f32(row[e])));
     for (int o = W / 2; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(FULL, m, o));
+    m = finite_max(m);
     if (bias != nullptr) {  // (without one, a common factor does not matter)
       z = 0.0;
       for (int e = lane; e < a.E; e += W) z += exp(static_cast<double>(to_f32(row[e])) - m);
@@ -250,8 +259,9 @@ __device__ __noinline__ bool groups64(const T* __restrict__ row, const float* __
     for (int j = 0; j < 2; ++j) {
       const int e = mask != 0 ? x.of(__ffsll(static_cast<long long>(mask)) - 1) : -1;
       mask &= mask - 1;  // (of none: none)
-      const double l = e >= 0 ? to_f32(row[e]) : 0.f;
-      s[j] = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : m == -INFINITY ? 0.0 : exp(l - m) / z;
+      double l = e >= 0 ? to_f32(row[e]) : 0.f;
+      if (bias == nullptr && l != l) l = -INFINITY;  // (the logits rank)
+      s[j] = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : z == 0.0 ? 0.0 : exp(l - m) / z;
       if (bias != nullptr && e >= 0) s[j] += static_cast<double>(bias[e]);
       if (e < 0 || s[j] != s[j]) s[j] = -INFINITY;
     }
@@ -351,12 +361,12 @@ __global__ void __launch_bounds__(32 * sel_warps<PL>, sel_ctas<PL>) select_fwd_k
     if (!a.sigmoid && (BIAS || !a.renorm)) {
 #pragma unroll
       for (int i = 0; i < PL; ++i) m = fmaxf(m, v[i]);
-      m = max_of<W>(cnt > 0 ? m : -INFINITY);
+      m = finite_max(max_of<W>(cnt > 0 ? m : -INFINITY));
       float z = 0.f;
 #pragma unroll
       for (int i = 0; i < PL; ++i) z += exp_key(v[i] - m);
       z = sum_of<W>(cnt > 0 ? z : 0.f);
-      rz = m == -INFINITY ? 0.f : 1.f / z;
+      rz = z == 0.f ? 0.f : 1.f / z;
     }
     if constexpr (BIAS) {
       if (a.sigmoid) {
@@ -364,7 +374,7 @@ __global__ void __launch_bounds__(32 * sel_warps<PL>, sel_ctas<PL>) select_fwd_k
         for (int i = 0; i < PL; ++i) v[i] = sigmoid_key(v[i]);
       } else {
 #pragma unroll
-        for (int i = 0; i < PL; ++i) v[i] = m == -INFINITY ? 0.f : exp_key(v[i] - m) * rz;
+        for (int i = 0; i < PL; ++i) v[i] = exp_key(v[i] - m) * rz;
       }
 #pragma unroll
       for (int i = 0; i < PL; ++i) v[i] += s_bias[(i / 4 * W + lane) * 4 + i % 4];
@@ -547,9 +557,7 @@ __global__ void __launch_bounds__(32 * sel_warps<PL>, sel_ctas<PL>) select_fwd_k
       return a.vec ? to_f32(reinterpret_cast<const T*>(here)[i]) : to_f32(__ldg(row + i));
     };
     float lj = logit(e);
-    const auto score = [&](float x) {
-      return a.sigmoid ? sigmoid32(x) : m == -INFINITY ? 0.f : expf(x - m) * rz;
-    };
+    const auto score = [&](float x) { return a.sigmoid ? sigmoid32(x) : expf(x - m) * rz; };
     float sj = BIAS || a.sigmoid || !a.renorm ? score(lj) : 0.f;
     if constexpr (BIAS) {
       // Pairs in doubt, each lane's with the next place's, the last one's with the first left out
@@ -629,9 +637,10 @@ __global__ void __launch_bounds__(32 * sel_warps<PL>, sel_ctas<PL>) select_fwd_k
       w = a.scale * (sj / (sum_of<W>(mine ? sj : 0.f) + SUM_EPS));
     } else {  // the softmax over the chosen
       const float big = max_of<W>(mine ? lj : -INFINITY);
-      const float ex = mine && big != -INFINITY ? expf(lj - big) : 0.f;
+      const float ex = mine && !(lj == -INFINITY) ? expf(lj - big) : 0.f;  // (of a NaN a NaN)
       const float sum = sum_of<W>(ex);
       w = sum == 0.f ? 0.f : a.scale * (ex / sum);
+      if (BIAS && sj != sj) w = sj;  // (a row whose scores are NaN)
     }
     if (mine && live) {
       topk_idx[t * a.k + lane] = e;
@@ -651,19 +660,20 @@ __device__ __noinline__ bool above(const T* __restrict__ row, const float* __res
   const float db = __ldg(bias + j) - __ldg(bias + i);
   if (dl == 0.f && db == 0.f) return false;
   const float d = a.sigmoid ? sigmoid32(lj) * sigmoid32(-li) * -expm1f(-dl)
-                            : (m == -INFINITY ? 0.f : expf(li - m) * rz) * expm1f(dl);
+                            : expf(li - m) * rz * expm1f(dl);
   const float far = a.sigmoid ? 64.f + fabsf(dl) : 128.f + fabsf(dl) + fabsf(li - m);
   const float tol = far * 0x1p-24f * fabsf(d) + 0x1p-23f * fabsf(db);
   if (fabsf(d + db) > tol) return d + db > 0.f;
   double s[2], dm = -INFINITY, z = 0.0;
   if (!a.sigmoid) {
     for (int e = 0; e < a.E; ++e) dm = fmax(dm, static_cast<double>(to_f32(row[e])));
+    dm = finite_max(dm);
     for (int e = 0; e < a.E; ++e) z += exp(static_cast<double>(to_f32(row[e])) - dm);
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const double x = h == 0 ? li : lj;
-    s[h] = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : dm == -INFINITY ? 0.0 : exp(x - dm) / z;
+    s[h] = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : z == 0.0 ? 0.0 : exp(x - dm) / z;
     s[h] += static_cast<double>(__ldg(bias + (h == 0 ? i : j)));
     if (s[h] != s[h]) s[h] = -INFINITY;
   }
@@ -699,14 +709,13 @@ __global__ void __launch_bounds__(128) select_small_kernel(
   if (!a.sigmoid && (BIAS || !a.renorm)) {
 #pragma unroll
     for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);
+    m = finite_max(m);
     float z = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) z += i < a.E ? expf(l[i] - m) : 0.f;
-    rz = m == -INFINITY ? 0.f : 1.f / z;
+    rz = z == 0.f ? 0.f : 1.f / z;
   }
-  const auto score = [&](float x) {
-    return a.sigmoid ? sigmoid32(x) : m == -INFINITY ? 0.f : expf(x - m) * rz;
-  };
+  const auto score = [&](float x) { return a.sigmoid ? sigmoid32(x) : expf(x - m) * rz; };
   float v[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -774,11 +783,12 @@ __global__ void __launch_bounds__(128) select_small_kernel(
   for (int i = 0; i < N; ++i) {
     const bool in = place[i] < a.k;
     w[i] = !in ? 0.f
-           : a.renorm && !a.sigmoid ? (big == -INFINITY ? 0.f : expf(l[i] - big))
+           : a.renorm && !a.sigmoid ? (l[i] == -INFINITY ? 0.f : expf(l[i] - big))
                                     : score(l[i]);
     sum += w[i];
   }
-  const float c = !a.renorm ? a.scale : a.sigmoid ? 1.f / (sum + SUM_EPS) : sum == 0.f ? 0.f : 1.f / sum;
+  float c = !a.renorm ? a.scale : a.sigmoid ? 1.f / (sum + SUM_EPS) : sum == 0.f ? 0.f : 1.f / sum;
+  if (BIAS && rz != rz) c = rz;  // (a row whose scores are NaN)
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (place[i] < a.k) {
