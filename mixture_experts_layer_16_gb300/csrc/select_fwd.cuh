@@ -61,6 +61,20 @@ __device__ __forceinline__ float sigmoid_key(float l) {
   return r;
 }
 
+// s(x) - s(y), exact to `tol` (some 2^-18 of itself, not of the scores), from the larger logit h and the
+// smaller one l: s(h) (1 - s(l)) (1 - e^(l - h)) for the sigmoid, s(h) (1 - e^(l - h)) for the softmax.  (From
+// s(l) and e^(h - l) a factor would be lost below fp32's range while the other leaves it above.)  What
+// underflows here is below 2^-120.  score: s; terms: the errors of a softmax's sum, in 2^-24 of it.
+template <typename F>
+__device__ __forceinline__ float score_difference(float x, float y, bool sigmoid, float m, float terms,
+                                                  F score, float& tol) {
+  const float h = fmaxf(x, y), l = fminf(x, y), dl = x - y;
+  float d = score(h) * -expm1f(-fabsf(dl));
+  if (sigmoid) d *= sigmoid32(-l);
+  tol = (sigmoid ? 64.f : terms + fabsf(h - m)) * 0x1p-24f * d + 0x1p-120f;
+  return dl < 0.f ? -d : d;
+}
+
 // Reductions over aligned sets of n lanes.
 template <typename F>
 __device__ __forceinline__ float lanes(float v, int n, F f) {
@@ -570,15 +584,13 @@ __global__ void __launch_bounds__(32 * sel_warps<PL>, sel_ctas<PL>) select_fwd_k
       };
       const bool near = close(after, lane + 1);
       if (__any_sync(FULL, near)) {
-        // The difference of two keys from that of the logits: s_i - s_j = s_i (1 - s_j) (1 - e^(l_j - l_i)),
-        // for the softmax s_j (e^(l_i - l_j) - 1), is exact to some 2^-18 of itself, not of the scores.
         bool swap = false, doubt = false;
         if (near) {
-          const float ln = logit(after), dl = lj - ln;
+          const float ln = logit(after);
           const float db = __ldg(bias + e) - __ldg(bias + after);
-          const float d = a.sigmoid ? sj * sigmoid32(-ln) * -expm1f(-dl) : score(ln) * expm1f(dl);
-          const float far = a.sigmoid ? 64.f + fabsf(dl) : 2 * PL + 64.f + fabsf(dl) + fabsf(ln - m);
-          const float tol = far * 0x1p-24f * fabsf(d) + 0x1p-23f * fabsf(db);
+          float tol;
+          const float d = score_difference(lj, ln, a.sigmoid, m, 2 * PL + 64.f, score, tol);
+          tol += 0x1p-23f * fabsf(db);
           const bool tie = lj == ln && db == 0.f;  // (in order then)
           swap = d + db < -tol;
           doubt = !(fabsf(d + db) > tol) && !tie;
@@ -651,33 +663,44 @@ __global__ void __launch_bounds__(32 * sel_warps<PL>, sel_ctas<PL>) select_fwd_k
 }
 
 // ------------------------------------------------------------------------ few experts
+// The largest logit and the sum of e^(l - m) in 64 bits (of a softmax), and a key from them.
+struct Row64 {
+  double m, z;
+};
+template <typename T>
+__device__ __forceinline__ Row64 row64(const T* __restrict__ row, const SelArgs& a) {
+  Row64 r{-INFINITY, 0.0};
+  if (a.sigmoid) return r;
+  for (int e = 0; e < a.E; ++e) r.m = fmax(r.m, static_cast<double>(to_f32(row[e])));
+  r.m = finite_max(r.m);
+  for (int e = 0; e < a.E; ++e) r.z += exp(static_cast<double>(to_f32(row[e])) - r.m);
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ double key64(const T* __restrict__ row, const float* __restrict__ bias,
+                                        const SelArgs& a, const Row64& r, int e) {
+  const double l = to_f32(row[e]);
+  const double s = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : r.z == 0.0 ? 0.0 : exp(l - r.m) / r.z;
+  const double key = s + static_cast<double>(bias[e]);
+  return key != key ? -INFINITY : key;
+}
+
 // Whether expert j's key (bias and all) lies above expert i's, for keys that fp32 does not tell apart: by
 // the difference of the logits (as in select_fwd_kernel), else in 64 bits.
 template <typename T>
 __device__ __noinline__ bool above(const T* __restrict__ row, const float* __restrict__ bias,
                                    const SelArgs a, float m, float rz, int i, int j) {
-  const float li = to_f32(__ldg(row + i)), lj = to_f32(__ldg(row + j)), dl = lj - li;
+  const float li = to_f32(__ldg(row + i)), lj = to_f32(__ldg(row + j));
   const float db = __ldg(bias + j) - __ldg(bias + i);
-  if (dl == 0.f && db == 0.f) return false;
-  const float d = a.sigmoid ? sigmoid32(lj) * sigmoid32(-li) * -expm1f(-dl)
-                            : expf(li - m) * rz * expm1f(dl);
-  const float far = a.sigmoid ? 64.f + fabsf(dl) : 128.f + fabsf(dl) + fabsf(li - m);
-  const float tol = far * 0x1p-24f * fabsf(d) + 0x1p-23f * fabsf(db);
+  if (lj == li && db == 0.f) return false;
+  float tol;
+  const float d = score_difference(
+      lj, li, a.sigmoid, m, 128.f,
+      [&](float x) { return a.sigmoid ? sigmoid32(x) : expf(x - m) * rz; }, tol);
+  tol += 0x1p-23f * fabsf(db);
   if (fabsf(d + db) > tol) return d + db > 0.f;
-  double s[2], dm = -INFINITY, z = 0.0;
-  if (!a.sigmoid) {
-    for (int e = 0; e < a.E; ++e) dm = fmax(dm, static_cast<double>(to_f32(row[e])));
-    dm = finite_max(dm);
-    for (int e = 0; e < a.E; ++e) z += exp(static_cast<double>(to_f32(row[e])) - dm);
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const double x = h == 0 ? li : lj;
-    s[h] = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : z == 0.0 ? 0.0 : exp(x - dm) / z;
-    s[h] += static_cast<double>(__ldg(bias + (h == 0 ? i : j)));
-    if (s[h] != s[h]) s[h] = -INFINITY;
-  }
-  return s[1] > s[0];
+  const Row64 r = row64(row, a);
+  return key64(row, bias, a, r, j) > key64(row, bias, a, r, i);
 }
 
 // Up to N experts, all groups taking part: a thread a token, its keys in registers, every expert's
