@@ -703,6 +703,23 @@ __device__ __noinline__ bool above(const T* __restrict__ row, const float* __res
   return key64(row, bias, a, r, j) > key64(row, bias, a, r, i);
 }
 
+// The experts' places by keys in 64 bits, four bits each.
+template <typename T>
+__device__ __noinline__ unsigned long long small_places64(const T* __restrict__ row,
+                                                          const float* __restrict__ bias,
+                                                          const SelArgs a) {
+  const Row64 r = row64(row, a);
+  double key[16];
+  for (int e = 0; e < a.E; ++e) key[e] = key64(row, bias, a, r, e);
+  unsigned long long places = 0;
+  for (int e = 0; e < a.E; ++e) {
+    int place = 0;
+    for (int o = 0; o < a.E; ++o) place += ahead(key[o], o, key[e], e);
+    places |= static_cast<unsigned long long>(place) << 4 * e;
+  }
+  return places;
+}
+
 // Up to N experts, all groups taking part: a thread a token, its keys in registers, every expert's
 // place the number of keys in front of its own; pairs within each other's errors are compared anew.
 // 131072 x 8 fp32 3.8 us (27 in eight lanes a token), 131072 x 16 9.1.
@@ -792,8 +809,15 @@ __global__ void __launch_bounds__(128) select_small_kernel(
           }
         }
       }
+      // A pair told apart by its difference, which can be finer than 64 bits of a key, and pairs that tie there
+      // can form a circle: then all are ranked in 64 bits.
+      uint32_t there = 0;
 #pragma unroll
-      for (int i = 0; i < N; ++i) place[i] = static_cast<int>(packed >> 4 * i & 15u);
+      for (int i = 0; i < N; ++i) there |= i < a.E ? 1u << (packed >> 4 * i & 15u) : 0u;
+      if (there != (1u << a.E) - 1u) packed = small_places64(row, bias, a);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        place[i] = i < a.E ? static_cast<int>(packed >> 4 * i & 15u) : N;
     }
   }
   // (absent experts come behind all: -inf, and of higher index)
