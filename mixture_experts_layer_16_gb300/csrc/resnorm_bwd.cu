@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_bwd_kernel
     group_sum3(s, s_sum[buf], c.g, a.GT);
     buf ^= 1;
     const float k1 = ro * ro * (ro * s[0] * inv);
-    const float cfd = rf * (s[1] - k1 * s[2]);  // sum c fh D
+    const float cfd = rf * (pre ? s[1] - k1 * s[2] : s[1]);  // sum c fh D (f may be infinite)
     if (live) {
       if (c.j == 0 && a.dgate_t != nullptr) {
         if (a.p32)
@@ -191,11 +191,11 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_bwd_kernel
           static_cast<T*>(a.dgate_t)[t] = from_f32<T>(cfd);
       }
       const f2 nk1 = f2_of(-k1), grf = f2_of(gt * rf);
-      const f2 nm2 = f2_of(post ? -(rf * rf) * (gt * cfd * inv) : 0.f);
+      const f2 nm2 = f2_of(-(rf * rf) * (gt * cfd * inv));
 #pragma unroll
       for (int i = 0; i < PIECES; ++i)
         if (c.has_piece(i)) {
-          f2 x[P], o[P], f[P], dn[P], cf[P], w[P];
+          f2 x[P], o[P], f[P], dn[P], cf[P], w[P], q[P];
           params(i, cf, w);
           if constexpr (KEEP) {
 #pragma unroll
@@ -209,9 +209,15 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_bwd_kernel
           for (int k = 0; k < P; ++k) {
             const int e = i * P + k;
             x[k] = f2_fma(nk1, o[k], x[k]);
-            const f2 q = f2_mul(grf, x[k]);
-            K[e] = f2_fma(f[k], q, K[e]);
-            f[k] = f2_fma(cf[k], q, f2_mul(nm2, f[k]));
+            q[k] = f2_mul(grf, x[k]);
+            K[e] = f2_fma(f[k], q[k], K[e]);
+          }
+          if (post) {
+#pragma unroll
+            for (int k = 0; k < P; ++k) f[k] = f2_fma(cf[k], q[k], f2_mul(nm2, f[k]));
+          } else {  // (df holds no f, which may be infinite)
+#pragma unroll
+            for (int k = 0; k < P; ++k) f[k] = f2_mul(cf[k], q[k]);
           }
           put_piece<R>(c, a.dx.row(t), i, x);
           if (has_f) put_piece<T>(c, a.df.row(t), i, f);
@@ -294,7 +300,7 @@ __global__ void __launch_bounds__(LOOP_THREADS) resnorm_dx_loop_kernel(const Bwd
     const float m1 = block_sum(s1, s) * inv;
     s2 = block_sum(s2, s);
     s3 = block_sum(s3, s);
-    const float cfd = s2 - ro * m1 * s3;
+    const float cfd = pre ? s2 - ro * m1 * s3 : s2;  // (f may be infinite)
     if (threadIdx.x == 0) {
       if (a.mean_ov != nullptr) a.mean_ov[t] = m1;
       if (a.dgate_t != nullptr) {
@@ -304,14 +310,15 @@ __global__ void __launch_bounds__(LOOP_THREADS) resnorm_dx_loop_kernel(const Bwd
           static_cast<T*>(a.dgate_t)[t] = from_f32<T>(cfd);
       }
     }
-    const float m2 = post ? gt * cfd * inv : 0.f;
+    const float m2 = gt * cfd * inv;
     for (int i = threadIdx.x * U; i < a.H; i += LOOP_THREADS * U) {
       float d[U], oh[U], v[U], fh[U], cf[U];
       unit(i, d, oh, v, fh, cf);
 #pragma unroll
       for (int j = 0; j < U; ++j) {
         d[j] = fmaf(ro, fmaf(-m1, oh[j], v[j]), d[j]);
-        fh[j] = rf * fmaf(-m2, fh[j], cf[j] * (gt * d[j]));
+        const float q = cf[j] * (gt * d[j]);
+        fh[j] = post ? rf * fmaf(-m2, fh[j], q) : q;  // (rf = 1 without the norm)
       }
       put_unit<R, U>(a.dx.row(t) + i, d);
       if (has_f) put_unit<T, U>(a.df.row(t) + i, fh);
