@@ -113,6 +113,8 @@ class MoEBlock:
         device: the gradients of the balance and the z loss (their coefficients).  With next_norm
         dnext is the gradient of next (dout may then be None); with first=False dn stands behind
         dx and the gradients: that of the forward's n, the block in front's dnext."""
+        if dnext is not None and not self.next_norm:
+            raise ValueError("dnext: this block gives no next (next_norm)")
         if self._kept is None:
             raise RuntimeError("backward needs a forward first")
         x, n, idx, w, seq_offsets, mask, *rest = self._kept
