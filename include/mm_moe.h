@@ -498,7 +498,7 @@ MM_MOE_API mm_moe_status mm_moe_select_backward(const mm_moe_select* select, con
 
 /* mm_moe_router_forward and _backward with this choice in the place of theirs.  select: the
  * shape's T, E and k, fp32 logits and a bf16 gradient (else MM_MOE_EINVAL); logits: the forward's;
- * dlogits_aux may be NULL. */
+ * dlogits_aux may be NULL; dlogits must not overlap either (MM_MOE_EINVAL). */
 MM_MOE_API mm_moe_status mm_moe_router_select_forward(
     const mm_moe_shape* shape, const mm_moe_select* select, const uint16_t* x,
     const uint16_t* W_router, const float* bias, float* logits, int32_t* topk_idx, float* topk_w,

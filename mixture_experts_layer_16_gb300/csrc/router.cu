@@ -278,7 +278,7 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_router_select_backward(
   if (!router_select_ok(shape, select)) return MM_MOE_EINVAL;
   if (!al(x, 16) || !al(W_router, 16) || !al(logits, 16) || !al(topk_idx, 4) || !al(dtopk_w, 4) ||
       (dlogits_aux != nullptr && !al(dlogits_aux, 4)) || !al(dlogits, 16) || !al(dx, 16) ||
-      !al(dW_router, 16))
+      !al(dW_router, 16) || !select_bwd_apart(select, logits, dlogits_aux, dlogits))
     return MM_MOE_EINVAL;
   int sms = 0;
   if (!device_ok(&sms)) return MM_MOE_ENOTSUP;

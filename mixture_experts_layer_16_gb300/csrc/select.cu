@@ -186,6 +186,18 @@ bool select_ok(const mm_moe_select* s) {
   return s->k <= s->E / s->groups * s->topk_groups;
 }
 
+bool select_bwd_apart(const mm_moe_select* s, const void* logits, const float* aux,
+                      const void* dlogits) {
+  const size_t n = static_cast<size_t>(s->T * s->E);
+  const uintptr_t out = reinterpret_cast<uintptr_t>(dlogits);
+  const uintptr_t end = out + n * dtype_bytes(s->grad_dtype);
+  const auto apart = [&](const void* p, size_t bytes) {
+    const uintptr_t in = reinterpret_cast<uintptr_t>(p);
+    return p == nullptr || out >= in + bytes || in >= end;
+  };
+  return apart(logits, n * dtype_bytes(s->dtype)) && apart(aux, n * 4);
+}
+
 static SelArgs make_args(const mm_moe_select* s) {
   SelArgs a{};
   a.T = static_cast<int>(s->T);
@@ -270,12 +282,6 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_select_forward(const mm_moe_select* s
   return op_status(launch_select_fwd(c, select, logits, bias, topk_idx, topk_w));
 }
 
-// whether [a, a + an) and [b, b + bn) share a byte
-static bool meet(const void* a, size_t an, const void* b, size_t bn) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + bn && y < x + an;
-}
-
 extern "C" MM_MOE_API mm_moe_status mm_moe_select_backward(
     const mm_moe_select* select, const void* logits, const int32_t* topk_idx,
     const float* dtopk_w, const float* dlogits_aux, void* dlogits, void* stream) {
@@ -283,11 +289,7 @@ extern "C" MM_MOE_API mm_moe_status mm_moe_select_backward(
       !al(dtopk_w, 4) || (dlogits_aux != nullptr && !al(dlogits_aux, 4)) ||
       !al(dlogits, dtype_bytes(select->grad_dtype)))
     return MM_MOE_EINVAL;
-  const size_t n = static_cast<size_t>(select->T * select->E);
-  const size_t out = n * dtype_bytes(select->grad_dtype);
-  if (meet(dlogits, out, logits, n * dtype_bytes(select->dtype)) ||
-      (dlogits_aux != nullptr && meet(dlogits, out, dlogits_aux, n * 4)))
-    return MM_MOE_EINVAL;
+  if (!select_bwd_apart(select, logits, dlogits_aux, dlogits)) return MM_MOE_EINVAL;
   const int sms = sm_count_103();
   if (sms == 0) return MM_MOE_ENOTSUP;
   int launches = 0;

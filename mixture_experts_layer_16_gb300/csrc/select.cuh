@@ -46,6 +46,10 @@ __device__ __forceinline__ V sum_of(V v) {
 }
 
 bool select_ok(const mm_moe_select* s);
+// Whether the backward's gradient lies apart from the logits and the auxiliary gradient, of which other
+// CTAs still read rows when it is written.
+bool select_bwd_apart(const mm_moe_select* s, const void* logits, const float* aux,
+                      const void* dlogits);
 cudaError_t launch_select_fwd(const Ctx& c, const mm_moe_select* s, const void* logits,
                               const float* bias, int32_t* idx, float* w);
 cudaError_t launch_select_bwd(const Ctx& c, const mm_moe_select* s, const void* logits,
