@@ -49,7 +49,8 @@ class MoEResidualNorm:
         self.workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
         self._rows, self._cols = torch.Size((self.T, self.H)), torch.Size((self.H,))
         self._gates = torch.Size((self.H if gate == "channel" else self.T,))
-        self._ran = None  # whether a forward has left what a backward reads, and whether it had an f
+        # whether a backward may have an f (False, True or both), once a forward has left what it reads
+        self._with_f: Tuple[bool, ...] = ()
         self._where = -1 if self.device.index is None else self.device.index
 
     def _check_rows(self, t, name, dtype):
@@ -92,7 +93,8 @@ class MoEResidualNorm:
         _on(self.device, B.mm_moe_resnorm_forward, self.shape, x, f, post_weight, gate, pre_weight,
             out, n, self.rstd_f, self.rstd_out,
             _stream(stream, self.device, out if has_f else None, n, self.rstd_f, self.rstd_out))
-        self._ran = has_f
+        # (without a norm behind the block a forward of the norm alone keeps what one with f would)
+        self._with_f = (True,) if has_f else (False,) if self.post else (False, True)
         return out, n
 
     def load_stats(self, rstd_f=None, rstd_out=None) -> None:
@@ -106,11 +108,10 @@ class MoEResidualNorm:
                 _need(t, name, torch.Size((self.T,)), torch.float32, self.device)
         if self.pre and rstd_out is None:
             raise ValueError("rstd_out: needed with a norm in front of the next block")
-        has_f = rstd_f is not None or not self.post
         for mine, t in ((self.rstd_f, rstd_f), (self.rstd_out, rstd_out)):
             if t is not None:
                 mine.copy_(t)
-        self._ran = has_f
+        self._with_f = (rstd_f is not None,) if self.post else (False, True)
 
     def backward(self, dout, dn=None, out=None, f=None, post_weight=None, gate=None,
                  pre_weight=None, stream=None
@@ -132,11 +133,10 @@ class MoEResidualNorm:
         if has_f:
             self._check_rows(f, "f", self.dtype)
         self._check_params(has_f, post_weight, gate, pre_weight)
-        if self._ran is None:
+        if not self._with_f:
             raise RuntimeError("backward needs a forward first")
-        if self._ran != has_f and (self.post or not has_f):
-            raise ValueError("f: as the forward had it" if self.post or self._ran else
-                             "f: the forward had none")
+        if has_f not in self._with_f:
+            raise ValueError("f: as the forward had it")
         dx = torch.empty(self._rows, dtype=self.res_dtype, device=self.device)
         df = torch.empty(self._rows, dtype=self.dtype, device=self.device) if has_f else None
         grads = {name: torch.empty_like(t) for name, t in
