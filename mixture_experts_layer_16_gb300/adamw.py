@@ -74,18 +74,27 @@ class MoEAdamW:
             self.m_scale = torch.zeros(total // 32, dtype=torch.uint8, device=d)
             self.v_scale = torch.zeros(total // 32, dtype=torch.uint8, device=d)
         self.counter = torch.zeros(4, dtype=torch.int64, device=d)
-        self.set_step(0)
+        self._put_step(0)
+
+    def _wait(self):
+        if self.device.type == "cuda":  # (a step may run on any stream)
+            torch.cuda.synchronize(self.device)
+
+    def _put_step(self, steps: int) -> None:
+        b1, b2 = self.betas
+        words = struct.unpack("<4q", struct.pack("<qddq", int(steps), b1 ** steps, b2 ** steps, 0))
+        self.counter.copy_(torch.tensor(words, dtype=torch.int64))
 
     def set_step(self, steps: int) -> None:
         """Says that `steps` steps lie behind (a checkpoint's moments); waits for the device."""
         if steps < 0:
             raise ValueError(f"steps must be >= 0, got {steps}")
-        b1, b2 = self.betas
-        words = struct.unpack("<4q", struct.pack("<qddq", int(steps), b1 ** steps, b2 ** steps, 0))
-        self.counter.copy_(torch.tensor(words, dtype=torch.int64))
+        self._wait()
+        self._put_step(steps)
 
     def steps(self) -> int:
         """The steps behind; waits for the device."""
+        self._wait()
         return int(self.counter[0])
 
     def _words(self, params, grads, masters):
