@@ -103,18 +103,18 @@ __global__ void __launch_bounds__(SEL_THREADS) select_bwd_kernel(
 #pragma unroll
       for (int j = 0; j < U; ++j) m = fmaxf(m, v[u][j]);
     }
-    m = max_of<W>(m);
+    m = finite_max(max_of<W>(m));
     float z = 0.f;
 #pragma unroll
     for (int u = 0; u < NU; ++u)
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        v[u][j] = m == -INFINITY ? 0.f : expf(v[u][j] - m);
+        v[u][j] = expf(v[u][j] - m);
         z += v[u][j];
       }
     z = sum_of<W>(z);
-    rz = m == -INFINITY ? 0.f : 1.f / z;
-    const float s = mine && m != -INFINITY ? expf(l - m) * rz : 0.f;
+    rz = z == 0.f ? 0.f : 1.f / z;
+    const float s = mine ? expf(l - m) * rz : 0.f;
     A = sum_of<W>(mine ? g * s : 0.f);
     d = s * g;  // (beside -s A, which every expert has)
     const float c = -a.scale * A * rz;
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(SEL_THREADS) select_bwd_kernel(
     d = mine ? a.scale * ds * s * sigmoid32(-l) : 0.f;
   } else {
     const float big = max_of<W>(l);
-    const float ex = mine && big != -INFINITY ? expf(l - big) : 0.f;
+    const float ex = mine && !(l == -INFINITY) ? expf(l - big) : 0.f;  // (of a NaN a NaN)
     const float sum = sum_of<W>(ex);
     const float q = sum == 0.f ? 0.f : ex / sum;
     d = a.scale * q * (g - sum_of<W>(mine ? g * q : 0.f));
@@ -159,8 +159,7 @@ __global__ void __launch_bounds__(SEL_THREADS) select_bwd_kernel(
   if (mine && __ffs(same) - 1 == sub * W + lane) {
     float f = sum;
     if constexpr (DENSE) {
-      const float s = m == -INFINITY ? 0.f : expf(l - m) * rz;
-      f = a.scale * (sum - s * A);
+      f = a.scale * (sum - expf(l - m) * rz * A);
     }
     if (ax != nullptr) f += __ldg(ax + e);
     out[e] = from_f32<O>(f);

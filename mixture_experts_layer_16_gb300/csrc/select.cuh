@@ -25,6 +25,13 @@ struct SelArgs {
 // The sigmoid within 10 2^-24 of itself.
 __device__ __forceinline__ float sigmoid32(float l) { return __fdividef(1.f, 1.f + expf(-l)); }
 
+// The largest of a row's logits (a NaN is passed over), in whose place e^(l - m) is finite.  Where all are
+// -inf it is 0: their sum is then 0, for scores of 0, and a NaN among them makes it NaN.
+template <typename F>
+__device__ __forceinline__ F finite_max(F m) {
+  return m == -INFINITY ? F(0) : m;
+}
+
 // Reductions over W lanes.
 template <int W>
 __device__ __forceinline__ float max_of(float v) {

@@ -42,12 +42,6 @@ namespace mmmoe {
 constexpr int SEL_FILL = 4;
 
 __device__ __forceinline__ float low_nan(float f) { return fmaxf(f, -INFINITY); }
-// The largest of a row's logits (a NaN is passed over), in whose place e^(l - m) is finite.  Where all are
-// -inf it is 0: their sum is then 0, for scores of 0, and a NaN among them makes it NaN.
-template <typename F>
-__device__ __forceinline__ F finite_max(F m) {
-  return m == -INFINITY ? F(0) : m;
-}
 // For the choice alone, with the hardware's approximations (each within 2 ulp, the exponential's
 // argument rounded): e^d within (|d| + 4) 2^-23 of itself, the sigmoid within 2^-21 of 1.
 __device__ __forceinline__ float exp_key(float d) {
