@@ -285,7 +285,8 @@ __device__ __noinline__ bool groups64(const T* __restrict__ row, const float* __
     t1 = fmax(fmin(t0, o0), fmax(t1, o1));
     t0 = fmax(t0, o0);
   }
-  const double g = a.top2 && a.gs > 1 ? t0 + t1 : t0;
+  double g = a.top2 && a.gs > 1 ? t0 + t1 : t0;
+  if (g != g) g = -INFINITY;  // (both infinities)
   const int mine = lane / a.lpg, within = lane % a.lpg;
   int rank = 0;
   for (int o = 0; o < a.G; o += a.lpg) {
