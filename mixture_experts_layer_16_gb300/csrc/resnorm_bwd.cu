@@ -39,16 +39,19 @@ constexpr int rn_bwd_steps(int params) {
   return std::max(1, std::min(4, (RN_SMEM - params) / (RN_THREADS * rn_bwd_bytes<T, R, NU, 8>)));
 }
 
-// S: steps of the ring (units of 8).  WHOLE: dout, dn and f are all there.  dx, df and the CTA's column
-// sums in one read; the column sums stay in the registers of the threads that own the columns, which
-// leaves none for c and w: they are read from shared memory (in registers, with 72 bytes of spills:
-// 16384 x 2048 bf16 92 us).
+// What a launch has: any of the operands; dout, dn and f; these and the norm behind the block (asked for
+// at run time that norm's term of df costs 3% of 16384 x 2048 bf16).
+enum Have { SOME, ALL, ALL_POST };
+
+// S: steps of the ring (units of 8).  dx, df and the CTA's column sums in one read; the column sums stay
+// in the registers of the threads that own the columns, which leaves none for c and w: they are read from
+// shared memory (in registers, with 72 bytes of spills: 16384 x 2048 bf16 92 us).
 // 16384 x 2048 with the launch that ends it: 68.4 us in bf16 (0.87 of the copy rate), 100.5 with an fp32
 // residual stream (0.89; its rows in halves of sectors 135, not on their way to L2 a row ahead 120); one
 // unit a thread, eight warps a row: 93 and 130.
-template <typename T, typename R, int NU, int U, int S, bool WHOLE>
+template <typename T, typename R, int NU, int U, int S, Have HAVE>
 __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_bwd_kernel(const BwdOps<T, R> a) {
-  constexpr bool SHARED = U == 8;
+  constexpr bool SHARED = U == 8, WHOLE = HAVE != SOME;
   using OT = Operand<T, NU, U>;
   using OR = Operand<R, NU, U>;
   extern __shared__ __align__(16) unsigned char ring_bytes[];
@@ -69,7 +72,7 @@ __global__ void __launch_bounds__(RN_THREADS, rn_ctas<NU, U>) resnorm_bwd_kernel
   const float inv = 1.f / static_cast<float>(a.H);
   const bool pre = WHOLE || a.dn.p != nullptr, has_f = WHOLE || a.f.p != nullptr,
              has_d = WHOLE || a.dout.p != nullptr;
-  const bool post = a.w_post != nullptr;
+  const bool post = HAVE == ALL_POST || a.w_post != nullptr;
   const auto issue = [&](uint32_t at) {
     if (ta < n) {
       if (has_d) OR::issue(c, a.dout.row(ta), at, piece);
@@ -317,11 +320,14 @@ __global__ void __launch_bounds__(LOOP_THREADS) resnorm_dx_loop_kernel(const Bwd
 #pragma unroll
       for (int j = 0; j < U; ++j) {
         d[j] = fmaf(ro, fmaf(-m1, oh[j], v[j]), d[j]);
-        const float q = cf[j] * (gt * d[j]);
-        fh[j] = post ? rf * fmaf(-m2, fh[j], q) : q;  // (rf = 1 without the norm)
+        cf[j] *= gt * d[j];
+      }
+      if (post) {  // (without the norm df holds no f, which may be infinite)
+#pragma unroll
+        for (int j = 0; j < U; ++j) cf[j] = rf * fmaf(-m2, fh[j], cf[j]);
       }
       put_unit<R, U>(a.dx.row(t) + i, d);
-      if (has_f) put_unit<T, U>(a.df.row(t) + i, fh);
+      if (has_f) put_unit<T, U>(a.df.row(t) + i, cf);
     }
   }
 }
@@ -415,9 +421,11 @@ static cudaError_t bwd_launch_steps(const Ctx& c, const BwdOps<T, R>& a, const N
   size_t smem = U == 8 ? static_cast<size_t>(S) * nt * rn_bwd_bytes<T, R, NU, U> + params
                        : static_cast<size_t>(a.steps) * a.step_bytes;
   if (g.groups > 1) smem = std::max(smem, sizeof(float) * 2 * g.groups * a.H);
-  const bool whole = a.dout.p != nullptr && a.dn.p != nullptr && a.f.p != nullptr;
-  auto* kern = whole ? resnorm_bwd_kernel<T, R, NU, U, S, true>
-                     : resnorm_bwd_kernel<T, R, NU, U, S, false>;
+  const bool all = a.dout.p != nullptr && a.dn.p != nullptr && a.f.p != nullptr;
+  auto* kern = all ? resnorm_bwd_kernel<T, R, NU, U, S, ALL> : resnorm_bwd_kernel<T, R, NU, U, S, SOME>;
+  if constexpr (U == 8) {
+    if (all && a.w_post != nullptr) kern = resnorm_bwd_kernel<T, R, NU, U, S, ALL_POST>;
+  }
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
   return launch_k(c.stream, kern, dim3(g.ctas), dim3(nt), smem, a);
