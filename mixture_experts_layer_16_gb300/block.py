@@ -95,6 +95,7 @@ class MoEBlock:
             n = self.norm.forward(x, p["norm_weight"], p["norm_bias"])
         elif self.first:
             n = self.norm.forward(x, pre_weight=p["norm_weight"])[1]
+        self._kept = None  # (from here on the handles hold parts of this forward)
         idx, w = self.router.forward(n, p["W_router"], bias=bias)
         losses, counts = self.balance.forward(self.router.logits, idx, seq_offsets, mask)
         f = self.layer.forward(n, idx, w, p["W_gate"], p["W_up"], p["W_down"])
