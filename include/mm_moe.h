@@ -565,7 +565,8 @@ typedef struct {
   uint32_t seed;        /* of the 8-bit states' rounding */
 } mm_moe_adamw;
 typedef struct {
-  void* param;         /* device, contiguous, aligned to its element; in and out */
+  void* param;         /* device, contiguous, aligned to its element; in and out.  Tensors whose
+                        * operands all lie on 16-byte (fp32: 32-byte) boundaries run faster */
   float* master;       /* of a 16-bit parameter, or NULL; in and out */
   const void* grad;
   int64_t numel;       /* >= 0 (0: the pointers are not looked at); at most 2^41 together */

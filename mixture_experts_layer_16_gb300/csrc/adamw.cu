@@ -22,7 +22,8 @@
 // Bytes bound the step: a bf16 parameter with a master and a bf16 gradient moves 28 bytes with fp32
 // moments, 16 with 8-bit ones.  The benchmark layer's 604 M parameters take 2.65 ms (0.94 of the copy
 // rate), 200 M in 48 tensors with 8-bit moments 0.57 (0.84: 75 instructions an element, two thirds of
-// the issue slots).
+// the issue slots).  A tensor with an operand on no vector boundary goes element by element: these 200 M 0.81,
+// 1.12 for 0.88 with fp32 moments.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -261,8 +261,8 @@ static cudaError_t fwd_launch(const Ctx& c, FwdOps<T, R> a) {
   constexpr bool MAY = U == 8 && NU > 1;  // (NU = 1: a row or two a group)
   const bool joint = MAY && a.GT > (sizeof(R) == 2 ? 32 : 128);
   // two groups of up to 384 threads (in 80 registers) where 512 threads would be one, which waits at its
-  // barrier: 6000 x 5120 bf16 52.5 -> 41.5 us, x 6144 88.7 -> 60.8; where more groups fit anyway 512 threads
-  // are as fast (x 3584) or faster (16384 x 2048 45.9, 47.6 with six groups for four)
+  // barrier: 6000 x 5120 bf16 52.5 -> 41.5 us, x 6144 88.7 -> 60.8 (elsewhere 51.8); where more groups fit
+  // anyway 512 threads are as fast (x 3584) or faster (16384 x 2048 45.9, 47.6 with six groups for four)
   constexpr int MORE = MAY && sizeof(R) == 2 ? 768 : RN_THREADS;
   const bool more = a.GT > RN_THREADS / 2 && 2 * a.GT <= MORE;
   const NormGrid g = rn_grid(a.GT, a.T_, c.num_sms * rn_ctas<NU, U>, more ? MORE : RN_THREADS);

@@ -46,7 +46,7 @@ enum Have { SOME, ALL, ALL_POST };
 // S: steps of the ring (units of 8).  dx, df and the CTA's column sums in one read; the column sums stay
 // in the registers of the threads that own the columns, which leaves none for c and w: they are read from
 // shared memory (in registers, with 72 bytes of spills: 16384 x 2048 bf16 92 us).
-// 16384 x 2048 with the launch that ends it: 68.4 us in bf16 (0.87 of the copy rate), 100.5 with an fp32
+// 16384 x 2048 with the launch that ends it: 68.0 us in bf16 (0.87 of the copy rate), 99.3 with an fp32
 // residual stream (0.89; its rows in halves of sectors 135, not on their way to L2 a row ahead 120); one
 // unit a thread, eight warps a row: 93 and 130.
 template <typename T, typename R, int NU, int U, int S, Have HAVE>

@@ -26,7 +26,7 @@
 
 namespace mmmoe {
 
-constexpr int SEL_THREADS = 256;  // of the backward's CTAs: a warp a token
+constexpr int SEL_THREADS = 256;  // of the backward's CTAs (8 to 32 lanes a token)
 
 // ----------------------------------------------------------------------- backward
 // U consecutive elements: 16-byte accesses for U > 1

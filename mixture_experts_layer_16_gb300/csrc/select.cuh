@@ -22,7 +22,8 @@ struct SelArgs {
   float scale;
 };
 
-// The sigmoid within 10 2^-24 of itself.
+// The sigmoid within 10 2^-24 of itself for l >= -87; below it falls to 0 (the division's result is 0 for
+// divisors above 2^126).
 __device__ __forceinline__ float sigmoid32(float l) { return __fdividef(1.f, 1.f + expf(-l)); }
 
 // The largest of a row's logits (a NaN is passed over), in whose place e^(l - m) is finite.  Where all are

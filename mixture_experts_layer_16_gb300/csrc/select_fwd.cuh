@@ -15,7 +15,7 @@
 // fp64 keys (131072 tokens x 256 experts of unit variance: some 80 pairs, a dozen groups).  So the indices
 // do not depend on how a kernel rounds.  Without a bias the keys are the logits as they are.
 //
-// 131072 x 256 fp32: 73 us with a bias and four of eight groups, 60 without groups, 47 without a bias
+// 131072 x 256 fp32: 72 us with a bias and four of eight groups, 59 without groups, 47 without a bias
 // (the row's bytes take 20): 410 instructions a token, issued in 64% of the cycles, the ALU pipe
 // (comparisons, selections) busy in 46%.  By rounds of a warp's largest head over sorted
 // lanes, a warp a token, it took 139; with 16 lanes a token 98; with the next row on its way meanwhile 87
@@ -42,7 +42,8 @@ namespace mmmoe {
 constexpr int SEL_FILL = 4;
 
 __device__ __forceinline__ float low_nan(float f) { return fmaxf(f, -INFINITY); }
-// For the choice alone, with the hardware's approximations (each within 2 ulp, the exponential's
+// For the choice and the sum under a softmax (whose terms' errors, weighted by the terms, stay within 2^-19
+// of it), with the hardware's approximations (each within 2 ulp, the exponential's
 // argument rounded): e^d within (|d| + 4) 2^-23 of itself, the sigmoid within 2^-21 of 1.
 __device__ __forceinline__ float exp_key(float d) {
   float r;
@@ -717,7 +718,8 @@ __device__ __noinline__ unsigned long long small_places64(const T* __restrict__ 
 
 // Up to N experts, all groups taking part: a thread a token, its keys in registers, every expert's
 // place the number of keys in front of its own; pairs within each other's errors are compared anew.
-// 131072 x 8 fp32 3.8 us (27 in eight lanes a token), 131072 x 16 9.1.
+// 131072 x 8 fp32 4.0 us (27 in eight lanes a token), 131072 x 16 9.4; with a bias 7.0 and 24 (sigmoid),
+// 8.2 and 35 (softmax).
 template <typename T, int N, bool BIAS>
 __global__ void __launch_bounds__(128) select_small_kernel(
     const T* __restrict__ logits, const float* __restrict__ bias, const SelArgs a,
